@@ -122,6 +122,17 @@ def load() -> ctypes.CDLL:
     FP = ctypes.POINTER(ctypes.c_float)
     lib.libconv_fold_batchnorm.argtypes = [FP] * 6 + [ctypes.c_float, I, I, FP, FP]
     lib.libconv_fold_batchnorm.restype = I
+    F = ctypes.c_float
+    lib.libconv_qk_norm_rope.argtypes = [P] * 12 + [I] * 10 + [F, I, P]
+    lib.libconv_qk_norm_rope.restype = I
+    lib.libconv_prefix_attention.argtypes = [P] * 9 + [I] * 7 + [F, I, I, P, LL, P]
+    lib.libconv_prefix_attention.restype = I
+    lib.libconv_prefix_attention_workspace.argtypes = [I] * 8
+    lib.libconv_prefix_attention_workspace.restype = LL
+    lib.libconv_lora_linear.argtypes = [P] * 9 + [I] * 6 + [LL, LL, I, P, LL, P]
+    lib.libconv_lora_linear.restype = I
+    lib.libconv_lora_workspace.argtypes = [I] * 7
+    lib.libconv_lora_workspace.restype = LL
     _lib = lib
     return lib
 
@@ -311,6 +322,43 @@ def libconv_forward_packed(x, packed_w, bias, y, N, C_in, T, H, W, C_out, KT, KH
     return load().libconv_forward_packed(x, packed_w, bias, y, N, C_in, T, H, W, C_out, KT, KH,
                                          KW, pad_t, pad_h, pad_w, stride_t, stride_h, stride_w,
                                          dtype, act, stream)
+
+
+def libconv_qk_norm_rope(q, k, v, q_out, k_out, v_out, q_weight, k_weight, freqs, positions,
+                         slots, strides, T, q_heads, k_heads, head_dim, rot_dim, pairs0, pairs1,
+                         pairs2, interleaved, out_rows, eps, dtype, stream) -> int:
+    """strides: ctypes array of 12 long longs (host)."""
+    return load().libconv_qk_norm_rope(q, k, v, q_out, k_out, v_out, q_weight, k_weight, freqs,
+                                       positions, slots, strides, T, q_heads, k_heads, head_dim,
+                                       rot_dim, pairs0, pairs1, pairs2, interleaved, out_rows,
+                                       eps, dtype, stream)
+
+
+def libconv_prefix_attention(q, k_prefix, v_prefix, k, v, lengths, out, lse, strides, B, Sq, P, S,
+                             q_heads, k_heads, head_dim, scale, causal, dtype, workspace,
+                             workspace_bytes, stream) -> int:
+    """strides: ctypes array of 16 long longs (host)."""
+    return load().libconv_prefix_attention(q, k_prefix, v_prefix, k, v, lengths, out, lse,
+                                           strides, B, Sq, P, S, q_heads, k_heads, head_dim,
+                                           scale, causal, dtype, workspace, workspace_bytes,
+                                           stream)
+
+
+def libconv_prefix_attention_workspace(B, Sq, P, S, q_heads, k_heads, head_dim, dtype) -> int:
+    return load().libconv_prefix_attention_workspace(B, Sq, P, S, q_heads, k_heads, head_dim,
+                                                     dtype)
+
+
+def libconv_lora_linear(x, w, bias, a, b, scales, row_starts, adapters, y, T, K, N, rank,
+                        n_adapters, n_requests, x_stride, y_stride, dtype, workspace,
+                        workspace_bytes, stream) -> int:
+    return load().libconv_lora_linear(x, w, bias, a, b, scales, row_starts, adapters, y, T, K, N,
+                                      rank, n_adapters, n_requests, x_stride, y_stride, dtype,
+                                      workspace, workspace_bytes, stream)
+
+
+def libconv_lora_workspace(T, K, N, rank, n_adapters, n_requests, dtype) -> int:
+    return load().libconv_lora_workspace(T, K, N, rank, n_adapters, n_requests, dtype)
 
 
 def libconv_query_algo(N, C_in, T, H, W, C_out, KT, KH, KW, pad_t, pad_h, pad_w,
@@ -841,3 +889,7 @@ def conv3d(x, w, b=None, stride=1, padding=0, act="none", algo="auto", out=None,
     if x.dim() != 5:
         raise ValueError("conv3d takes NCDHW")
     return conv_nd(x, w, b, stride, padding, act, algo, out, stream, workspace)
+
+
+from .attention import (  # noqa: E402  (the helpers above are what these call)
+    lora_linear, prefix_attention, qk_norm_rope, rotary_frequencies)

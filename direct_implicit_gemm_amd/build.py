@@ -29,6 +29,8 @@ SAN_LIB_PATH = os.path.join(HERE, "libconv_san.so")
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
              "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
 SOURCES = ["api.cpp", "direct.hip", "igemm.hip", "layout.hip",
+           # the attention-layer operators
+           "layer_api.cpp", "rope.hip", "attention.hip", "lora.hip",
            # the implicit-GEMM tiles, one unit per group so that they build in parallel
            "igemm_inst_a.hip", "igemm_inst_b.hip", "igemm_inst_c.hip", "igemm_inst_d.hip",
            "igemm_inst_e.hip"]

@@ -452,6 +452,16 @@ libconv_status plan_query(Problem& p, int algo, int flags, Plan* plan) {
 
 }  // namespace
 
+bool current_device(int* cus) {
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || !device_ok(dev)) {
+    (void)hipGetLastError();
+    return false;
+  }
+  *cus = g_dev_cus[dev];
+  return true;
+}
+
 }  // namespace libconv
 
 using namespace libconv;

@@ -135,6 +135,77 @@ template <> struct Elem<DT_BF16> {
   }
 };
 
+// Wait until at most N of this wave's global reads are outstanding (gfx9
+// s_waitcnt encoding: vmcnt in bits 3:0 and 15:14; expcnt and lgkmcnt left
+// at their maxima, i.e. not waited for).
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  constexpr int n = N > 63 ? 63 : N;
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Workgroup barrier for LDS hand-over: this wave's LDS writes complete, then
+// s_barrier.  Unlike __syncthreads() it does not wait for outstanding global
+// reads (those of later stages stay in flight); the "memory" clobber keeps the
+// compiler from moving LDS accesses across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// One 16-byte global read per lane written straight into LDS: lane l's
+// vector lands at dst + 16 l (dst is wave-uniform).  Kept out of the generic
+// lambdas of the kernel: inside them the host pass drops the kernel's launch
+// stub.
+__device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* dst,
+                                              int off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16,
+                                           off, 0, 0, 0);
+}
+
+// This wave's LDS accesses so far are complete and none of the later ones
+// is moved above this point (a wave-private LDS region changes hands between
+// lanes of the same wave).
+__device__ __forceinline__ void lds_fence() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// One MFMA k-step over a pair of 16-byte slots.  KSUB is the number of
+// instructions a slot pair takes; step(.., k) issues sub-step k.
+template <int DT> struct Mma;
+
+template <> struct Mma<DT_F16> {
+  static constexpr int SE = 8;  // elements per 16-byte slot
+  static constexpr int KSUB = 1;
+  __device__ static __forceinline__ void step(const u32x4_t& a, const u32x4_t& b, float16_t& c,
+                                              int) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, a),
+                                               __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+  }
+};
+
+template <> struct Mma<DT_BF16> {
+  static constexpr int SE = 8;
+  static constexpr int KSUB = 1;
+  __device__ static __forceinline__ void step(const u32x4_t& a, const u32x4_t& b, float16_t& c,
+                                              int) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  }
+};
+
+// fp32: 32x32x2, lanes 0-31 give K index 0 (slot 2p), lanes 32-63 K index 1
+// (slot 2p+1); sub-step k multiplies element k of both slots.  The fragment
+// is reinterpreted as a whole float4 before indexing: bit-casting a single
+// vector element has been seen to compile to element 0 for every k.
+template <> struct Mma<DT_F32> {
+  static constexpr int SE = 4;
+  static constexpr int KSUB = 4;
+  __device__ static __forceinline__ void step(const u32x4_t& a, const u32x4_t& b, float16_t& c,
+                                              int k) {
+    const float4_t af = __builtin_bit_cast(float4_t, a);
+    const float4_t bf = __builtin_bit_cast(float4_t, b);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(af[k], bf[k], c, 0, 0, 0);
+  }
+};
+
 // Bias + activation, applied to the fp32 accumulator before the one rounding
 // to the storage dtype.  ReLU maps NaN to 0, like max(v, 0) on the host.
 __device__ __forceinline__ float epilogue(float acc, float bias, int relu) {

@@ -90,6 +90,12 @@ long long cpack_bytes(int N, int C, long long spatial, int dtype);
 libconv_status layout_launch(const void* src, void* dst, int N, int C, long long spatial,
                              int dtype, bool to_packed, hipStream_t stream);
 
+// Whether the current device is a gfx950; its compute units.
+bool current_device(int* cus);
+// Compute units that plans of the attention-layer operators count on (their
+// workspace sizes are asked for without a device).
+constexpr int kPlanCus = 256;
+
 const char* direct_tile_name(int id);
 const char* igemm_tile_name(int id);
 

@@ -1,0 +1,550 @@
+// lora.hip -- a projection shared by all rows with a low-rank adapter for
+// each request beside it.
+//
+//   y[t] = W x[t] + bias + s_a B_a (A_a x[t])
+//
+// Two launches.  The first forms the low-rank values A_a x[t] in fp32 (for
+// the rows of a tile: adapter by adapter, each lane keeping the result of its
+// own row's).  The second is the projection; a workgroup starts its sums with
+// the low-rank term of its tile, so y is written once.  That term's values
+// enter the matrix instructions as two bfloat16 numbers, high and low part
+// (16 significant bits): one would round the low-rank term to 8 bits before
+// the sum.  fp16 adapters are split the same way (three products), because a
+// low-rank value may be past fp16's range where y is not.
+//
+// The projection is formed transposed (outputs n on the rows of the matrix
+// instructions, tokens on their columns), so that a lane holds 4 consecutive
+// outputs of one token.  Both operands have their sums' axis dense: a stage
+// is 128 bytes of it, copied straight into LDS, double-buffered.  Up to 64
+// rows are bound by reading W once: a workgroup takes 16 outputs and its 8
+// waves split the sum's axis, reading W and x straight into registers.
+#include "device_common.h"
+#include "layer.h"
+
+namespace libconv {
+namespace {
+
+constexpr int kLowRows = 32;      // rows of a tile of the first launch
+constexpr int kLowWaves = 4;
+constexpr int kMaxRank = 128;
+
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int off) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// Adapter of each row of [row0, row0 + n) into LDS, -1 where there is none.
+// Threads take requests in turn and write the rows they have in the range.
+template <int THREADS>
+__device__ __forceinline__ void row_adapters(const LoraArgs& a, int row0, int n, int* out) {
+  for (int i = threadIdx.x; i < n; i += THREADS) out[i] = -1;
+  lds_barrier();
+  for (int r = threadIdx.x; r < a.n_requests; r += THREADS) {
+    const int ad = a.adapters[r];
+    if (ad < 0 || ad >= a.n_adapters) continue;
+    const int s0 = a.starts[r], s1 = a.starts[r + 1];
+    const int lo = s0 > row0 ? s0 : row0, hi = s1 < row0 + n ? s1 : row0 + n;
+    for (int t = lo; t < hi; ++t) out[t - row0] = ad;
+  }
+  lds_barrier();
+}
+
+// low[split][t][r] = sum over the split's part of K of x[t][k] A[r][k].
+template <int DT>
+__global__ __launch_bounds__(64 * kLowWaves) void low_kernel(const LoraArgs a) {
+  constexpr int EB = Elem<DT>::bytes;
+  __shared__ int ad_of[kLowRows];
+  __shared__ float red[kLowWaves][32][33];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, half = lane >> 5;
+  const int row0 = blockIdx.x * kLowRows, split = blockIdx.y;
+  row_adapters<64 * kLowWaves>(a, row0, kLowRows, ad_of);
+
+  const int row_bytes = a.K * EB;
+  const int steps = (row_bytes + 31) / 32;
+  const int parts = a.low_splits * kLowWaves, part = split * kLowWaves + wave;
+  const int k0 = (int)((long long)steps * part / parts);
+  const int k1 = (int)((long long)steps * (part + 1) / parts);
+
+  const bool row_ok = row0 + l32 < a.T;
+  const int mine = ad_of[l32];
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)row0 * a.x_row, 0x7ffffff0u);
+  const int x_off = l32 * (int)a.x_row;
+
+  for (int r0 = 0; r0 < a.low_width; r0 += 32) {
+    float16_t res = {};
+    uint64_t left = __ballot(mine >= 0 && row_ok);
+    const bool rank_ok = r0 + l32 < a.rank;
+    while (left) {
+      const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+      left &= ~__ballot(mine == ad);
+      const __amdgpu_buffer_rsrc_t ra =
+          make_rsrc(a.a + ((long long)ad * a.rank + r0) * row_bytes, 0x7ffffff0u);
+      const int a_off = l32 * row_bytes;
+      float16_t acc = {};
+      constexpr int U = 4;
+      for (int k = k0; k < k1; k += U) {
+        u32x4_t xf[U], af[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int off = (k + u) * 32 + half * 16;
+          const bool in = k + u < k1 && off < row_bytes;
+          xf[u] = load16(rx, guard_offset(in && row_ok, x_off + off));
+          af[u] = load16(ra, guard_offset(in && rank_ok, a_off + off));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(af[u], xf[u], acc, e);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) res[i] = mine == ad ? acc[i] : res[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) red[wave][l32][(i & 3) + 8 * (i >> 2) + 4 * half] = res[i];
+    lds_barrier();
+    for (int i = threadIdx.x; i < 32 * 32; i += 64 * kLowWaves) {
+      const int t = i >> 5, r = i & 31;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kLowWaves; ++w) sum += red[w][t][r];
+      if (row0 + t < a.T)
+        a.low[((long long)split * a.T + row0 + t) * a.low_width + r0 + r] = sum;
+    }
+    lds_barrier();
+  }
+}
+
+// The tile's low-rank values, summed over the splits, times the adapter's
+// scale, in LDS: fp32, or a high and a low bfloat16 part ([n][width] each).
+template <int DT, int THREADS>
+__device__ __forceinline__ void low_to_lds(const LoraArgs& a, int row0, int n, const int* ad_of,
+                                           unsigned char* lds) {
+  const int width = a.low_width;
+  for (int i = threadIdx.x; i < n * width; i += THREADS) {
+    const int t = i / width, r = i - t * width, ad = ad_of[t];
+    float v = 0.0f;
+    if (ad >= 0 && row0 + t < a.T) {
+      const float* p = a.low + (long long)(row0 + t) * width + r;
+      for (int s = 0; s < a.low_splits; ++s) v += p[(long long)s * a.T * width];
+      v *= a.scales[ad];
+    }
+    if constexpr (DT == DT_F32) {
+      reinterpret_cast<float*>(lds)[i] = v;
+    } else {
+      const uint16_t hi = Elem<DT_BF16>::from_f32(v);
+      const float rest = v - Elem<DT_BF16>::bits_to_f32(hi);
+      reinterpret_cast<uint16_t*>(lds)[i] = hi;
+      reinterpret_cast<uint16_t*>(lds)[n * width + i] = Elem<DT_BF16>::from_f32(rest);
+    }
+  }
+  lds_barrier();
+}
+
+// 16 bytes of row n of adapter ad's B, from component r on; 0 past the rank.
+template <int DT>
+__device__ __forceinline__ u32x4_t load_b(const LoraArgs& a, __amdgpu_buffer_rsrc_t rb, int n,
+                                          int r) {
+  constexpr int EB = Elem<DT>::bytes, E = 16 / EB;
+  const bool ok = n < a.N;
+  const int at = (n * a.rank + r) * EB;
+  if (a.rank % E == 0) return load16(rb, guard_offset(ok && r < a.rank, at));
+  u32x4_t v = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint32_t x = Elem<DT>::load_bits(rb, guard_offset(ok && r + e < a.rank, at + e * EB));
+    v[e * EB / 4] |= EB == 4 ? x : (x & 0xffffu) << (16 * (e & 1));
+  }
+  return v;
+}
+
+// 8 fp16 values as a high and a low bfloat16 part (8 + 8 bits hold all 11).
+__device__ __forceinline__ void split_f16(const u32x4_t& v, u32x4_t* hi, u32x4_t* lo) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float x0 = Elem<DT_F16>::bits_to_f32(v[j] & 0xffffu);
+    const float x1 = Elem<DT_F16>::bits_to_f32(v[j] >> 16);
+    const uint32_t h0 = Elem<DT_BF16>::from_f32(x0), h1 = Elem<DT_BF16>::from_f32(x1);
+    (*hi)[j] = h0 | (h1 << 16);
+    const uint32_t l0 = Elem<DT_BF16>::from_f32(x0 - Elem<DT_BF16>::bits_to_f32(h0));
+    const uint32_t l1 = Elem<DT_BF16>::from_f32(x1 - Elem<DT_BF16>::bits_to_f32(h1));
+    (*lo)[j] = l0 | (l1 << 16);
+  }
+}
+
+// The matrix instructions of a tile: 32 outputs x 32 tokens, 32 bytes of the
+// sums' axis a step (Big), or 16 x 16 and 64 bytes.
+template <int DT, bool Big> struct Step;
+template <int DT> struct Step<DT, true> {
+  using Acc = float16_t;
+  __device__ static __forceinline__ void run(const u32x4_t& w, const u32x4_t& x, Acc& c) {
+#pragma unroll
+    for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(w, x, c, e);
+  }
+};
+template <int DT> struct Step<DT, false> {
+  using Acc = float4_t;
+  __device__ static __forceinline__ void run(const u32x4_t& w, const u32x4_t& x, Acc& c) {
+    if constexpr (DT == DT_F32) {
+      const float4_t wf = __builtin_bit_cast(float4_t, w), xf = __builtin_bit_cast(float4_t, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[e], xf[e], c, 0, 0, 0);
+    } else if constexpr (DT == DT_F16) {
+      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w),
+                                                 __builtin_bit_cast(half8_t, x), c, 0, 0, 0);
+    } else {
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w),
+                                                  __builtin_bit_cast(bf16x8_t, x), c, 0, 0, 0);
+    }
+  }
+};
+
+// One step of the low-rank term: bf holds B, hi and lo the low-rank values
+// (for fp32, hi is the value itself).
+template <int DT, bool Big>
+__device__ __forceinline__ void low_step(const u32x4_t& bf, const u32x4_t& hi, const u32x4_t& lo,
+                                         typename Step<DT, Big>::Acc& c) {
+  if constexpr (DT == DT_F32) {
+    Step<DT, Big>::run(bf, hi, c);
+  } else if constexpr (DT == DT_BF16) {
+    Step<DT, Big>::run(bf, hi, c);
+    Step<DT, Big>::run(bf, lo, c);
+  } else {
+    u32x4_t bh, bl;
+    split_f16(bf, &bh, &bl);
+    Step<DT_BF16, Big>::run(bh, hi, c);
+    Step<DT_BF16, Big>::run(bh, lo, c);
+    Step<DT_BF16, Big>::run(bl, hi, c);
+  }
+}
+
+// 4 consecutive outputs of a token.
+template <int DT>
+__device__ __forceinline__ void store4(const LoraArgs& a, int t, int n, const float* v) {
+  constexpr int EB = Elem<DT>::bytes;
+  float o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    o[j] = v[j];
+    if (a.bias && n + j < a.N) {
+      if constexpr (DT == DT_F32)
+        o[j] += static_cast<const float*>(a.bias)[n + j];
+      else
+        o[j] += Elem<DT>::bits_to_f32(static_cast<const uint16_t*>(a.bias)[n + j]);
+    }
+  }
+  char* at = a.y + t * a.y_row + (long long)n * EB;
+  if (n + 4 <= a.N && (reinterpret_cast<uintptr_t>(at) & (4 * EB - 1)) == 0) {
+    if constexpr (DT == DT_F32)
+      *reinterpret_cast<float4_t*>(at) = float4_t{o[0], o[1], o[2], o[3]};
+    else
+      *reinterpret_cast<u32x2_t*>(at) =
+          u32x2_t{(uint32_t)Elem<DT>::from_f32(o[0]) | ((uint32_t)Elem<DT>::from_f32(o[1]) << 16),
+                  (uint32_t)Elem<DT>::from_f32(o[2]) | ((uint32_t)Elem<DT>::from_f32(o[3]) << 16)};
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n + j < a.N) {
+      if constexpr (DT == DT_F32) reinterpret_cast<float*>(at)[j] = o[j];
+      else reinterpret_cast<uint16_t*>(at)[j] = Elem<DT>::from_f32(o[j]);
+    }
+}
+
+// Position of the 16-byte chunk c of a 128-byte row in LDS: the 16 lanes that
+// read one chunk of 16 rows at a time hit all banks.
+__device__ __forceinline__ int chunk_at(int row, int c) { return c ^ ((row >> 1) & 7); }
+
+// Many rows: BM tokens x BN outputs, WM x WN waves.
+template <int DT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, int tiles_m,
+                                                            int tiles_n) {
+  constexpr int EB = Elem<DT>::bytes;
+  constexpr int THREADS = 64 * WM * WN;
+  constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks of a wave
+  constexpr int STAGE = (BM + BN) * 128;
+  static_assert(BM * kMaxRank * 4 <= 2 * STAGE, "the low-rank values fit the stages");
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
+  __shared__ int ad_of[BM];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, half = lane >> 5;
+  const int wm = wave % WM, wn = wave / WM;
+
+  // workgroups of one XCD follow one another over a band of 4 tiles of
+  // outputs, so that its L2 holds the x and W tiles they share
+  const int n_tiles = tiles_m * tiles_n;
+  const int per = n_tiles >> 3, more = n_tiles & 7, xcd = blockIdx.x & 7;
+  const int id = xcd * per + (xcd < more ? xcd : more) + (blockIdx.x >> 3);
+  constexpr int BAND = 4;
+  const int band = id / (BAND * tiles_m), in_band = id - band * BAND * tiles_m;
+  const int width_n = tiles_n - band * BAND < BAND ? tiles_n - band * BAND : BAND;
+  const int m0 = in_band / width_n * BM;
+  const int n0 = (band * BAND + in_band % width_n) * BN;
+
+  float16_t acc[NB][MB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < MB; ++j) acc[i][j] = float16_t{};
+
+  if (a.n_adapters > 0) {
+    row_adapters<THREADS>(a, m0, BM, ad_of);
+    low_to_lds<DT, THREADS>(a, m0, BM, ad_of, lds);
+    const int width = a.low_width;
+    constexpr int LB = DT == DT_F32 ? 4 : 2;   // bytes of a low-rank value in LDS
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int t = (wm * MB + j) * 32 + l32;
+      const int mine = ad_of[t];
+      uint64_t left = __ballot(mine >= 0);
+      while (left) {
+        const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+        left &= ~__ballot(mine == ad);
+        const __amdgpu_buffer_rsrc_t rb =
+            make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
+        for (int s = 0; s < (a.rank * LB + 31) / 32; ++s) {
+          const unsigned char* at = lds + t * width * LB + s * 32 + half * 16;
+          u32x4_t hi = *reinterpret_cast<const u32x4_t*>(at), lo = {0, 0, 0, 0};
+          if constexpr (DT != DT_F32)
+            lo = *reinterpret_cast<const u32x4_t*>(at + BM * width * LB);
+          if (mine != ad) hi = lo = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const u32x4_t bf = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32,
+                                          (s * 32 + half * 16) / LB);
+            low_step<DT, true>(bf, hi, lo, acc[i][j]);
+          }
+        }
+      }
+    }
+    lds_barrier();   // the stages take the low-rank values' place
+  }
+
+  // stages
+  const int row_bytes = a.K * EB;
+  const int stages = (row_bytes + 127) / 128;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)m0 * a.x_row, 0x7ffffff0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row_bytes, 0x7ffffff0u);
+  constexpr int CX = BM * 8 / THREADS, CW = BN * 8 / THREADS;   // copies a thread
+  int x_off[CX], w_off[CW];   // of stage 0; past the end where the row is
+  int x_chunk[CX], w_chunk[CW];
+#pragma unroll
+  for (int c = 0; c < CX; ++c) {
+    const int unit = c * THREADS + threadIdx.x, row = unit >> 3;
+    x_chunk[c] = chunk_at(row, unit & 7) * 16;
+    x_off[c] = m0 + row < a.T ? row * (int)a.x_row + x_chunk[c] : kOobOffset;
+  }
+#pragma unroll
+  for (int c = 0; c < CW; ++c) {
+    const int unit = c * THREADS + threadIdx.x, row = unit >> 3;
+    w_chunk[c] = chunk_at(row, unit & 7) * 16;
+    w_off[c] = n0 + row < a.N ? row * row_bytes + w_chunk[c] : kOobOffset;
+  }
+#define LIBCONV_COPY_STAGE(st)                                                                  \
+  {                                                                                             \
+    unsigned char* to = lds + ((st) & 1) * STAGE;                                               \
+    const int k = (st) * 128;                                                                   \
+    _Pragma("unroll") for (int c = 0; c < CX; ++c) copy16_to_lds(                               \
+        rx, to + (c * THREADS + wave * 64) * 16,                                                \
+        guard_offset(x_off[c] >= 0 && k + x_chunk[c] < row_bytes, x_off[c] + k));               \
+    _Pragma("unroll") for (int c = 0; c < CW; ++c) copy16_to_lds(                               \
+        rw, to + BM * 128 + (c * THREADS + wave * 64) * 16,                                     \
+        guard_offset(w_off[c] >= 0 && k + w_chunk[c] < row_bytes, w_off[c] + k));               \
+  }
+  LIBCONV_COPY_STAGE(0)
+  for (int st = 0; st < stages; ++st) {
+    wait_vmcnt<0>();
+    lds_barrier();
+    if (st + 1 < stages) LIBCONV_COPY_STAGE(st + 1)
+    const unsigned char* xs = lds + (st & 1) * STAGE;
+    const unsigned char* ws = xs + BM * 128;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      u32x4_t wf[NB], xf[MB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int row = (wn * NB + i) * 32 + l32;
+        wf[i] = *reinterpret_cast<const u32x4_t*>(ws + row * 128 + chunk_at(row, 2 * k + half) * 16);
+      }
+#pragma unroll
+      for (int j = 0; j < MB; ++j) {
+        const int row = (wm * MB + j) * 32 + l32;
+        xf[j] = *reinterpret_cast<const u32x4_t*>(xs + row * 128 + chunk_at(row, 2 * k + half) * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) Step<DT, true>::run(wf[i], xf[j], acc[i][j]);
+    }
+  }
+#undef LIBCONV_COPY_STAGE
+
+#pragma unroll
+  for (int j = 0; j < MB; ++j) {
+    const int t = m0 + (wm * MB + j) * 32 + l32;
+    if (t >= a.T) continue;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = n0 + (wn * NB + i) * 32 + 8 * r + 4 * half;
+        const float v[4] = {acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
+                            acc[i][j][4 * r + 3]};
+        if (n < a.N) store4<DT>(a, t, n, v);
+      }
+  }
+}
+
+// Up to 16 * RB rows: 16 outputs a workgroup, the sum's axis split over 8
+// waves, joined in the order of the waves.
+constexpr int kFewWaves = 8;
+template <int DT, int RB>
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const LoraArgs a) {
+  constexpr int EB = Elem<DT>::bytes;
+  constexpr int THREADS = 64 * kFewWaves, ROWS = 16 * RB;
+  constexpr int LOW = ROWS * kMaxRank * 4, JOIN = kFewWaves * ROWS * 20 * 4;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[LOW > JOIN ? LOW : JOIN];
+  __shared__ int ad_of[64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l16 = lane & 15, quarter = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+
+  float4_t acc[RB];
+#pragma unroll
+  for (int j = 0; j < RB; ++j) acc[j] = float4_t{0, 0, 0, 0};
+
+  const int row_bytes = a.K * EB;
+  const int steps = (row_bytes + 63) / 64;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, 0x7ffffff0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row_bytes, 0x7ffffff0u);
+  const bool n_ok = n0 + l16 < a.N;
+  // U neighbouring steps to a wave, so that its reads cover whole lines
+  constexpr int U = RB <= 2 ? 8 : 4;
+  for (int k = wave * U; k < steps; k += kFewWaves * U) {
+    u32x4_t wf[U], xf[U][RB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int off = (k + u) * 64 + quarter * 16;
+      const bool in = off < row_bytes;
+      wf[u] = load16(rw, guard_offset(in && n_ok, l16 * row_bytes + off));
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+        xf[u][j] = load16(rx, guard_offset(in && j * 16 + l16 < a.T,
+                                           (j * 16 + l16) * (int)a.x_row + off));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < RB; ++j) Step<DT, false>::run(wf[u], xf[u][j], acc[j]);
+  }
+
+  if (a.n_adapters > 0) {
+    row_adapters<THREADS>(a, 0, 64, ad_of);
+    low_to_lds<DT, THREADS>(a, 0, ROWS, ad_of, lds);
+    const int width = a.low_width;
+    constexpr int LB = DT == DT_F32 ? 4 : 2;
+    // the waves take the adapters in turn
+    const int here = ad_of[lane];
+    uint64_t left = __ballot(here >= 0 && lane < a.T);
+    for (int turn = 0; left; ++turn) {
+      const int ad = __builtin_amdgcn_readlane(here, __builtin_ctzll(left));
+      left &= ~__ballot(here == ad);
+      if (turn % kFewWaves != wave) continue;
+      const __amdgpu_buffer_rsrc_t rb =
+          make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
+      for (int s = 0; s < (a.rank * LB + 63) / 64; ++s) {
+        const u32x4_t bf = load_b<DT>(a, rb, n0 + l16, (s * 64 + quarter * 16) / LB);
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+          const unsigned char* at = lds + (j * 16 + l16) * width * LB + s * 64 + quarter * 16;
+          u32x4_t hi = *reinterpret_cast<const u32x4_t*>(at), lo = {0, 0, 0, 0};
+          if constexpr (DT != DT_F32)
+            lo = *reinterpret_cast<const u32x4_t*>(at + ROWS * width * LB);
+          if (ad_of[j * 16 + l16] != ad) hi = lo = u32x4_t{0, 0, 0, 0};
+          low_step<DT, false>(bf, hi, lo, acc[j]);
+        }
+      }
+    }
+    lds_barrier();   // the join takes the low-rank values' place
+  }
+
+  // [wave][token][output], 20 floats a token: writes and reads without conflicts
+  float* join = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int j = 0; j < RB; ++j)
+    *reinterpret_cast<float4_t*>(join + ((wave * ROWS + j * 16 + l16) * 20 + quarter * 4)) = acc[j];
+  lds_barrier();
+  for (int i = threadIdx.x; i < ROWS * 4; i += THREADS) {
+    const int t = i >> 2, q = i & 3;
+    float v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+      const float4_t p = *reinterpret_cast<const float4_t*>(join + ((w * ROWS + t) * 20 + q * 4));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += p[j];
+    }
+    if (t < a.T && n0 + q * 4 < a.N) store4<DT>(a, t, n0 + q * 4, v);
+  }
+}
+
+template <int DT, int BM, int BN, int WM, int WN>
+void launch_tile(const LoraArgs& a, hipStream_t stream) {
+  const int tm = (a.T + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  hipLaunchKernelGGL((tile_kernel<DT, BM, BN, WM, WN>), dim3((unsigned)(tm * tn)),
+                     dim3(64 * WM * WN), 0, stream, a, tm, tn);
+}
+
+// Time of a launch in units of one 256 x 256 tile: rounds of workgroups over
+// the compute units, each as long as its workgroups together on one unit.
+double tile_cost(const LoraArgs& a, int cus, int bm, int bn, int per_cu, double speed) {
+  const double tiles = (double)((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+  const double rounds = (double)(long long)((tiles + (double)cus * per_cu - 1) / (cus * per_cu));
+  const double share = tiles < (double)cus * per_cu ? (tiles > cus ? tiles / cus : 1.0) : per_cu;
+  return rounds * share * bm * bn / speed;
+}
+
+template <int DT>
+void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
+  if (a.n_adapters > 0)
+    hipLaunchKernelGGL((low_kernel<DT>),
+                       dim3((unsigned)((a.T + kLowRows - 1) / kLowRows), (unsigned)a.low_splits),
+                       dim3(64 * kLowWaves), 0, stream, a);
+  if (a.T <= 64) {
+    const dim3 grid((unsigned)((a.N + 15) / 16)), threads(64 * kFewWaves);
+    if (a.T <= 16) hipLaunchKernelGGL((few_kernel<DT, 1>), grid, threads, 0, stream, a);
+    else if (a.T <= 32) hipLaunchKernelGGL((few_kernel<DT, 2>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((few_kernel<DT, 4>), grid, threads, 0, stream, a);
+    return;
+  }
+  const double c256 = tile_cost(a, cus, 256, 256, 1, 1.0);
+  const double c128 = tile_cost(a, cus, 128, 128, 2, 0.75);
+  const double c64 = tile_cost(a, cus, 64, 64, 4, 0.4);
+  if (c256 <= c128 && c256 <= c64) launch_tile<DT, 256, 256, 4, 2>(a, stream);
+  else if (c128 <= c64) launch_tile<DT, 128, 128, 2, 2>(a, stream);
+  else launch_tile<DT, 64, 64, 2, 2>(a, stream);
+}
+
+}  // namespace
+
+long long lora_plan(LoraArgs* a, int dtype, int cus) {
+  const int eb = dtype == LIBCONV_F32 ? 4 : 2;
+  a->low_splits = 0;
+  a->low_width = 0;
+  if (a->n_adapters == 0 || a->T == 0) return 0;
+  a->low_width = (a->rank + 31) / 32 * 32;
+  const long long tiles = (a->T + kLowRows - 1) / kLowRows;
+  // a workgroup for each compute unit, 512 bytes of a row or more to a wave
+  long long s = (cus + tiles - 1) / tiles;
+  const long long most = (long long)a->K * eb / (512 * kLowWaves);
+  if (s > most) s = most;
+  a->low_splits = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+  return (long long)a->low_splits * a->T * a->low_width * 4;
+}
+
+libconv_status lora_launch(LoraArgs a, int dtype, int cus, hipStream_t stream) {
+  if (dtype == LIBCONV_F32) launch_dt<DT_F32>(a, cus, stream);
+  else if (dtype == LIBCONV_F16) launch_dt<DT_F16>(a, cus, stream);
+  else launch_dt<DT_BF16>(a, cus, stream);
+  return hipGetLastError() == hipSuccess ? LIBCONV_OK : LIBCONV_ERR_LAUNCH;
+}
+
+}  // namespace libconv

@@ -98,9 +98,11 @@ typedef enum {
   LIBCONV_ERR_BAD_ALGO = 9,       /* algo is not a libconv_algo */
   LIBCONV_ERR_TOO_LARGE = 10,     /* a tensor (or the packed weights) spans 2^31 bytes or more */
   LIBCONV_ERR_OUT_OF_MEMORY = 11, /* not returned by this version (no call allocates) */
-  LIBCONV_ERR_MISALIGNED = 12,    /* a workspace is not 256-byte aligned */
+  LIBCONV_ERR_MISALIGNED = 12,    /* a workspace is not 256-byte aligned, or an operand of
+                                     the attention-layer operators not as they require */
   LIBCONV_ERR_SCRATCH_TOO_SMALL = 13 /* conv3d_forward_noalloc: the plan needs more than the
-                                        library's scratch array holds */
+                                        library's scratch array holds; libconv_lora_linear:
+                                        the workspace is too small */
 } libconv_status;
 
 /*
@@ -543,6 +545,134 @@ int libconv_out_size(int in, int k, int pad, int stride);
 /* The same with pad_lo before and pad_hi after the input (the frame axis of
  * conv3d_forward_tpad): floor((in + pad_lo + pad_hi - k) / stride) + 1, or -1. */
 int libconv_out_size2(int in, int k, int pad_lo, int pad_hi, int stride);
+
+/* ------------------------------------------------------------------------
+ * Operators of the attention layers that stand beside the convolutions: the
+ * attention blocks of a diffusion U-Net, the video transformer between a
+ * video VAE's encoder and decoder (windows of video tokens that all attend to
+ * the same text tokens), a decoder that answers many prompts about one page's
+ * features.  One such layer is libconv_lora_linear (the projections),
+ * libconv_qk_norm_rope (norms, position rotation and the cache write) and
+ * libconv_prefix_attention.  The conventions above hold, except that
+ *   - strides are in elements, >= 0, and may exceed 32 bits where the
+ *     declaration says long long: offsets are formed in 64 bits, and the
+ *     operands may span more than 2^31 bytes;
+ *   - operands whose rows are read 16 bytes at a time have to lie on 16-byte
+ *     boundaries (pointer and strides), else LIBCONV_ERR_MISALIGNED;
+ *   - integer operands on the device (lengths, slots, row starts, adapter
+ *     numbers) cannot be checked before the launch: values out of range read
+ *     and write nothing out of range (each declaration says what they do).
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Norms of queries and keys for each head, the position rotation, and
+ * (optionally) the write of keys and values into a cache, in one pass:
+ *   n = x / sqrt(mean_d(x^2) + eps) * weight
+ *   pair i of n turned by the angle positions[axis(i)][t] * freqs[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * q [T][q_heads][head_dim], k and v [T][k_heads][head_dim]; outputs alike.
+ *   strides   host array of 12: row stride and head stride of q, k, v, q_out,
+ *             k_out, v_out (the head_dim axis is dense)
+ *   q_weight, k_weight   [head_dim] of the call's dtype, or NULL (ones)
+ *   freqs     [rot_dim / 2] doubles on the device, radians a position
+ *   positions [axes][T] ints on the device
+ *   pairs0..2 pairs that turn with axis 0, 1, 2 (in this order); their sum is
+ *             rot_dim / 2, and axes is 1 + the last one that is not 0
+ *   interleaved  0: pair i is (i, i + rot_dim / 2); 1: (2 i, 2 i + 1).
+ *             Components from rot_dim on are normed only.
+ *   v, v_out  both NULL (values untouched) or both given: v is copied
+ *   slots     [T] ints on the device or NULL: row slots[t] of k_out and v_out
+ *             receives token t; a slot outside [0, out_rows) writes nothing.
+ *             No two tokens may have the same slot.  NULL: row t.
+ * Sums, norm, angle (64 bits, reduced to one turn) and rotation are formed in
+ * fp32 or more and rounded once.  q_out may be q and k_out may be k (the same
+ * pointer and strides, slots NULL); other overlaps are LIBCONV_ERR_ALIAS.
+ * head_dim: a multiple of 8 up to 256; rot_dim: even, <= head_dim, a multiple
+ * of 16 where interleaved is 0; else LIBCONV_ERR_UNSUPPORTED.  T may be 0.
+ */
+libconv_status libconv_qk_norm_rope(const void* q, const void* k, const void* v,
+                                    void* q_out, void* k_out, void* v_out,
+                                    const void* q_weight, const void* k_weight,
+                                    const double* freqs, const int* positions, const int* slots,
+                                    const long long* strides, int T, int q_heads, int k_heads,
+                                    int head_dim, int rot_dim, int pairs0, int pairs1, int pairs2,
+                                    int interleaved, int out_rows, float eps,
+                                    int dtype, void* stream);
+
+/*
+ * Attention of B entries over P keys they all share and each entry's own:
+ *   out[b][i][h] = sum_j p_j v_j,  p = softmax_j(scale * <q[b][i][h], k_j>)
+ * over the prefix keys 0 <= j < P and the entry's own keys 0 <= j < lengths[b]
+ * (causal: and j <= lengths[b] - Sq + i, so that the last query sees every own
+ * key).  A query with no key to see gives 0 (and lse -inf).
+ *   q, out    [B][Sq][q_heads][head_dim]      lse [B][q_heads][Sq] fp32 or NULL
+ *   k_prefix, v_prefix  [P][k_heads][head_dim]       (may be NULL if P is 0)
+ *   k, v      [B][S][k_heads][head_dim], S rows for each entry's own keys (may
+ *             be NULL if S is 0)
+ *   lengths   [B] ints on the device; clamped to [0, S]
+ *   strides   host array of 16: q (batch, row, head), k_prefix (row, head),
+ *             v_prefix (row, head), k (batch, row, head), v (batch, row,
+ *             head), out (batch, row, head)
+ *   lse       natural log of sum_j exp(scale * <q, k_j>)
+ * q_heads is a multiple of k_heads: query head h reads key head
+ * h / (q_heads / k_heads).  head_dim: a multiple of 8 up to 128, else
+ * LIBCONV_ERR_UNSUPPORTED.  Rows of k and v from lengths[b] on are not read
+ * into any result, whatever they hold; a non-finite value in a row that a
+ * causal mask hides from a query can reach that query.
+ * Scores, softmax and sums are fp32; the probabilities are rounded to the
+ * dtype for the second product and `out` is rounded once.
+ *   workspace  device, 256-byte aligned, at least
+ *             libconv_prefix_attention_workspace bytes for the best plan,
+ *             which reads the prefix once for all entries and splits long
+ *             rows of keys over workgroups; NULL or smaller: a plan without.
+ * B, Sq, P and S may be 0 (0 keys: out is 0).
+ */
+libconv_status libconv_prefix_attention(const void* q, const void* k_prefix,
+                                        const void* v_prefix, const void* k, const void* v,
+                                        const int* lengths, void* out, float* lse,
+                                        const long long* strides, int B, int Sq, int P, int S,
+                                        int q_heads, int k_heads, int head_dim, float scale,
+                                        int causal, int dtype, void* workspace,
+                                        long long workspace_bytes, void* stream);
+
+/* Workspace bytes of the best plan (0: none), or -1 for invalid arguments.
+ * Pure host arithmetic. */
+long long libconv_prefix_attention_workspace(int B, int Sq, int P, int S, int q_heads,
+                                             int k_heads, int head_dim, int dtype);
+
+/*
+ * A projection shared by all rows with a low-rank adapter for each request:
+ *   y[t] = w x[t] + bias + scales[a] * b[a] (a_[a] x[t])
+ * for the rows row_starts[r] <= t < row_starts[r + 1] of request r, whose
+ * adapter is a = adapters[r].
+ *   x    [T][K], rows x_stride apart       y [T][N], rows y_stride apart
+ *   w    [N][K]     bias [N] or NULL
+ *   a    [n_adapters][rank][K]             b [n_adapters][N][rank]
+ *   scales     [n_adapters] fp32, device
+ *   row_starts [n_requests + 1] ints, device, ascending
+ *   adapters   [n_requests] ints, device
+ * Rows of no request, and requests whose adapter is outside [0, n_adapters),
+ * get the shared projection alone.  Adapters of a smaller rank are padded with
+ * zeros.  Products are summed in fp32; the low-rank values a x[t] stay fp32
+ * (for 16-bit types they enter the second product as two bfloat16 terms,
+ * 16 significant bits) and y is rounded once.
+ * K: a multiple of 8; rank 1 to 128; x, w, a on 16-byte boundaries.
+ * n_adapters or n_requests 0: the projection alone (a, b, scales, row_starts
+ * and adapters may be NULL).
+ *   workspace  device, 256-byte aligned, at least libconv_lora_workspace
+ *             bytes, else LIBCONV_ERR_SCRATCH_TOO_SMALL
+ */
+libconv_status libconv_lora_linear(const void* x, const void* w, const void* bias,
+                                   const void* a, const void* b, const float* scales,
+                                   const int* row_starts, const int* adapters, void* y,
+                                   int T, int K, int N, int rank, int n_adapters, int n_requests,
+                                   long long x_stride, long long y_stride, int dtype,
+                                   void* workspace, long long workspace_bytes, void* stream);
+
+/* Workspace bytes libconv_lora_linear needs (0 without adapters or requests),
+ * or -1 for invalid arguments.  Pure host arithmetic. */
+long long libconv_lora_workspace(int T, int K, int N, int rank, int n_adapters, int n_requests,
+                                 int dtype);
 
 /* Static description of a status code; never NULL.  Failures are reported,
  * never turned into an abort (the fault-tolerant backend bring-up of
