@@ -24,48 +24,60 @@ def _base():
     return L
 
 
-def _check(what, tensors, like, dims=None):
-    """Device, dtype and dense last axis of the operands that are given."""
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or t.device != like.device:
-            raise ValueError(f"{what}: operands must be device tensors of one device")
-        if t.dtype != like.dtype:
-            raise ValueError(f"{what}: operands must have one dtype")
-        if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-            raise ValueError(f"{what}: expected {dims} axes with the last one dense")
+def _check(what, t, device, dtype, dims):
+    """Device (its index), dtype and dense last axis of an operand."""
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{what}: operands must be device tensors of one device")
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: operands must have one dtype")
+    if t.dim() != dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{what}: expected {dims} axes with the last one dense")
 
 
 def _ints(what, t, shape, device):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or \
-            t.device != device:
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != device:
         raise ValueError(f"{what} must be a contiguous int32 device tensor of shape {shape}")
     return t.data_ptr()
 
 
-def _call(device, stream, what, call, need=0, workspace=True):
-    """Runs call(workspace pointer, bytes, stream) with `device` current."""
-    import torch
-    L = _base()
-    with torch.cuda.device(device):
-        foreign = stream is not None
-        if not foreign:
-            stream = torch.cuda.current_stream(device).cuda_stream
-        ptr, size, buf = None, 0, None
-        if workspace is not None and workspace is not False:
-            if workspace is True:
-                if need > 0:
-                    buf = torch.empty(need, dtype=torch.uint8, device=device)
-                    ptr, size = buf.data_ptr(), need
-            else:
-                ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        st = call(ptr, size, stream)
-        if buf is not None and foreign:  # its memory is used on that stream until then
-            buf.record_stream(torch.cuda.ExternalStream(stream, device=device))
-    if st != 0:
-        raise L.LibconvError(st, what)
+class _Launch:
+    """The stream and workspace of one call: ``stream`` is a handle (default: the
+    current stream of the device), ``workspace`` True (allocate ``need`` bytes
+    through torch), False / None (none) or a device tensor.  The calls are
+    short: nothing here is done twice or for later."""
+
+    __slots__ = ("stream", "ptr", "size", "_buffer", "_foreign", "_device")
+
+    def __init__(self, device, stream, need, workspace):
+        import torch
+        self._device, self._foreign, self._buffer = device, stream is not None, None
+        # the current stream's handle, as torch.cuda.current_stream() has it,
+        # without the stream object
+        self.stream = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream
+        self.ptr, self.size = None, 0
+        if workspace is True:
+            if need > 0:
+                self._buffer = torch.empty(need, dtype=torch.uint8, device=device)
+                self.ptr, self.size = self._buffer.data_ptr(), need
+        elif workspace is not None and workspace is not False:
+            self.ptr = workspace.data_ptr()
+            self.size = workspace.numel() * workspace.element_size()
+
+    def run(self, what, function, *args):
+        import torch
+        if torch.cuda.current_device() == self._device:
+            status = function(*args, self.stream)
+        else:
+            with torch.cuda.device(self._device):
+                status = function(*args, self.stream)
+        if self._foreign and self._buffer is not None:
+            # its memory is that stream's until then
+            self._buffer.record_stream(
+                torch.cuda.ExternalStream(self.stream, device=self._device))
+        if status != 0:
+            raise _base().LibconvError(status, what)
 
 
 def rotary_frequencies(rot_dim: int, theta: float = 10000.0,
@@ -89,53 +101,70 @@ def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: floa
     slots (int32 [T]), keys and values go to rows slots[t] of k_out / v_out.
     Returns (q_out, k_out) or (q_out, k_out, v_out)."""
     import torch
-    L = _base()
-    _check("qk_norm_rope", (q, k, v), q, 3)
+    what = "qk_norm_rope"
+    lib, dev, dtype = _base().load(), q.get_device(), q.dtype
+    _check(what, q, dev, dtype, 3)
+    _check(what, k, dev, dtype, 3)
     T, Hq, D = q.shape
     Hk = k.shape[1]
-    if k.shape != (T, Hk, D) or (v is not None and v.shape != k.shape):
+    if k.shape != (T, Hk, D):
         raise ValueError("qk_norm_rope: q [T, Hq, D], k and v [T, Hk, D]")
     if slots is not None and (k_out is None or (v is not None and v_out is None)):
         raise ValueError("qk_norm_rope: slots need k_out (and v_out)")
-    if v is None and v_out is not None:
-        raise ValueError("qk_norm_rope: v_out without v")
-    pos = positions if positions.dim() == 2 else positions.unsqueeze(0)
+    if positions.dim() == 1:
+        positions = positions.unsqueeze(0)
     pairs = freqs.numel()
-    sections = [pairs] if sections is None else [int(n) for n in sections]
-    if len(sections) > 3 or sum(sections) != pairs or min(sections, default=0) < 0 or \
-            2 * pairs > D or pos.shape[0] < len(sections):
+    n0, n1, n2, *more = list(sections) + [0, 0, 0] if sections is not None else (pairs, 0, 0)
+    axes = 3 if n2 else 2 if n1 else 1
+    if any(more) or n0 + n1 + n2 != pairs or min(n0, n1, n2) < 0 or 2 * pairs > D or \
+            positions.shape[0] < axes:
         raise ValueError("qk_norm_rope: up to 3 sections that add up to the pairs of freqs, "
                          "with a row of positions each")
-    pos_ptr = _ints("positions", pos, (pos.shape[0], T), q.device)
-    if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.device != q.device:
+    pos_ptr = _ints("positions", positions, (positions.shape[0], T), dev)
+    if freqs.dtype != torch.float64 or not freqs.is_contiguous() or freqs.get_device() != dev:
         raise ValueError("freqs must be a contiguous float64 device tensor")
-    for w in (q_weight, k_weight):
+    w_ptr = [None, None]
+    for i, w in enumerate((q_weight, k_weight)):
         if w is not None:
-            _check("qk_norm_rope", (w,), q, 1)
+            _check(what, w, dev, dtype, 1)
             if w.shape[0] != D:
                 raise ValueError("qk_norm_rope: weights [D]")
-    q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device) if k_out is None else k_out
-    if v is not None and v_out is None:
-        v_out = torch.empty((T, Hk, D), dtype=q.dtype, device=q.device)
-    _check("qk_norm_rope", (q_out, k_out, v_out), q, 3)
-    rows = T if slots is None else k_out.shape[0]
-    if q_out.shape != q.shape or k_out.shape != (rows, Hk, D) or \
-            (v is not None and v_out.shape != (rows, Hk, D)):
+            w_ptr[i] = w.data_ptr()
+    rows, slot_ptr = T, None
+    if slots is not None:
+        rows, slot_ptr = k_out.shape[0], _ints("slots", slots, (T,), dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+    else:
+        _check(what, q_out, dev, dtype, 3)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev)
+    else:
+        _check(what, k_out, dev, dtype, 3)
+    if q_out.shape != q.shape or k_out.shape != (rows, Hk, D):
         raise ValueError("qk_norm_rope: bad output tensor")
-    slot_ptr = None if slots is None else _ints("slots", slots, (T,), q.device)
+    v_ptr = vo_ptr = None
+    v_st = vo_st = (0, 0, 0)
+    if v is not None:
+        _check(what, v, dev, dtype, 3)
+        v_out = torch.empty((T, Hk, D), dtype=dtype, device=dev) if v_out is None else v_out
+        _check(what, v_out, dev, dtype, 3)
+        if v.shape != k.shape or v_out.shape != (rows, Hk, D):
+            raise ValueError("qk_norm_rope: v [T, Hk, D] and v_out as k_out")
+        v_ptr, vo_ptr, v_st, vo_st = v.data_ptr(), v_out.data_ptr(), v.stride(), v_out.stride()
+    elif v_out is not None:
+        raise ValueError("qk_norm_rope: v_out without v")
     result = (q_out, k_out) if v is None else (q_out, k_out, v_out)
     if T == 0:
         return result
-    st = []
-    for t in (q, k, v, q_out, k_out, v_out):
-        st += [0, 0] if t is None else [t.stride(0), t.stride(1)]
-    n = sections + [0] * (3 - len(sections))
-    _call(q.device, stream, "libconv_qk_norm_rope", lambda _p, _n, s: L.libconv_qk_norm_rope(
-        L._ptr(q), L._ptr(k), L._ptr(v), L._ptr(q_out), L._ptr(k_out), L._ptr(v_out),
-        L._ptr(q_weight), L._ptr(k_weight), freqs.data_ptr(), pos_ptr, slot_ptr,
-        _STRIDES12(*st), T, Hq, Hk, D, 2 * pairs, n[0], n[1], n[2], int(bool(interleaved)), rows,
-        float(eps), L._dtype_code(q), s))
+    a, b, c, d = q.stride(), k.stride(), q_out.stride(), k_out.stride()
+    strides = _STRIDES12(a[0], a[1], b[0], b[1], v_st[0], v_st[1], c[0], c[1], d[0], d[1],
+                         vo_st[0], vo_st[1])
+    _Launch(dev, stream, 0, False).run(
+        "libconv_qk_norm_rope", lib.libconv_qk_norm_rope, q.data_ptr(), k.data_ptr(), v_ptr,
+        q_out.data_ptr(), k_out.data_ptr(), vo_ptr, w_ptr[0], w_ptr[1], freqs.data_ptr(), pos_ptr,
+        slot_ptr, strides, T, Hq, Hk, D, 2 * pairs, n0, n1, n2, 1 if interleaved else 0, rows,
+        eps, _base()._dtype_code(q))
     return result
 
 
@@ -149,39 +178,55 @@ def prefix_attention(q, k_prefix, v_prefix, k, v, lengths, scale: Optional[float
     [B, Hq, Sq] float32).  workspace: True (allocate what the best plan takes),
     False (none), or a uint8 device tensor."""
     import torch
+    what = "prefix_attention"
     L = _base()
-    _check("prefix_attention", (q, k, v, out), q, 4)
-    _check("prefix_attention", (k_prefix, v_prefix), q, 3)
+    lib, dev, dtype = L.load(), q.get_device(), q.dtype
+    _check(what, q, dev, dtype, 4)
     B, Sq, Hq, D = q.shape
     if (k is None) != (v is None) or (k_prefix is None) != (v_prefix is None):
         raise ValueError("prefix_attention: keys and values come together")
     if k is None and k_prefix is None:
         raise ValueError("prefix_attention: neither a prefix nor own keys")
     Hk = (k if k is not None else k_prefix).shape[-2]
-    P = 0 if k_prefix is None else k_prefix.shape[0]
-    S = 0 if k is None else k.shape[1]
-    if (k is not None and (k.shape != (B, S, Hk, D) or v.shape != k.shape)) or \
-            (P and (k_prefix.shape != (P, Hk, D) or v_prefix.shape != k_prefix.shape)):
-        raise ValueError("prefix_attention: k, v [B, S, Hk, D], k_prefix, v_prefix [P, Hk, D]")
-    len_ptr = _ints("lengths", lengths, (B,), q.device)
-    out = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=q.device) if out is None else out
-    if out.shape != q.shape:
-        raise ValueError("prefix_attention: bad output tensor")
-    lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if return_lse else None
+    P = S = 0
+    kp_ptr = vp_ptr = k_ptr = v_ptr = None
+    kp_st = vp_st = k_st = v_st = (0, 0, 0)
+    if k_prefix is not None:
+        _check(what, k_prefix, dev, dtype, 3)
+        _check(what, v_prefix, dev, dtype, 3)
+        P = k_prefix.shape[0]
+        if k_prefix.shape != (P, Hk, D) or v_prefix.shape != (P, Hk, D):
+            raise ValueError("prefix_attention: k_prefix, v_prefix [P, Hk, D]")
+        kp_ptr, vp_ptr = k_prefix.data_ptr(), v_prefix.data_ptr()
+        kp_st, vp_st = k_prefix.stride(), v_prefix.stride()
+    if k is not None:
+        _check(what, k, dev, dtype, 4)
+        _check(what, v, dev, dtype, 4)
+        S = k.shape[1]
+        if k.shape != (B, S, Hk, D) or v.shape != (B, S, Hk, D):
+            raise ValueError("prefix_attention: k, v [B, S, Hk, D]")
+        k_ptr, v_ptr, k_st, v_st = k.data_ptr(), v.data_ptr(), k.stride(), v.stride()
+    len_ptr = _ints("lengths", lengths, (B,), dev)
+    if out is None:
+        out = torch.empty((B, Sq, Hq, D), dtype=dtype, device=dev)
+    else:
+        _check(what, out, dev, dtype, 4)
+        if out.shape != q.shape:
+            raise ValueError("prefix_attention: bad output tensor")
+    lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev) if return_lse else None
     if B == 0 or Sq == 0:
         return (out, lse) if return_lse else out
-    scale = D ** -0.5 if scale is None else float(scale)
     dt = L._dtype_code(q)
-    need = L.load().libconv_prefix_attention_workspace(B, Sq, P, S, Hq, Hk, D, dt) \
+    need = lib.libconv_prefix_attention_workspace(B, Sq, P, S, Hq, Hk, D, dt) \
         if workspace is True else 0
-    st = []
-    for t, n in ((q, 3), (k_prefix, 2), (v_prefix, 2), (k, 3), (v, 3), (out, 3)):
-        st += [0] * n if t is None else t.stride()[:n]
-    _call(q.device, stream, "libconv_prefix_attention",
-          lambda p, n, s: L.libconv_prefix_attention(
-              L._ptr(q), L._ptr(k_prefix), L._ptr(v_prefix), L._ptr(k), L._ptr(v), len_ptr,
-              L._ptr(out), L._ptr(lse), _STRIDES16(*st), B, Sq, P, S, Hq, Hk, D, scale,
-              int(bool(causal)), dt, p, n, s), need, workspace)
+    a, o = q.stride(), out.stride()
+    strides = _STRIDES16(a[0], a[1], a[2], kp_st[0], kp_st[1], vp_st[0], vp_st[1], k_st[0],
+                         k_st[1], k_st[2], v_st[0], v_st[1], v_st[2], o[0], o[1], o[2])
+    call = _Launch(dev, stream, need, workspace)
+    call.run("libconv_prefix_attention", lib.libconv_prefix_attention, q.data_ptr(), kp_ptr,
+             vp_ptr, k_ptr, v_ptr, len_ptr, out.data_ptr(), L._ptr(lse), strides, B, Sq, P, S, Hq,
+             Hk, D, D ** -0.5 if scale is None else scale, 1 if causal else 0, dt, call.ptr,
+             call.size)
     return (out, lse) if return_lse else out
 
 
@@ -193,42 +238,50 @@ def lora_linear(x, w, bias, a, b, scales, row_starts, adapters, out=None, stream
     row_starts int32 [R + 1], adapters int32 [R] (outside [0, n): none).
     a .. adapters may all be None: the projection alone."""
     import torch
+    what = "lora_linear"
     L = _base()
-    _check("lora_linear", (x, w, out), x, 2)
+    lib, dev, dtype = L.load(), x.get_device(), x.dtype
+    _check(what, x, dev, dtype, 2)
+    _check(what, w, dev, dtype, 2)
     T, K = x.shape
     N = w.shape[0]
     if w.shape != (N, K) or not w.is_contiguous():
         raise ValueError("lora_linear: w must be a contiguous [N, K]")
     if bias is not None:
-        _check("lora_linear", (bias,), x, 1)
-        if bias.shape != (N,):
+        _check(what, bias, dev, dtype, 1)
+        if bias.shape[0] != N:
             raise ValueError("lora_linear: bias must be [N]")
-    low = (a, b, scales, row_starts, adapters)
     n = rank = R = 0
-    starts_ptr = adapters_ptr = None
-    if any(t is not None for t in low):
-        if any(t is None for t in low):
-            raise ValueError("lora_linear: a, b, scales, row_starts and adapters come together")
-        _check("lora_linear", (a, b), x, 3)
+    a_ptr = b_ptr = scales_ptr = starts_ptr = adapters_ptr = None
+    given = [t is not None for t in (a, b, scales, row_starts, adapters)]
+    if all(given):
+        _check(what, a, dev, dtype, 3)
+        _check(what, b, dev, dtype, 3)
         n, rank = a.shape[0], a.shape[1]
         if a.shape != (n, rank, K) or b.shape != (n, N, rank) or not a.is_contiguous() or \
                 not b.is_contiguous():
             raise ValueError("lora_linear: contiguous a [n, rank, K] and b [n, N, rank]")
         if scales.dtype != torch.float32 or scales.shape != (n,) or \
-                not scales.is_contiguous() or scales.device != x.device:
+                not scales.is_contiguous() or scales.get_device() != dev:
             raise ValueError("lora_linear: scales must be a contiguous float32 device tensor [n]")
         R = adapters.shape[0]
-        adapters_ptr = _ints("adapters", adapters, (R,), x.device)
-        starts_ptr = _ints("row_starts", row_starts, (R + 1,), x.device)
-    out = torch.empty((T, N), dtype=x.dtype, device=x.device) if out is None else out
-    if out.shape != (T, N):
-        raise ValueError("lora_linear: bad output tensor")
+        adapters_ptr = _ints("adapters", adapters, (R,), dev)
+        starts_ptr = _ints("row_starts", row_starts, (R + 1,), dev)
+        a_ptr, b_ptr, scales_ptr = a.data_ptr(), b.data_ptr(), scales.data_ptr()
+    elif any(given):
+        raise ValueError("lora_linear: a, b, scales, row_starts and adapters come together")
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype, device=dev)
+    else:
+        _check(what, out, dev, dtype, 2)
+        if out.shape != (T, N):
+            raise ValueError("lora_linear: bad output tensor")
     if T == 0:
         return out
     dt = L._dtype_code(x)
-    need = L.load().libconv_lora_workspace(T, K, N, rank, n, R, dt)
-    _call(x.device, stream, "libconv_lora_linear", lambda p, m, s: L.libconv_lora_linear(
-        L._ptr(x), L._ptr(w), L._ptr(bias), L._ptr(a), L._ptr(b), L._ptr(scales), starts_ptr,
-        adapters_ptr, L._ptr(out), T, K, N, rank, n, R, x.stride(0), out.stride(0), dt, p, m, s),
-        need, workspace)
+    need = lib.libconv_lora_workspace(T, K, N, rank, n, R, dt) if workspace is True else 0
+    call = _Launch(dev, stream, need, workspace)
+    call.run("libconv_lora_linear", lib.libconv_lora_linear, x.data_ptr(), w.data_ptr(),
+             L._ptr(bias), a_ptr, b_ptr, scales_ptr, starts_ptr, adapters_ptr, out.data_ptr(), T,
+             K, N, rank, n, R, x.stride(0), out.stride(0), dt, call.ptr, call.size)
     return out

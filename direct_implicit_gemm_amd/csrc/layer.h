@@ -58,11 +58,12 @@ struct LoraArgs {
   char* y;
   int T, K, N, rank, n_adapters, n_requests;  // n_adapters 0: no low-rank term
   long long x_row, y_row;
-  float* low;               // [low_splits][T][low_width] partial sums of a x
-  int low_splits, low_width;
+  unsigned char* low;       // [T][low_width] low-rank values, 4 bytes each
+  int* adapter_of;          // [T]
+  int low_width;
 };
-// Splits and width of the low-rank sums, and the bytes they take.
-long long lora_plan(LoraArgs* a, int dtype, int cus);
+// Width of the low-rank values, and the bytes they and the rows' adapters take.
+long long lora_plan(LoraArgs* a);
 libconv_status lora_launch(LoraArgs a, int dtype, int cus, hipStream_t stream);
 
 }  // namespace libconv

@@ -130,7 +130,8 @@ libconv_status lora_shape(int T, int K, int N, int rank, int n_adapters, int n_r
   if (K % 8 != 0 || (low && rank > 128)) return LIBCONV_ERR_UNSUPPORTED;
   const long long eb = dtype_bytes(dtype);
   // offsets inside a tile of W, of an adapter's B, and workgroups: 31 bits
-  if (K * eb > kMaxRowBytes || (low && (long long)N * rank * eb >= kMaxInt - 1024) ||
+  if (K * eb > kMaxRowBytes || T > kMaxInt - 1024 ||
+      (low && (long long)N * rank * eb >= kMaxInt - 1024) ||
       ((double)T / 64 + 1) * ((double)N / 64 + 1) > (double)kMaxInt)
     return LIBCONV_ERR_TOO_LARGE;
   return LIBCONV_OK;
@@ -321,7 +322,7 @@ long long libconv_lora_workspace(int T, int K, int N, int rank, int n_adapters, 
   a.T = T; a.K = K; a.N = N; a.rank = rank;
   a.n_adapters = n_requests > 0 ? n_adapters : 0;
   a.n_requests = n_requests;
-  return lora_plan(&a, dtype, kPlanCus);
+  return lora_plan(&a);
 }
 
 libconv_status libconv_lora_linear(const void* x, const void* w, const void* bias, const void* a,
@@ -379,9 +380,10 @@ libconv_status libconv_lora_linear(const void* x, const void* w, const void* bia
   l.n_requests = n_requests;
   l.x_row = vx.s[1];
   l.y_row = vy.s[1];
-  if (lora_plan(&l, dtype, kPlanCus) > (workspace ? workspace_bytes : 0))
+  if (lora_plan(&l) > (workspace ? workspace_bytes : 0))
     return LIBCONV_ERR_SCRATCH_TOO_SMALL;
-  l.low = static_cast<float*>(workspace);
+  l.low = static_cast<unsigned char*>(workspace);
+  l.adapter_of = reinterpret_cast<int*>(l.low + (long long)T * l.low_width * 4);
   int cus = 0;
   if (!current_device(&cus)) return LIBCONV_ERR_NO_DEVICE;
   return lora_launch(l, dtype, cus, reinterpret_cast<hipStream_t>(stream));

@@ -3,14 +3,16 @@
 //
 //   y[t] = W x[t] + bias + s_a B_a (A_a x[t])
 //
-// Two launches.  The first forms the low-rank values A_a x[t] in fp32 (for
-// the rows of a tile: adapter by adapter, each lane keeping the result of its
-// own row's).  The second is the projection; a workgroup starts its sums with
-// the low-rank term of its tile, so y is written once.  That term's values
-// enter the matrix instructions as two bfloat16 numbers, high and low part
-// (16 significant bits): one would round the low-rank term to 8 bits before
-// the sum.  fp16 adapters are split the same way (three products), because a
-// low-rank value may be past fp16's range where y is not.
+// Two launches.  The first finds each row's adapter and forms the low-rank
+// values s_a A_a x[t] in fp32 (for 32 rows: adapter by adapter, each lane
+// keeping the result of its own row's; the sum's axis is split over the waves
+// of a workgroup, so that nothing is left to add up).  The second is the
+// projection; a workgroup starts its sums with the low-rank term of its tile,
+// so y is written once.  The low-rank values of 16-bit types enter the matrix
+// instructions as two bfloat16 numbers, high and low part (16 significant
+// bits): one would round the low-rank term to 8 bits before the sum.  fp16
+// adapters are split the same way (three products), because a low-rank value
+// may be past fp16's range where y is not.
 //
 // The projection is formed transposed (outputs n on the rows of the matrix
 // instructions, tokens on their columns), so that a lane holds 4 consecutive
@@ -24,120 +26,114 @@
 namespace libconv {
 namespace {
 
-constexpr int kLowRows = 32;      // rows of a tile of the first launch
-constexpr int kLowWaves = 4;
-constexpr int kMaxRank = 128;
+constexpr int kLowRows = 32;      // rows of a workgroup of the first launch
 
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// Adapter of each row of [row0, row0 + n) into LDS, -1 where there is none.
-// Threads take requests in turn and write the rows they have in the range.
-template <int THREADS>
-__device__ __forceinline__ void row_adapters(const LoraArgs& a, int row0, int n, int* out) {
-  for (int i = threadIdx.x; i < n; i += THREADS) out[i] = -1;
-  lds_barrier();
-  for (int r = threadIdx.x; r < a.n_requests; r += THREADS) {
-    const int ad = a.adapters[r];
-    if (ad < 0 || ad >= a.n_adapters) continue;
-    const int s0 = a.starts[r], s1 = a.starts[r + 1];
-    const int lo = s0 > row0 ? s0 : row0, hi = s1 < row0 + n ? s1 : row0 + n;
-    for (int t = lo; t < hi; ++t) out[t - row0] = ad;
-  }
-  lds_barrier();
-}
-
-// low[split][t][r] = sum over the split's part of K of x[t][k] A[r][k].
-template <int DT>
-__global__ __launch_bounds__(64 * kLowWaves) void low_kernel(const LoraArgs a) {
+// The first launch.  Writes, for every row t, adapter_of[t] (-1: none) and,
+// for rows that have one, width values from low + 4 width t on: fp32 ones, or
+// (16-bit types) width high bfloat16 parts and then width low parts.  Values
+// from the rank on are 0.  Grid: row tiles x shares of the adapters of a tile
+// (with few rows there are as many adapters as rows, and few tiles) x 32 of
+// the rank.
+template <int DT, int NW>
+__global__ __launch_bounds__(64 * NW) void low_kernel(const LoraArgs a) {
   constexpr int EB = Elem<DT>::bytes;
+  constexpr int THREADS = 64 * NW;
   __shared__ int ad_of[kLowRows];
-  __shared__ float red[kLowWaves][32][33];
+  __shared__ float red[NW][32][33];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
-  const int row0 = blockIdx.x * kLowRows, split = blockIdx.y;
-  row_adapters<64 * kLowWaves>(a, row0, kLowRows, ad_of);
+  const int row0 = blockIdx.x * kLowRows, r0 = blockIdx.z * 32;
+
+  // threads take requests in turn and write the rows they have in the tile
+  if (threadIdx.x < kLowRows) ad_of[threadIdx.x] = -1;
+  lds_barrier();
+  for (int r = threadIdx.x; r < a.n_requests; r += THREADS) {
+    const int ad = a.adapters[r], s0 = a.starts[r], s1 = a.starts[r + 1];
+    if (ad < 0 || ad >= a.n_adapters) continue;
+    const int lo = s0 > row0 ? s0 : row0, hi = s1 < row0 + kLowRows ? s1 : row0 + kLowRows;
+    for (int t = lo; t < hi; ++t) ad_of[t - row0] = ad;
+  }
+  lds_barrier();
+  const bool row_ok = row0 + l32 < a.T;
+  const int mine = row_ok ? ad_of[l32] : -1;
+  if (blockIdx.y == 0 && blockIdx.z == 0 && wave == 0 && half == 0 && row_ok)
+    a.adapter_of[row0 + l32] = mine;
 
   const int row_bytes = a.K * EB;
   const int steps = (row_bytes + 31) / 32;
-  const int parts = a.low_splits * kLowWaves, part = split * kLowWaves + wave;
-  const int k0 = (int)((long long)steps * part / parts);
-  const int k1 = (int)((long long)steps * (part + 1) / parts);
-
-  const bool row_ok = row0 + l32 < a.T;
-  const int mine = ad_of[l32];
+  const int k0 = (int)((long long)steps * wave / NW);
+  const int k1 = (int)((long long)steps * (wave + 1) / NW);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)row0 * a.x_row, 0x7ffffff0u);
-  const int x_off = l32 * (int)a.x_row;
+  const int x_off = l32 * (int)a.x_row, a_off = l32 * row_bytes;
+  const bool rank_ok = r0 + l32 < a.rank;
 
-  for (int r0 = 0; r0 < a.low_width; r0 += 32) {
-    float16_t res = {};
-    uint64_t left = __ballot(mine >= 0 && row_ok);
-    const bool rank_ok = r0 + l32 < a.rank;
-    while (left) {
-      const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-      left &= ~__ballot(mine == ad);
-      const __amdgpu_buffer_rsrc_t ra =
-          make_rsrc(a.a + ((long long)ad * a.rank + r0) * row_bytes, 0x7ffffff0u);
-      const int a_off = l32 * row_bytes;
-      float16_t acc = {};
-      constexpr int U = 4;
-      for (int k = k0; k < k1; k += U) {
-        u32x4_t xf[U], af[U];
+  float16_t res = {};
+  bool kept = false;   // this lane's row is this workgroup's to write
+  uint64_t left = __ballot(mine >= 0);
+  for (int turn = 0; left; ++turn) {
+    const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+    left &= ~__ballot(mine == ad);
+    if (turn % gridDim.y != blockIdx.y) continue;
+    const __amdgpu_buffer_rsrc_t ra =
+        make_rsrc(a.a + ((long long)ad * a.rank + r0) * row_bytes, 0x7ffffff0u);
+    float16_t acc = {};
+    constexpr int U = 8;
+    for (int k = k0; k < k1; k += U) {
+      u32x4_t xf[U], af[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int off = (k + u) * 32 + half * 16;
-          const bool in = k + u < k1 && off < row_bytes;
-          xf[u] = load16(rx, guard_offset(in && row_ok, x_off + off));
-          af[u] = load16(ra, guard_offset(in && rank_ok, a_off + off));
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(af[u], xf[u], acc, e);
+      for (int u = 0; u < U; ++u) {
+        const int off = (k + u) * 32 + half * 16;
+        const bool in = k + u < k1 && off < row_bytes;
+        xf[u] = load16(rx, guard_offset(in && row_ok, x_off + off));
+        af[u] = load16(ra, guard_offset(in && rank_ok, a_off + off));
       }
+      __builtin_amdgcn_sched_barrier(0);   // all of a batch's reads in flight together
 #pragma unroll
-      for (int i = 0; i < 16; ++i) res[i] = mine == ad ? acc[i] : res[i];
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(af[u], xf[u], acc, e);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) red[wave][l32][(i & 3) + 8 * (i >> 2) + 4 * half] = res[i];
-    lds_barrier();
-    for (int i = threadIdx.x; i < 32 * 32; i += 64 * kLowWaves) {
-      const int t = i >> 5, r = i & 31;
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kLowWaves; ++w) sum += red[w][t][r];
-      if (row0 + t < a.T)
-        a.low[((long long)split * a.T + row0 + t) * a.low_width + r0 + r] = sum;
-    }
-    lds_barrier();
+    for (int i = 0; i < 16; ++i) res[i] = mine == ad ? acc[i] : res[i];
+    kept = kept || mine == ad;
   }
-}
-
-// The tile's low-rank values, summed over the splits, times the adapter's
-// scale, in LDS: fp32, or a high and a low bfloat16 part ([n][width] each).
-template <int DT, int THREADS>
-__device__ __forceinline__ void low_to_lds(const LoraArgs& a, int row0, int n, const int* ad_of,
-                                           unsigned char* lds) {
-  const int width = a.low_width;
-  for (int i = threadIdx.x; i < n * width; i += THREADS) {
-    const int t = i / width, r = i - t * width, ad = ad_of[t];
+  const uint64_t rows = __ballot(kept);   // the same in all waves
+  if (rows == 0) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) red[wave][l32][(i & 3) + 8 * (i >> 2) + 4 * half] = res[i];
+  lds_barrier();
+  for (int i = threadIdx.x; i < 32 * 32; i += THREADS) {
+    const int t = i >> 5, r = i & 31;
+    if (!(rows >> t & 1)) continue;
     float v = 0.0f;
-    if (ad >= 0 && row0 + t < a.T) {
-      const float* p = a.low + (long long)(row0 + t) * width + r;
-      for (int s = 0; s < a.low_splits; ++s) v += p[(long long)s * a.T * width];
-      v *= a.scales[ad];
-    }
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += red[w][t][r];
+    v *= a.scales[ad_of[t]];
+    unsigned char* at = a.low + (long long)(row0 + t) * a.low_width * 4;
     if constexpr (DT == DT_F32) {
-      reinterpret_cast<float*>(lds)[i] = v;
+      reinterpret_cast<float*>(at)[r0 + r] = v;
     } else {
       const uint16_t hi = Elem<DT_BF16>::from_f32(v);
       const float rest = v - Elem<DT_BF16>::bits_to_f32(hi);
-      reinterpret_cast<uint16_t*>(lds)[i] = hi;
-      reinterpret_cast<uint16_t*>(lds)[n * width + i] = Elem<DT_BF16>::from_f32(rest);
+      reinterpret_cast<uint16_t*>(at)[r0 + r] = hi;
+      reinterpret_cast<uint16_t*>(at)[a.low_width + r0 + r] = Elem<DT_BF16>::from_f32(rest);
     }
   }
-  lds_barrier();
+}
+
+// 16 bytes of row t's low-rank values (and of their low parts), 0 where the
+// row is not one of adapter ad's.
+template <int DT>
+__device__ __forceinline__ void load_low(const LoraArgs& a, __amdgpu_buffer_rsrc_t rl, int t,
+                                         bool ok, int off, u32x4_t* hi, u32x4_t* lo) {
+  const int at = t * a.low_width * 4 + off;
+  *hi = load16(rl, guard_offset(ok, at));
+  if constexpr (DT == DT_F32) *lo = u32x4_t{0, 0, 0, 0};
+  else *lo = load16(rl, guard_offset(ok, at + a.low_width * 2));
 }
 
 // 16 bytes of row n of adapter ad's B, from component r on; 0 past the rank.
@@ -262,9 +258,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
   constexpr int THREADS = 64 * WM * WN;
   constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks of a wave
   constexpr int STAGE = (BM + BN) * 128;
-  static_assert(BM * kMaxRank * 4 <= 2 * STAGE, "the low-rank values fit the stages");
   __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
-  __shared__ int ad_of[BM];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
@@ -287,14 +281,13 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
     for (int j = 0; j < MB; ++j) acc[i][j] = float16_t{};
 
   if (a.n_adapters > 0) {
-    row_adapters<THREADS>(a, m0, BM, ad_of);
-    low_to_lds<DT, THREADS>(a, m0, BM, ad_of, lds);
-    const int width = a.low_width;
-    constexpr int LB = DT == DT_F32 ? 4 : 2;   // bytes of a low-rank value in LDS
+    constexpr int LB = DT == DT_F32 ? 4 : 2;   // bytes of a low-rank value
+    const __amdgpu_buffer_rsrc_t rl =
+        make_rsrc(a.low + (long long)m0 * a.low_width * 4, 0x7ffffff0u);
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
       const int t = (wm * MB + j) * 32 + l32;
-      const int mine = ad_of[t];
+      const int mine = m0 + t < a.T ? a.adapter_of[m0 + t] : -1;
       uint64_t left = __ballot(mine >= 0);
       while (left) {
         const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
@@ -302,21 +295,16 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
         const __amdgpu_buffer_rsrc_t rb =
             make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
         for (int s = 0; s < (a.rank * LB + 31) / 32; ++s) {
-          const unsigned char* at = lds + t * width * LB + s * 32 + half * 16;
-          u32x4_t hi = *reinterpret_cast<const u32x4_t*>(at), lo = {0, 0, 0, 0};
-          if constexpr (DT != DT_F32)
-            lo = *reinterpret_cast<const u32x4_t*>(at + BM * width * LB);
-          if (mine != ad) hi = lo = u32x4_t{0, 0, 0, 0};
+          u32x4_t hi, lo, bf[NB];
+          load_low<DT>(a, rl, t, mine == ad, s * 32 + half * 16, &hi, &lo);
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const u32x4_t bf = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32,
-                                          (s * 32 + half * 16) / LB);
-            low_step<DT, true>(bf, hi, lo, acc[i][j]);
-          }
+          for (int i = 0; i < NB; ++i)
+            bf[i] = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32, (s * 32 + half * 16) / LB);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) low_step<DT, true>(bf[i], hi, lo, acc[i][j]);
         }
       }
     }
-    lds_barrier();   // the stages take the low-rank values' place
   }
 
   // stages
@@ -401,50 +389,44 @@ template <int DT, int RB>
 __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const LoraArgs a) {
   constexpr int EB = Elem<DT>::bytes;
   constexpr int THREADS = 64 * kFewWaves, ROWS = 16 * RB;
-  constexpr int LOW = ROWS * kMaxRank * 4, JOIN = kFewWaves * ROWS * 20 * 4;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[LOW > JOIN ? LOW : JOIN];
-  __shared__ int ad_of[64];
+  __shared__ __attribute__((aligned(16))) float join[kFewWaves * ROWS * 20];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l16 = lane & 15, quarter = lane >> 4;
   const int n0 = blockIdx.x * 16;
+  const int here = a.n_adapters > 0 && lane < a.T ? a.adapter_of[lane] : -1;
+
+  const int row_bytes = a.K * EB;
+  const int steps = (row_bytes + 63) / 64;
+  const int k0 = steps * wave / kFewWaves, k1 = steps * (wave + 1) / kFewWaves;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, 0x7ffffff0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row_bytes, 0x7ffffff0u);
+  const bool n_ok = n0 + l16 < a.N;
+  // W is what the call reads from memory: 16 steps of it are on their way at
+  // a time, the first before anything else is waited for
+  constexpr int UW = 16, UX = 4;
+  u32x4_t wf[UW];
+  auto fetch_w = [&](int k) {
+#pragma unroll
+    for (int u = 0; u < UW; ++u) {
+      const int off = (k + u) * 64 + quarter * 16;
+      wf[u] = load16(rw, guard_offset(n_ok && k + u < k1 && off < row_bytes,
+                                      l16 * row_bytes + off));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  fetch_w(k0);
 
   float4_t acc[RB];
 #pragma unroll
   for (int j = 0; j < RB; ++j) acc[j] = float4_t{0, 0, 0, 0};
-
-  const int row_bytes = a.K * EB;
-  const int steps = (row_bytes + 63) / 64;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, 0x7ffffff0u);
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row_bytes, 0x7ffffff0u);
-  const bool n_ok = n0 + l16 < a.N;
-  // U neighbouring steps to a wave, so that its reads cover whole lines
-  constexpr int U = RB <= 2 ? 8 : 4;
-  for (int k = wave * U; k < steps; k += kFewWaves * U) {
-    u32x4_t wf[U], xf[U][RB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int off = (k + u) * 64 + quarter * 16;
-      const bool in = off < row_bytes;
-      wf[u] = load16(rw, guard_offset(in && n_ok, l16 * row_bytes + off));
-#pragma unroll
-      for (int j = 0; j < RB; ++j)
-        xf[u][j] = load16(rx, guard_offset(in && j * 16 + l16 < a.T,
-                                           (j * 16 + l16) * (int)a.x_row + off));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < RB; ++j) Step<DT, false>::run(wf[u], xf[u][j], acc[j]);
-  }
-
   if (a.n_adapters > 0) {
-    row_adapters<THREADS>(a, 0, 64, ad_of);
-    low_to_lds<DT, THREADS>(a, 0, ROWS, ad_of, lds);
-    const int width = a.low_width;
     constexpr int LB = DT == DT_F32 ? 4 : 2;
+    const __amdgpu_buffer_rsrc_t rl = make_rsrc(a.low, 0x7ffffff0u);
+    int mine[RB];
+#pragma unroll
+    for (int j = 0; j < RB; ++j) mine[j] = __shfl(here, j * 16 + l16);
     // the waves take the adapters in turn
-    const int here = ad_of[lane];
-    uint64_t left = __ballot(here >= 0 && lane < a.T);
+    uint64_t left = __ballot(here >= 0);
     for (int turn = 0; left; ++turn) {
       const int ad = __builtin_amdgcn_readlane(here, __builtin_ctzll(left));
       left &= ~__ballot(here == ad);
@@ -453,22 +435,39 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const LoraArgs a) {
           make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
       for (int s = 0; s < (a.rank * LB + 63) / 64; ++s) {
         const u32x4_t bf = load_b<DT>(a, rb, n0 + l16, (s * 64 + quarter * 16) / LB);
+        u32x4_t hi[RB], lo[RB];
 #pragma unroll
-        for (int j = 0; j < RB; ++j) {
-          const unsigned char* at = lds + (j * 16 + l16) * width * LB + s * 64 + quarter * 16;
-          u32x4_t hi = *reinterpret_cast<const u32x4_t*>(at), lo = {0, 0, 0, 0};
-          if constexpr (DT != DT_F32)
-            lo = *reinterpret_cast<const u32x4_t*>(at + ROWS * width * LB);
-          if (ad_of[j * 16 + l16] != ad) hi = lo = u32x4_t{0, 0, 0, 0};
-          low_step<DT, false>(bf, hi, lo, acc[j]);
-        }
+        for (int j = 0; j < RB; ++j)
+          load_low<DT>(a, rl, j * 16 + l16, mine[j] == ad, s * 64 + quarter * 16, &hi[j], &lo[j]);
+#pragma unroll
+        for (int j = 0; j < RB; ++j) low_step<DT, false>(bf, hi[j], lo[j], acc[j]);
       }
     }
-    lds_barrier();   // the join takes the low-rank values' place
+  }
+
+  for (int k = k0; k < k1; k += UW) {
+    if (k != k0) fetch_w(k);
+#pragma unroll
+    for (int v = 0; v < UW; v += UX) {
+      if (k + v >= k1) break;
+      u32x4_t xf[UX][RB];
+#pragma unroll
+      for (int u = 0; u < UX; ++u)
+#pragma unroll
+        for (int j = 0; j < RB; ++j) {
+          const int off = (k + v + u) * 64 + quarter * 16;
+          xf[u][j] = load16(rx, guard_offset(k + v + u < k1 && off < row_bytes &&
+                                                 j * 16 + l16 < a.T,
+                                             (j * 16 + l16) * (int)a.x_row + off));
+        }
+#pragma unroll
+      for (int u = 0; u < UX; ++u)
+#pragma unroll
+        for (int j = 0; j < RB; ++j) Step<DT, false>::run(wf[v + u], xf[u][j], acc[j]);
+    }
   }
 
   // [wave][token][output], 20 floats a token: writes and reads without conflicts
-  float* join = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int j = 0; j < RB; ++j)
     *reinterpret_cast<float4_t*>(join + ((wave * ROWS + j * 16 + l16) * 20 + quarter * 4)) = acc[j];
@@ -504,10 +503,19 @@ double tile_cost(const LoraArgs& a, int cus, int bm, int bn, int per_cu, double 
 
 template <int DT>
 void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
-  if (a.n_adapters > 0)
-    hipLaunchKernelGGL((low_kernel<DT>),
-                       dim3((unsigned)((a.T + kLowRows - 1) / kLowRows), (unsigned)a.low_splits),
-                       dim3(64 * kLowWaves), 0, stream, a);
+  if (a.n_adapters > 0) {
+    // with few row tiles, 16 waves to one and the tile's adapters dealt out
+    const int tiles = (a.T + kLowRows - 1) / kLowRows;
+    int shares = cus / tiles;
+    const int most = a.n_adapters < kLowRows ? a.n_adapters : kLowRows;
+    if (shares > most) shares = most;
+    const dim3 grid((unsigned)tiles, (unsigned)(shares < 1 ? 1 : shares),
+                    (unsigned)(a.low_width / 32));
+    if (tiles < cus)
+      hipLaunchKernelGGL((low_kernel<DT, 16>), grid, dim3(64 * 16), 0, stream, a);
+    else
+      hipLaunchKernelGGL((low_kernel<DT, 8>), grid, dim3(64 * 8), 0, stream, a);
+  }
   if (a.T <= 64) {
     const dim3 grid((unsigned)((a.N + 15) / 16)), threads(64 * kFewWaves);
     if (a.T <= 16) hipLaunchKernelGGL((few_kernel<DT, 1>), grid, threads, 0, stream, a);
@@ -525,19 +533,11 @@ void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
 
 }  // namespace
 
-long long lora_plan(LoraArgs* a, int dtype, int cus) {
-  const int eb = dtype == LIBCONV_F32 ? 4 : 2;
-  a->low_splits = 0;
+long long lora_plan(LoraArgs* a) {
   a->low_width = 0;
   if (a->n_adapters == 0 || a->T == 0) return 0;
   a->low_width = (a->rank + 31) / 32 * 32;
-  const long long tiles = (a->T + kLowRows - 1) / kLowRows;
-  // a workgroup for each compute unit, 512 bytes of a row or more to a wave
-  long long s = (cus + tiles - 1) / tiles;
-  const long long most = (long long)a->K * eb / (512 * kLowWaves);
-  if (s > most) s = most;
-  a->low_splits = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
-  return (long long)a->low_splits * a->T * a->low_width * 4;
+  return (long long)a->T * (a->low_width + 1) * 4;
 }
 
 libconv_status lora_launch(LoraArgs a, int dtype, int cus, hipStream_t stream) {
