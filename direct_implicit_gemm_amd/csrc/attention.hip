@@ -25,24 +25,30 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kLowest = -3.402823466e38f;   // the maximum of no keys: finite, so that no
+                                              // difference of maxima is a NaN
+constexpr float kSlack = 8.0f;   // log2 of how far a maximum may fall behind
 
 template <int DT, int DP, int WK> struct Shape {
   static constexpr int EB = Elem<DT>::bytes;
-  static constexpr int RB = DP * EB;                       // bytes of a row of K or V in LDS
+  static constexpr int RB = (DP <= 64 ? 64 : 128) * EB;    // bytes of a row of K or V in LDS
   static constexpr int CPR = RB / 16;                      // 16-byte chunks of it
   static constexpr int KPW = EB == 4 ? 32 : WK == 1 ? 64 : 32;  // keys a wave takes of a tile
   static constexpr int BN = KPW * WK;                      // keys of a tile
   static constexpr int ROWS = 128 / WK;                    // rows of a workgroup
   static constexpr int TILE = BN * RB;
   static constexpr int LDS = 4 * TILE;                     // K and V, two stages
+  static constexpr int WAVES = 2 * LDS <= 160 * 1024 ? 2 : 1;   // workgroups a compute unit, at least
 };
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 // 16-byte chunk of a row of K (V) in LDS is kept at chunk ^ swizzle(row): the
-// 16 lanes that read one chunk of 16 rows at a time then hit all banks.
+// 16 lanes that read one chunk of 16 rows at a time then hit all banks (in
+// rows of 512 bytes, twice: a copy covers 8 rows there, and a thread's chunk
+// is the same for all of its copies; the fp32 product is far slower anyway).
 template <int CPR> __device__ __forceinline__ int k_swizzle(int row) {
-  return CPR >= 16 ? row & 15 : (row >> 1) & 7;
+  return CPR == 32 ? row & 7 : CPR == 16 ? row & 15 : (row >> 1) & 7;
 }
 // V is read 64 contiguous bytes of each of 4 rows at a time (16-bit types), or
 // 128 bytes of two rows 4 apart (fp32).
@@ -51,49 +57,69 @@ template <int EB, int CPR> __device__ __forceinline__ int v_swizzle(int row) {
   return CPR >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
 }
 
+// The larger of v in this lane and in the lane 32 away.
 __device__ __forceinline__ float swap_halves_max(float v) {
-  return fmaxf(v, __shfl_xor(v, 32));
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+}
+
+// 4 elements of one column of 16-bit elements: the 16 lanes of a quarter wave
+// name 8 bytes each of 4 rows.  `p` is restrict so that the read has a scope of
+// its own: without one, the compiler lets it wait for every copy to LDS that
+// is on its way, those of the next tile among them.
+__device__ __forceinline__ u32x2_t read_column(const unsigned char* __restrict p) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4_t*)p));
 }
 
 // Lane's 4 probabilities -> 2 words of the 16-bit type.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)Elem<DT>::from_f32(a) | ((uint32_t)Elem<DT>::from_f32(b) << 16);
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {a, b};
+  if constexpr (DT == DT_F16) {
+    typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2_t));
+  } else {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+  }
 }
 
-struct KeyRun {          // keys one tile copy reads
-  const char *k, *v;     // row 0 of the tile
-  int k_row, v_row;      // row strides in bytes (below 2^24)
-  int valid;             // rows that exist
+// A walk over a workgroup's tiles of K or of V: prefix, then own keys.
+struct Cursor {
+  const char* p;        // row 0 of the tile
+  int stride;           // of its rows in bytes (below 2^24)
+  int left;             // rows from there to the end of the run; <= 0 past the end
+  int off;              // this lane's bytes of its first row, past any end without such
+  const char* own_p;    // the own keys' first tile, where the run follows
+  int own_stride, own_left, own_off;
 };
 
-// Copies a tile's rows of K and V into LDS, 16 bytes a lane.  Rows from
-// `valid` on and components from D on arrive as zeros (offsets past the
-// resource's end).
-template <int DT, int DP, int WK>
-__device__ __forceinline__ void copy_tile(const KeyRun& t, unsigned char* lds, int wave, int lane,
-                                          int d_chunks) {
+// Copies a tile's rows into LDS, 16 bytes a lane, and moves on.  Rows past the
+// run's end and components from D on arrive as zeros: they lie past the
+// resource's end (rows that lie closer than their own length repeat bytes of
+// valid rows instead, whose scores are masked).
+template <int DT, int DP, int WK, bool V>
+__device__ __forceinline__ void copy_tile(Cursor& c, unsigned char* lds, int row_bytes) {
   using Z = Shape<DT, DP, WK>;
-  const __amdgpu_buffer_rsrc_t rk = make_rsrc(t.k, 0x7ffffff0u);
-  const __amdgpu_buffer_rsrc_t rv = make_rsrc(t.v, 0x7ffffff0u);
-  constexpr int N = Z::TILE / 16 / kThreads;
+  constexpr int PASS = kThreads / Z::CPR;   // rows of a copy of the workgroup
+  const int rows = c.left < Z::BN ? c.left : Z::BN;
+  const __amdgpu_buffer_rsrc_t r =
+      make_rsrc(c.p, rows > 0 ? (uint32_t)((rows - 1) * c.stride + row_bytes) : 0u);
+  unsigned char* to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63) * 16;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    // key-splitting waves copy the rows they read themselves
-    const int unit = (wave * N + j) * 64 + lane;
-    const int row = unit / Z::CPR, slot = unit % Z::CPR;
-    const int chunk = slot ^ k_swizzle<Z::CPR>(row);
-    const bool ok = row < t.valid && chunk < d_chunks;
-    copy16_to_lds(rk, lds + (wave * N + j) * 1024, guard_offset(ok, row * t.k_row + chunk * 16));
-  }
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int unit = (wave * N + j) * 64 + lane;
-    const int row = unit / Z::CPR, slot = unit % Z::CPR;
-    const int chunk = slot ^ v_swizzle<Z::EB, Z::CPR>(row);
-    const bool ok = row < t.valid && chunk < d_chunks;
-    copy16_to_lds(rv, lds + Z::TILE + (wave * N + j) * 1024,
-                  guard_offset(ok, row * t.v_row + chunk * 16));
+  for (int j = 0; j < Z::BN / PASS; ++j)
+    copy16_to_lds(r, to + j * kThreads * 16, c.off, j * PASS * c.stride);
+  c.p += (long long)Z::BN * c.stride;
+  c.left -= Z::BN;
+  if (c.left <= 0) {   // the own keys; past them there is nothing
+    c.p = c.own_p;
+    c.stride = c.own_stride;
+    c.left = c.own_left;
+    c.off = c.own_off;
+    c.own_left = 0;
   }
 }
 
@@ -111,13 +137,13 @@ template <int DT, int DP, int WK>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsigned char* lds) {
   using Z = Shape<DT, DP, WK>;
   constexpr int EB = Z::EB, RB = Z::RB, CPR = Z::CPR, KPW = Z::KPW, BN = Z::BN;
-  constexpr int KS = RB / 32;   // steps of the first product
-  constexpr int NB = KPW / 32;  // blocks of 32 keys a wave
-  constexpr int DB = DP / 32;   // blocks of 32 components
+  constexpr int KS = DP * EB / 32;  // steps of the first product
+  constexpr int NB = KPW / 32;      // blocks of 32 keys a wave
+  constexpr int DB = DP / 32;       // blocks of 32 components
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int wr = wave / WK, wk = wave % WK;   // row block, key share
-  const int d_chunks = a.D * EB / 16;
+  const int row_bytes = a.D * EB, d_chunks = row_bytes / 16;
 
   // this lane's query
   const int local = wr * 32 + l32;
@@ -163,22 +189,37 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
   const char* vp = a.vp + job.hk * a.vp_h;
   const char* ko = a.k + job.b * a.k_b + job.hk * a.k_h;
   const char* vo = a.v + job.b * a.v_b + job.hk * a.v_h;
-  auto run_of = [&](int t) {
-    KeyRun r;
-    if (t < tiles_p) {
-      const long long key = (long long)t * BN;
-      r = {kp + key * a.kp_r, vp + key * a.vp_r, (int)a.kp_r, (int)a.vp_r, (int)(a.P - key)};
-    } else {
-      const long long key = (long long)(t - tiles_p) * BN;
-      r = {ko + key * a.k_r, vo + key * a.v_r, (int)a.k_r, (int)a.v_r, (int)(end_own - key)};
+  // a thread's rows of a copy lie a multiple of 16 (rows of 512 bytes: 8) apart: its
+  // chunk of them is the same for all
+  const int c_row = threadIdx.x / CPR, c_slot = threadIdx.x % CPR;
+  auto cursor = [&](const char* p, long long stride, const char* o, long long own_stride,
+                    int chunk) {
+    Cursor c;
+    c.own_p = o;
+    c.own_stride = (int)own_stride;
+    c.own_left = end_own;
+    c.own_off = chunk < d_chunks ? c_row * (int)own_stride + chunk * 16 : kFarOffset;
+    c.p = p + (long long)t0 * BN * stride;
+    c.stride = (int)stride;
+    c.left = a.P - t0 * BN;
+    c.off = chunk < d_chunks ? c_row * (int)stride + chunk * 16 : kFarOffset;
+    if (t0 >= tiles_p) {
+      c.p = o + (long long)(t0 - tiles_p) * BN * own_stride;
+      c.stride = (int)own_stride;
+      c.left = end_own - (t0 - tiles_p) * BN;
+      c.off = c.own_off;
+      c.own_left = 0;
     }
-    return r;
+    return c;
   };
+  static_assert(kThreads / CPR % (CPR == 32 ? 8 : 16) == 0, "one swizzle for a thread's rows");
+  Cursor ck = cursor(kp, a.kp_r, ko, a.k_r, c_slot ^ k_swizzle<CPR>(c_row));
+  Cursor cv = cursor(vp, a.vp_r, vo, a.v_r, c_slot ^ v_swizzle<EB, CPR>(c_row));
 
   float16_t acc[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) acc[d] = float16_t{};
-  float m = kNegInf, l = 0.0f;   // maximum (times scale, log2) and sum of this lane's half
+  float m = kLowest, l = 0.0f;   // maximum (times scale, log2) and sum of this lane's half
 
   // LDS offsets that do not change from tile to tile
   const int krow = (wk * KPW + l32) * RB;
@@ -187,104 +228,194 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
   const int vrow16 = 4 * half + (i16 >> 2);
   const int vchunk16 = ((lane >> 4) & 1) * 2 + ((i16 & 3) >> 1);
 
-  if (t0 < t1) copy_tile<DT, DP, WK>(run_of(t0), lds, wave, lane, d_chunks);
-  for (int t = t0; t < t1; ++t) {
-    unsigned char* kt = lds + ((t - t0) & 1) * 2 * Z::TILE;
-    unsigned char* vt = kt + Z::TILE;
-    // this wave's copies have arrived; after the barrier everyone's have, and
-    // nobody reads the other stage any more
-    wait_vmcnt<0>();
-    lds_barrier();
-    if (t + 1 < t1)
-      copy_tile<DT, DP, WK>(run_of(t + 1), lds + ((t + 1 - t0) & 1) * 2 * Z::TILE, wave, lane,
-                            d_chunks);
-
-    float16_t s[NB];
+  // scores of a block of 32 keys of a tile, key on the rows, query on the columns
+  auto score = [&](const unsigned char* kt, int b, float16_t& s) {
+    s = float16_t{};
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      s[b] = float16_t{};
+    for (int ks = 0; ks < KS; ++ks) {
+      const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(kt + krow + b * 32 * RB +
+                                                           (ksw ^ (ks * 32)));
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(kt + krow + b * 32 * RB +
-                                                             (ksw ^ (ks * 32)));
-#pragma unroll
-        for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(kf, qf[ks], s[b], e);
-      }
+      for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(kf, qf[ks], s, e);
     }
-
-    // keys past the end and keys the causal mask hides
-    const int key0 = (t < tiles_p ? t : t - tiles_p) * BN + wk * KPW;
-    const int lane_lim = t < tiles_p ? a.P : lim;
-    if (key0 + KPW > (t < tiles_p ? a.P : lim_wave)) {
+  };
+  // keys past the end and keys the causal mask hides; key0: the block's first
+  auto mask = [&](int t, int b, float16_t& s) {
+    const bool own = t >= tiles_p;
+    const int key0 = (own ? t - tiles_p : t) * BN + wk * KPW + b * 32;
+    if (key0 + 32 > (own ? lim_wave : a.P)) {
+      const int lane_lim = (own ? lim : a.P) - key0 - 4 * half;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int r = 0; r < 16; ++r)
+        s[r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[r] : kNegInf;
+    }
+  };
+  auto top_of = [&](const float16_t& s) {
+    float top = s[0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = key0 + b * 32 + (r & 3) + 8 * (r >> 2) + 4 * half;
-          s[b][r] = key < lane_lim ? s[b][r] : kNegInf;
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+    return swap_halves_max(top) * a.scale;
+  };
+  // probabilities times 2^(their maximum - m), added to the sum
+  auto probabilities = [&](float16_t& s) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale, -m));
+      l += s[r];
+    }
+  };
+  auto rescale = [&](float f) {
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[d][r] *= f;
+  };
+  // 16 keys a step of the second product: this lane's are 4 half + {0..3, 8..11}
+  auto pack = [&](const float16_t& s, u32x4_t* pf) {
+    if constexpr (EB == 2) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pf[c][e] = pack2<DT>(s[c * 8 + 2 * e], s[c * 8 + 2 * e + 1]);
+    }
+  };
+  auto add_values = [&](const unsigned char* vt, int b, const u32x4_t* pf) {
+    if constexpr (EB == 2) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          const int chunk = (d * 4 + vchunk16) ^ v_swizzle<EB, CPR>(vrow16);
+          const unsigned char* at =
+              vt + (wk * KPW + b * 32 + c * 16 + vrow16) * RB + chunk * 16 + (i16 & 1) * 8;
+          const u32x2_t lo = read_column(at), hi = read_column(at + 8 * RB);
+          const u32x4_t vf = {lo[0], lo[1], hi[0], hi[1]};
+          Mma<DT>::step(vf, pf[c], acc[d], 0);
         }
     }
+  };
 
-    float top = s[0][0];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
-    top = swap_halves_max(top) * a.scale;
-    if (__any(top > m)) {
-      const float m_new = fmaxf(m, top);
-      // rows that have seen no key yet keep 0 (their sums are 0 too)
-      const float f = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+  if constexpr (EB == 2 && WK == 1) {
+    // Pipelined over blocks of 32 keys: while the vector units form a block's
+    // probabilities, the matrix units form the scores of the next block and
+    // add the values of the block before, in the same wave.  K is therefore a
+    // tile ahead of V.
+    static_assert(NB == 2, "a tile is two blocks");
+    unsigned char* const kt = lds;
+    unsigned char* const vt = lds + 2 * Z::TILE;
+    constexpr int COPIES = Z::BN * CPR / kThreads;   // of a tile, a thread
+    const int n = t1 - t0;
+    float16_t s0, s1;      // scores of two blocks
+    u32x4_t p0[2], p1[2];  // probabilities of two blocks
+    float f;               // what a block's maximum makes of the sums so far
+    // The maximum moves only when it falls behind by 2^8, which fp16
+    // probabilities bear too: the sums are hardly ever rescaled.
+    auto move_up = [&](const float16_t& s) {
+      const float top = top_of(s);
+      const float m_new = top > m + kSlack ? top : m;
+      f = __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
       l *= f;
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[d][r] *= f;
-    }
-    const float base = m == kNegInf ? 0.0f : m;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], a.scale, -base));
-        l += s[b][r];
+    };
+    // `p` is formed up to here (its first use is past a branch, where the
+    // compiler would take its computation, away from the matrix instructions)
+    auto follow = [&](u32x4_t* p) {
+      asm volatile("" : "+v"(p[0]), "+v"(p[1]), "+v"(l));
+      if (__any(f != 1.0f)) rescale(f);
+    };
+    if (n > 0) {
+      copy_tile<DT, DP, WK, false>(ck, kt, row_bytes);
+      copy_tile<DT, DP, WK, true>(cv, vt, row_bytes);
+      copy_tile<DT, DP, WK, false>(ck, kt + Z::TILE, row_bytes);
+      wait_vmcnt<2 * COPIES>();
+      lds_barrier();
+      score(kt, 0, s0);
+      score(kt, 1, s1);
+      mask(t0, 0, s0);
+      move_up(s0);   // nothing to rescale yet
+      probabilities(s0);
+      pack(s0, p0);
+      for (int i = 0; i < n - 1; ++i) {
+        // K of tile i + 1 and V of tile i have arrived for this wave, after the
+        // barrier for all, and nobody reads K of tile i and V of i - 1 any more
+        const unsigned char* k1 = kt + ((i + 1) & 1) * Z::TILE;
+        const unsigned char* v0 = vt + (i & 1) * Z::TILE;
+        wait_vmcnt<0>();
+        lds_barrier();
+        copy_tile<DT, DP, WK, true>(cv, vt + ((i + 1) & 1) * Z::TILE, row_bytes);
+        copy_tile<DT, DP, WK, false>(ck, kt + (i & 1) * Z::TILE, row_bytes);
+        mask(t0 + i, 1, s1);
+        move_up(s1);
+        score(k1, 0, s0);
+        probabilities(s1);
+        pack(s1, p1);
+        add_values(v0, 0, p0);
+        follow(p1);
+        mask(t0 + i + 1, 0, s0);
+        move_up(s0);
+        score(k1, 1, s1);
+        probabilities(s0);
+        pack(s0, p0);
+        add_values(v0, 1, p1);
+        follow(p0);
       }
-
-    if constexpr (EB == 4) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
+      const unsigned char* v0 = vt + ((n - 1) & 1) * Z::TILE;
+      wait_vmcnt<0>();
+      lds_barrier();
+      mask(t1 - 1, 1, s1);
+      move_up(s1);
+      probabilities(s1);
+      pack(s1, p1);
+      add_values(v0, 0, p0);
+      follow(p1);
+      add_values(v0, 1, p1);
+    }
+  } else {
+    if (t0 < t1) {
+      copy_tile<DT, DP, WK, false>(ck, lds, row_bytes);
+      copy_tile<DT, DP, WK, true>(cv, lds + Z::TILE, row_bytes);
+    }
+    for (int t = t0; t < t1; ++t) {
+      unsigned char* kt = lds + ((t - t0) & 1) * 2 * Z::TILE;
+      unsigned char* vt = kt + Z::TILE;
+      // this wave's copies have arrived; after the barrier everyone's have, and
+      // nobody reads the other stage any more
+      wait_vmcnt<0>();
+      lds_barrier();
+      if (t + 1 < t1) {
+        unsigned char* next = lds + ((t + 1 - t0) & 1) * 2 * Z::TILE;
+        copy_tile<DT, DP, WK, false>(ck, next, row_bytes);
+        copy_tile<DT, DP, WK, true>(cv, next + Z::TILE, row_bytes);
+      }
+      static_assert(NB == 1, "32 keys a wave");
+      float16_t s;
+      score(kt, 0, s);
+      mask(t, 0, s);
+      const float top = top_of(s);
+      if (__any(top > m)) {
+        const float m_new = fmaxf(m, top);
+        const float f = __builtin_amdgcn_exp2f(m - m_new);
+        m = m_new;
+        l *= f;
+        rescale(f);
+      }
+      probabilities(s);
+      if constexpr (EB == 4) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int vr = wk * KPW + b * 32 + (r & 3) + 8 * (r >> 2) + 4 * half;
+          const int vr = wk * KPW + (r & 3) + 8 * (r >> 2) + 4 * half;
 #pragma unroll
           for (int d = 0; d < DB; ++d) {
             const int chunk = (d * 8 + (l32 >> 2)) ^ v_swizzle<EB, CPR>(vr);
             const float vf = *reinterpret_cast<const float*>(vt + vr * RB + chunk * 16 +
                                                              (l32 & 3) * 4);
-            acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, s[b][r], acc[d], 0, 0, 0);
+            acc[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, s[r], acc[d], 0, 0, 0);
           }
         }
-    } else {
-      // 16 keys a step: this lane's are base + 4 half + {0..3, 8..11}
-#pragma unroll
-      for (int c = 0; c < KPW / 16; ++c) {
-        u32x4_t pf;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          pf[e] = pack2<DT>(s[c >> 1][(c & 1) * 8 + 2 * e], s[c >> 1][(c & 1) * 8 + 2 * e + 1]);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          const int chunk = (d * 4 + vchunk16) ^ v_swizzle<EB, CPR>(vrow16);
-          unsigned char* at = vt + (wk * KPW + c * 16 + vrow16) * RB + chunk * 16 + (i16 & 1) * 8;
-          const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4_t*)at);
-          const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4_t*)(at + 8 * RB));
-          const u32x2_t lw = __builtin_bit_cast(u32x2_t, lo), hw = __builtin_bit_cast(u32x2_t, hi);
-          const u32x4_t vf = {lw[0], lw[1], hw[0], hw[1]};
-          Mma<DT>::step(vf, pf, acc[d], 0);
-        }
+      } else {
+        u32x4_t pf[2];
+        pack(s, pf);
+        add_values(vt, 0, pf);
       }
     }
   }
@@ -317,7 +448,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
 #pragma unroll
     for (int w = 1; w < WK; ++w)
       m_all = fmaxf(m_all, reinterpret_cast<const float*>(room + (w - 1) * PER)[l32]);
-    const float f = m_all == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - m_all);
+    const float f = __builtin_amdgcn_exp2f(m - m_all);
     l *= f;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -326,7 +457,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
 #pragma unroll
     for (int w = 1; w < WK; ++w) {
       const float* o = reinterpret_cast<const float*>(room + (w - 1) * PER);
-      const float g = m_all == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(o[l32] - m_all);
+      const float g = __builtin_amdgcn_exp2f(o[l32] - m_all);
       l = fmaf(o[32 + l32], g, l);
 #pragma unroll
       for (int d = 0; d < DB; ++d)
@@ -386,7 +517,7 @@ __device__ __forceinline__ int xcd_order(int id, int n) {
 
 // Each entry's rows over its prefix and own keys.
 template <int DT, int DP, int WK>
-__global__ __launch_bounds__(kThreads) void attn_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(kThreads, (Shape<DT, DP, WK>::WAVES)) void attn_kernel(const AttnArgs a) {
   using Z = Shape<DT, DP, WK>;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Z::LDS];
   const int per_entry = a.Sq * a.G;
@@ -411,7 +542,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(const AttnArgs a) {
 
 // Rows of all entries, side by side, over the prefix.
 template <int DT, int DP, int WK>
-__global__ __launch_bounds__(kThreads) void attn_prefix_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(kThreads, (Shape<DT, DP, WK>::WAVES)) void attn_prefix_kernel(const AttnArgs a) {
   using Z = Shape<DT, DP, WK>;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Z::LDS];
   const int all = a.B * a.Sq * a.G;
@@ -510,6 +641,7 @@ void launch(const AttnArgs& a, hipStream_t stream) {
 template <int DT>
 void launch_dt(const AttnArgs& a, hipStream_t stream) {
   if (a.D <= 64) launch<DT, 64>(a, stream);
+  else if (a.D <= 96) launch<DT, 96>(a, stream);
   else launch<DT, 128>(a, stream);
 }
 

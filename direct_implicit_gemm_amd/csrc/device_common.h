@@ -153,13 +153,14 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // One 16-byte global read per lane written straight into LDS: lane l's
-// vector lands at dst + 16 l (dst is wave-uniform).  Kept out of the generic
+// vector lands at dst + 16 l (dst and soff, which adds to the lanes' offsets,
+// are wave-uniform).  Kept out of the generic
 // lambdas of the kernel: inside them the host pass drops the kernel's launch
 // stub.
 __device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* dst,
-                                              int off) {
+                                              int off, int soff = 0) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16,
-                                           off, 0, 0, 0);
+                                           off, soff, 0, 0);
 }
 
 // This wave's LDS accesses so far are complete and none of the later ones
