@@ -14,8 +14,10 @@
 //
 // Rows: the queries of all heads that share a key head lie side by side (row
 // = ((entry, query), head of the group)), 32 to a wave.  A workgroup of four
-// waves holds 128, 64 or 32 rows; with fewer rows the waves share a row block
-// and split the keys of a tile (WK), and join at the end through LDS.
+// waves holds 128 rows that share their tiles of keys (WK = 1), or, with few
+// rows, 32, and its waves take a quarter of each tile's keys (WK = 4): such a
+// wave copies the keys it reads itself, waits for nobody until the four join
+// through LDS at the end, and is bound by the keys it reads from memory.
 #include "device_common.h"
 #include "layer.h"
 
@@ -30,16 +32,18 @@ constexpr float kLowest = -3.402823466e38f;   // the maximum of no keys: finite,
 constexpr float kSlack = 8.0f;   // log2 of how far a maximum may fall behind
 
 template <int DT, int DP, int WK> struct Shape {
+  static_assert(WK == 1 || WK == 4, "rows or keys split over the four waves");
   static constexpr int EB = Elem<DT>::bytes;
   static constexpr int RB = (DP <= 64 ? 64 : 128) * EB;    // bytes of a row of K or V in LDS
   static constexpr int CPR = RB / 16;                      // 16-byte chunks of it
-  static constexpr int KPW = EB == 4 ? 32 : WK == 1 ? 64 : 32;  // keys a wave takes of a tile
+  static constexpr int KPW = EB == 4 || WK == 4 ? 32 : 64; // keys a wave takes of a tile
   static constexpr int BN = KPW * WK;                      // keys of a tile
   static constexpr int ROWS = 128 / WK;                    // rows of a workgroup
   static constexpr int TILE = BN * RB;
-  static constexpr int LDS = 4 * TILE;                     // K and V, two stages
-  static constexpr int WAVES = 2 * LDS <= 160 * 1024 ? 2 : 1;   // workgroups a compute unit, at least
+  static constexpr int LDS = (WK == 1 ? 4 : 2) * TILE;     // K and V; two stages where shared
 };
+// Workgroups that a compute unit's LDS holds, at most 2 counted.
+constexpr int fit(int lds) { return 2 * lds <= 160 * 1024 ? 2 : 1; }
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -87,50 +91,57 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-// A walk over a workgroup's tiles of K or of V: prefix, then own keys.
+// A walk over the tiles of K or of V: prefix, then own keys.
 struct Cursor {
-  const char* p;        // row 0 of the tile
-  int stride;           // of its rows in bytes (below 2^24)
-  int left;             // rows from there to the end of the run; <= 0 past the end
-  int off;              // this lane's bytes of its first row, past any end without such
+  const char* p;        // this copy's first row of the tile
+  int stride;           // of rows in bytes (below 2^24)
+  int left;             // rows from there to the end of the run; <= 0 past it
   const char* own_p;    // the own keys' first tile, where the run follows
-  int own_stride, own_left, own_off;
+  int own_stride, own_left;
 };
+__device__ __forceinline__ void advance(Cursor& c, int keys, int skip) {
+  // after the run the own keys, past them nothing (selects: a branch would
+  // part the code it stands in)
+  const char* const p = c.p + (unsigned)keys * (unsigned)c.stride;
+  const int left = c.left - keys;
+  const bool more = left + skip > 0;
+  c.p = more ? p : c.own_p;
+  c.stride = more ? c.stride : c.own_stride;
+  c.left = more ? left : c.own_left;
+  c.own_left = more ? c.own_left : -skip;
+}
 
-// Copies a tile's rows into LDS, 16 bytes a lane, and moves on.  Rows past the
-// run's end and components from D on arrive as zeros: they lie past the
-// resource's end (rows that lie closer than their own length repeat bytes of
-// valid rows instead, whose scores are masked).
-template <int DT, int DP, int WK, bool V>
-__device__ __forceinline__ void copy_tile(Cursor& c, unsigned char* lds, int row_bytes) {
-  using Z = Shape<DT, DP, WK>;
-  constexpr int PASS = kThreads / Z::CPR;   // rows of a copy of the workgroup
-  const int rows = c.left < Z::BN ? c.left : Z::BN;
-  const __amdgpu_buffer_rsrc_t r =
-      make_rsrc(c.p, rows > 0 ? (uint32_t)((rows - 1) * c.stride + row_bytes) : 0u);
-  unsigned char* to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63) * 16;
+// Copies N * LANES / CPR rows into LDS, 16 bytes a lane, thread t of LANES.
+// Rows past the run's end and components from D on arrive as zeros: they lie
+// past the resource's end (rows that lie closer than their own length repeat
+// bytes of valid rows instead, whose scores are masked).
+template <int EB, int CPR, int LANES, int N, bool V>
+__device__ __forceinline__ void copy_rows(const Cursor& c, unsigned char* lds, int t,
+                                          int row_bytes) {
+  constexpr int PASS = LANES / CPR;   // rows of a copy
+  const int rows = c.left < N * PASS ? c.left : N * PASS;
+  const int bytes = (rows - 1) * c.stride + row_bytes;
+  const __amdgpu_buffer_rsrc_t r = make_rsrc(c.p, rows > 0 ? bytes : 0);
+  const int row = t / CPR, slot = t % CPR;
+  const int at = row * c.stride;
 #pragma unroll
-  for (int j = 0; j < Z::BN / PASS; ++j)
-    copy16_to_lds(r, to + j * kThreads * 16, c.off, j * PASS * c.stride);
-  c.p += (long long)Z::BN * c.stride;
-  c.left -= Z::BN;
-  if (c.left <= 0) {   // the own keys; past them there is nothing
-    c.p = c.own_p;
-    c.stride = c.own_stride;
-    c.left = c.own_left;
-    c.off = c.own_off;
-    c.own_left = 0;
+  for (int j = 0; j < N; ++j) {
+    const int in = row + j * PASS;
+    const int chunk = slot ^ (V ? v_swizzle<EB, CPR>(in) : k_swizzle<CPR>(in));
+    copy16_to_lds(r, lds + j * LANES * 16, chunk * 16 < row_bytes ? at + chunk * 16 : kFarOffset,
+                  j * PASS * c.stride);
   }
 }
 
 // What a workgroup computes: rows [row0, row0 + rows) of key head hk (rows are
 // counted over the entries), prefix keys [0, P) and own keys of entry b, of
-// whose tiles it takes share `split` of `splits`; slot: where its partial
-// result goes (-1: straight to the output).
+// whose tiles it takes share `split` of `splits` (splits 0: those of run
+// `split` of `chunk` keys, if any); slot: where its partial result goes (-1:
+// straight to the output).
 struct Job {
   int row0, rows, hk, b;
   bool prefix, own;
-  int split, splits, slot;
+  int split, splits, chunk, slot;
 };
 
 template <int DT, int DP, int WK>
@@ -182,39 +193,59 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
   }
   const int tiles_p = job.prefix ? (a.P + BN - 1) / BN : 0;
   const int tiles = tiles_p + (end_own + BN - 1) / BN;
-  const int t0 = (int)((long long)tiles * job.split / job.splits);
-  const int t1 = (int)((long long)tiles * (job.split + 1) / job.splits);
+  int t0, t1;
+  if (job.splits > 0) {
+    t0 = (int)((long long)tiles * job.split / job.splits);
+    t1 = (int)((long long)tiles * (job.split + 1) / job.splits);
+  } else {
+    // nothing to leave where the entry has no such keys: the join knows
+    if ((long long)job.split * job.chunk >= n_own) return;
+    t0 = job.split * (job.chunk / BN);
+    t1 = t0 + job.chunk / BN;
+    t1 = t1 < tiles ? t1 : tiles;
+  }
 
   const char* kp = a.kp + job.hk * a.kp_h;
   const char* vp = a.vp + job.hk * a.vp_h;
   const char* ko = a.k + job.b * a.k_b + job.hk * a.k_h;
   const char* vo = a.v + job.b * a.v_b + job.hk * a.v_h;
-  // a thread's rows of a copy lie a multiple of 16 (rows of 512 bytes: 8) apart: its
-  // chunk of them is the same for all
-  const int c_row = threadIdx.x / CPR, c_slot = threadIdx.x % CPR;
-  auto cursor = [&](const char* p, long long stride, const char* o, long long own_stride,
-                    int chunk) {
+  // this workgroup's or this wave's keys of tiles t0 .. t1 - 1; past them it
+  // reads nothing
+  const int end_p = t1 < tiles_p ? t1 * BN : a.P;
+  const int last_own = t1 <= tiles_p ? 0 : (t1 - tiles_p) * BN < end_own ? (t1 - tiles_p) * BN
+                                                                         : end_own;
+  auto cursor = [&](const char* p, long long stride, const char* o, long long own_stride) {
+    const int skip = wk * KPW;
     Cursor c;
-    c.own_p = o;
+    c.own_p = o + skip * own_stride;
     c.own_stride = (int)own_stride;
-    c.own_left = end_own;
-    c.own_off = chunk < d_chunks ? c_row * (int)own_stride + chunk * 16 : kFarOffset;
-    c.p = p + (long long)t0 * BN * stride;
+    c.own_left = last_own - skip;
+    c.p = p + ((long long)t0 * BN + skip) * stride;
     c.stride = (int)stride;
-    c.left = a.P - t0 * BN;
-    c.off = chunk < d_chunks ? c_row * (int)stride + chunk * 16 : kFarOffset;
+    c.left = end_p - t0 * BN - skip;
     if (t0 >= tiles_p) {
-      c.p = o + (long long)(t0 - tiles_p) * BN * own_stride;
+      c.p = o + ((long long)(t0 - tiles_p) * BN + skip) * own_stride;
       c.stride = (int)own_stride;
-      c.left = end_own - (t0 - tiles_p) * BN;
-      c.off = c.own_off;
-      c.own_left = 0;
+      c.left = last_own - (t0 - tiles_p) * BN - skip;
+      c.own_left = -skip;
     }
     return c;
   };
-  static_assert(kThreads / CPR % (CPR == 32 ? 8 : 16) == 0, "one swizzle for a thread's rows");
-  Cursor ck = cursor(kp, a.kp_r, ko, a.k_r, c_slot ^ k_swizzle<CPR>(c_row));
-  Cursor cv = cursor(vp, a.vp_r, vo, a.v_r, c_slot ^ v_swizzle<EB, CPR>(c_row));
+  Cursor ck = cursor(kp, a.kp_r, ko, a.k_r);
+  Cursor cv = cursor(vp, a.vp_r, vo, a.v_r);
+  // The part of a tile that comes next; lanes: those that copy it together.
+  constexpr int LANES = WK == 1 ? kThreads : 64;
+  constexpr int COPIES = KPW * CPR / LANES;
+  const int lane_id = WK == 1 ? threadIdx.x : lane;
+  const int wave_to = WK == 1 ? wave * 1024 : 0;
+  auto copy_k = [&](unsigned char* to) {
+    copy_rows<EB, CPR, LANES, COPIES, false>(ck, to + wave_to, lane_id, row_bytes);
+    advance(ck, BN, wk * KPW);
+  };
+  auto copy_v = [&](unsigned char* to) {
+    copy_rows<EB, CPR, LANES, COPIES, true>(cv, to + wave_to, lane_id, row_bytes);
+    advance(cv, BN, wk * KPW);
+  };
 
   float16_t acc[DB];
 #pragma unroll
@@ -222,7 +253,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
   float m = kLowest, l = 0.0f;   // maximum (times scale, log2) and sum of this lane's half
 
   // LDS offsets that do not change from tile to tile
-  const int krow = (wk * KPW + l32) * RB;
+  const int krow = l32 * RB;
   const int ksw = (half ^ k_swizzle<CPR>(l32)) * 16;
   const int i16 = lane & 15;
   const int vrow16 = 4 * half + (i16 >> 2);
@@ -239,12 +270,13 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
       for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(kf, qf[ks], s, e);
     }
   };
-  // keys past the end and keys the causal mask hides; key0: the block's first
+  // keys past the end and keys the causal mask hides: of blocks that begin
+  // from whole_p on in the prefix and from whole_own on in the own keys
+  const int whole_p = job.prefix ? a.P & ~31 : 0, whole_own = (lim_wave & ~31) + tiles_p * BN;
   auto mask = [&](int t, int b, float16_t& s) {
-    const bool own = t >= tiles_p;
-    const int key0 = (own ? t - tiles_p : t) * BN + wk * KPW + b * 32;
-    if (key0 + 32 > (own ? lim_wave : a.P)) {
-      const int lane_lim = (own ? lim : a.P) - key0 - 4 * half;
+    const int key0 = t * BN + wk * KPW + b * 32;   // counted over both
+    if (key0 >= whole_p && (key0 < tiles_p * BN || key0 >= whole_own)) {
+      const int lane_lim = (t < tiles_p ? a.P : lim + tiles_p * BN) - key0 - 4 * half;
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         s[r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[r] : kNegInf;
@@ -287,7 +319,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
         for (int d = 0; d < DB; ++d) {
           const int chunk = (d * 4 + vchunk16) ^ v_swizzle<EB, CPR>(vrow16);
           const unsigned char* at =
-              vt + (wk * KPW + b * 32 + c * 16 + vrow16) * RB + chunk * 16 + (i16 & 1) * 8;
+              vt + (b * 32 + c * 16 + vrow16) * RB + chunk * 16 + (i16 & 1) * 8;
           const u32x2_t lo = read_column(at), hi = read_column(at + 8 * RB);
           const u32x4_t vf = {lo[0], lo[1], hi[0], hi[1]};
           Mma<DT>::step(vf, pf[c], acc[d], 0);
@@ -303,7 +335,6 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
     static_assert(NB == 2, "a tile is two blocks");
     unsigned char* const kt = lds;
     unsigned char* const vt = lds + 2 * Z::TILE;
-    constexpr int COPIES = Z::BN * CPR / kThreads;   // of a tile, a thread
     const int n = t1 - t0;
     float16_t s0, s1;      // scores of two blocks
     u32x4_t p0[2], p1[2];  // probabilities of two blocks
@@ -324,9 +355,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
       if (__any(f != 1.0f)) rescale(f);
     };
     if (n > 0) {
-      copy_tile<DT, DP, WK, false>(ck, kt, row_bytes);
-      copy_tile<DT, DP, WK, true>(cv, vt, row_bytes);
-      copy_tile<DT, DP, WK, false>(ck, kt + Z::TILE, row_bytes);
+      copy_k(kt);
+      copy_v(vt);
+      copy_k(kt + Z::TILE);
       wait_vmcnt<2 * COPIES>();
       lds_barrier();
       score(kt, 0, s0);
@@ -342,11 +373,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
         const unsigned char* v0 = vt + (i & 1) * Z::TILE;
         wait_vmcnt<0>();
         lds_barrier();
-        copy_tile<DT, DP, WK, true>(cv, vt + ((i + 1) & 1) * Z::TILE, row_bytes);
-        copy_tile<DT, DP, WK, false>(ck, kt + (i & 1) * Z::TILE, row_bytes);
         mask(t0 + i, 1, s1);
         move_up(s1);
         score(k1, 0, s0);
+        // behind the first matrix instructions, which cover their scalar work
+        copy_v(vt + ((i + 1) & 1) * Z::TILE);
+        copy_k(kt + (i & 1) * Z::TILE);
         probabilities(s1);
         pack(s1, p1);
         add_values(v0, 0, p0);
@@ -371,25 +403,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
       add_values(v0, 1, p1);
     }
   } else {
-    if (t0 < t1) {
-      copy_tile<DT, DP, WK, false>(ck, lds, row_bytes);
-      copy_tile<DT, DP, WK, true>(cv, lds + Z::TILE, row_bytes);
-    }
-    for (int t = t0; t < t1; ++t) {
-      unsigned char* kt = lds + ((t - t0) & 1) * 2 * Z::TILE;
-      unsigned char* vt = kt + Z::TILE;
-      // this wave's copies have arrived; after the barrier everyone's have, and
-      // nobody reads the other stage any more
-      wait_vmcnt<0>();
-      lds_barrier();
-      if (t + 1 < t1) {
-        unsigned char* next = lds + ((t + 1 - t0) & 1) * 2 * Z::TILE;
-        copy_tile<DT, DP, WK, false>(ck, next, row_bytes);
-        copy_tile<DT, DP, WK, true>(cv, next + Z::TILE, row_bytes);
-      }
-      static_assert(NB == 1, "32 keys a wave");
-      float16_t s;
-      score(kt, 0, s);
+    static_assert(NB == 1, "32 keys a wave");
+    float16_t s;
+    auto softmax = [&](int t) {
       mask(t, 0, s);
       const float top = top_of(s);
       if (__any(top > m)) {
@@ -400,10 +416,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
         rescale(f);
       }
       probabilities(s);
+    };
+    auto add = [&](const unsigned char* vt) {
       if constexpr (EB == 4) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int vr = wk * KPW + (r & 3) + 8 * (r >> 2) + 4 * half;
+          const int vr = (r & 3) + 8 * (r >> 2) + 4 * half;
 #pragma unroll
           for (int d = 0; d < DB; ++d) {
             const int chunk = (d * 8 + (l32 >> 2)) ^ v_swizzle<EB, CPR>(vr);
@@ -417,6 +435,51 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
         pack(s, pf);
         add_values(vt, 0, pf);
       }
+    };
+    if constexpr (WK == 1) {
+      if (t0 < t1) {
+        copy_k(lds);
+        copy_v(lds + Z::TILE);
+      }
+      for (int t = t0; t < t1; ++t) {
+        unsigned char* kt = lds + ((t - t0) & 1) * 2 * Z::TILE;
+        // this wave's copies have arrived; after the barrier everyone's have, and
+        // nobody reads the other stage any more
+        wait_vmcnt<0>();
+        lds_barrier();
+        if (t + 1 < t1) {
+          unsigned char* next = lds + ((t + 1 - t0) & 1) * 2 * Z::TILE;
+          copy_k(next);
+          copy_v(next + Z::TILE);
+        }
+        score(kt, 0, s);
+        softmax(t);
+        add(kt + Z::TILE);
+      }
+    } else {
+      // a wave's own 32 keys of a tile, K and V one stage each: the next copy
+      // to a stage starts when its reads are done (and past the last tile
+      // reads nothing, so that the counts stay the same)
+      unsigned char* const kt = lds + wave * (2 * 32 * RB);
+      unsigned char* const vt = kt + 32 * RB;
+      if (t0 < t1) {
+        copy_k(kt);
+        copy_v(vt);
+      }
+      for (int t = t0; t < t1; ++t) {
+        wait_vmcnt<COPIES>();
+        lds_fence();
+        score(kt, 0, s);
+        lds_fence();
+        copy_k(kt);
+        softmax(t);
+        wait_vmcnt<COPIES>();
+        lds_fence();
+        add(vt);
+        lds_fence();
+        copy_v(vt);
+      }
+      wait_vmcnt<0>();
     }
   }
 
@@ -425,9 +488,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
     // join the waves that split this row block's keys: each leaves maximum,
     // sum and outputs (32 rows, DP components, rows fastest) in LDS
     constexpr int PER = 32 * (DP + 2) * 4;
-    static_assert(4 / WK * (WK - 1) * PER <= Z::LDS, "the join fits the stages");
-    lds_barrier();   // every wave is done with the stages (its copies have arrived)
-    unsigned char* room = lds + wr * (WK - 1) * PER;   // of the row block's waves 1, 2, ..
+    static_assert((WK - 1) * PER <= Z::LDS, "the join fits the stages");
+    lds_barrier();   // every wave is done with its stages, no copy is on its way
+    unsigned char* room = lds;   // of the waves 1, 2, ..
     float* mine = reinterpret_cast<float*>(room + (wk - 1) * PER);
     if (wk > 0) {
       if (half == 0) {
@@ -517,7 +580,8 @@ __device__ __forceinline__ int xcd_order(int id, int n) {
 
 // Each entry's rows over its prefix and own keys.
 template <int DT, int DP, int WK>
-__global__ __launch_bounds__(kThreads, (Shape<DT, DP, WK>::WAVES)) void attn_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(kThreads, fit((Shape<DT, DP, WK>::LDS))) void attn_kernel(
+    const AttnArgs a) {
   using Z = Shape<DT, DP, WK>;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Z::LDS];
   const int per_entry = a.Sq * a.G;
@@ -534,39 +598,68 @@ __global__ __launch_bounds__(kThreads, (Shape<DT, DP, WK>::WAVES)) void attn_ker
   job.row0 = job.b * per_entry + tile * Z::ROWS;
   job.rows = per_entry - tile * Z::ROWS < Z::ROWS ? per_entry - tile * Z::ROWS : Z::ROWS;
   job.splits = a.splits;
-  job.prefix = !a.shared;
+  job.chunk = 0;
+  job.prefix = true;
   job.own = true;
-  job.slot = a.part ? (a.shared ? a.prefix_splits : 0) + job.split : -1;
+  job.slot = a.part ? job.split : -1;
   attend<DT, DP, WK>(a, job, lds);
 }
 
-// Rows of all entries, side by side, over the prefix.
-template <int DT, int DP, int WK>
-__global__ __launch_bounds__(kThreads, (Shape<DT, DP, WK>::WAVES)) void attn_prefix_kernel(const AttnArgs a) {
-  using Z = Shape<DT, DP, WK>;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[Z::LDS];
-  const int all = a.B * a.Sq * a.G;
-  const int row_tiles = (all + Z::ROWS - 1) / Z::ROWS;
-  int id = xcd_order(blockIdx.x, gridDim.x);
+// The prefix once for all entries: the first `prefix_jobs` workgroups take the
+// rows of all entries, side by side, over shares of the prefix (WP: how they
+// split); the others take each entry's rows over runs of its own keys.
+template <int DT, int DP, int WP>
+__global__ __launch_bounds__(kThreads, fit((Shape<DT, DP, WP>::LDS > Shape<DT, DP, 4>::LDS
+                                                ? Shape<DT, DP, WP>::LDS
+                                                : Shape<DT, DP, 4>::LDS)))
+void attn_shared_kernel(const AttnArgs a, int prefix_jobs) {
+  using Z = Shape<DT, DP, WP>;
+  using ZO = Shape<DT, DP, 4>;
+  constexpr int LDS = Z::LDS > ZO::LDS ? Z::LDS : ZO::LDS;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[LDS];
+  const int per_entry = a.Sq * a.G;
   Job job;
-  const int tile = id % row_tiles;
-  id /= row_tiles;
-  job.split = id % a.prefix_splits;
-  job.hk = id / a.prefix_splits;
-  job.b = 0;
-  job.row0 = tile * Z::ROWS;
-  job.rows = all - job.row0 < Z::ROWS ? all - job.row0 : Z::ROWS;
-  job.splits = a.prefix_splits;
-  job.prefix = true;
-  job.own = false;
-  job.slot = job.split;
-  attend<DT, DP, WK>(a, job, lds);
+  if ((int)blockIdx.x < prefix_jobs) {
+    const int all = a.B * per_entry;
+    const int row_tiles = (all + Z::ROWS - 1) / Z::ROWS;
+    int id = xcd_order(blockIdx.x, prefix_jobs);
+    const int tile = id % row_tiles;
+    id /= row_tiles;
+    job.split = id % a.prefix_splits;
+    job.hk = id / a.prefix_splits;
+    job.b = 0;
+    job.row0 = tile * Z::ROWS;
+    job.rows = all - job.row0 < Z::ROWS ? all - job.row0 : Z::ROWS;
+    job.splits = a.prefix_splits;
+    job.chunk = 0;
+    job.prefix = true;
+    job.own = false;
+    job.slot = job.split;
+    attend<DT, DP, WP>(a, job, lds);
+  } else {
+    const int row_tiles = (per_entry + ZO::ROWS - 1) / ZO::ROWS;
+    int id = blockIdx.x - prefix_jobs;
+    const int tile = id % row_tiles;
+    id /= row_tiles;
+    job.hk = id % a.Hk;
+    id /= a.Hk;
+    job.b = id % a.B;
+    job.split = id / a.B;
+    job.row0 = job.b * per_entry + tile * ZO::ROWS;
+    job.rows = per_entry - tile * ZO::ROWS < ZO::ROWS ? per_entry - tile * ZO::ROWS : ZO::ROWS;
+    job.splits = 0;
+    job.chunk = a.chunk;
+    job.prefix = false;
+    job.own = true;
+    job.slot = a.prefix_splits + job.split;
+    attend<DT, DP, 4>(a, job, lds);
+  }
 }
 
 // Joins the partial results of one row: out = sum_s 2^(lse_s - lse) o_s, in
 // the order of the slots.  A wave a row, two components a lane.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a, int slots) {
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const long long per = (long long)a.B * a.Sq * a.G, all = per * a.Hk;
   const long long at = (long long)blockIdx.x * 4 + wave;
@@ -574,27 +667,46 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a, i
   const int hk = (int)(at / per), row = (int)(at % per);
   const int per_entry = a.Sq * a.G;
   const int b = row / per_entry, i = row % per_entry / a.G, g = row % a.G;
-  float m = kNegInf;
+  int slots = a.splits;
+  if (a.shared) {   // own keys: the slots that have any
+    int n = a.lengths[b];
+    n = n < 0 ? 0 : n > a.S ? a.S : n;
+    slots = a.prefix_splits + (n + a.chunk - 1) / a.chunk;
+  }
+  float m = kLowest;
   for (int s = lane; s < slots; s += 64) m = fmaxf(m, a.part_lse[s * all + at]);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-  const float base = m == kNegInf ? 0.0f : m;
   float sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
   const bool live = 2 * lane < a.D;
-  for (int s = 0; s < slots; ++s) {
-    const float w = __builtin_amdgcn_exp2f(a.part_lse[s * all + at] - base);
-    sum += w;
-    if (live) {
-      const float2 v = *reinterpret_cast<const float2*>(a.part + (s * all + at) * a.D + 2 * lane);
-      o0 = fmaf(w, v.x, o0);
-      o1 = fmaf(w, v.y, o1);
+  const float* part = a.part + at * a.D + (live ? 2 * lane : 0);
+  for (int s0 = 0; s0 < slots; s0 += 64) {
+    const float mine =
+        s0 + lane < slots ? __builtin_amdgcn_exp2f(a.part_lse[(s0 + lane) * all + at] - m) : 0.0f;
+    const int n = slots - s0 < 64 ? slots - s0 : 64;
+    for (int s = 0; s < n; s += 8) {   // 8 reads on their way at a time
+      float2 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int at_slot = s0 + (s + u < n ? s + u : n - 1);
+        v[u] = *reinterpret_cast<const float2*>(part + at_slot * all * a.D);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), s + u));
+        if (s + u >= n) break;
+        sum += w;
+        o0 = fmaf(w, v[u].x, o0);
+        o1 = fmaf(w, v[u].y, o1);
+      }
     }
   }
   const float inv = sum > 0.0f ? 1.0f / sum : sum;
   const int head = hk * a.G + g;
   if (a.lse && lane == 0)
     a.lse[((long long)b * a.Hk * a.G + head) * a.Sq + i] =
-        sum == 0.0f ? kNegInf : (base + __builtin_amdgcn_logf(sum)) * kLn2;
+        sum == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
   if (!live) return;
   char* op = a.out + b * a.o_b + i * a.o_r + head * a.o_h;
   if constexpr (DT == DT_F32)
@@ -603,39 +715,37 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a, i
     *reinterpret_cast<uint32_t*>(op + 4 * lane) = pack2<DT>(o0 * inv, o1 * inv);
 }
 
-int key_waves(long long rows, int eb) {
-  const int wk = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-  return eb == 4 && wk == 4 ? 2 : wk;   // fp32: four stages of 128 keys would not fit
+// How many of a workgroup's waves split its keys, and its rows.
+int key_waves(long long rows) { return rows <= 64 ? 4 : 1; }
+long long row_tiles(long long rows) {
+  const int r = 128 / key_waves(rows);
+  return (rows + r - 1) / r;
 }
-int tile_keys(int wk, int eb) { return eb == 4 ? 32 * wk : wk == 4 ? 128 : 64; }
 
 template <int DT, int DP>
 void launch(const AttnArgs& a, hipStream_t stream) {
   const long long per_entry = (long long)a.Sq * a.G, all = a.B * per_entry;
-  constexpr int EB = Elem<DT>::bytes;
-  const int wk = key_waves(per_entry, EB), wp = key_waves(all, EB);
   const dim3 threads(kThreads);
   if (a.shared) {
-    const long long tiles = (all + 128 / wp - 1) / (128 / wp);
-    const dim3 grid((unsigned)(tiles * a.prefix_splits * a.Hk));
-    if (wp == 1)
-      hipLaunchKernelGGL((attn_prefix_kernel<DT, DP, 1>), grid, threads, 0, stream, a);
-    else if (wp == 2)
-      hipLaunchKernelGGL((attn_prefix_kernel<DT, DP, 2>), grid, threads, 0, stream, a);
-    else if constexpr (EB == 2)
-      hipLaunchKernelGGL((attn_prefix_kernel<DT, DP, 4>), grid, threads, 0, stream, a);
+    const int prefix_jobs = (int)(row_tiles(all) * a.prefix_splits * a.Hk);
+    const long long own_jobs = row_tiles(per_entry) * a.splits * a.Hk * a.B;
+    const dim3 grid((unsigned)(prefix_jobs + own_jobs));
+    if (key_waves(all) == 1)
+      hipLaunchKernelGGL((attn_shared_kernel<DT, DP, 1>), grid, threads, 0, stream, a,
+                         prefix_jobs);
+    else
+      hipLaunchKernelGGL((attn_shared_kernel<DT, DP, 4>), grid, threads, 0, stream, a,
+                         prefix_jobs);
+  } else {
+    const dim3 grid((unsigned)(row_tiles(per_entry) * a.splits * a.Hk * a.B));
+    if (key_waves(per_entry) == 1)
+      hipLaunchKernelGGL((attn_kernel<DT, DP, 1>), grid, threads, 0, stream, a);
+    else
+      hipLaunchKernelGGL((attn_kernel<DT, DP, 4>), grid, threads, 0, stream, a);
   }
-  const long long tiles = (per_entry + 128 / wk - 1) / (128 / wk);
-  const dim3 grid((unsigned)(tiles * a.splits * a.Hk * a.B));
-  if (wk == 1)
-    hipLaunchKernelGGL((attn_kernel<DT, DP, 1>), grid, threads, 0, stream, a);
-  else if (wk == 2)
-    hipLaunchKernelGGL((attn_kernel<DT, DP, 2>), grid, threads, 0, stream, a);
-  else if constexpr (EB == 2)
-    hipLaunchKernelGGL((attn_kernel<DT, DP, 4>), grid, threads, 0, stream, a);
   if (a.part)
     hipLaunchKernelGGL((attn_join_kernel<DT>), dim3((unsigned)((all * a.Hk + 3) / 4)), threads, 0,
-                       stream, a, a.splits + (a.shared ? a.prefix_splits : 0));
+                       stream, a);
 }
 
 template <int DT>
@@ -647,34 +757,39 @@ void launch_dt(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-long long attn_plan(AttnArgs* a, int dtype, int cus, bool allowed) {
-  const int eb = dtype == LIBCONV_F32 ? 4 : 2;
+long long attn_plan(AttnArgs* a, int cus, bool allowed) {
   const long long per_entry = (long long)a->Sq * a->G, all = a->B * per_entry;
   a->shared = 0;
   a->splits = a->prefix_splits = 1;
+  a->chunk = 0;
   if (!allowed || all == 0) return 0;
-  // Workgroups wanted: two a compute unit.
-  const long long want = 2LL * cus;
-  // Splits so that `groups` workgroups become `want`, each with 256 keys or more.
-  auto split = [&](long long groups, long long keys) {
+  // Splits so that `groups` workgroups become `want`, each with `least` keys
+  // or more.
+  auto split = [&](long long want, long long groups, long long keys, long long least) {
     long long s = groups > 0 ? want / groups : 1;
-    if (s > keys / 256) s = keys / 256;
+    if (s > keys / least) s = keys / least;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   };
-  const int wk = key_waves(per_entry, eb);
-  const long long groups = a->B * a->Hk * ((per_entry + 128 / wk - 1) / (128 / wk));
+  const long long groups = a->B * a->Hk * row_tiles(per_entry);
   // The prefix once for all entries: with few rows an entry, reading it for
   // each of them would be what the call spends its time on.
   if (a->B > 1 && per_entry <= 64 && a->P >= 128) {
-    const int wp = key_waves(all, eb);
     a->shared = 1;
-    a->prefix_splits = split(a->Hk * ((all + 128 / wp - 1) / (128 / wp)), a->P);
-    a->splits = split(groups, a->S);
+    // a share of the prefix leaves a partial result of every row: with many
+    // rows it has to be long
+    const long long least = 4 * all < 256 ? 256 : 4 * all > 1024 ? 1024 : 4 * all;
+    a->prefix_splits = split(2LL * cus, a->Hk * row_tiles(all), a->P, least);
+    // own keys: runs of one length, so that long entries do not hold up the
+    // end; about half of them will have keys
+    const long long runs = split(8LL * cus, groups, a->S, 256);
+    const long long chunk = ((a->S + runs - 1) / runs + 127) / 128 * 128;
+    a->chunk = (int)(chunk < 128 ? 128 : chunk);
+    a->splits = (a->S + a->chunk - 1) / a->chunk;
   } else {
-    a->splits = split(groups, (long long)a->P + a->S);
+    a->splits = split(2LL * cus, groups, (long long)a->P + a->S, 256);
   }
   const int slots = a->splits + (a->shared ? a->prefix_splits : 0);
-  if (slots == 1) return 0;
+  if (!a->shared && slots == 1) return 0;
   return slots * a->Hk * all * (a->D + 1LL) * 4;
 }
 

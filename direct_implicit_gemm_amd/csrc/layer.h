@@ -41,12 +41,13 @@ struct AttnArgs {
   // plan
   int shared;               // prefix rows stacked over the entries, then joined
   int splits, prefix_splits;
+  int chunk;                // shared: own keys of a split (a multiple of 128)
   float* part;              // [slots][Hk][B*Sq*G][D] partial outputs
   float* part_lse;          // [slots][Hk][B*Sq*G], log2; null: written directly
 };
 // Fills the plan for `cus` compute units and returns the workspace bytes it
 // takes; with a smaller workspace the plan has to be made with allowed = false.
-long long attn_plan(AttnArgs* a, int dtype, int cus, bool allowed);
+long long attn_plan(AttnArgs* a, int cus, bool allowed);
 libconv_status attn_launch(AttnArgs a, int dtype, hipStream_t stream);
 
 // libconv_lora_linear; strides in bytes.
