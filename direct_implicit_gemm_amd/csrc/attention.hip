@@ -19,6 +19,7 @@
 // wave copies the keys it reads itself, waits for nobody until the four join
 // through LDS at the end, and is bound by the keys it reads from memory.
 #include "device_common.h"
+#include "internal.h"
 #include "layer.h"
 
 namespace libconv {
@@ -656,13 +657,14 @@ void attn_shared_kernel(const AttnArgs a, int prefix_jobs) {
   }
 }
 
-// Joins the partial results of one row: out = sum_s 2^(lse_s - lse) o_s, in
-// the order of the slots.  A wave a row, two components a lane.
-template <int DT>
+// Joins the partial results of each row: out = sum_s 2^(lse_s - lse) o_s, in
+// the order of the slots.  LPR lanes a row, 4 components a lane; one pass, 8
+// slots' reads on their way at a time.
+template <int DT, int LPR>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int lane = threadIdx.x % LPR;
   const long long per = (long long)a.B * a.Sq * a.G, all = per * a.Hk;
-  const long long at = (long long)blockIdx.x * 4 + wave;
+  const long long at = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
   if (at >= all) return;
   const int hk = (int)(at / per), row = (int)(at % per);
   const int per_entry = a.Sq * a.G;
@@ -673,33 +675,37 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
     n = n < 0 ? 0 : n > a.S ? a.S : n;
     slots = a.prefix_splits + (n + a.chunk - 1) / a.chunk;
   }
-  float m = kLowest;
-  for (int s = lane; s < slots; s += 64) m = fmaxf(m, a.part_lse[s * all + at]);
+  const bool live = 4 * lane < a.D;
+  const float* lse = a.part_lse + at;
+  const float* part = a.part + at * a.D + (live ? 4 * lane : 0);
+  float m = kLowest, sum = 0.0f;
+  float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int U = 8;
+  for (int s = 0; s < slots; s += U) {
+    float w[U];
+    float4_t v[U];
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-  float sum = 0.0f, o0 = 0.0f, o1 = 0.0f;
-  const bool live = 2 * lane < a.D;
-  const float* part = a.part + at * a.D + (live ? 2 * lane : 0);
-  for (int s0 = 0; s0 < slots; s0 += 64) {
-    const float mine =
-        s0 + lane < slots ? __builtin_amdgcn_exp2f(a.part_lse[(s0 + lane) * all + at] - m) : 0.0f;
-    const int n = slots - s0 < 64 ? slots - s0 : 64;
-    for (int s = 0; s < n; s += 8) {   // 8 reads on their way at a time
-      float2 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int at_slot = s0 + (s + u < n ? s + u : n - 1);
-        v[u] = *reinterpret_cast<const float2*>(part + at_slot * all * a.D);
+    for (int u = 0; u < U; ++u) {
+      w[u] = kNegInf;
+      v[u] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      if (s + u < slots) {
+        w[u] = lse[(s + u) * all];
+        v[u] = *reinterpret_cast<const float4_t*>(part + (s + u) * all * a.D);
       }
+    }
+    float m_new = m;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float w = __builtin_bit_cast(
-            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, mine), s + u));
-        if (s + u >= n) break;
-        sum += w;
-        o0 = fmaf(w, v[u].x, o0);
-        o1 = fmaf(w, v[u].y, o1);
-      }
+    for (int u = 0; u < U; ++u) m_new = fmaxf(m_new, w[u]);
+    const float f = __builtin_amdgcn_exp2f(m - m_new);
+    m = m_new;
+    sum *= f;
+    o *= f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float p = __builtin_amdgcn_exp2f(w[u] - m);
+      sum += p;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[u][j], o[j]);
     }
   }
   const float inv = sum > 0.0f ? 1.0f / sum : sum;
@@ -710,15 +716,22 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const AttnArgs a) {
   if (!live) return;
   char* op = a.out + b * a.o_b + i * a.o_r + head * a.o_h;
   if constexpr (DT == DT_F32)
-    *reinterpret_cast<float2*>(op + 8 * lane) = make_float2(o0 * inv, o1 * inv);
+    *reinterpret_cast<float4_t*>(op + 16 * lane) = o * inv;
   else
-    *reinterpret_cast<uint32_t*>(op + 4 * lane) = pack2<DT>(o0 * inv, o1 * inv);
+    *reinterpret_cast<u32x2_t*>(op + 8 * lane) =
+        u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
 }
 
-// How many of a workgroup's waves split its keys, and its rows.
-int key_waves(long long rows) { return rows <= 64 ? 4 : 1; }
-long long row_tiles(long long rows) {
-  const int r = 128 / key_waves(rows);
+// How many of a workgroup's waves split its keys: all with up to 64 rows (the
+// rows of `sets` row sets), and where workgroups of 128 rows would leave half
+// the compute units idle.  Measured with heads of 128: 8 heads of 4 entries of
+// 500 queries over 600 keys (128 workgroups of 128 rows) 17 us against 25, over
+// 3000 keys 46 against 45; 8 entries (256) 29 against 32, 90 against 73.
+int key_waves(long long rows, long long sets) {
+  return rows <= 64 || (rows + 127) / 128 * sets <= kPlanCus / 2 ? 4 : 1;
+}
+long long row_tiles(long long rows, int waves) {
+  const int r = 128 / waves;
   return (rows + r - 1) / r;
 }
 
@@ -727,25 +740,28 @@ void launch(const AttnArgs& a, hipStream_t stream) {
   const long long per_entry = (long long)a.Sq * a.G, all = a.B * per_entry;
   const dim3 threads(kThreads);
   if (a.shared) {
-    const int prefix_jobs = (int)(row_tiles(all) * a.prefix_splits * a.Hk);
-    const long long own_jobs = row_tiles(per_entry) * a.splits * a.Hk * a.B;
+    const int prefix_jobs = (int)(row_tiles(all, a.prefix_waves) * a.prefix_splits * a.Hk);
+    const long long own_jobs = row_tiles(per_entry, 4) * a.splits * a.Hk * a.B;
     const dim3 grid((unsigned)(prefix_jobs + own_jobs));
-    if (key_waves(all) == 1)
+    if (a.prefix_waves == 1)
       hipLaunchKernelGGL((attn_shared_kernel<DT, DP, 1>), grid, threads, 0, stream, a,
                          prefix_jobs);
     else
       hipLaunchKernelGGL((attn_shared_kernel<DT, DP, 4>), grid, threads, 0, stream, a,
                          prefix_jobs);
   } else {
-    const dim3 grid((unsigned)(row_tiles(per_entry) * a.splits * a.Hk * a.B));
-    if (key_waves(per_entry) == 1)
+    const dim3 grid((unsigned)(row_tiles(per_entry, a.waves) * a.splits * a.Hk * a.B));
+    if (a.waves == 1)
       hipLaunchKernelGGL((attn_kernel<DT, DP, 1>), grid, threads, 0, stream, a);
     else
       hipLaunchKernelGGL((attn_kernel<DT, DP, 4>), grid, threads, 0, stream, a);
   }
-  if (a.part)
-    hipLaunchKernelGGL((attn_join_kernel<DT>), dim3((unsigned)((all * a.Hk + 3) / 4)), threads, 0,
-                       stream, a);
+  if (a.part) {
+    constexpr int LPR = DP <= 64 ? 16 : 32;
+    const long long per = kThreads / LPR;
+    hipLaunchKernelGGL((attn_join_kernel<DT, LPR>),
+                       dim3((unsigned)((all * a.Hk + per - 1) / per)), threads, 0, stream, a);
+  }
 }
 
 template <int DT>
@@ -762,6 +778,7 @@ long long attn_plan(AttnArgs* a, int cus, bool allowed) {
   a->shared = 0;
   a->splits = a->prefix_splits = 1;
   a->chunk = 0;
+  a->waves = key_waves(per_entry, (long long)a->B * a->Hk);
   if (!allowed || all == 0) return 0;
   // Splits so that `groups` workgroups become `want`, each with `least` keys
   // or more.
@@ -770,7 +787,7 @@ long long attn_plan(AttnArgs* a, int cus, bool allowed) {
     if (s > keys / least) s = keys / least;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   };
-  const long long groups = a->B * a->Hk * row_tiles(per_entry);
+  const long long groups = a->B * a->Hk * row_tiles(per_entry, a->waves);
   // The prefix once for all entries: with few rows an entry, reading it for
   // each of them would be what the call spends its time on.
   if (a->B > 1 && per_entry <= 64 && a->P >= 128) {
@@ -778,7 +795,9 @@ long long attn_plan(AttnArgs* a, int cus, bool allowed) {
     // a share of the prefix leaves a partial result of every row: with many
     // rows it has to be long
     const long long least = 4 * all < 256 ? 256 : 4 * all > 1024 ? 1024 : 4 * all;
-    a->prefix_splits = split(2LL * cus, a->Hk * row_tiles(all), a->P, least);
+    a->waves = 4;
+    a->prefix_waves = all <= 64 ? 4 : 1;
+    a->prefix_splits = split(2LL * cus, a->Hk * row_tiles(all, a->prefix_waves), a->P, least);
     // own keys: runs of one length, so that long entries do not hold up the
     // end; about half of them will have keys
     const long long runs = split(8LL * cus, groups, a->S, 256);
@@ -786,6 +805,7 @@ long long attn_plan(AttnArgs* a, int cus, bool allowed) {
     a->chunk = (int)(chunk < 128 ? 128 : chunk);
     a->splits = (a->S + a->chunk - 1) / a->chunk;
   } else {
+        // twice as many gained nothing (24 800 rows of heads of 80: 48 us either way)
     a->splits = split(2LL * cus, groups, (long long)a->P + a->S, 256);
   }
   const int slots = a->splits + (a->shared ? a->prefix_splits : 0);

@@ -40,6 +40,7 @@ struct AttnArgs {
   int causal;
   // plan
   int shared;               // prefix rows stacked over the entries, then joined
+  int waves, prefix_waves;  // that split a workgroup's keys: 1 (none) or 4
   int splits, prefix_splits;
   int chunk;                // shared: own keys of a split (a multiple of 128)
   float* part;              // [slots][Hk][B*Sq*G][D] partial outputs
