@@ -135,6 +135,37 @@ template <> struct Elem<DT_BF16> {
   }
 };
 
+// The 16 / bytes elements of a 16-byte vector, and back.
+template <int DT>
+__device__ __forceinline__ void unpack(const u32x4_t& v, float* f) {
+  if constexpr (DT == DT_F32) {
+    const float4_t x = __builtin_bit_cast(float4_t, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = x[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = Elem<DT>::bits_to_f32(v[j] & 0xffffu);
+      f[2 * j + 1] = Elem<DT>::bits_to_f32(v[j] >> 16);
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4_t pack(const float* f) {
+  u32x4_t v;
+  if constexpr (DT == DT_F32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(uint32_t, f[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = (uint32_t)Elem<DT>::from_f32(f[2 * j]) |
+             ((uint32_t)Elem<DT>::from_f32(f[2 * j + 1]) << 16);
+  }
+  return v;
+}
+
 // Wait until at most N of this wave's global reads are outstanding (gfx9
 // s_waitcnt encoding: vmcnt in bits 3:0 and 15:14; expcnt and lgkmcnt left
 // at their maxima, i.e. not waited for).

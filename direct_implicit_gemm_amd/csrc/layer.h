@@ -63,9 +63,12 @@ struct LoraArgs {
   unsigned char* low;       // [T][low_width] low-rank values, 4 bytes each
   int* adapter_of;          // [T]
   int low_width;
+  float* part;              // few rows: [splits][T][N up to 64s], sums of runs
+  int splits, run;          // runs of the sum's axis, their bytes
+  long long part_at;        // where `part` begins in the workspace
 };
-// Width of the low-rank values, and the bytes they and the rows' adapters take.
-long long lora_plan(LoraArgs* a);
+// Fills the plan, and returns the workspace bytes it takes.
+long long lora_plan(LoraArgs* a, int dtype, int cus);
 libconv_status lora_launch(LoraArgs a, int dtype, int cus, hipStream_t stream);
 
 }  // namespace libconv

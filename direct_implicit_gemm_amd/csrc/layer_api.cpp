@@ -322,7 +322,7 @@ long long libconv_lora_workspace(int T, int K, int N, int rank, int n_adapters, 
   a.T = T; a.K = K; a.N = N; a.rank = rank;
   a.n_adapters = n_requests > 0 ? n_adapters : 0;
   a.n_requests = n_requests;
-  return lora_plan(&a);
+  return lora_plan(&a, dtype, kPlanCus);
 }
 
 libconv_status libconv_lora_linear(const void* x, const void* w, const void* bias, const void* a,
@@ -380,10 +380,11 @@ libconv_status libconv_lora_linear(const void* x, const void* w, const void* bia
   l.n_requests = n_requests;
   l.x_row = vx.s[1];
   l.y_row = vy.s[1];
-  if (lora_plan(&l) > (workspace ? workspace_bytes : 0))
+  if (lora_plan(&l, dtype, kPlanCus) > (workspace ? workspace_bytes : 0))
     return LIBCONV_ERR_SCRATCH_TOO_SMALL;
   l.low = static_cast<unsigned char*>(workspace);
   l.adapter_of = reinterpret_cast<int*>(l.low + (long long)T * l.low_width * 4);
+  l.part = reinterpret_cast<float*>(l.low + l.part_at);
   int cus = 0;
   if (!current_device(&cus)) return LIBCONV_ERR_NO_DEVICE;
   return lora_launch(l, dtype, cus, reinterpret_cast<hipStream_t>(stream));

@@ -27,9 +27,23 @@ namespace libconv {
 namespace {
 
 constexpr int kLowRows = 32;      // rows of a workgroup of the first launch
+constexpr int kFewRows = 64;      // up to which W is read once, and bounds the call
 
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// Low-rank value r of a row, at the row's values.
+template <int DT>
+__device__ __forceinline__ void store_low(const LoraArgs& a, unsigned char* at, int r, float v) {
+  if constexpr (DT == DT_F32) {
+    reinterpret_cast<float*>(at)[r] = v;
+  } else {
+    const uint16_t hi = Elem<DT_BF16>::from_f32(v);
+    const float rest = v - Elem<DT_BF16>::bits_to_f32(hi);
+    reinterpret_cast<uint16_t*>(at)[r] = hi;
+    reinterpret_cast<uint16_t*>(at)[a.low_width + r] = Elem<DT_BF16>::from_f32(rest);
+  }
 }
 
 // The first launch.  Writes, for every row t, adapter_of[t] (-1: none) and,
@@ -113,15 +127,7 @@ __global__ __launch_bounds__(64 * NW) void low_kernel(const LoraArgs a) {
 #pragma unroll
     for (int w = 0; w < NW; ++w) v += red[w][t][r];
     v *= a.scales[ad_of[t]];
-    unsigned char* at = a.low + (long long)(row0 + t) * a.low_width * 4;
-    if constexpr (DT == DT_F32) {
-      reinterpret_cast<float*>(at)[r0 + r] = v;
-    } else {
-      const uint16_t hi = Elem<DT_BF16>::from_f32(v);
-      const float rest = v - Elem<DT_BF16>::bits_to_f32(hi);
-      reinterpret_cast<uint16_t*>(at)[r0 + r] = hi;
-      reinterpret_cast<uint16_t*>(at)[a.low_width + r0 + r] = Elem<DT_BF16>::from_f32(rest);
-    }
+    store_low<DT>(a, a.low + (long long)(row0 + t) * a.low_width * 4, r0 + r, v);
   }
 }
 
@@ -382,18 +388,17 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
   }
 }
 
-// Up to 16 * RB rows: 16 outputs a workgroup, the sum's axis split over 8
-// waves, joined in the order of the waves.
+// Up to 16 * RB rows without adapters: 16 outputs a workgroup, the sum's axis
+// split over 8 waves, joined in the order of the waves.
 constexpr int kFewWaves = 8;
 template <int DT, int RB>
-__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const LoraArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(const LoraArgs a) {
   constexpr int EB = Elem<DT>::bytes;
   constexpr int THREADS = 64 * kFewWaves, ROWS = 16 * RB;
   __shared__ __attribute__((aligned(16))) float join[kFewWaves * ROWS * 20];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l16 = lane & 15, quarter = lane >> 4;
   const int n0 = blockIdx.x * 16;
-  const int here = a.n_adapters > 0 && lane < a.T ? a.adapter_of[lane] : -1;
 
   const int row_bytes = a.K * EB;
   const int steps = (row_bytes + 63) / 64;
@@ -402,68 +407,49 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const LoraArgs a) {
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row_bytes, 0x7ffffff0u);
   const bool n_ok = n0 + l16 < a.N;
   // W is what the call reads from memory: 16 steps of it are on their way at
-  // a time, the first before anything else is waited for
-  constexpr int UW = 16, UX = 4;
-  u32x4_t wf[UW];
-  auto fetch_w = [&](int k) {
+  // a time, the first before anything else is waited for; x comes from L2, a
+  // group of 4 steps ahead
+  constexpr int U = 4, AHEAD = 4;
+  const int groups = (k1 - k0 + U - 1) / U;
+  u32x4_t wf[AHEAD][U], xf[2][U][RB];
+  auto fetch_w = [&](int g, u32x4_t* w) {
 #pragma unroll
-    for (int u = 0; u < UW; ++u) {
-      const int off = (k + u) * 64 + quarter * 16;
-      wf[u] = load16(rw, guard_offset(n_ok && k + u < k1 && off < row_bytes,
-                                      l16 * row_bytes + off));
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + g * U + u, off = k * 64 + quarter * 16;
+      w[u] = load16(rw, guard_offset(n_ok && k < k1 && off < row_bytes, l16 * row_bytes + off));
     }
-    __builtin_amdgcn_sched_barrier(0);
   };
-  fetch_w(k0);
+  auto fetch_x = [&](int g, u32x4_t (*x)[RB]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        const int k = k0 + g * U + u, off = k * 64 + quarter * 16;
+        x[u][j] = load16(rx, guard_offset(k < k1 && off < row_bytes && j * 16 + l16 < a.T,
+                                          (j * 16 + l16) * (int)a.x_row + off));
+      }
+  };
+#pragma unroll
+  for (int g = 0; g < AHEAD; ++g) fetch_w(g, wf[g]);
+  fetch_x(0, xf[0]);
+
+  __builtin_amdgcn_sched_barrier(0);
 
   float4_t acc[RB];
 #pragma unroll
   for (int j = 0; j < RB; ++j) acc[j] = float4_t{0, 0, 0, 0};
-  if (a.n_adapters > 0) {
-    constexpr int LB = DT == DT_F32 ? 4 : 2;
-    const __amdgpu_buffer_rsrc_t rl = make_rsrc(a.low, 0x7ffffff0u);
-    int mine[RB];
+  for (int g0 = 0; g0 < groups; g0 += AHEAD) {
 #pragma unroll
-    for (int j = 0; j < RB; ++j) mine[j] = __shfl(here, j * 16 + l16);
-    // the waves take the adapters in turn
-    uint64_t left = __ballot(here >= 0);
-    for (int turn = 0; left; ++turn) {
-      const int ad = __builtin_amdgcn_readlane(here, __builtin_ctzll(left));
-      left &= ~__ballot(here == ad);
-      if (turn % kFewWaves != wave) continue;
-      const __amdgpu_buffer_rsrc_t rb =
-          make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
-      for (int s = 0; s < (a.rank * LB + 63) / 64; ++s) {
-        const u32x4_t bf = load_b<DT>(a, rb, n0 + l16, (s * 64 + quarter * 16) / LB);
-        u32x4_t hi[RB], lo[RB];
+    for (int v = 0; v < AHEAD; ++v) {
+      if (g0 + v >= groups) break;
+      fetch_x(g0 + v + 1, xf[(v + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < RB; ++j)
-          load_low<DT>(a, rl, j * 16 + l16, mine[j] == ad, s * 64 + quarter * 16, &hi[j], &lo[j]);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int j = 0; j < RB; ++j) low_step<DT, false>(bf, hi[j], lo[j], acc[j]);
-      }
-    }
-  }
-
-  for (int k = k0; k < k1; k += UW) {
-    if (k != k0) fetch_w(k);
-#pragma unroll
-    for (int v = 0; v < UW; v += UX) {
-      if (k + v >= k1) break;
-      u32x4_t xf[UX][RB];
-#pragma unroll
-      for (int u = 0; u < UX; ++u)
-#pragma unroll
-        for (int j = 0; j < RB; ++j) {
-          const int off = (k + v + u) * 64 + quarter * 16;
-          xf[u][j] = load16(rx, guard_offset(k + v + u < k1 && off < row_bytes &&
-                                                 j * 16 + l16 < a.T,
-                                             (j * 16 + l16) * (int)a.x_row + off));
-        }
-#pragma unroll
-      for (int u = 0; u < UX; ++u)
-#pragma unroll
-        for (int j = 0; j < RB; ++j) Step<DT, false>::run(wf[v + u], xf[u][j], acc[j]);
+        for (int j = 0; j < RB; ++j) Step<DT, false>::run(wf[v][u], xf[v & 1][u][j], acc[j]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (g0 + AHEAD < groups) fetch_w(g0 + v + AHEAD, wf[v]);
     }
   }
 
@@ -485,6 +471,193 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const LoraArgs a) {
   }
 }
 
+// Up to 64 rows with adapters, in two launches: the shared product in runs of
+// the sum's axis beside the low-rank values, then the sum of all.
+
+// Low-rank values r0 .. r0 + 15 of row t (fp32) and the row's adapter: 16 bytes
+// of x and of each row of A a lane, dense reads that are all on their way at
+// once.
+template <int DT>
+__device__ __forceinline__ void low_row(const LoraArgs& a, int t, int r0, unsigned char* lds) {
+  constexpr int E = 16 / Elem<DT>::bytes, R = 16, THREADS = 256;
+  int* found = reinterpret_cast<int*>(lds);
+  float* red = reinterpret_cast<float*>(lds + 16);   // [4][R]
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int row_bytes = a.K * Elem<DT>::bytes;
+  if (threadIdx.x == 0) *found = -1;
+  lds_barrier();
+  for (int r = threadIdx.x; r < a.n_requests; r += THREADS) {
+    const int ad = a.adapters[r], s0 = a.starts[r], s1 = a.starts[r + 1];
+    if (s0 <= t && t < s1 && ad >= 0 && ad < a.n_adapters) *found = ad;
+  }
+  lds_barrier();
+  const int ad = __builtin_amdgcn_readfirstlane(*found);
+  if (r0 == 0 && threadIdx.x == 0) a.adapter_of[t] = ad;
+  if (ad < 0) return;
+  const float scale = a.scales[ad];
+  const int ranks = a.rank - r0 < R ? a.rank - r0 : R;   // <= 0: padding, zeros
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + t * a.x_row, row_bytes);
+  const __amdgpu_buffer_rsrc_t ra =
+      make_rsrc(a.a + ((long long)ad * a.rank + (ranks > 0 ? r0 : 0)) * row_bytes,
+                ranks > 0 ? (uint32_t)(ranks * row_bytes) : 0u);
+  float sum[R] = {};
+  for (int off = threadIdx.x * 16; off < row_bytes; off += THREADS * 16) {
+    const u32x4_t xv = load16(rx, off);
+    u32x4_t av[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) av[r] = load16(ra, r * row_bytes + off);
+    __builtin_amdgcn_sched_barrier(0);
+    float x[E];
+    unpack<DT>(xv, x);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float w[E];
+      unpack<DT>(av[r], w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[r] = fmaf(x[e], w[e], sum[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) sum[r] += __shfl_xor(sum[r], m);
+  if (lane == 0)
+#pragma unroll
+    for (int r = 0; r < R; ++r) red[wave * R + r] = sum[r];
+  lds_barrier();
+  if (threadIdx.x < R) {
+    const int r = threadIdx.x;
+    const float v = red[r] + red[R + r] + red[2 * R + r] + red[3 * R + r];
+    reinterpret_cast<float*>(a.low)[(long long)t * a.low_width + r0 + r] = v * scale;
+  }
+}
+
+// Four waves take 16 outputs each and a run of the sum's axis: x arrives in
+// LDS, W straight in registers (each of its values has one reader), all of a
+// run on its way at once.  The first `low_jobs` workgroups take the low-rank
+// values meanwhile.
+constexpr int kRun = 1024;   // bytes of a run, at most
+template <int DT, int RB>
+__global__ __launch_bounds__(256, 2) void run_kernel(const LoraArgs a, int low_jobs) {
+  constexpr int EB = Elem<DT>::bytes, ROWS = 16 * RB, STEPS = kRun / 64;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[ROWS * kRun];
+  if ((int)blockIdx.x < low_jobs) {
+    low_row<DT>(a, (int)blockIdx.x % a.T, (int)blockIdx.x / a.T * 16, lds);
+    return;
+  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l16 = lane & 15, quarter = lane >> 4;
+  const int id = blockIdx.x - low_jobs;
+  const int split = id % a.splits, n0 = id / a.splits * 64 + wave * 16;
+  const int row_bytes = a.K * EB;
+  const int c0 = split * a.run, c1 = c0 + a.run < row_bytes ? c0 + a.run : row_bytes;
+  const int stages = (c1 - c0 + 127) / 128;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x, 0x7ffffff0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row_bytes, 0x7ffffff0u);
+  // x: 128 bytes of all rows after 128 bytes of all rows
+#pragma unroll
+  for (int j = 0; j < ROWS * kRun / 16 / 256; ++j) {
+    const int unit = j * 256 + threadIdx.x;
+    const int row = unit / 8 % ROWS;
+    const int off = c0 + unit / (ROWS * 8) * 128 + chunk_at(row, unit & 7) * 16;
+    if (j * 256 < stages * ROWS * 8)
+      copy16_to_lds(rx, lds + (j * 256 + wave * 64) * 16,
+                    guard_offset(row < a.T && off < c1, row * (int)a.x_row + off));
+  }
+  u32x4_t wf[STEPS];
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    const int off = c0 + k * 64 + quarter * 16;
+    wf[k] = load16(rw, guard_offset(n0 + l16 < a.N && off < c1, l16 * row_bytes + off));
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vmcnt<STEPS>();
+  lds_barrier();
+  float4_t acc[RB];
+#pragma unroll
+  for (int j = 0; j < RB; ++j) acc[j] = float4_t{0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    if (k * 64 < c1 - c0) {
+#pragma unroll
+      for (int j = 0; j < RB; ++j) {
+        const int row = j * 16 + l16;
+        const u32x4_t xf = *reinterpret_cast<const u32x4_t*>(
+            lds + (k / 2 * ROWS + row) * 128 + chunk_at(row, (k & 1) * 4 + quarter) * 16);
+        Step<DT, false>::run(wf[k], xf, acc[j]);
+      }
+    }
+  }
+  const long long n_pad = (a.N + 63) / 64 * 64;
+#pragma unroll
+  for (int j = 0; j < RB; ++j) {
+    const int t = j * 16 + l16;
+    if (t < a.T)
+      *reinterpret_cast<float4_t*>(a.part + ((long long)split * a.T + t) * n_pad + n0 +
+                                   quarter * 4) = acc[j];
+  }
+}
+
+// y of row blockIdx.y: the runs in their order, the bias, the low-rank term.
+template <int DT>
+__global__ __launch_bounds__(256) void sum_kernel(const LoraArgs a) {
+  constexpr int EB = Elem<DT>::bytes, E = 16 / EB;
+  const int n = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  if (n >= a.N) return;
+  const int ad = __builtin_amdgcn_readfirstlane(a.adapter_of[t]);
+  const long long n_pad = (a.N + 63) / 64 * 64;
+  const float* part = a.part + t * n_pad + n;
+  float v = 0.0f;
+  for (int s = 0; s < a.splits; s += 8) {
+    float p[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      p[u] = s + u < a.splits ? part[(long long)(s + u) * a.T * n_pad] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += p[u];
+  }
+  if (a.bias) {
+    if constexpr (DT == DT_F32) v += static_cast<const float*>(a.bias)[n];
+    else v += Elem<DT>::bits_to_f32(static_cast<const uint16_t*>(a.bias)[n]);
+  }
+  if (ad >= 0) {
+    const char* b = a.b + ((long long)ad * a.N + n) * a.rank * EB;
+    const float* low = reinterpret_cast<const float*>(a.low) + (long long)t * a.low_width;
+    if (a.rank % E == 0) {
+      for (int r = 0; r < a.rank; r += E) {
+        float w[E];
+        unpack<DT>(*reinterpret_cast<const u32x4_t*>(b + r * EB), w);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v = fmaf(low[r + e], w[e], v);
+      }
+    } else {
+      for (int r = 0; r < a.rank; ++r) {
+        float w;
+        if constexpr (DT == DT_F32) w = reinterpret_cast<const float*>(b)[r];
+        else w = Elem<DT>::bits_to_f32(reinterpret_cast<const uint16_t*>(b)[r]);
+        v = fmaf(low[r], w, v);
+      }
+    }
+  }
+  char* y = a.y + t * a.y_row + (long long)n * EB;
+  if constexpr (DT == DT_F32) *reinterpret_cast<float*>(y) = v;
+  else *reinterpret_cast<uint16_t*>(y) = Elem<DT>::from_f32(v);
+}
+
+template <int DT>
+void launch_runs(const LoraArgs& a, hipStream_t stream) {
+  const int low_jobs = a.T * ((a.rank + 15) / 16);
+  const dim3 grid((unsigned)(low_jobs + (a.N + 63) / 64 * a.splits)), threads(256);
+  if (a.T <= 16)
+    hipLaunchKernelGGL((run_kernel<DT, 1>), grid, threads, 0, stream, a, low_jobs);
+  else if (a.T <= 32)
+    hipLaunchKernelGGL((run_kernel<DT, 2>), grid, threads, 0, stream, a, low_jobs);
+  else
+    hipLaunchKernelGGL((run_kernel<DT, 4>), grid, threads, 0, stream, a, low_jobs);
+  hipLaunchKernelGGL((sum_kernel<DT>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.T), threads,
+                     0, stream, a);
+}
+
 template <int DT, int BM, int BN, int WM, int WN>
 void launch_tile(const LoraArgs& a, hipStream_t stream) {
   const int tm = (a.T + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
@@ -503,6 +676,10 @@ double tile_cost(const LoraArgs& a, int cus, int bm, int bn, int per_cu, double 
 
 template <int DT>
 void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
+  if (a.n_adapters > 0 && a.T <= kFewRows) {
+    launch_runs<DT>(a, stream);
+    return;
+  }
   if (a.n_adapters > 0) {
     // with few row tiles, 16 waves to one and the tile's adapters dealt out
     const int tiles = (a.T + kLowRows - 1) / kLowRows;
@@ -516,7 +693,7 @@ void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
     else
       hipLaunchKernelGGL((low_kernel<DT, 8>), grid, dim3(64 * 8), 0, stream, a);
   }
-  if (a.T <= 64) {
+  if (a.T <= kFewRows) {
     const dim3 grid((unsigned)((a.N + 15) / 16)), threads(64 * kFewWaves);
     if (a.T <= 16) hipLaunchKernelGGL((few_kernel<DT, 1>), grid, threads, 0, stream, a);
     else if (a.T <= 32) hipLaunchKernelGGL((few_kernel<DT, 2>), grid, threads, 0, stream, a);
@@ -533,11 +710,23 @@ void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
 
 }  // namespace
 
-long long lora_plan(LoraArgs* a) {
-  a->low_width = 0;
+long long lora_plan(LoraArgs* a, int dtype, int cus) {
+  a->low_width = a->splits = a->run = 0;
   if (a->n_adapters == 0 || a->T == 0) return 0;
   a->low_width = (a->rank + 31) / 32 * 32;
-  return (long long)a->T * (a->low_width + 1) * 4;
+  const long long low = (long long)a->T * (a->low_width + 1) * 4;
+  a->part_at = (low + 255) / 256 * 256;
+  if (a->T > kFewRows) return low;
+  // runs of the sum's axis: two workgroups a compute unit if they have 256
+  // bytes or more
+  const int row_bytes = a->K * (dtype == LIBCONV_F32 ? 4 : 2);
+  const int tiles = (a->N + 63) / 64;
+  int runs = 2 * cus / tiles;
+  if (runs > row_bytes / 256) runs = row_bytes / 256;
+  if (runs < (row_bytes + kRun - 1) / kRun) runs = (row_bytes + kRun - 1) / kRun;
+  a->run = ((row_bytes + runs - 1) / runs + 127) / 128 * 128;
+  a->splits = (row_bytes + a->run - 1) / a->run;
+  return a->part_at + (long long)a->splits * a->T * tiles * 64 * 4;
 }
 
 libconv_status lora_launch(LoraArgs a, int dtype, int cus, hipStream_t stream) {

@@ -19,36 +19,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kUnroll = 4;   // steps whose loads are issued together
 
-template <int DT>
-__device__ __forceinline__ void unpack(const u32x4_t& v, float* f) {
-  if constexpr (DT == DT_F32) {
-    const float4_t x = __builtin_bit_cast(float4_t, v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = x[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = Elem<DT>::bits_to_f32(v[j] & 0xffffu);
-      f[2 * j + 1] = Elem<DT>::bits_to_f32(v[j] >> 16);
-    }
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ u32x4_t pack(const float* f) {
-  u32x4_t v;
-  if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(uint32_t, f[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = (uint32_t)Elem<DT>::from_f32(f[2 * j]) |
-             ((uint32_t)Elem<DT>::from_f32(f[2 * j + 1]) << 16);
-  }
-  return v;
-}
-
 template <int DT, int LPH>
 __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a) {
   constexpr int E = 16 / Elem<DT>::bytes;   // elements a lane holds of a head
