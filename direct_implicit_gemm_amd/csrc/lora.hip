@@ -257,14 +257,14 @@ __device__ __forceinline__ void store4(const LoraArgs& a, int t, int n, const fl
 __device__ __forceinline__ int chunk_at(int row, int c) { return c ^ ((row >> 1) & 7); }
 
 // Many rows: BM tokens x BN outputs, WM x WN waves.
-template <int DT, int BM, int BN, int WM, int WN>
+template <int DT, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, int tiles_m,
                                                             int tiles_n) {
   constexpr int EB = Elem<DT>::bytes;
   constexpr int THREADS = 64 * WM * WN;
   constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks of a wave
   constexpr int STAGE = (BM + BN) * 128;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[2 * STAGE];
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * STAGE];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
@@ -286,33 +286,6 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
 #pragma unroll
     for (int j = 0; j < MB; ++j) acc[i][j] = float16_t{};
 
-  if (a.n_adapters > 0) {
-    constexpr int LB = DT == DT_F32 ? 4 : 2;   // bytes of a low-rank value
-    const __amdgpu_buffer_rsrc_t rl =
-        make_rsrc(a.low + (long long)m0 * a.low_width * 4, 0x7ffffff0u);
-#pragma unroll
-    for (int j = 0; j < MB; ++j) {
-      const int t = (wm * MB + j) * 32 + l32;
-      const int mine = m0 + t < a.T ? a.adapter_of[m0 + t] : -1;
-      uint64_t left = __ballot(mine >= 0);
-      while (left) {
-        const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-        left &= ~__ballot(mine == ad);
-        const __amdgpu_buffer_rsrc_t rb =
-            make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
-        for (int s = 0; s < (a.rank * LB + 31) / 32; ++s) {
-          u32x4_t hi, lo, bf[NB];
-          load_low<DT>(a, rl, t, mine == ad, s * 32 + half * 16, &hi, &lo);
-#pragma unroll
-          for (int i = 0; i < NB; ++i)
-            bf[i] = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32, (s * 32 + half * 16) / LB);
-#pragma unroll
-          for (int i = 0; i < NB; ++i) low_step<DT, true>(bf[i], hi, lo, acc[i][j]);
-        }
-      }
-    }
-  }
-
   // stages
   const int row_bytes = a.K * EB;
   const int stages = (row_bytes + 127) / 128;
@@ -333,9 +306,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
     w_chunk[c] = chunk_at(row, unit & 7) * 16;
     w_off[c] = n0 + row < a.N ? row * row_bytes + w_chunk[c] : kOobOffset;
   }
-#define LIBCONV_COPY_STAGE(st)                                                                  \
+#define LIBCONV_COPY_STAGE(st, at)                                                              \
   {                                                                                             \
-    unsigned char* to = lds + ((st) & 1) * STAGE;                                               \
+    unsigned char* to = lds + (at) * STAGE;                                                     \
     const int k = (st) * 128;                                                                   \
     _Pragma("unroll") for (int c = 0; c < CX; ++c) copy16_to_lds(                               \
         rx, to + (c * THREADS + wave * 64) * 16,                                                \
@@ -344,12 +317,52 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
         rw, to + BM * 128 + (c * THREADS + wave * 64) * 16,                                     \
         guard_offset(w_off[c] >= 0 && k + w_chunk[c] < row_bytes, w_off[c] + k));               \
   }
-  LIBCONV_COPY_STAGE(0)
+  // NS - 1 stages are on their way at a time; those past the last read nothing
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) LIBCONV_COPY_STAGE(st, st)
+
+  if (a.n_adapters > 0) {
+    constexpr int LB = DT == DT_F32 ? 4 : 2;   // bytes of a low-rank value
+    const __amdgpu_buffer_rsrc_t rl =
+        make_rsrc(a.low + (long long)m0 * a.low_width * 4, 0x7ffffff0u);
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int t = (wm * MB + j) * 32 + l32;
+      const int mine = m0 + t < a.T ? a.adapter_of[m0 + t] : -1;
+      uint64_t left = __ballot(mine >= 0);
+      while (left) {
+        const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+        left &= ~__ballot(mine == ad);
+        const __amdgpu_buffer_rsrc_t rb =
+            make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
+        const int steps = (a.rank * LB + 31) / 32;
+        for (int s = 0; s < steps; s += 2) {   // two steps' reads together
+          u32x4_t hi[2], lo[2], bf[2][NB];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int off = (s + u) * 32 + half * 16;
+            load_low<DT>(a, rl, t, mine == ad && s + u < steps, off, &hi[u], &lo[u]);
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+              bf[u][i] = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32, off / LB);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) low_step<DT, true>(bf[u][i], hi[u], lo[u], acc[i][j]);
+        }
+      }
+    }
+  }
+
+  int at = 0, free = NS - 1;   // stages in use and to be filled
   for (int st = 0; st < stages; ++st) {
-    wait_vmcnt<0>();
+    wait_vmcnt<(NS - 2) * (CX + CW)>();
     lds_barrier();
-    if (st + 1 < stages) LIBCONV_COPY_STAGE(st + 1)
-    const unsigned char* xs = lds + (st & 1) * STAGE;
+    LIBCONV_COPY_STAGE(st + NS - 1, free)
+    const unsigned char* xs = lds + at * STAGE;
+    free = at;
+    at = at + 1 < NS ? at + 1 : 0;
     const unsigned char* ws = xs + BM * 128;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -658,10 +671,10 @@ void launch_runs(const LoraArgs& a, hipStream_t stream) {
                      0, stream, a);
 }
 
-template <int DT, int BM, int BN, int WM, int WN>
+template <int DT, int BM, int BN, int WM, int WN, int NS>
 void launch_tile(const LoraArgs& a, hipStream_t stream) {
   const int tm = (a.T + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
-  hipLaunchKernelGGL((tile_kernel<DT, BM, BN, WM, WN>), dim3((unsigned)(tm * tn)),
+  hipLaunchKernelGGL((tile_kernel<DT, BM, BN, WM, WN, NS>), dim3((unsigned)(tm * tn)),
                      dim3(64 * WM * WN), 0, stream, a, tm, tn);
 }
 
@@ -703,9 +716,9 @@ void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
   const double c256 = tile_cost(a, cus, 256, 256, 1, 1.0);
   const double c128 = tile_cost(a, cus, 128, 128, 2, 0.75);
   const double c64 = tile_cost(a, cus, 64, 64, 4, 0.4);
-  if (c256 <= c128 && c256 <= c64) launch_tile<DT, 256, 256, 4, 2>(a, stream);
-  else if (c128 <= c64) launch_tile<DT, 128, 128, 2, 2>(a, stream);
-  else launch_tile<DT, 64, 64, 2, 2>(a, stream);
+  if (c256 <= c128 && c256 <= c64) launch_tile<DT, 256, 256, 4, 2, 2>(a, stream);
+  else if (c128 <= c64) launch_tile<DT, 128, 128, 2, 2, 2>(a, stream);
+  else launch_tile<DT, 64, 64, 2, 2, 4>(a, stream);
 }
 
 }  // namespace
