@@ -63,8 +63,10 @@ struct LoraArgs {
   unsigned char* low;       // [T][low_width] low-rank values, 4 bytes each
   int* adapter_of;          // [T]
   int low_width;
-  float* part;              // few rows: [splits][T][N up to 64s], sums of runs
-  int splits, run;          // runs of the sum's axis, their bytes
+  // not too many rows: sums of runs of the sum's axis [splits][T][N up to 64s],
+  // the runs' bytes and the tile they are formed in; splits 0 otherwise
+  float* part;
+  int splits, run, tile;
   long long part_at;        // where `part` begins in the workspace
 };
 // Fills the plan, and returns the workspace bytes it takes.

@@ -3,12 +3,13 @@
 //
 //   y[t] = W x[t] + bias + s_a B_a (A_a x[t])
 //
-// Two launches.  The first finds each row's adapter and forms the low-rank
-// values s_a A_a x[t] in fp32 (for 32 rows: adapter by adapter, each lane
-// keeping the result of its own row's; the sum's axis is split over the waves
-// of a workgroup, so that nothing is left to add up).  The second is the
-// projection; a workgroup starts its sums with the low-rank term of its tile,
-// so y is written once.  The low-rank values of 16-bit types enter the matrix
+// Two launches, in one of two ways.  Up to about 1000 rows: the first forms the
+// product in fp32 (in runs of the sum's axis, if it has too few tiles to fill
+// the GPU) and, beside it, the low-rank values s_a A_a x[t]; the second adds
+// the runs, the bias and the low-rank term.  Many rows: the first finds each
+// row's adapter and forms the low-rank values; the second is the projection,
+// whose workgroups start their sums with the low-rank term of their tile, so y
+// is written once.  There the low-rank values of 16-bit types enter the matrix
 // instructions as two bfloat16 numbers, high and low part (16 significant
 // bits): one would round the low-rank term to 8 bits before the sum.  fp16
 // adapters are split the same way (three products), because a low-rank value
@@ -17,9 +18,8 @@
 // The projection is formed transposed (outputs n on the rows of the matrix
 // instructions, tokens on their columns), so that a lane holds 4 consecutive
 // outputs of one token.  Both operands have their sums' axis dense: a stage
-// is 128 bytes of it, copied straight into LDS, double-buffered.  Up to 64
-// rows are bound by reading W once: a workgroup takes 16 outputs and its 8
-// waves split the sum's axis, reading W and x straight into registers.
+// is 128 bytes of it, copied straight into LDS.  Up to 64 rows are bound by
+// reading W once.
 #include "device_common.h"
 #include "layer.h"
 
@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kLowRows = 32;      // rows of a workgroup of the first launch
 constexpr int kFewRows = 64;      // up to which W is read once, and bounds the call
+constexpr int kLowGroup = 4;      // rows that share their reads of A, where more
 
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
@@ -46,18 +47,68 @@ __device__ __forceinline__ void store_low(const LoraArgs& a, unsigned char* at, 
   }
 }
 
+// 32 rows of x times 32 rows of another operand: both arrive in LDS 256 bytes
+// of the sums' axis at a time, NS - 1 such stages on their way; the four waves
+// take 64 bytes of each, so acc holds a quarter of the sums.  off: of this
+// thread's copies (rows 16 apart, two of x and two of the other; see
+// offsets32).  Chunk c of row r is kept at c ^ (r & 15), so that 16 rows'
+// reads of one chunk hit all banks.
+constexpr int kStage32 = 64 * 256;
+__device__ __forceinline__ int column32() {   // bytes of a thread's chunk in a row
+  return ((threadIdx.x & 15) ^ (threadIdx.x >> 4)) * 16;
+}
+__device__ __forceinline__ void offsets32(int* off, int rows, int stride) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int row = c * 16 + (threadIdx.x >> 4);
+    off[c] = row < rows ? row * stride + column32() : kOobOffset;
+  }
+}
+template <int DT, int NS>
+__device__ __forceinline__ void product32(__amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t rw,
+                                          const int* off, int row_bytes, unsigned char* lds,
+                                          float16_t& acc) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, half = lane >> 5;
+  const int stages = (row_bytes + 255) / 256, column = column32();
+#define LIBCONV_COPY_STAGE(st, at)                                                              \
+  {                                                                                             \
+    const int k = (st) * 256;                                                                   \
+    _Pragma("unroll") for (int c = 0; c < 4; ++c) copy16_to_lds(                                \
+        c < 2 ? rx : rw, lds + (at) * kStage32 + (c * 256 + wave * 64) * 16,                    \
+        guard_offset(off[c] >= 0 && k + column < row_bytes, off[c] + k));                       \
+  }
+  // past the last stage they read nothing
+#pragma unroll
+  for (int st = 0; st < NS - 1; ++st) LIBCONV_COPY_STAGE(st, st)
+  for (int st = 0; st < stages; ++st) {
+    wait_vmcnt<(NS - 2) * 4>();
+    lds_barrier();
+    LIBCONV_COPY_STAGE(st + NS - 1, (st + NS - 1) % NS)
+    const unsigned char* xs = lds + st % NS * kStage32 + l32 * 256;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int at = ((wave * 4 + u * 2 + half) ^ (l32 & 15)) * 16;
+      const u32x4_t xf = *reinterpret_cast<const u32x4_t*>(xs + at);
+      const u32x4_t wf = *reinterpret_cast<const u32x4_t*>(xs + 32 * 256 + at);
+#pragma unroll
+      for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(wf, xf, acc, e);
+    }
+  }
+#undef LIBCONV_COPY_STAGE
+  wait_vmcnt<0>();
+}
+
 // The first launch.  Writes, for every row t, adapter_of[t] (-1: none) and,
 // for rows that have one, width values from low + 4 width t on: fp32 ones, or
 // (16-bit types) width high bfloat16 parts and then width low parts.  Values
 // from the rank on are 0.  Grid: row tiles x shares of the adapters of a tile
-// (with few rows there are as many adapters as rows, and few tiles) x 32 of
-// the rank.
-template <int DT, int NW>
-__global__ __launch_bounds__(64 * NW) void low_kernel(const LoraArgs a) {
-  constexpr int EB = Elem<DT>::bytes;
-  constexpr int THREADS = 64 * NW;
+// x 32 of the rank.
+template <int DT, int NS>
+__global__ __launch_bounds__(256, NS <= 4 ? 2 : 1) void low_kernel(const LoraArgs a) {
+  constexpr int EB = Elem<DT>::bytes, THREADS = 256;
   __shared__ int ad_of[kLowRows];
-  __shared__ float red[NW][32][33];
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * kStage32];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int row0 = blockIdx.x * kLowRows, r0 = blockIdx.z * 32;
@@ -78,56 +129,49 @@ __global__ __launch_bounds__(64 * NW) void low_kernel(const LoraArgs a) {
     a.adapter_of[row0 + l32] = mine;
 
   const int row_bytes = a.K * EB;
-  const int steps = (row_bytes + 31) / 32;
-  const int k0 = (int)((long long)steps * wave / NW);
-  const int k1 = (int)((long long)steps * (wave + 1) / NW);
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)row0 * a.x_row, 0x7ffffff0u);
-  const int x_off = l32 * (int)a.x_row, a_off = l32 * row_bytes;
-  const bool rank_ok = r0 + l32 < a.rank;
+  int off[4];
+  offsets32(off, a.T - row0, (int)a.x_row);
+  offsets32(off + 2, a.rank - r0, row_bytes);
 
   float16_t res = {};
   bool kept = false;   // this lane's row is this workgroup's to write
   uint64_t left = __ballot(mine >= 0);
-  for (int turn = 0; left; ++turn) {
+  for (int turn = 0; left; turn = turn + 1 < (int)gridDim.y ? turn + 1 : 0) {
     const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
     left &= ~__ballot(mine == ad);
-    if (turn % gridDim.y != blockIdx.y) continue;
+    if (turn != (int)blockIdx.y) continue;
+    const float scale = a.scales[ad];
     const __amdgpu_buffer_rsrc_t ra =
         make_rsrc(a.a + ((long long)ad * a.rank + r0) * row_bytes, 0x7ffffff0u);
+    if (kept) lds_barrier();   // the last adapter's stages are read
     float16_t acc = {};
-    constexpr int U = 8;
-    for (int k = k0; k < k1; k += U) {
-      u32x4_t xf[U], af[U];
+    product32<DT, NS>(rx, ra, off, row_bytes, lds, acc);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int off = (k + u) * 32 + half * 16;
-        const bool in = k + u < k1 && off < row_bytes;
-        xf[u] = load16(rx, guard_offset(in && row_ok, x_off + off));
-        af[u] = load16(ra, guard_offset(in && rank_ok, a_off + off));
-      }
-      __builtin_amdgcn_sched_barrier(0);   // all of a batch's reads in flight together
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(af[u], xf[u], acc, e);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) res[i] = mine == ad ? acc[i] : res[i];
-    kept = kept || mine == ad;
+    for (int i = 0; i < 16; ++i) res[i] = mine == ad ? acc[i] * scale : res[i];
+    kept = true;
   }
-  const uint64_t rows = __ballot(kept);   // the same in all waves
-  if (rows == 0) return;
+  if (!kept) return;   // the same in all waves
+  // rows of this workgroup's adapters
+  uint64_t rows = 0;
+  {
+    uint64_t rest = __ballot(mine >= 0);
+    for (int turn = 0; rest; turn = turn + 1 < (int)gridDim.y ? turn + 1 : 0) {
+      const uint64_t same = __ballot(mine == __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest)));
+      rest &= ~same;
+      if (turn == (int)blockIdx.y) rows |= same;
+    }
+  }
+  float(*red)[32][33] = reinterpret_cast<float(*)[32][33]>(lds);
+  lds_barrier();
 #pragma unroll
   for (int i = 0; i < 16; ++i) red[wave][l32][(i & 3) + 8 * (i >> 2) + 4 * half] = res[i];
   lds_barrier();
   for (int i = threadIdx.x; i < 32 * 32; i += THREADS) {
     const int t = i >> 5, r = i & 31;
-    if (!(rows >> t & 1)) continue;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[w][t][r];
-    v *= a.scales[ad_of[t]];
-    store_low<DT>(a, a.low + (long long)(row0 + t) * a.low_width * 4, r0 + r, v);
+    if (rows >> t & 1)
+      store_low<DT>(a, a.low + (long long)(row0 + t) * a.low_width * 4, r0 + r,
+                    red[0][t][r] + red[1][t][r] + red[2][t][r] + red[3][t][r]);
   }
 }
 
@@ -256,10 +300,116 @@ __device__ __forceinline__ void store4(const LoraArgs& a, int t, int n, const fl
 // read one chunk of 16 rows at a time hit all banks.
 __device__ __forceinline__ int chunk_at(int row, int c) { return c ^ ((row >> 1) & 7); }
 
-// Many rows: BM tokens x BN outputs, WM x WN waves.
-template <int DT, int BM, int BN, int WM, int WN, int NS>
+// Fewer rows, in two launches: the shared product in runs of the sum's axis
+// beside the low-rank values, then the sum of all (sum_kernel).
+
+// Sums of N values over the wave, N a power of 2: each step halves the values a
+// lane keeps, so lane l ends with value l * N / 64.
+template <int N, int M = 32>
+__device__ __forceinline__ float wave_sum(float* v) {
+  if constexpr (M == 0) {
+    return v[0];
+  } else if constexpr (N == 1) {
+    v[0] += __shfl_xor(v[0], M);
+  } else {
+    const bool upper = (threadIdx.x & M) != 0;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float keep = upper ? v[i + N / 2] : v[i], give = upper ? v[i] : v[i + N / 2];
+      v[i] = keep + __shfl_xor(give, M);
+    }
+  }
+  return wave_sum<(N > 1 ? N / 2 : 1), M / 2>(v);
+}
+
+// Low-rank values r0 .. r0 + 15 of RT rows from t0 on (fp32), and the rows'
+// adapters: 16 bytes of x and of each row of A a lane, dense reads that are all
+// on their way at once.  256 threads.
+template <int DT, int RT>
+__device__ __forceinline__ void low_rows(const LoraArgs& a, int t0, int r0, unsigned char* lds) {
+  constexpr int E = 16 / Elem<DT>::bytes, R = 16, THREADS = 256;
+  int* found = reinterpret_cast<int*>(lds);
+  float* red = reinterpret_cast<float*>(lds + 64);   // [4][RT * R]
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int row_bytes = a.K * Elem<DT>::bytes;
+  if (threadIdx.x < RT) found[threadIdx.x] = -1;
+  lds_barrier();
+  for (int r = threadIdx.x; r < a.n_requests; r += THREADS) {
+    const int ad = a.adapters[r], s0 = a.starts[r], s1 = a.starts[r + 1];
+    if (ad < 0 || ad >= a.n_adapters) continue;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      if (s0 <= t0 + i && t0 + i < s1) found[i] = ad;
+  }
+  lds_barrier();
+  int of[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    of[i] = t0 + i < a.T ? __builtin_amdgcn_readfirstlane(found[i]) : -1;
+  if (r0 == 0 && threadIdx.x < RT && t0 + (int)threadIdx.x < a.T)
+    a.adapter_of[t0 + threadIdx.x] = found[threadIdx.x];
+  const int ranks = a.rank - r0 < R ? a.rank - r0 : R;   // <= 0: padding, zeros
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + t0 * a.x_row, 0x7ffffff0u);
+#pragma unroll
+  for (int turn = 0; turn < RT; ++turn) {
+    const int ad = of[turn];
+    bool first = ad >= 0;   // of the rows with this adapter
+#pragma unroll
+    for (int i = 0; i < turn; ++i) first = first && of[i] != ad;
+    if (!first) continue;
+    const float scale = a.scales[ad];
+    const __amdgpu_buffer_rsrc_t ra =
+        make_rsrc(a.a + ((long long)ad * a.rank + (ranks > 0 ? r0 : 0)) * row_bytes,
+                  ranks > 0 ? (uint32_t)(ranks * row_bytes) : 0u);
+    float sum[RT * R] = {};
+    for (int off = threadIdx.x * 16; off < row_bytes; off += THREADS * 16) {
+      u32x4_t xv[RT], av[R];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        xv[i] = load16(rx, guard_offset(of[i] == ad, i * (int)a.x_row + off));
+#pragma unroll
+      for (int r = 0; r < R; ++r) av[r] = load16(ra, r * row_bytes + off);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float w[E];
+        unpack<DT>(av[r], w);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          float x[E];
+          unpack<DT>(xv[i], x);
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum[i * R + r] = fmaf(x[e], w[e], sum[i * R + r]);
+        }
+      }
+    }
+    const float v = wave_sum<RT * R>(sum);
+    constexpr int LANES = 64 / (RT * R);
+    if (turn > 0) lds_barrier();   // the last sums are read
+    if (lane % LANES == 0) red[wave * RT * R + lane / LANES] = v;
+    lds_barrier();
+    if (threadIdx.x < RT * R) {
+      const int i = threadIdx.x;
+      if (found[i / R] == ad)
+        reinterpret_cast<float*>(a.low)[(long long)(t0 + i / R) * a.low_width + r0 + i % R] =
+            (red[i] + red[RT * R + i] + red[2 * RT * R + i] + red[3 * RT * R + i]) * scale;
+    }
+  }
+}
+
+// Tile of the fp32 sums of run `split`, 4 consecutive outputs of a token.
+__device__ __forceinline__ void store_part(const LoraArgs& a, int split, int t, int n, float4_t v) {
+  const long long n_pad = (a.N + 63) / 64 * 64;
+  if (t < a.T && n < n_pad)
+    *reinterpret_cast<float4_t*>(a.part + ((long long)split * a.T + t) * n_pad + n) = v;
+}
+
+// BM tokens x BN outputs, WM x WN waves, NS - 1 stages on their way.  Runs: the
+// first `low_jobs` workgroups form low-rank values, the others the sums of a
+// run of the sum's axis.
+template <int DT, int BM, int BN, int WM, int WN, int NS, bool Runs>
 __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, int tiles_m,
-                                                            int tiles_n) {
+                                                            int tiles_n, int low_jobs) {
   constexpr int EB = Elem<DT>::bytes;
   constexpr int THREADS = 64 * WM * WN;
   constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks of a wave
@@ -269,11 +419,22 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
   const int l32 = lane & 31, half = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
 
+  int block = blockIdx.x, split = 0;
+  if constexpr (Runs) {
+    if (block < low_jobs) {
+      const int groups = (a.T + kLowGroup - 1) / kLowGroup;
+      low_rows<DT, kLowGroup>(a, block % groups * kLowGroup, block / groups * 16, lds);
+      return;
+    }
+    block -= low_jobs;
+    split = block / (tiles_m * tiles_n);
+    block -= split * tiles_m * tiles_n;
+  }
   // workgroups of one XCD follow one another over a band of 4 tiles of
   // outputs, so that its L2 holds the x and W tiles they share
   const int n_tiles = tiles_m * tiles_n;
-  const int per = n_tiles >> 3, more = n_tiles & 7, xcd = blockIdx.x & 7;
-  const int id = xcd * per + (xcd < more ? xcd : more) + (blockIdx.x >> 3);
+  const int per = n_tiles >> 3, more = n_tiles & 7, xcd = block & 7;
+  const int id = xcd * per + (xcd < more ? xcd : more) + (block >> 3);
   constexpr int BAND = 4;
   const int band = id / (BAND * tiles_m), in_band = id - band * BAND * tiles_m;
   const int width_n = tiles_n - band * BAND < BAND ? tiles_n - band * BAND : BAND;
@@ -287,24 +448,26 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
     for (int j = 0; j < MB; ++j) acc[i][j] = float16_t{};
 
   // stages
-  const int row_bytes = a.K * EB;
+  const int row = a.K * EB;   // bytes of a row of W
+  const int begin = Runs ? split * a.run : 0;
+  const int row_bytes = Runs && begin + a.run < row ? a.run : row - begin;   // of this run
   const int stages = (row_bytes + 127) / 128;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)m0 * a.x_row, 0x7ffffff0u);
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row_bytes, 0x7ffffff0u);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)m0 * a.x_row + begin, 0x7ffffff0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row + begin, 0x7ffffff0u);
   constexpr int CX = BM * 8 / THREADS, CW = BN * 8 / THREADS;   // copies a thread
   int x_off[CX], w_off[CW];   // of stage 0; past the end where the row is
   int x_chunk[CX], w_chunk[CW];
 #pragma unroll
   for (int c = 0; c < CX; ++c) {
-    const int unit = c * THREADS + threadIdx.x, row = unit >> 3;
-    x_chunk[c] = chunk_at(row, unit & 7) * 16;
-    x_off[c] = m0 + row < a.T ? row * (int)a.x_row + x_chunk[c] : kOobOffset;
+    const int unit = c * THREADS + threadIdx.x, r = unit >> 3;
+    x_chunk[c] = chunk_at(r, unit & 7) * 16;
+    x_off[c] = m0 + r < a.T ? r * (int)a.x_row + x_chunk[c] : kOobOffset;
   }
 #pragma unroll
   for (int c = 0; c < CW; ++c) {
-    const int unit = c * THREADS + threadIdx.x, row = unit >> 3;
-    w_chunk[c] = chunk_at(row, unit & 7) * 16;
-    w_off[c] = n0 + row < a.N ? row * row_bytes + w_chunk[c] : kOobOffset;
+    const int unit = c * THREADS + threadIdx.x, r = unit >> 3;
+    w_chunk[c] = chunk_at(r, unit & 7) * 16;
+    w_off[c] = n0 + r < a.N ? r * row + w_chunk[c] : kOobOffset;
   }
 #define LIBCONV_COPY_STAGE(st, at)                                                              \
   {                                                                                             \
@@ -321,36 +484,53 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
 #pragma unroll
   for (int st = 0; st < NS - 1; ++st) LIBCONV_COPY_STAGE(st, st)
 
-  if (a.n_adapters > 0) {
+  if (!Runs && a.n_adapters > 0) {
     constexpr int LB = DT == DT_F32 ? 4 : 2;   // bytes of a low-rank value
     const __amdgpu_buffer_rsrc_t rl =
         make_rsrc(a.low + (long long)m0 * a.low_width * 4, 0x7ffffff0u);
+    constexpr int U = MB * NB <= 4 ? 4 : 2;   // steps whose reads are issued together
+    int mine[MB];
+    uint64_t left[MB];
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
-      const int t = (wm * MB + j) * 32 + l32;
-      const int mine = m0 + t < a.T ? a.adapter_of[m0 + t] : -1;
-      uint64_t left = __ballot(mine >= 0);
-      while (left) {
-        const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-        left &= ~__ballot(mine == ad);
-        const __amdgpu_buffer_rsrc_t rb =
-            make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
-        const int steps = (a.rank * LB + 31) / 32;
-        for (int s = 0; s < steps; s += 2) {   // two steps' reads together
-          u32x4_t hi[2], lo[2], bf[2][NB];
+      const int t = m0 + (wm * MB + j) * 32 + l32;
+      mine[j] = t < a.T ? a.adapter_of[t] : -1;
+    }
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int off = (s + u) * 32 + half * 16;
-            load_low<DT>(a, rl, t, mine == ad && s + u < steps, off, &hi[u], &lo[u]);
+    for (int j = 0; j < MB; ++j) left[j] = __ballot(mine[j] >= 0);
+    const int steps = (a.rank * LB + 31) / 32;
+    for (;;) {   // the adapters of the wave's tokens
+      int ad = -1;
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+        if (ad < 0 && left[j]) ad = __builtin_amdgcn_readlane(mine[j], __builtin_ctzll(left[j]));
+      if (ad < 0) break;
+#pragma unroll
+      for (int j = 0; j < MB; ++j) left[j] &= ~__ballot(mine[j] == ad);
+      const __amdgpu_buffer_rsrc_t rb =
+          make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
+      for (int s = 0; s < steps; s += U) {
+        u32x4_t hi[U][MB], lo[U][MB], bf[U][NB];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int off = (s + u) * 32 + half * 16;
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+            load_low<DT>(a, rl, (wm * MB + j) * 32 + l32, mine[j] == ad && s + u < steps, off,
+                         &hi[u][j], &lo[u][j]);
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            bf[u][i] = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32, off / LB);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (s + u < steps)
 #pragma unroll
             for (int i = 0; i < NB; ++i)
-              bf[u][i] = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32, off / LB);
-          }
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < NB; ++i) low_step<DT, true>(bf[u][i], hi[u], lo[u], acc[i][j]);
-        }
+              for (int j = 0; j < MB; ++j)
+                low_step<DT, true>(bf[u][i], hi[u][j], lo[u][j], acc[i][j]);
       }
     }
   }
@@ -369,13 +549,13 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
       u32x4_t wf[NB], xf[MB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        const int row = (wn * NB + i) * 32 + l32;
-        wf[i] = *reinterpret_cast<const u32x4_t*>(ws + row * 128 + chunk_at(row, 2 * k + half) * 16);
+        const int r = (wn * NB + i) * 32 + l32;
+        wf[i] = *reinterpret_cast<const u32x4_t*>(ws + r * 128 + chunk_at(r, 2 * k + half) * 16);
       }
 #pragma unroll
       for (int j = 0; j < MB; ++j) {
-        const int row = (wm * MB + j) * 32 + l32;
-        xf[j] = *reinterpret_cast<const u32x4_t*>(xs + row * 128 + chunk_at(row, 2 * k + half) * 16);
+        const int r = (wm * MB + j) * 32 + l32;
+        xf[j] = *reinterpret_cast<const u32x4_t*>(xs + r * 128 + chunk_at(r, 2 * k + half) * 16);
       }
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -396,9 +576,85 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
         const int n = n0 + (wn * NB + i) * 32 + 8 * r + 4 * half;
         const float v[4] = {acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
                             acc[i][j][4 * r + 3]};
-        if (n < a.N) store4<DT>(a, t, n, v);
+        if constexpr (Runs)
+          store_part(a, split, t, n, float4_t{v[0], v[1], v[2], v[3]});
+        else if (n < a.N)
+          store4<DT>(a, t, n, v);
       }
   }
+}
+
+// 32 tokens x 32 outputs, the sums' axis split over the four waves: for fp32,
+// whose matrix instructions are slow enough to leave most compute units
+// without a larger tile idle.
+template <int DT, bool Runs>
+__global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low_jobs) {
+  constexpr int EB = Elem<DT>::bytes, NS = 4;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * kStage32];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, half = lane >> 5;
+  const int tiles_n = (a.N + 31) / 32;
+  int block = blockIdx.x, split = 0;
+  if constexpr (Runs) {
+    if (block < low_jobs) {
+      const int groups = (a.T + kLowGroup - 1) / kLowGroup;
+      low_rows<DT, kLowGroup>(a, block % groups * kLowGroup, block / groups * 16, lds);
+      return;
+    }
+    block -= low_jobs;
+    const int tiles = tiles_n * ((a.T + 31) / 32);
+    split = block / tiles;
+    block -= split * tiles;
+  }
+  const int m0 = block / tiles_n * 32, n0 = block % tiles_n * 32;
+  const int row = a.K * EB;   // bytes of a row of W
+  const int begin = Runs ? split * a.run : 0;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)m0 * a.x_row + begin, 0x7ffffff0u);
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row + begin, 0x7ffffff0u);
+  int off[4];
+  offsets32(off, a.T - m0, (int)a.x_row);
+  offsets32(off + 2, a.N - n0, row);
+  float16_t acc = {};
+  product32<DT, NS>(rx, rw, off, Runs && begin + a.run < row ? a.run : row - begin, lds, acc);
+  if (!Runs && a.n_adapters > 0) {
+    constexpr int LB = DT == DT_F32 ? 4 : 2;
+    const __amdgpu_buffer_rsrc_t rl =
+        make_rsrc(a.low + (long long)m0 * a.low_width * 4, 0x7ffffff0u);
+    const int mine = m0 + l32 < a.T ? a.adapter_of[m0 + l32] : -1;
+    const int steps = (a.rank * LB + 31) / 32;
+    uint64_t left = __ballot(mine >= 0);
+    while (left) {
+      const int ad = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+      left &= ~__ballot(mine == ad);
+      const __amdgpu_buffer_rsrc_t rb =
+          make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
+      for (int s = wave; s < steps; s += 4) {   // the waves take steps in turn
+        const int at = s * 32 + half * 16;
+        u32x4_t hi, lo;
+        load_low<DT>(a, rl, l32, mine == ad, at, &hi, &lo);
+        low_step<DT, true>(load_b<DT>(a, rb, n0 + l32, at / LB), hi, lo, acc);
+      }
+    }
+  }
+  float(*red)[32][36] = reinterpret_cast<float(*)[32][36]>(lds);
+  lds_barrier();
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    *reinterpret_cast<float4_t*>(&red[wave][l32][8 * r + 4 * half]) =
+        float4_t{acc[4 * r], acc[4 * r + 1], acc[4 * r + 2], acc[4 * r + 3]};
+  lds_barrier();
+  const int t = threadIdx.x >> 3, n = (threadIdx.x & 7) * 4;
+  float v[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float4_t p = *reinterpret_cast<const float4_t*>(&red[w][t][n]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += p[j];
+  }
+  if constexpr (Runs)
+    store_part(a, split, m0 + t, n0 + n, float4_t{v[0], v[1], v[2], v[3]});
+  else if (m0 + t < a.T && n0 + n < a.N)
+    store4<DT>(a, m0 + t, n0 + n, v);
 }
 
 // Up to 16 * RB rows without adapters: 16 outputs a workgroup, the sum's axis
@@ -484,67 +740,6 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(const LoraArgs a
   }
 }
 
-// Up to 64 rows with adapters, in two launches: the shared product in runs of
-// the sum's axis beside the low-rank values, then the sum of all.
-
-// Low-rank values r0 .. r0 + 15 of row t (fp32) and the row's adapter: 16 bytes
-// of x and of each row of A a lane, dense reads that are all on their way at
-// once.
-template <int DT>
-__device__ __forceinline__ void low_row(const LoraArgs& a, int t, int r0, unsigned char* lds) {
-  constexpr int E = 16 / Elem<DT>::bytes, R = 16, THREADS = 256;
-  int* found = reinterpret_cast<int*>(lds);
-  float* red = reinterpret_cast<float*>(lds + 16);   // [4][R]
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int row_bytes = a.K * Elem<DT>::bytes;
-  if (threadIdx.x == 0) *found = -1;
-  lds_barrier();
-  for (int r = threadIdx.x; r < a.n_requests; r += THREADS) {
-    const int ad = a.adapters[r], s0 = a.starts[r], s1 = a.starts[r + 1];
-    if (s0 <= t && t < s1 && ad >= 0 && ad < a.n_adapters) *found = ad;
-  }
-  lds_barrier();
-  const int ad = __builtin_amdgcn_readfirstlane(*found);
-  if (r0 == 0 && threadIdx.x == 0) a.adapter_of[t] = ad;
-  if (ad < 0) return;
-  const float scale = a.scales[ad];
-  const int ranks = a.rank - r0 < R ? a.rank - r0 : R;   // <= 0: padding, zeros
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + t * a.x_row, row_bytes);
-  const __amdgpu_buffer_rsrc_t ra =
-      make_rsrc(a.a + ((long long)ad * a.rank + (ranks > 0 ? r0 : 0)) * row_bytes,
-                ranks > 0 ? (uint32_t)(ranks * row_bytes) : 0u);
-  float sum[R] = {};
-  for (int off = threadIdx.x * 16; off < row_bytes; off += THREADS * 16) {
-    const u32x4_t xv = load16(rx, off);
-    u32x4_t av[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) av[r] = load16(ra, r * row_bytes + off);
-    __builtin_amdgcn_sched_barrier(0);
-    float x[E];
-    unpack<DT>(xv, x);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float w[E];
-      unpack<DT>(av[r], w);
-#pragma unroll
-      for (int e = 0; e < E; ++e) sum[r] = fmaf(x[e], w[e], sum[r]);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) sum[r] += __shfl_xor(sum[r], m);
-  if (lane == 0)
-#pragma unroll
-    for (int r = 0; r < R; ++r) red[wave * R + r] = sum[r];
-  lds_barrier();
-  if (threadIdx.x < R) {
-    const int r = threadIdx.x;
-    const float v = red[r] + red[R + r] + red[2 * R + r] + red[3 * R + r];
-    reinterpret_cast<float*>(a.low)[(long long)t * a.low_width + r0 + r] = v * scale;
-  }
-}
-
 // Four waves take 16 outputs each and a run of the sum's axis: x arrives in
 // LDS, W straight in registers (each of its values has one reader), all of a
 // run on its way at once.  The first `low_jobs` workgroups take the low-rank
@@ -555,7 +750,7 @@ __global__ __launch_bounds__(256, 2) void run_kernel(const LoraArgs a, int low_j
   constexpr int EB = Elem<DT>::bytes, ROWS = 16 * RB, STEPS = kRun / 64;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[ROWS * kRun];
   if ((int)blockIdx.x < low_jobs) {
-    low_row<DT>(a, (int)blockIdx.x % a.T, (int)blockIdx.x / a.T * 16, lds);
+    low_rows<DT, 1>(a, (int)blockIdx.x % a.T, (int)blockIdx.x / a.T * 16, lds);
     return;
   }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -601,110 +796,172 @@ __global__ __launch_bounds__(256, 2) void run_kernel(const LoraArgs a, int low_j
       }
     }
   }
-  const long long n_pad = (a.N + 63) / 64 * 64;
 #pragma unroll
-  for (int j = 0; j < RB; ++j) {
-    const int t = j * 16 + l16;
-    if (t < a.T)
-      *reinterpret_cast<float4_t*>(a.part + ((long long)split * a.T + t) * n_pad + n0 +
-                                   quarter * 4) = acc[j];
-  }
+  for (int j = 0; j < RB; ++j) store_part(a, split, j * 16 + l16, n0 + quarter * 4, acc[j]);
 }
 
-// y of row blockIdx.y: the runs in their order, the bias, the low-rank term.
-template <int DT>
+// y of TT rows from TT blockIdx.y on: the runs in their order, the bias, the
+// low-rank term.  A thread an output; rows of one adapter share their reads of
+// B.
+template <int DT, int TT>
 __global__ __launch_bounds__(256) void sum_kernel(const LoraArgs a) {
   constexpr int EB = Elem<DT>::bytes, E = 16 / EB;
-  const int n = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  const int n = blockIdx.x * 256 + threadIdx.x, t0 = blockIdx.y * TT;
   if (n >= a.N) return;
-  const int ad = __builtin_amdgcn_readfirstlane(a.adapter_of[t]);
   const long long n_pad = (a.N + 63) / 64 * 64;
-  const float* part = a.part + t * n_pad + n;
-  float v = 0.0f;
-  for (int s = 0; s < a.splits; s += 8) {
-    float p[8];
+  const float* part = a.part + t0 * n_pad + n;
+  const int rows = a.T - t0 < TT ? a.T - t0 : TT;
+  int of[TT];
+  float v[TT];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
-      p[u] = s + u < a.splits ? part[(long long)(s + u) * a.T * n_pad] : 0.0f;
+  for (int i = 0; i < TT; ++i) {
+    of[i] = i < rows ? __builtin_amdgcn_readfirstlane(a.adapter_of[t0 + i]) : -1;
+    v[i] = 0.0f;
+  }
+  constexpr int U = 8 / TT;
+  for (int s = 0; s < a.splits; s += U) {
+    float p[U][TT];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v += p[u];
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+        p[u][i] = s + u < a.splits && i < rows ? part[((long long)(s + u) * a.T + i) * n_pad] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < TT; ++i) v[i] += p[u][i];
   }
   if (a.bias) {
-    if constexpr (DT == DT_F32) v += static_cast<const float*>(a.bias)[n];
-    else v += Elem<DT>::bits_to_f32(static_cast<const uint16_t*>(a.bias)[n]);
+    float bias;
+    if constexpr (DT == DT_F32) bias = static_cast<const float*>(a.bias)[n];
+    else bias = Elem<DT>::bits_to_f32(static_cast<const uint16_t*>(a.bias)[n]);
+#pragma unroll
+    for (int i = 0; i < TT; ++i) v[i] += bias;
   }
-  if (ad >= 0) {
+  const float* low = reinterpret_cast<const float*>(a.low) + (long long)t0 * a.low_width;
+#pragma unroll
+  for (int turn = 0; turn < TT; ++turn) {
+    const int ad = of[turn];
+    bool first = ad >= 0;   // of the rows with this adapter
+#pragma unroll
+    for (int i = 0; i < turn; ++i) first = first && of[i] != ad;
+    if (!first) continue;
     const char* b = a.b + ((long long)ad * a.N + n) * a.rank * EB;
-    const float* low = reinterpret_cast<const float*>(a.low) + (long long)t * a.low_width;
     if (a.rank % E == 0) {
       for (int r = 0; r < a.rank; r += E) {
         float w[E];
         unpack<DT>(*reinterpret_cast<const u32x4_t*>(b + r * EB), w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v = fmaf(low[r + e], w[e], v);
+        for (int i = turn; i < TT; ++i)
+          if (of[i] == ad)
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[i] = fmaf(low[i * a.low_width + r + e], w[e], v[i]);
       }
     } else {
       for (int r = 0; r < a.rank; ++r) {
         float w;
         if constexpr (DT == DT_F32) w = reinterpret_cast<const float*>(b)[r];
         else w = Elem<DT>::bits_to_f32(reinterpret_cast<const uint16_t*>(b)[r]);
-        v = fmaf(low[r], w, v);
+#pragma unroll
+        for (int i = turn; i < TT; ++i)
+          if (of[i] == ad) v[i] = fmaf(low[i * a.low_width + r], w, v[i]);
       }
     }
   }
-  char* y = a.y + t * a.y_row + (long long)n * EB;
-  if constexpr (DT == DT_F32) *reinterpret_cast<float*>(y) = v;
-  else *reinterpret_cast<uint16_t*>(y) = Elem<DT>::from_f32(v);
+#pragma unroll
+  for (int i = 0; i < TT; ++i) {
+    if (i >= rows) continue;
+    char* y = a.y + (t0 + i) * a.y_row + (long long)n * EB;
+    if constexpr (DT == DT_F32) *reinterpret_cast<float*>(y) = v[i];
+    else *reinterpret_cast<uint16_t*>(y) = Elem<DT>::from_f32(v[i]);
+  }
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int NS, bool Runs>
+void launch_tile(const LoraArgs& a, int low_jobs, hipStream_t stream) {
+  const int tm = (a.T + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  hipLaunchKernelGGL((tile_kernel<DT, BM, BN, WM, WN, NS, Runs>),
+                     dim3((unsigned)(low_jobs + tm * tn * (Runs ? a.splits : 1))),
+                     dim3(64 * WM * WN), 0, stream, a, tm, tn, low_jobs);
 }
 
 template <int DT>
 void launch_runs(const LoraArgs& a, hipStream_t stream) {
-  const int low_jobs = a.T * ((a.rank + 15) / 16);
-  const dim3 grid((unsigned)(low_jobs + (a.N + 63) / 64 * a.splits)), threads(256);
-  if (a.T <= 16)
-    hipLaunchKernelGGL((run_kernel<DT, 1>), grid, threads, 0, stream, a, low_jobs);
-  else if (a.T <= 32)
-    hipLaunchKernelGGL((run_kernel<DT, 2>), grid, threads, 0, stream, a, low_jobs);
-  else
-    hipLaunchKernelGGL((run_kernel<DT, 4>), grid, threads, 0, stream, a, low_jobs);
-  hipLaunchKernelGGL((sum_kernel<DT>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.T), threads,
-                     0, stream, a);
-}
-
-template <int DT, int BM, int BN, int WM, int WN, int NS>
-void launch_tile(const LoraArgs& a, hipStream_t stream) {
-  const int tm = (a.T + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
-  hipLaunchKernelGGL((tile_kernel<DT, BM, BN, WM, WN, NS>), dim3((unsigned)(tm * tn)),
-                     dim3(64 * WM * WN), 0, stream, a, tm, tn);
+  const int parts = (a.rank + 15) / 16;
+  const dim3 threads(256);
+  if (a.T <= kFewRows) {
+    const int low_jobs = a.T * parts;
+    const dim3 grid((unsigned)(low_jobs + (a.N + 63) / 64 * a.splits));
+    if (a.T <= 16)
+      hipLaunchKernelGGL((run_kernel<DT, 1>), grid, threads, 0, stream, a, low_jobs);
+    else if (a.T <= 32)
+      hipLaunchKernelGGL((run_kernel<DT, 2>), grid, threads, 0, stream, a, low_jobs);
+    else
+      hipLaunchKernelGGL((run_kernel<DT, 4>), grid, threads, 0, stream, a, low_jobs);
+    hipLaunchKernelGGL((sum_kernel<DT, 1>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.T),
+                       threads, 0, stream, a);
+    return;
+  }
+  const int low_jobs = (a.T + kLowGroup - 1) / kLowGroup * parts;
+  if (a.tile == 128) {
+    launch_tile<DT, 128, 128, 2, 2, 2, true>(a, low_jobs, stream);
+  } else if (a.tile == 64) {
+    launch_tile<DT, 64, 64, 2, 2, 4, true>(a, low_jobs, stream);
+  } else if constexpr (DT == DT_F32) {
+    const int tiles = (a.T + 31) / 32 * ((a.N + 31) / 32);
+    hipLaunchKernelGGL((small_kernel<DT, true>), dim3((unsigned)(low_jobs + tiles * a.splits)),
+                       threads, 0, stream, a, low_jobs);
+  }
+  hipLaunchKernelGGL((sum_kernel<DT, 4>),
+                     dim3((unsigned)((a.N + 255) / 256), (unsigned)((a.T + 3) / 4)), threads, 0,
+                     stream, a);
 }
 
 // Time of a launch in units of one 256 x 256 tile: rounds of workgroups over
 // the compute units, each as long as its workgroups together on one unit.
-double tile_cost(const LoraArgs& a, int cus, int bm, int bn, int per_cu, double speed) {
-  const double tiles = (double)((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+double tile_cost(const LoraArgs& a, int cus, int splits, int b, int per_cu, double speed) {
+  const double tiles = (double)((a.T + b - 1) / b) * ((a.N + b - 1) / b) * splits;
   const double rounds = (double)(long long)((tiles + (double)cus * per_cu - 1) / (cus * per_cu));
   const double share = tiles < (double)cus * per_cu ? (tiles > cus ? tiles / cus : 1.0) : per_cu;
-  return rounds * share * bm * bn / speed;
+  return rounds * share * b * b / splits / speed;
+}
+
+// Side of the tiles the product is formed in.  fp32 is bound by the matrix
+// instructions: what the fullest compute unit has to do.
+int pick_tile(const LoraArgs& a, int eb, int cus, int splits) {
+  if (eb == 4) {
+    auto work = [&](long long b) {
+      const long long tiles = ((a.T + b - 1) / b) * ((a.N + b - 1) / b) * splits;
+      return (double)((tiles + cus - 1) / cus * b * b);
+    };
+    const double w128 = work(128) * 0.85, w64 = work(64) * 0.92, w32 = work(32);
+    return w128 <= w64 && w128 <= w32 ? 128 : w64 <= w32 ? 64 : 32;
+  }
+  const double c256 = tile_cost(a, cus, splits, 256, 1, 1.0);
+  const double c128 = tile_cost(a, cus, splits, 128, 2, 0.75);
+  const double c64 = tile_cost(a, cus, splits, 64, 4, 0.4);
+  return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
 }
 
 template <int DT>
 void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
-  if (a.n_adapters > 0 && a.T <= kFewRows) {
+  if (a.splits > 0) {
     launch_runs<DT>(a, stream);
     return;
   }
   if (a.n_adapters > 0) {
-    // with few row tiles, 16 waves to one and the tile's adapters dealt out
-    const int tiles = (a.T + kLowRows - 1) / kLowRows;
-    int shares = cus / tiles;
+    // with few row tiles, the adapters of a tile are dealt out
+    const int tiles = (a.T + kLowRows - 1) / kLowRows, parts = a.low_width / 32;
+    int shares = 2 * cus / (tiles * parts);
     const int most = a.n_adapters < kLowRows ? a.n_adapters : kLowRows;
     if (shares > most) shares = most;
-    const dim3 grid((unsigned)tiles, (unsigned)(shares < 1 ? 1 : shares),
-                    (unsigned)(a.low_width / 32));
-    if (tiles < cus)
-      hipLaunchKernelGGL((low_kernel<DT, 16>), grid, dim3(64 * 16), 0, stream, a);
+    if (shares < 1) shares = 1;
+    const dim3 grid((unsigned)tiles, (unsigned)shares, (unsigned)parts);
+    // alone on its compute unit, a workgroup has twice the stages on their way
+    if (tiles * shares * parts > cus)
+      hipLaunchKernelGGL((low_kernel<DT, 4>), grid, dim3(256), 0, stream, a);
     else
-      hipLaunchKernelGGL((low_kernel<DT, 8>), grid, dim3(64 * 8), 0, stream, a);
+      hipLaunchKernelGGL((low_kernel<DT, 8>), grid, dim3(256), 0, stream, a);
   }
   if (a.T <= kFewRows) {
     const dim3 grid((unsigned)((a.N + 15) / 16)), threads(64 * kFewWaves);
@@ -713,33 +970,57 @@ void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
     else hipLaunchKernelGGL((few_kernel<DT, 4>), grid, threads, 0, stream, a);
     return;
   }
-  const double c256 = tile_cost(a, cus, 256, 256, 1, 1.0);
-  const double c128 = tile_cost(a, cus, 128, 128, 2, 0.75);
-  const double c64 = tile_cost(a, cus, 64, 64, 4, 0.4);
-  if (c256 <= c128 && c256 <= c64) launch_tile<DT, 256, 256, 4, 2, 2>(a, stream);
-  else if (c128 <= c64) launch_tile<DT, 128, 128, 2, 2, 2>(a, stream);
-  else launch_tile<DT, 64, 64, 2, 2, 4>(a, stream);
+  const int tile = pick_tile(a, DT == DT_F32 ? 4 : 2, cus, 1);
+  if constexpr (DT == DT_F32) {
+    if (tile == 128) launch_tile<DT, 128, 128, 2, 2, 2, false>(a, 0, stream);
+    else if (tile == 64) launch_tile<DT, 64, 64, 2, 2, 4, false>(a, 0, stream);
+    else
+      hipLaunchKernelGGL((small_kernel<DT, false>),
+                         dim3((unsigned)((a.T + 31) / 32 * ((a.N + 31) / 32))), dim3(256), 0,
+                         stream, a, 0);
+  } else {
+    if (tile == 256) launch_tile<DT, 256, 256, 4, 2, 2, false>(a, 0, stream);
+    else if (tile == 128) launch_tile<DT, 128, 128, 2, 2, 2, false>(a, 0, stream);
+    else launch_tile<DT, 64, 64, 2, 2, 4, false>(a, 0, stream);
+  }
 }
 
 }  // namespace
 
 long long lora_plan(LoraArgs* a, int dtype, int cus) {
-  a->low_width = a->splits = a->run = 0;
+  a->low_width = a->splits = a->run = a->tile = 0;
   if (a->n_adapters == 0 || a->T == 0) return 0;
   a->low_width = (a->rank + 31) / 32 * 32;
   const long long low = (long long)a->T * (a->low_width + 1) * 4;
   a->part_at = (low + 255) / 256 * 256;
-  if (a->T > kFewRows) return low;
-  // runs of the sum's axis: two workgroups a compute unit if they have 256
-  // bytes or more
-  const int row_bytes = a->K * (dtype == LIBCONV_F32 ? 4 : 2);
-  const int tiles = (a->N + 63) / 64;
-  int runs = 2 * cus / tiles;
-  if (runs > row_bytes / 256) runs = row_bytes / 256;
-  if (runs < (row_bytes + kRun - 1) / kRun) runs = (row_bytes + kRun - 1) / kRun;
-  a->run = ((row_bytes + runs - 1) / runs + 127) / 128 * 128;
-  a->splits = (row_bytes + a->run - 1) / a->run;
-  return a->part_at + (long long)a->splits * a->T * tiles * 64 * 4;
+  const int eb = dtype == LIBCONV_F32 ? 4 : 2;
+  const long long row_bytes = (long long)a->K * eb, n_pad = (a->N + 63) / 64 * 64;
+  long long runs;
+  if (a->T <= kFewRows) {
+    // two workgroups a compute unit if they have 256 bytes or more
+    runs = 2 * cus / (n_pad / 64);
+    if (runs > row_bytes / 256) runs = row_bytes / 256;
+    if (runs < (row_bytes + kRun - 1) / kRun) runs = (row_bytes + kRun - 1) / kRun;
+  } else {
+    // the low-rank values row by row read A again for each group of rows, the
+    // sum reads and writes y again in fp32: for few rows only.  Measured
+    // against low_kernel and tile_kernel one after the other, K and N 4096,
+    // rank 16: 128 rows 20 us against 41, 512 rows 42 against 49, 1024 rows 60
+    // against 68; K and N 640: 1000 rows 14.5 against 13.6
+    const double again = (double)((a->T + kLowGroup - 1) / kLowGroup) *
+                         ((a->rank + 15) / 16 * 16) * row_bytes;
+    if (a->T > 1024 || again > 128e6) return low;
+    a->tile = pick_tile(*a, eb, cus, 1);
+    if (a->tile == 256) a->tile = 128;
+    const long long tiles = ((a->T + a->tile - 1) / a->tile) * ((a->N + a->tile - 1) / a->tile);
+    runs = cus / tiles;
+    if (runs > row_bytes / 1024) runs = row_bytes / 1024;
+    if (runs > 8) runs = 8;
+    if (runs < 1) runs = 1;
+  }
+  a->run = (int)(((row_bytes + runs - 1) / runs + 255) / 256 * 256);
+  a->splits = (int)((row_bytes + a->run - 1) / a->run);
+  return a->part_at + a->splits * a->T * n_pad * 4;
 }
 
 libconv_status lora_launch(LoraArgs a, int dtype, int cus, hipStream_t stream) {
