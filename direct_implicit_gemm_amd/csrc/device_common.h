@@ -135,6 +135,11 @@ template <> struct Elem<DT_BF16> {
   }
 };
 
+// 16 bytes of a call's output, streamed out (see kOutPolicy).
+__device__ __forceinline__ void store_out16(char* p, const u32x4_t& v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+}
+
 // The 16 / bytes elements of a 16-byte vector, and back.
 template <int DT>
 __device__ __forceinline__ void unpack(const u32x4_t& v, float* f) {

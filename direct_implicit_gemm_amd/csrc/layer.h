@@ -24,6 +24,7 @@ struct RopeArgs {
   int interleaved, out_rows;
   float eps;
   int steps, chunks;        // filled by the launch
+  int step_k, step_v;       // first steps of the keys and of the values
 };
 libconv_status rope_launch(RopeArgs a, int dtype, hipStream_t stream);
 
