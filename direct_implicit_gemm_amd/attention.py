@@ -21,13 +21,14 @@ _STRIDES16 = ctypes.c_longlong * 16
 
 # The calls below take as long on the host as small ones take on the GPU, so
 # what does not change from call to call is looked up once, by _load().
-_lib = _codes = _raw_stream = _current_device = None
+_lib = _codes = _int32 = _float32 = _raw_stream = _current_device = None
 
 
 def _load():
     import torch
     import direct_implicit_gemm_amd as L
-    global _lib, _codes, _raw_stream, _current_device
+    global _lib, _codes, _int32, _float32, _raw_stream, _current_device
+    _int32, _float32 = torch.int32, torch.float32
     _codes = {torch.float32: L.F32, torch.float16: L.F16, torch.bfloat16: L.BF16}
     # as torch.cuda.current_stream() and current_device() have them, without
     # the objects (a call that gets this far has a device tensor)
@@ -56,8 +57,7 @@ def _bad(t, device, dtype, strides, shape):
 
 
 def _bad_ints(t, device, shape):
-    import torch
-    return (t.get_device() != device or t.dtype is not torch.int32 or t.shape != shape or
+    return (t.get_device() != device or t.dtype is not _int32 or t.shape != shape or
             not t.is_contiguous())
 
 
@@ -149,19 +149,29 @@ def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: floa
         if _bad_ints(slots, dev, (T,)):
             _refuse(what, "slots must be a contiguous int32 device tensor [T]")
         slot_ptr = slots.data_ptr()
+    qo, ko, vt, vo = (Hq * D, D), (Hk * D, D), (0, 0), (0, 0)
     if q_out is None:
         q_out = q.new_empty((T, Hq, D))
+    else:
+        qo = q_out.stride()
+        if _bad(q_out, dev, dtype, qo, (T, Hq, D)):
+            _refuse(what, "bad output tensor; " + _OPERANDS)
     if k_out is None:
-        k_out = k.new_empty((T, Hk, D))
-    qo, ko, vt, vo = q_out.stride(), k_out.stride(), (0, 0, 0), (0, 0, 0)
-    if _bad(q_out, dev, dtype, qo, (T, Hq, D)) or _bad(k_out, dev, dtype, ko, (rows, Hk, D)):
-        _refuse(what, "bad output tensor; " + _OPERANDS)
+        k_out = q.new_empty((T, Hk, D))
+    else:
+        ko = k_out.stride()
+        if _bad(k_out, dev, dtype, ko, (rows, Hk, D)):
+            _refuse(what, "bad output tensor; " + _OPERANDS)
     if v is not None:
+        vt, vo = v.stride(), (Hk * D, D)
+        if _bad(v, dev, dtype, vt, (T, Hk, D)):
+            _refuse(what, "v [T, Hk, D]; " + _OPERANDS)
         if v_out is None:
-            v_out = v.new_empty((T, Hk, D))
-        vt, vo = v.stride(), v_out.stride()
-        if _bad(v, dev, dtype, vt, (T, Hk, D)) or _bad(v_out, dev, dtype, vo, (rows, Hk, D)):
-            _refuse(what, "v [T, Hk, D] and v_out as k_out; " + _OPERANDS)
+            v_out = q.new_empty((T, Hk, D))
+        else:
+            vo = v_out.stride()
+            if _bad(v_out, dev, dtype, vo, (rows, Hk, D)):
+                _refuse(what, "v_out as k_out; " + _OPERANDS)
         v_ptr, vo_ptr = v.data_ptr(), v_out.data_ptr()
     elif v_out is not None:
         _refuse(what, "v_out without v")
@@ -218,14 +228,14 @@ def prefix_attention(q, k_prefix, v_prefix, k, v, lengths, scale: Optional[float
     if _bad_ints(lengths, dev, (B,)):
         _refuse(what, "lengths must be a contiguous int32 device tensor [B]")
     if out is None:
-        out = q.new_empty(qs)
-    ot = out.stride()
-    if _bad(out, dev, dtype, ot, qs):
-        _refuse(what, "bad output tensor; " + _OPERANDS)
+        out, ot = q.new_empty(qs), (Sq * Hq * D, Hq * D, D)
+    else:
+        ot = out.stride()
+        if _bad(out, dev, dtype, ot, qs):
+            _refuse(what, "bad output tensor; " + _OPERANDS)
     lse = lse_ptr = buffer = None
     if return_lse:
-        import torch
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, Hq, Sq), dtype=_float32)
         lse_ptr = lse.data_ptr()
     if B > 0 and Sq > 0:
         dt = _codes[dtype]
@@ -277,8 +287,8 @@ def lora_linear(x, w, bias, a, b, scales, row_starts, adapters, out=None, stream
         if _bad(a, dev, dtype, a.stride(), (n, rank, K)) or not a.is_contiguous() or \
                 _bad(b, dev, dtype, b.stride(), (n, N, rank)) or not b.is_contiguous():
             _refuse(what, "contiguous a [n, rank, K] and b [n, N, rank]; " + _OPERANDS)
-        if scales.get_device() != dev or scales.shape != (n,) or scales.itemsize != 4 or \
-                not scales.is_floating_point() or not scales.is_contiguous():
+        if scales.get_device() != dev or scales.shape != (n,) or \
+                scales.dtype is not _float32 or not scales.is_contiguous():
             _refuse(what, "scales must be a contiguous float32 device tensor [n]")
         if _bad_ints(adapters, dev, (R,)) or _bad_ints(row_starts, dev, (R + 1,)):
             _refuse(what, "row_starts [R + 1] and adapters [R] must be contiguous int32 device "
@@ -288,11 +298,14 @@ def lora_linear(x, w, bias, a, b, scales, row_starts, adapters, out=None, stream
     elif not (a is None and b is None and scales is None and row_starts is None and
               adapters is None):
         _refuse(what, "a, b, scales, row_starts and adapters come together")
+    y_stride = N
     if out is None:
         out = x.new_empty((T, N))
-    ot = out.stride()
-    if _bad(out, dev, dtype, ot, (T, N)):
-        _refuse(what, "bad output tensor; " + _OPERANDS)
+    else:
+        ot = out.stride()
+        if _bad(out, dev, dtype, ot, (T, N)):
+            _refuse(what, "bad output tensor; " + _OPERANDS)
+        y_stride = ot[0]
     if T > 0:
         dt, buffer = _codes[dtype], None
         if workspace is True:
@@ -306,6 +319,6 @@ def lora_linear(x, w, bias, a, b, scales, row_starts, adapters, out=None, stream
             ws, size = _given_workspace(workspace)
         _run("libconv_lora_linear", lib.libconv_lora_linear,
              (x.data_ptr(), w.data_ptr(), bias_ptr, a_ptr, b_ptr, scales_ptr, starts_ptr,
-              adapters_ptr, out.data_ptr(), T, K, N, rank, n, R, xt[0], ot[0], dt, ws, size), dev,
+              adapters_ptr, out.data_ptr(), T, K, N, rank, n, R, xt[0], y_stride, dt, ws, size), dev,
              stream, buffer)
     return out
