@@ -66,7 +66,9 @@ template <int EB, int CPR> __device__ __forceinline__ int v_swizzle(int row) {
 __device__ __forceinline__ float swap_halves_max(float v) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__builtin_bit_cast(float, r[0]), __builtin_bit_cast(float, r[1]));
+  // (through scalars: a bit cast of a vector's element takes element 0)
+  const uint32_t lower = r[0], upper = r[1];
+  return fmaxf(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
 }
 
 // 4 elements of one column of 16-bit elements: the 16 lanes of a quarter wave

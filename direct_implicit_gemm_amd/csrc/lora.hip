@@ -41,7 +41,8 @@ __device__ __forceinline__ void store_low(const LoraArgs& a, unsigned char* at, 
     reinterpret_cast<float*>(at)[r] = v;
   } else {
     const uint16_t hi = Elem<DT_BF16>::from_f32(v);
-    const float rest = v - Elem<DT_BF16>::bits_to_f32(hi);
+    // (an infinity has no rest)
+    const float rest = (hi & 0x7f80u) == 0x7f80u ? 0.0f : v - Elem<DT_BF16>::bits_to_f32(hi);
     reinterpret_cast<uint16_t*>(at)[r] = hi;
     reinterpret_cast<uint16_t*>(at)[a.low_width + r] = Elem<DT_BF16>::from_f32(rest);
   }
@@ -263,6 +264,62 @@ __device__ __forceinline__ void low_step(const u32x4_t& bf, const u32x4_t& hi, c
   }
 }
 
+// Where tokens of several adapters share a block, the others' low-rank values
+// are 0 for an adapter's step, but 0 times an infinity or a NaN of its B would
+// reach them.  Such values take no part in the step: drop_not_finite sets them
+// to 0, and add_not_finite adds what they give their own tokens to the written
+// outputs (which are not finite then, whatever else they are).
+template <int DT>
+__device__ __forceinline__ bool drop_not_finite(u32x4_t& v) {
+  bool any = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t w = v[j];
+    if constexpr (DT == DT_F32) {
+      const bool bad = (w & 0x7f800000u) == 0x7f800000u;
+      w = bad ? 0u : w;
+      any = any || bad;
+    } else {
+      constexpr uint32_t E = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+      const bool low = (w & E) == E, high = (w & (E << 16)) == E << 16;
+      w &= low ? 0xffff0000u : 0xffffffffu;
+      w &= high ? 0x0000ffffu : 0xffffffffu;
+      any = any || low || high;
+    }
+    v[j] = w;
+  }
+  return any;
+}
+// Output n of token t, written by this lane.
+template <int DT>
+__device__ __forceinline__ void add_not_finite(const LoraArgs& a, int t, int n) {
+  constexpr int EB = Elem<DT>::bytes;
+  const int ad = a.adapter_of[t];
+  if (ad < 0) return;
+  const char* b = a.b + ((long long)ad * a.N + n) * a.rank * EB;
+  const unsigned char* low = a.low + (long long)t * a.low_width * 4;
+  float extra = 0.0f;
+  for (int r = 0; r < a.rank; ++r) {
+    float w, v;
+    if constexpr (DT == DT_F32) {
+      w = reinterpret_cast<const float*>(b)[r];
+      v = reinterpret_cast<const float*>(low)[r];
+    } else {
+      w = Elem<DT>::bits_to_f32(reinterpret_cast<const uint16_t*>(b)[r]);
+      v = Elem<DT_BF16>::bits_to_f32(reinterpret_cast<const uint16_t*>(low)[r]);
+    }
+    if (!__builtin_isfinite(w)) extra = fmaf(w, v, extra);
+  }
+  if (extra == 0.0f) return;
+  char* y = a.y + t * a.y_row + (long long)n * EB;
+  if constexpr (DT == DT_F32) {
+    *reinterpret_cast<float*>(y) += extra;
+  } else {
+    uint16_t* h = reinterpret_cast<uint16_t*>(y);
+    *h = Elem<DT>::from_f32(Elem<DT>::bits_to_f32(*h) + extra);
+  }
+}
+
 // 4 consecutive outputs of a token.
 template <int DT>
 __device__ __forceinline__ void store4(const LoraArgs& a, int t, int n, const float* v) {
@@ -408,7 +465,7 @@ __device__ __forceinline__ void store_part(const LoraArgs& a, int split, int t, 
 // first `low_jobs` workgroups form low-rank values, the others the sums of a
 // run of the sum's axis.
 template <int DT, int BM, int BN, int WM, int WN, int NS, bool Runs>
-__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, int tiles_m,
+__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LoraArgs a, int tiles_m,
                                                             int tiles_n, int low_jobs) {
   constexpr int EB = Elem<DT>::bytes;
   constexpr int THREADS = 64 * WM * WN;
@@ -484,6 +541,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
 #pragma unroll
   for (int st = 0; st < NS - 1; ++st) LIBCONV_COPY_STAGE(st, st)
 
+  bool dropped = false;   // values of B that are not finite
   if (!Runs && a.n_adapters > 0) {
     constexpr int LB = DT == DT_F32 ? 4 : 2;   // bytes of a low-rank value
     const __amdgpu_buffer_rsrc_t rl =
@@ -507,6 +565,10 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
       if (ad < 0) break;
 #pragma unroll
       for (int j = 0; j < MB; ++j) left[j] &= ~__ballot(mine[j] == ad);
+      bool mixed = false;
+#pragma unroll
+      for (int j = 0; j < MB; ++j)
+        mixed = mixed || __any(mine[j] != ad && m0 + (wm * MB + j) * 32 + l32 < a.T);
       const __amdgpu_buffer_rsrc_t rb =
           make_rsrc(a.b + (long long)ad * a.N * a.rank * EB, 0x7ffffff0u);
       for (int s = 0; s < steps; s += U) {
@@ -523,6 +585,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
             bf[u][i] = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32, off / LB);
         }
         __builtin_amdgcn_sched_barrier(0);
+        if (mixed) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < NB; ++i) dropped |= drop_not_finite<DT>(bf[u][i]);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (s + u < steps)
@@ -582,6 +650,13 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(const LoraArgs a, in
           store4<DT>(a, t, n, v);
       }
   }
+  if (!Runs && __any(dropped)) {
+    for (int k = 0; k < 16 * NB * MB; ++k) {
+      const int t = m0 + (wm * MB + k / (16 * NB)) * 32 + l32;
+      const int n = n0 + (wn * NB + k / 16 % NB) * 32 + 8 * (k / 4 % 4) + 4 * half + k % 4;
+      if (t < a.T && n < a.N) add_not_finite<DT>(a, t, n);
+    }
+  }
 }
 
 // 32 tokens x 32 outputs, the sums' axis split over the four waves: for fp32,
@@ -591,8 +666,10 @@ template <int DT, bool Runs>
 __global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low_jobs) {
   constexpr int EB = Elem<DT>::bytes, NS = 4;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * kStage32];
+  __shared__ int dropped;   // whether values of B were not finite
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
+  if (threadIdx.x == 0) dropped = 0;
   const int tiles_n = (a.N + 31) / 32;
   int block = blockIdx.x, split = 0;
   if constexpr (Runs) {
@@ -632,7 +709,9 @@ __global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low
         const int at = s * 32 + half * 16;
         u32x4_t hi, lo;
         load_low<DT>(a, rl, l32, mine == ad, at, &hi, &lo);
-        low_step<DT, true>(load_b<DT>(a, rb, n0 + l32, at / LB), hi, lo, acc);
+        u32x4_t bf = load_b<DT>(a, rb, n0 + l32, at / LB);
+        if (__any(drop_not_finite<DT>(bf))) dropped = 1;
+        low_step<DT, true>(bf, hi, lo, acc);
       }
     }
   }
@@ -653,8 +732,12 @@ __global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low
   }
   if constexpr (Runs)
     store_part(a, split, m0 + t, n0 + n, float4_t{v[0], v[1], v[2], v[3]});
-  else if (m0 + t < a.T && n0 + n < a.N)
+  else if (m0 + t < a.T && n0 + n < a.N) {
     store4<DT>(a, m0 + t, n0 + n, v);
+    if (dropped)
+      for (int j = 0; j < 4; ++j)
+        if (n0 + n + j < a.N) add_not_finite<DT>(a, m0 + t, n0 + n + j);
+  }
 }
 
 // Up to 16 * RB rows without adapters: 16 outputs a workgroup, the sum's axis

@@ -162,3 +162,62 @@ def test_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(out, L.prefix_attention(q, kp, vp, k, v, n)), i
         torch.cuda.synchronize()
+
+
+MORE = [  # B, Sq, P, S, query heads, key heads, head_dim, causal, dtype, lengths
+    # more workgroups of 128 rows than half the compute units: tiles shared by their waves
+    (2, 300, 77, 310, 33, 33, 64, True, "bf16", [310, 171]),
+    (2, 290, 150, 200, 50, 25, 80, True, "f16", [200, 1]),
+    (3, 260, 65, 128, 22, 22, 128, False, "bf16", [128, 0, 65]),
+    (1, 700, 0, 700, 25, 25, 96, True, "f16", [640]),
+    (2, 200, 191, 64, 35, 35, 128, True, "bf16", [64, 40]),
+    (2, 280, 33, 130, 30, 30, 72, True, "f32", [130, 20]),
+    # the prefix once, own keys in several runs, one ending at a run's end
+    (4, 1, 700, 3000, 4, 1, 64, True, "bf16", [0, 256, 257, 3000]),
+    (6, 2, 2500, 1200, 16, 2, 128, True, "f16", [1200, 1, 128, 129, 384, 700]),
+    (40, 1, 1100, 300, 8, 2, 80, True, "bf16", [7 * i for i in range(40)]),
+    (3, 9, 300, 500, 4, 1, 128, True, "f32", [500, 5, 131]),
+    # many keys for few rows: more than 8 partial results to join
+    (1, 1, 5000, 6000, 2, 1, 64, True, "bf16", [5555]),
+    (2, 17, 130, 0, 4, 2, 8, False, "f16", [0, 0]),
+]
+
+
+@pytest.mark.parametrize("case", MORE, ids=str)
+@pytest.mark.parametrize("workspace", [True, False])
+def test_more_shapes_against_64_bits(case, workspace):
+    B, Sq, P, S, hq, hk, d, causal, dtype, lengths = case
+    check(*make(B, Sq, P, S, hq, hk, d, dtype, lengths, seed=6), causal, what=str(case),
+          workspace=workspace)
+
+
+def test_stale_rows_with_shared_tiles():
+    """As above, for rows enough that the waves of a workgroup share their tiles."""
+    q, kp, vp, k, v, n = make(3, 270, 70, 300, 24, 24, 64, "bf16", [0, 70, 129])
+    want = check(q, kp, vp, k, v, n, True, what="clean")
+    for b, m in enumerate(n.tolist()):
+        k[b, m:], v[b, m:] = math.nan, math.inf
+    got = L.prefix_attention(q, kp, vp, k, v, n, causal=True)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("Sq,hk", [(1, 2), (300, 33)])
+def test_scores_that_climb_and_fall(Sq, hk):
+    """Keys in order of growing and of falling scores, far beyond what the exponential holds."""
+    q, kp, vp, k, v, n = make(2, Sq, 400, 90, hk, hk, 64, "f16", [90, 50])
+    q = q.abs()
+    for ramp in (torch.linspace(-3.0, 3.0, 400), torch.linspace(3.0, -3.0, 400)):
+        keys = kp.abs() * ramp.half().cuda()[:, None, None]
+        check(q * 3, keys, vp, k, v, n, True, what=f"ramp from {float(ramp[0])}")
+
+
+def test_not_finite_values_stay_with_their_entry():
+    q, kp, vp, k, v, n = make(5, 1, 300, 200, 4, 2, 64, "bf16", [200, 150, 1, 0, 64])
+    want = check(q, kp, vp, k, v, n, True, what="finite")
+    k[1, 7], v[1, 7], q[4] = math.nan, math.inf, math.nan
+    got = L.prefix_attention(q, kp, vp, k, v, n)
+    torch.cuda.synchronize()
+    for b in (0, 2, 3):
+        assert torch.equal(got[b], want[b]), b
+    assert bool(torch.isnan(got[1]).all()) and bool(torch.isnan(got[4]).all())

@@ -118,3 +118,43 @@ def test_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(y, L.lora_linear(*s.values())), i
         torch.cuda.synchronize()
+
+
+MORE = [  # T, K, N, rank, adapters, row_starts, ids, dtype, bias
+    # runs of the sums' axis beside the low-rank values; groups of 4 rows with up to 4 adapters
+    (66, 2056, 200, 8, 4, [0, 1, 2, 3, 64, 66], [3, -1, 1, 0, 2], "bf16", True),
+    (128, 4096, 320, 33, 2, [0, 63, 128], [1, 0], "f16", True),
+    (257, 1544, 129, 64, 3, [0, 2, 129, 130, 257], [0, 1, 2, 0], "bf16", False),
+    (1000, 1032, 4104, 16, 9, list(range(0, 1000, 125)) + [1000], list(range(8)), "bf16", True),
+    (1024, 72, 65, 128, 2, [0, 1022, 1024], [0, 1], "f16", True),
+    (130, 2064, 70, 9, 3, [0, 65, 130], [2, 0], "f32", True),
+    (700, 520, 1100, 32, 3, [0, 300, 301, 700], [1, 0, 2], "f32", True),
+    # low-rank values first, then the product
+    (1025, 136, 192, 128, 3, [0, 500, 501, 1025], [2, 0, 1], "f16", True),
+    (3000, 264, 2500, 64, 6, [0, 1, 40, 700, 701, 2999, 3000], [5, 4, -1, 2, 1, 0], "bf16", True),
+    (1500, 520, 2052, 24, 2, [0, 1499, 1500], [0, 1], "f32", True),
+    (1100, 2048, 70, 128, 2, [0, 40, 1100], [0, 1], "f32", False),
+]
+
+
+@pytest.mark.parametrize("case", MORE, ids=lambda c: "-".join(map(str, c[:5])) + "-" + c[7])
+def test_more_rows_against_64_bits(case):
+    T, K, N, rank, n, starts, ids, dtype, bias = case
+    check(make(T, K, N, rank, n, starts, ids, dtype, bias, seed=4), str(case[:5]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T", [7, 200, 1400])
+def test_an_adapter_that_is_not_finite_stays_with_its_rows(T, dtype):
+    """Infinities and NaN in one request's adapter do not reach the others' rows."""
+    cut = [0, 3, T // 2, T - 2, T]
+    s = make(T, 128, 96, 16, 4, cut, [0, 1, 2, -1], dtype)
+    want, bound = C.lora(*s.values())
+    s["a"][1].fill_(float("inf"))
+    s["b"][1].fill_(float("nan"))
+    s["b"][3].fill_(float("nan"))   # nobody's
+    y = L.lora_linear(*s.values())
+    torch.cuda.synchronize()
+    rows = torch.tensor([t for t in range(T) if not 3 <= t < T // 2])
+    C.assert_within(y.cpu()[rows], want[rows], bound[rows], f"rows of other adapters, {T}")
+    assert bool(torch.isnan(y[3:T // 2]).all())

@@ -117,3 +117,48 @@ def test_head_major_outputs_and_another_stream():
     for got, x, wt in ((qo, q, w[0]), (ko, k, w[1])):
         want, bound = C.rope(x, wt, pos, freqs, sec, 1e-6, False)
         C.assert_within(got, want, bound, "head-major")
+
+
+MORE = [  # T, query heads, key heads, head_dim, rot_dim, axes, positions to, interleaved, dtype
+    (11, 9, 2, 24, 16, 1, 100, False, "bf16"),
+    (5, 3, 3, 40, 16, 1, 100, False, "f16"),
+    (6, 2, 1, 104, 48, 3, 5000, False, "bf16"),
+    (9, 5, 1, 200, 176, 2, 5000, False, "bf16"),
+    (21, 4, 2, 256, 16, 1, 5000, False, "f32"),
+    (8, 3, 1, 8, 6, 1, 5000, True, "bf16"),
+    (10, 2, 2, 136, 130, 3, 5000, True, "f16"),
+    (2500, 1, 1, 128, 128, 1, 2500, False, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", MORE, ids=str)
+def test_more_shapes_against_64_bits(case):
+    test_against_64_bits(case)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_an_infinity_beside_what_does_not_turn(interleaved):
+    """Of a head with an infinity only the infinity's own pair is lost; other heads are not."""
+    _, q, k, v, sec, freqs, pos, w = make(4, 3, 1, 64, 32, 1, 100, "bf16", 8)
+    want, bound = C.rope(q, w[0], pos, freqs, sec, 1e-6, interleaved)
+    q = q.clone()
+    q[2, 1, 50] = float("inf")    # past what turns
+    got, _ = L.qk_norm_rope(q, k, pos, freqs, w[0], w[1], sections=sec, interleaved=interleaved)
+    torch.cuda.synchronize()
+    hit = torch.zeros(q.shape, dtype=torch.bool)
+    hit[2, 1] = True
+    C.assert_within(got.cpu()[~hit], want[~hit], bound[~hit], "other heads")
+    rest = got.cpu()[2, 1].float()
+    assert bool(torch.isnan(rest[50]))
+    assert bool((torch.cat([rest[:50], rest[51:]]) == 0).all())   # divided by an infinite norm
+
+
+def test_tiny_values_without_eps():
+    """The root of a mean square below what its fast form takes."""
+    _, q, k, v, sec, freqs, pos, w = make(3, 2, 1, 64, 64, 1, 100, "f32", 9)
+    q = q * 1e-20
+    got, _ = L.qk_norm_rope(q, k, pos, freqs, w[0], w[1], eps=0.0)
+    torch.cuda.synchronize()
+    want, bound = C.rope(q, w[0], pos, freqs, sec, 0.0, False)
+    # squares of 1e-20 keep 10 to 20 bits of theirs: the norm of 64 of them is off by 2^-10
+    C.assert_within(got, want, bound + 2.0 ** -10 * want.abs().amax(-1, keepdim=True), "tiny")
