@@ -461,7 +461,7 @@ __device__ __forceinline__ void store_part(const LoraArgs& a, int split, int t, 
     *reinterpret_cast<float4_t*>(a.part + ((long long)split * a.T + t) * n_pad + n) = v;
 }
 
-// BM tokens x BN outputs, WM x WN waves, NS - 1 stages on their way.  Runs: the
+// BM tokens x BN outputs, WM x WN waves, NS stages in LDS or on their way.  Runs: the
 // first `low_jobs` workgroups form low-rank values, the others the sums of a
 // run of the sum's axis.
 template <int DT, int BM, int BN, int WM, int WN, int NS, bool Runs>
@@ -509,37 +509,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LoraArgs a,
   const int begin = Runs ? split * a.run : 0;
   const int row_bytes = Runs && begin + a.run < row ? a.run : row - begin;   // of this run
   const int stages = (row_bytes + 127) / 128;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)m0 * a.x_row + begin, 0x7ffffff0u);
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row + begin, 0x7ffffff0u);
-  constexpr int CX = BM * 8 / THREADS, CW = BN * 8 / THREADS;   // copies a thread
-  int x_off[CX], w_off[CW];   // of stage 0; past the end where the row is
-  int x_chunk[CX], w_chunk[CW];
-#pragma unroll
-  for (int c = 0; c < CX; ++c) {
-    const int unit = c * THREADS + threadIdx.x, r = unit >> 3;
-    x_chunk[c] = chunk_at(r, unit & 7) * 16;
-    x_off[c] = m0 + r < a.T ? r * (int)a.x_row + x_chunk[c] : kOobOffset;
-  }
-#pragma unroll
-  for (int c = 0; c < CW; ++c) {
-    const int unit = c * THREADS + threadIdx.x, r = unit >> 3;
-    w_chunk[c] = chunk_at(r, unit & 7) * 16;
-    w_off[c] = n0 + r < a.N ? r * row + w_chunk[c] : kOobOffset;
-  }
+  // a thread copies one 16-byte chunk of rows PASS apart: its place in them is
+  // the same, and the rows are told apart by a scalar offset.  Rows that do not
+  // exist lie past the resource's end.
+  constexpr int PASS = THREADS / 8;
+  static_assert(PASS % 16 == 0, "one chunk for a thread's rows");
+  const int rows_x = a.T - m0 < BM ? a.T - m0 : BM, rows_w = a.N - n0 < BN ? a.N - n0 : BN;
+  const int x_row = (int)a.x_row;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (long long)m0 * a.x_row + begin,
+                                              (uint32_t)((rows_x - 1) * x_row + row_bytes));
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + (long long)n0 * row + begin,
+                                              (uint32_t)((rows_w - 1) * row + row_bytes));
+  const int chunk = chunk_at(threadIdx.x >> 3, threadIdx.x & 7) * 16;
+  const int x_off = (int)(threadIdx.x >> 3) * x_row + chunk;
+  const int w_off = (int)(threadIdx.x >> 3) * row + chunk;
+  constexpr int CX = BM / PASS, CW = BN / PASS;   // copies a thread
 #define LIBCONV_COPY_STAGE(st, at)                                                              \
   {                                                                                             \
-    unsigned char* to = lds + (at) * STAGE;                                                     \
+    unsigned char* to = lds + (at) * STAGE + wave * 1024;                                       \
     const int k = (st) * 128;                                                                   \
-    _Pragma("unroll") for (int c = 0; c < CX; ++c) copy16_to_lds(                               \
-        rx, to + (c * THREADS + wave * 64) * 16,                                                \
-        guard_offset(x_off[c] >= 0 && k + x_chunk[c] < row_bytes, x_off[c] + k));               \
-    _Pragma("unroll") for (int c = 0; c < CW; ++c) copy16_to_lds(                               \
-        rw, to + BM * 128 + (c * THREADS + wave * 64) * 16,                                     \
-        guard_offset(w_off[c] >= 0 && k + w_chunk[c] < row_bytes, w_off[c] + k));               \
+    const bool in = k + chunk < row_bytes;                                                      \
+    const int xo = in ? x_off + k : kFarOffset, wo = in ? w_off + k : kFarOffset;               \
+    _Pragma("unroll") for (int c = 0; c < CX; ++c)                                              \
+        copy16_to_lds(rx, to + c * THREADS * 16, xo, c * PASS * x_row);                         \
+    _Pragma("unroll") for (int c = 0; c < CW; ++c)                                              \
+        copy16_to_lds(rw, to + BM * 128 + c * THREADS * 16, wo, c * PASS * row);                \
   }
-  // NS - 1 stages are on their way at a time; those past the last read nothing
+  // NS stages are in LDS or on their way; those past the last read nothing
 #pragma unroll
-  for (int st = 0; st < NS - 1; ++st) LIBCONV_COPY_STAGE(st, st)
+  for (int st = 0; st < NS; ++st) LIBCONV_COPY_STAGE(st, st)
 
   bool dropped = false;   // values of B that are not finite
   if (!Runs && a.n_adapters > 0) {
@@ -603,33 +601,49 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LoraArgs a,
     }
   }
 
-  int at = 0, free = NS - 1;   // stages in use and to be filled
+  // 32 bytes of the sums' axis a step, whose operands are read a step ahead:
+  // those of a stage's first step before the last matrix instructions of the
+  // stage before, which cover the barrier between
+  u32x4_t wf[2][NB], xf[2][MB];
+  auto read = [&](const unsigned char* xs, int k, u32x4_t* w, u32x4_t* x) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int r = (wn * NB + i) * 32 + l32;
+      w[i] = *reinterpret_cast<const u32x4_t*>(xs + (BM + r) * 128 +
+                                               chunk_at(r, 2 * k + half) * 16);
+    }
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int r = (wm * MB + j) * 32 + l32;
+      x[j] = *reinterpret_cast<const u32x4_t*>(xs + r * 128 + chunk_at(r, 2 * k + half) * 16);
+    }
+  };
+  wait_vmcnt<(NS - 1) * (CX + CW)>();
+  lds_barrier();
+  read(lds, 0, wf[0], xf[0]);
+  int at = 0;   // the stage in use
   for (int st = 0; st < stages; ++st) {
-    wait_vmcnt<(NS - 2) * (CX + CW)>();
-    lds_barrier();
-    LIBCONV_COPY_STAGE(st + NS - 1, free)
     const unsigned char* xs = lds + at * STAGE;
-    free = at;
-    at = at + 1 < NS ? at + 1 : 0;
-    const unsigned char* ws = xs + BM * 128;
+    const int next = at + 1 < NS ? at + 1 : 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      u32x4_t wf[NB], xf[MB];
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int r = (wn * NB + i) * 32 + l32;
-        wf[i] = *reinterpret_cast<const u32x4_t*>(ws + r * 128 + chunk_at(r, 2 * k + half) * 16);
+      if (k < 3) {
+        read(xs, k + 1, wf[(k + 1) & 1], xf[(k + 1) & 1]);
+      } else {
+        // nobody reads this stage any more, the next one has arrived
+        wait_vmcnt<(NS - 2) * (CX + CW)>();
+        lds_barrier();
+        LIBCONV_COPY_STAGE(st + NS, at)
+        read(lds + next * STAGE, 0, wf[0], xf[0]);
       }
-#pragma unroll
-      for (int j = 0; j < MB; ++j) {
-        const int r = (wm * MB + j) * 32 + l32;
-        xf[j] = *reinterpret_cast<const u32x4_t*>(xs + r * 128 + chunk_at(r, 2 * k + half) * 16);
-      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < MB; ++j) Step<DT, true>::run(wf[i], xf[j], acc[i][j]);
+        for (int j = 0; j < MB; ++j)
+          Step<DT, true>::run(wf[k & 1][i], xf[k & 1][j], acc[i][j]);
     }
+    at = next;
   }
 #undef LIBCONV_COPY_STAGE
 
