@@ -775,13 +775,21 @@ void launch_dt(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-long long attn_plan(AttnArgs* a, int cus, bool allowed) {
+long long attn_plan(AttnArgs* a, int dtype, int cus, bool allowed) {
   const long long per_entry = (long long)a->Sq * a->G, all = a->B * per_entry;
   a->shared = 0;
   a->splits = a->prefix_splits = 1;
   a->chunk = 0;
   a->waves = key_waves(per_entry, (long long)a->B * a->Hk);
   if (!allowed || all == 0) return 0;
+  // Few keys: one launch, and nothing to join.  Measured for one query of 4
+  // entries with 8 key heads, heads of 64 in 16 bits (128 bytes a key): 552 keys
+  // 8.5 us against 8.9 in two launches, 1000 keys 10.6 against 9.6, where the
+  // second launch and the workspace take the host another 4 us; 1540 keys 12.8
+  // against 9.7.  Heads of 128: 552 keys 11.2 against 11.6, 1000 keys 14.2
+  // against 12.7.
+  const long long key_bytes = a->D * (dtype == LIBCONV_F32 ? 4LL : 2LL);
+  if (a->waves == 4 && ((long long)a->P + a->S) * key_bytes <= 160 * 1024) return 0;
   // Splits so that `groups` workgroups become `want`, each with `least` keys
   // or more.
   auto split = [&](long long want, long long groups, long long keys, long long least) {
@@ -794,12 +802,12 @@ long long attn_plan(AttnArgs* a, int cus, bool allowed) {
   // each of them would be what the call spends its time on.
   if (a->B > 1 && per_entry <= 64 && a->P >= 128) {
     a->shared = 1;
-    // a share of the prefix leaves a partial result of every row: with many
-    // rows it has to be long
-    const long long least = 4 * all < 256 ? 256 : 4 * all > 1024 ? 1024 : 4 * all;
+    // (a share of the prefix leaves a partial result of every row: few with
+    // many rows)
     a->waves = 4;
     a->prefix_waves = all <= 64 ? 4 : 1;
-    a->prefix_splits = split(2LL * cus, a->Hk * row_tiles(all, a->prefix_waves), a->P, least);
+    a->prefix_splits = split(2LL * cus, a->Hk * row_tiles(all, a->prefix_waves), a->P, 256);
+    if (all > 64 && a->prefix_splits > 8) a->prefix_splits = 8;
     // own keys: runs of one length, so that long entries do not hold up the
     // end; about half of them will have keys
     const long long runs = split(8LL * cus, groups, a->S, 256);

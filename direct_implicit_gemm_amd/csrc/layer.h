@@ -49,7 +49,7 @@ struct AttnArgs {
 };
 // Fills the plan for `cus` compute units and returns the workspace bytes it
 // takes; with a smaller workspace the plan has to be made with allowed = false.
-long long attn_plan(AttnArgs* a, int cus, bool allowed);
+long long attn_plan(AttnArgs* a, int dtype, int cus, bool allowed);
 libconv_status attn_launch(AttnArgs a, int dtype, hipStream_t stream);
 
 // libconv_lora_linear; strides in bytes.

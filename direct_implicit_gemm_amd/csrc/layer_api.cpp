@@ -234,7 +234,7 @@ long long libconv_prefix_attention_workspace(int B, int Sq, int P, int S, int q_
   if (attn_shape(B, Sq, P, S, q_heads, k_heads, head_dim, dtype) != LIBCONV_OK) return -1;
   AttnArgs a;
   attn_sizes(&a, B, Sq, P, S, q_heads, k_heads, head_dim);
-  return attn_plan(&a, kPlanCus, true);
+  return attn_plan(&a, dtype, kPlanCus, true);
 }
 
 libconv_status libconv_prefix_attention(const void* q, const void* k_prefix, const void* v_prefix,
@@ -301,14 +301,14 @@ libconv_status libconv_prefix_attention(const void* q, const void* k_prefix, con
   a.scale = scale == 0.0f ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
   a.flip = scale == 0.0f ? 1 : scale < 0.0f ? -1 : 0;
   a.causal = causal != 0;
-  const long long need = attn_plan(&a, kPlanCus, true);
+  const long long need = attn_plan(&a, dtype, kPlanCus, true);
   if (need > 0) {
     if (workspace && workspace_bytes >= need) {
       const long long slots = a.splits + (a.shared ? a.prefix_splits : 0);
       a.part = static_cast<float*>(workspace);
       a.part_lse = a.part + slots * a.Hk * a.B * a.Sq * a.G * a.D;
     } else {
-      attn_plan(&a, kPlanCus, false);
+      attn_plan(&a, dtype, kPlanCus, false);
     }
   }
   return attn_launch(a, dtype, reinterpret_cast<hipStream_t>(stream));
