@@ -1,10 +1,12 @@
 // device_common.h -- device-side helpers shared by the libconv kernels:
 // storage-dtype conversions and bounds-checked buffer access.
 //
-// Every global load and store in libconv goes through a buffer resource whose
-// size is the tensor's byte size: an access outside the tensor reads zero and
-// a store outside it is dropped by the hardware, so an indexing mistake can
-// produce a wrong value but never a memory fault.
+// Every global load and store of the convolutions goes through a buffer
+// resource whose size is the tensor's byte size: an access outside the tensor
+// reads zero and a store outside it is dropped by the hardware, so an indexing
+// mistake can produce a wrong value but never a memory fault.  (The operands
+// of the attention-layer operators may be larger than a resource reaches:
+// those kernels make one for each tile, or check each row and column.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -190,9 +192,8 @@ __device__ __forceinline__ void lds_barrier() {
 
 // One 16-byte global read per lane written straight into LDS: lane l's
 // vector lands at dst + 16 l (dst and soff, which adds to the lanes' offsets,
-// are wave-uniform).  Kept out of the generic
-// lambdas of the kernel: inside them the host pass drops the kernel's launch
-// stub.
+// are wave-uniform).  Kept out of the generic lambdas of the convolution
+// kernel: inside them the host pass drops the kernel's launch stub.
 __device__ __forceinline__ void copy16_to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* dst,
                                               int off, int soff = 0) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16,
