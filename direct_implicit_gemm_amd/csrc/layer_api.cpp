@@ -18,6 +18,7 @@ constexpr long long kMaxInt = 0x7fffffff;
 constexpr long long kMaxStride = 1LL << 40;
 // Tiles are addressed with 32-bit offsets from their first row: 256 rows.
 constexpr long long kMaxRowBytes = (1LL << 23) - 16;
+constexpr int kMaxRows = (1 << 26) - 64;   // of a launch with a wave to a row
 
 bool good_dtype(int dt) { return dt == LIBCONV_F32 || dt == LIBCONV_F16 || dt == LIBCONV_BF16; }
 
@@ -107,9 +108,12 @@ libconv_status attn_shape(int B, int Sq, int P, int S, int q_heads, int k_heads,
       q_heads % k_heads != 0)
     return LIBCONV_ERR_BAD_SHAPE;
   if (head_dim > 128 || head_dim % 8 != 0) return LIBCONV_ERR_UNSUPPORTED;
-  // rows, and workgroups of 32 rows with up to 64 splits, are counted in 31 bits
+  // rows and keys are counted in 31 bits, the lanes of a launch (256 to 32 rows
+  // of a key head) in 32
   const double rows = (double)B * Sq * q_heads;
-  if (rows > (double)(kMaxInt / 64) || (double)P + S > (double)(kMaxInt - 1024))
+  const double groups = (double)B * k_heads * (((double)Sq * (q_heads / k_heads) + 31) / 32);
+  if (rows > (double)(kMaxInt / 64) || groups > (double)((1 << 24) - 4096) ||
+      (double)P + S > (double)(kMaxInt - 1024))
     return LIBCONV_ERR_TOO_LARGE;
   return LIBCONV_OK;
 }
@@ -129,10 +133,11 @@ libconv_status lora_shape(int T, int K, int N, int rank, int n_adapters, int n_r
   if (low && rank < 1) return LIBCONV_ERR_BAD_SHAPE;
   if (K % 8 != 0 || (low && rank > 128)) return LIBCONV_ERR_UNSUPPORTED;
   const long long eb = dtype_bytes(dtype);
-  // offsets inside a tile of W, of an adapter's B, and workgroups: 31 bits
-  if (K * eb > kMaxRowBytes || T > kMaxInt - 1024 ||
+  // offsets inside a tile of W and of an adapter's B: 31 bits; the lanes of a
+  // launch (256 to 32 rows, or to a tile of 64 x 64): 32
+  if (K * eb > kMaxRowBytes || T > kMaxRows ||
       (low && (long long)N * rank * eb >= kMaxInt - 1024) ||
-      ((double)T / 64 + 1) * ((double)N / 64 + 1) > (double)kMaxInt)
+      ((double)T / 64 + 1) * ((double)N / 64 + 1) > (double)(1 << 24))
     return LIBCONV_ERR_TOO_LARGE;
   return LIBCONV_OK;
 }
@@ -161,7 +166,8 @@ libconv_status libconv_qk_norm_rope(const void* q, const void* k, const void* v,
     return LIBCONV_ERR_BAD_SHAPE;
   if (head_dim > 256 || head_dim % 8 != 0 || (!interleaved && rot_dim % 16 != 0))
     return LIBCONV_ERR_UNSUPPORTED;
-  if ((long long)q_heads + 2LL * k_heads > (1 << 24)) return LIBCONV_ERR_TOO_LARGE;
+  if ((long long)q_heads + 2LL * k_heads > (1 << 24) || T > kMaxRows)
+    return LIBCONV_ERR_TOO_LARGE;
   if (!strides || !q || !k || !q_out || !k_out || (!v != !v_out)) return LIBCONV_ERR_NULL_POINTER;
   if (rot_dim > 0 && (!freqs || !positions)) return LIBCONV_ERR_NULL_POINTER;
   if (!good_strides(strides, 12)) return LIBCONV_ERR_BAD_SHAPE;

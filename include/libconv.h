@@ -588,7 +588,8 @@ int libconv_out_size2(int in, int k, int pad_lo, int pad_hi, int stride);
  * fp32 or more and rounded once.  q_out may be q and k_out may be k (the same
  * pointer and strides, slots NULL); other overlaps are LIBCONV_ERR_ALIAS.
  * head_dim: a multiple of 8 up to 256; rot_dim: even, <= head_dim, a multiple
- * of 16 where interleaved is 0; else LIBCONV_ERR_UNSUPPORTED.  T may be 0.
+ * of 16 where interleaved is 0; else LIBCONV_ERR_UNSUPPORTED.  T may be 0, and
+ * has to be below 2^26 - 64.
  */
 libconv_status libconv_qk_norm_rope(const void* q, const void* k, const void* v,
                                     void* q_out, void* k_out, void* v_out,
@@ -625,7 +626,9 @@ libconv_status libconv_qk_norm_rope(const void* q, const void* k, const void* v,
  *             libconv_prefix_attention_workspace bytes for the best plan,
  *             which reads the prefix once for all entries and splits long
  *             rows of keys over workgroups; NULL or smaller: a plan without.
- * B, Sq, P and S may be 0 (0 keys: out is 0).
+ * B, Sq, P and S may be 0 (0 keys: out is 0).  B * k_heads times the queries
+ * of a key head in 32s (rounded up) has to be below 2^24 - 4096, and a row of
+ * keys or values below 2^23 bytes from the next.
  */
 libconv_status libconv_prefix_attention(const void* q, const void* k_prefix,
                                         const void* v_prefix, const void* k, const void* v,
@@ -656,7 +659,9 @@ long long libconv_prefix_attention_workspace(int B, int Sq, int P, int S, int q_
  * zeros.  Products are summed in fp32; the low-rank values a x[t] stay fp32
  * (for 16-bit types they enter the second product as two bfloat16 terms,
  * 16 significant bits) and y is rounded once.
- * K: a multiple of 8; rank 1 to 128; x, w, a on 16-byte boundaries.
+ * K: a multiple of 8; rank 1 to 128; x, w, a, b on 16-byte boundaries; rows of
+ * x and w below 2^23 bytes, T below 2^26 - 64.  An infinity or a NaN of one
+ * adapter stays with its own rows.
  * n_adapters or n_requests 0: the projection alone (a, b, scales, row_starts
  * and adapters may be NULL).
  *   workspace  device, 256-byte aligned, at least libconv_lora_workspace

@@ -202,3 +202,37 @@ def test_rotary_frequencies():
     assert f.tolist() == pytest.approx([1.0, 0.1] * 3, rel=1e-15)
     with pytest.raises(ValueError):
         L.rotary_frequencies(8, 10000.0, [3], device="cpu")
+
+
+# ------------------------------------------------------------------- sizes a launch cannot have
+@pytest.mark.parametrize("kw", [dict(T=1 << 26), dict(T=(1 << 31) - 1), dict(q_heads=1 << 24)])
+def test_rope_too_large(kw):
+    assert rope(**{**kw, "strides": (1 << 31, 64) * 6}) == LARGE
+
+
+@pytest.mark.parametrize("kw", [dict(B=1 << 24, Sq=1), dict(B=1 << 20, Sq=1024), dict(P=1 << 30, S=1 << 30)])
+def test_attention_too_large(kw):
+    assert attention(**kw) == LARGE
+    a = {**ATTN, **kw}
+    assert L.libconv_prefix_attention_workspace(a["B"], a["Sq"], a["P"], a["S"], a["q_heads"],
+                                                a["k_heads"], a["head_dim"], a["dtype"]) == -1
+
+
+@pytest.mark.parametrize("kw", [dict(T=1 << 26), dict(T=1 << 22, N=1 << 20)])
+def test_lora_too_large(kw):
+    assert lora(**kw) == LARGE
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 64, 65, 700, 1024, 1025, 9000])
+@pytest.mark.parametrize("dtype", [L.F32, L.F16, L.BF16])
+def test_lora_workspace_holds_the_low_rank_values(T, dtype):
+    """At least a row's low-rank values and its adapter; never more than the split product."""
+    for K, N, rank in ((8, 1, 1), (640, 1920, 8), (4096, 4096, 128), (1000, 8192, 33)):
+        n = L.libconv_lora_workspace(T, K, N, rank, 3, 2, dtype)
+        low = T * (rank + 1) * 4
+        assert low <= n <= T * (128 + 32 + 1) * 4 + 256 + 64 * T * (N + 63) * 4, (T, K, N, rank)
+
+
+def test_attention_workspace_of_few_keys_is_none():
+    assert L.libconv_prefix_attention_workspace(4, 1, 960, 40, 20, 20, 64, L.BF16) == 0
+    assert L.libconv_prefix_attention_workspace(4, 1, 9600, 40, 20, 20, 64, L.BF16) > 0
