@@ -47,13 +47,16 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a) {
   const int s0 = (int)((long long)a.steps * chunk / a.chunks);
   const int s1 = (int)((long long)a.steps * (chunk + 1) / a.chunks);
 
-  // this lane's two chunks of 16 bytes: the same of both halves where they
-  // turn; neighbours past them, or of interleaved pairs
-  const int sub = lane % LPH, group = lane / LPH;
+  // this lane's two chunks of 16 bytes: the same of both halves of what turns;
+  // of what does not, and of interleaved pairs, also one of either half (a
+  // step's lanes then read and write whole lines at a time: neighbouring chunks
+  // a lane had 1.7 times the bytes written)
+  const int sub = lane % LPH, group = lane / LPH, chunks = a.D / E;
   const int paired = Interleaved ? 0 : a.half / E;
-  const bool turns = sub < paired;
-  const int c1 = turns ? sub : 2 * sub, c2 = turns ? sub + paired : 2 * sub + 1;
-  const bool live1 = c1 * E < a.D, live2 = c2 * E < a.D;
+  const int rest = (chunks - 2 * paired + 1) / 2;   // lanes past the paired ones
+  const int c1 = sub < paired ? sub : paired + sub;
+  const int c2 = c1 + (sub < paired ? paired : rest);
+  const bool live1 = sub < paired + rest, live2 = live1 && c2 < chunks;
   const int row_out = a.slots ? a.slots[token] : token;
   const bool row_ok = !a.slots || (row_out >= 0 && row_out < a.out_rows);
 
@@ -94,7 +97,7 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kernel(const RopeArgs a) {
   bool on[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) {
-    const int pair = Interleaved ? (j < E / 2 ? c1 : c2 - 1) * (E / 2) + j : sub * E + j;
+    const int pair = Interleaved ? (j < E / 2 ? c1 : c2) * (E / 2) + j % (E / 2) : sub * E + j;
     on[j] = pair < a.half;
     const float2 t = table[wave][on[j] ? pair : 0];
     c[j] = on[j] ? t.x : 1.0f;
