@@ -369,19 +369,21 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
       move_up(s0);   // nothing to rescale yet
       probabilities(s0);
       pack(s0, p0);
-      for (int i = 0; i < n - 1; ++i) {
+      // Two blocks: tile i's second and tile i + 1's first.  odd is i & 1, a
+      // constant where it is called, so that the stages' addresses are.
+      auto two_blocks = [&](int i, int odd) __attribute__((always_inline)) {
         // K of tile i + 1 and V of tile i have arrived for this wave, after the
         // barrier for all, and nobody reads K of tile i and V of i - 1 any more
-        const unsigned char* k1 = kt + ((i + 1) & 1) * Z::TILE;
-        const unsigned char* v0 = vt + (i & 1) * Z::TILE;
+        const unsigned char* k1 = kt + (1 - odd) * Z::TILE;
+        const unsigned char* v0 = vt + odd * Z::TILE;
         wait_vmcnt<0>();
         lds_barrier();
         mask(t0 + i, 1, s1);
         move_up(s1);
         score(k1, 0, s0);
         // behind the first matrix instructions, which cover their scalar work
-        copy_v(vt + ((i + 1) & 1) * Z::TILE);
-        copy_k(kt + (i & 1) * Z::TILE);
+        copy_v(vt + (1 - odd) * Z::TILE);
+        copy_k(kt + odd * Z::TILE);
         probabilities(s1);
         pack(s1, p1);
         add_values(v0, 0, p0);
@@ -393,7 +395,13 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
         pack(s0, p0);
         add_values(v0, 1, p1);
         follow(p0);
+      };
+      int i = 0;
+      for (; i + 2 < n; i += 2) {
+        two_blocks(i, 0);
+        two_blocks(i + 1, 1);
       }
+      if (i + 1 < n) two_blocks(i, 0);
       const unsigned char* v0 = vt + ((n - 1) & 1) * Z::TILE;
       wait_vmcnt<0>();
       lds_barrier();
