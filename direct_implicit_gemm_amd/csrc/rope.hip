@@ -10,7 +10,10 @@
 // what turns, so that both members of a pair are in one lane and nothing but
 // the sum of squares crosses lanes.  The angles are the same for all heads of a
 // token: the wave's lanes form cos and sin of one pair each, once, and the
-// heads' lanes read theirs back from LDS.
+// heads' lanes read theirs back from LDS.  Measured: 38400 tokens of 40 heads of
+// 128 in bf16 (787 MB) 144 us, 5.46 TB/s (a lane with 16 bytes of a head and its
+// partner's fetched from another lane: 246 us); 2053 tokens of 20 heads of 128
+// in fp32 8.1 us, 5.2 TB/s; 8 tokens of 60 heads of 64 4.8 us, latency.
 #include "device_common.h"
 #include "layer.h"
 
