@@ -110,8 +110,10 @@ __device__ __forceinline__ void product32(__amdgpu_buffer_rsrc_t rx, __amdgpu_bu
 template <int DT, int NS>
 __global__ __launch_bounds__(256, NS <= 4 ? 2 : 1) void low_kernel(const LoraArgs a) {
   constexpr int EB = Elem<DT>::bytes, THREADS = 256;
-  __shared__ int ad_of[kLowRows];
+  // (nothing beside the stages: with 64 KB and a little the workgroup would be
+  // alone on its compute unit)
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * kStage32];
+  int* const ad_of = reinterpret_cast<int*>(lds);   // until the stages fill
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int row0 = blockIdx.x * kLowRows, r0 = blockIdx.z * 32;
@@ -128,6 +130,7 @@ __global__ __launch_bounds__(256, NS <= 4 ? 2 : 1) void low_kernel(const LoraArg
   lds_barrier();
   const bool row_ok = row0 + l32 < a.T;
   const int mine = row_ok ? ad_of[l32] : -1;
+  lds_barrier();
   if (blockIdx.y == 0 && blockIdx.z == 0 && wave == 0 && half == 0 && row_ok)
     a.adapter_of[row0 + l32] = mine;
 
@@ -686,10 +689,8 @@ template <int DT, bool Runs>
 __global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low_jobs) {
   constexpr int EB = Elem<DT>::bytes, NS = 4;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * kStage32];
-  __shared__ int dropped;   // whether values of B were not finite
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
-  if (threadIdx.x == 0) dropped = 0;
   const int tiles_n = (a.N + 31) / 32;
   int block = blockIdx.x, split = 0;
   if constexpr (Runs) {
@@ -713,6 +714,7 @@ __global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low
   offsets32(off + 2, a.N - n0, row);
   float16_t acc = {};
   product32<DT, NS>(rx, rw, off, Runs && begin + a.run < row ? a.run : row - begin, lds, acc);
+  int dropped = 0;   // whether values of B were not finite
   if (!Runs && a.n_adapters > 0) {
     constexpr int LB = DT == DT_F32 ? 4 : 2;
     const __amdgpu_buffer_rsrc_t rl =
@@ -736,7 +738,9 @@ __global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low
     }
   }
   float(*red)[32][36] = reinterpret_cast<float(*)[32][36]>(lds);
+  int* flags = reinterpret_cast<int*>(lds + 4 * 32 * 36 * 4);
   lds_barrier();
+  if (lane == 0) flags[wave] = dropped;
 #pragma unroll
   for (int r = 0; r < 4; ++r)
     *reinterpret_cast<float4_t*>(&red[wave][l32][8 * r + 4 * half]) =
@@ -754,7 +758,7 @@ __global__ __launch_bounds__(256, 2) void small_kernel(const LoraArgs a, int low
     store_part(a, split, m0 + t, n0 + n, float4_t{v[0], v[1], v[2], v[3]});
   else if (m0 + t < a.T && n0 + n < a.N) {
     store4<DT>(a, m0 + t, n0 + n, v);
-    if (dropped)
+    if (flags[0] | flags[1] | flags[2] | flags[3])
       for (int j = 0; j < 4; ++j)
         if (n0 + n + j < a.N) add_not_finite<DT>(a, m0 + t, n0 + n + j);
   }
