@@ -851,9 +851,12 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(const LoraArgs a
 // Four waves take 16 outputs each and a run of the sum's axis: x arrives in
 // LDS, W straight in registers (each of its values has one reader), all of a
 // run on its way at once.  The first `low_jobs` workgroups take the low-rank
-// values meanwhile.  64 rows, 4096 -> 4096, rank 16 in bf16: 13.5 us (42 MB, and
-// x from L2 for each 64 outputs).
-constexpr int kRun = 1024;   // bytes of a run, at most
+// values meanwhile.  64 rows, 4096 -> 4096, rank 16 in bf16: 13 us (42 MB, and x
+// from L2 for each 64 outputs).
+// Bytes of a run, at most: x of 64 rows then takes 48 KB, and three workgroups
+// share a compute unit (4096 -> 4096, 64 rows 16.7 us with the sum; runs of 1024
+// 17.4, of 512 17.8; a row of 4160 17.1, 19.6 and 18.8).
+constexpr int kRun = 768;
 template <int DT, int RB>
 __global__ __launch_bounds__(256, 2) void run_kernel(const LoraArgs a, int low_jobs) {
   constexpr int EB = Elem<DT>::bytes, ROWS = 16 * RB, STEPS = kRun / 64;
