@@ -1,9 +1,11 @@
-"""Build libconv.so (HIP, gfx950) in-tree.
+"""Build libconv.so (HIP, gfx950) and _torch_calls.so (host C++) in-tree.
 
     python -m direct_implicit_gemm_amd.build [--sanitize]
 
 Compiles each source with hipcc for gfx950 only, in parallel, and links the
-shared library next to this file.  Every build recompiles.
+shared library next to this file; _torch_calls.so (csrc/torch_calls.cpp) looks
+torch's tensors over for the attention-layer operators and is built with g++
+against torch's headers.  Every build recompiles.
 
 --sanitize builds libconv_san.so instead: the host code (validation, output
 extents, planning, the chunk and frame-window arithmetic, the launch
@@ -24,6 +26,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libconv.so")
+CALLS_PATH = os.path.join(HERE, "_torch_calls.so")
 SAN_LIB_PATH = os.path.join(HERE, "libconv_san.so")
 # host-only sanitizer flags: each -fsanitize= applies to the host pass only
 SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
@@ -35,6 +38,7 @@ SOURCES = ["api.cpp", "direct.hip", "igemm.hip", "layout.hip",
            "igemm_inst_a.hip", "igemm_inst_b.hip", "igemm_inst_c.hip", "igemm_inst_d.hip",
            "igemm_inst_e.hip"]
 
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950",
@@ -85,12 +89,31 @@ def _check_stubs(lib: str) -> None:
         raise RuntimeError("kernel launch stubs missing from libconv.so:\n" + "\n".join(missing))
 
 
+def _build_calls() -> None:
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")   # found, not imported
+    if spec is None:
+        raise RuntimeError("torch is not installed: _torch_calls.so is built against its headers")
+    torch = list(spec.submodule_search_locations)[0]
+    out_tmp = CALLS_PATH + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Werror", "-I", INCLUDE,
+           "-isystem", os.path.join(torch, "include"), "-I", sysconfig.get_path("include"),
+           os.path.join(CSRC, "torch_calls.cpp"), "-o", out_tmp,
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for torch_calls.cpp:\n{r.stderr}")
+    os.replace(out_tmp, CALLS_PATH)
+
+
 def build(verbose: bool = True, sanitize: bool = False) -> str:
     extra = SAN_FLAGS if sanitize else []
     out = SAN_LIB_PATH if sanitize else LIB_PATH
     with tempfile.TemporaryDirectory(prefix="libconv_build_") as tmp:
         objs = [os.path.join(tmp, s.rsplit(".", 1)[0] + ".o") for s in SOURCES]
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
+            calls = None if sanitize else ex.submit(_build_calls)
             list(ex.map(lambda a: _compile(*a, extra), zip(SOURCES, objs)))
         out_tmp = out + ".tmp"
         cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *extra, "-o", out_tmp, *objs]
@@ -98,7 +121,7 @@ def build(verbose: bool = True, sanitize: bool = False) -> str:
         _check_stubs(out_tmp)
         os.replace(out_tmp, out)
     if verbose:
-        print(f"built {out}")
+        print(f"built {out}" + ("" if sanitize else f", {CALLS_PATH}"))
     return out
 
 
