@@ -105,8 +105,8 @@ __device__ __forceinline__ void product32(__amdgpu_buffer_rsrc_t rx, __amdgpu_bu
 // (16-bit types) width high bfloat16 parts and then width low parts.  Values
 // from the rank on are 0.  Grid: row tiles x shares of the adapters of a tile
 // x 32 of the rank.  Bound by latency (a stage 0.28 us) and by what a compute
-// unit reads of L2: 2167 rows of 1280, rank 64 in 10 us, 8192 rows of 4096, rank
-// 32 in 26 us (67 MB of x; registers in place of LDS: 34 us).
+// unit reads of L2: 2167 rows of 1280, rank 64 in 8.6 us, 8192 rows of 4096, rank
+// 32 in 24 us (67 MB of x; registers in place of LDS: 34 us).
 template <int DT, int NS>
 __global__ __launch_bounds__(256, NS <= 4 ? 2 : 1) void low_kernel(const LoraArgs a) {
   constexpr int EB = Elem<DT>::bytes, THREADS = 256;
@@ -470,7 +470,7 @@ __device__ __forceinline__ void store_part(const LoraArgs& a, int split, int t, 
 // BM tokens x BN outputs, WM x WN waves, NS stages in LDS or on their way.  Runs: the
 // first `low_jobs` workgroups form low-rank values, the others the sums of a
 // run of the sum's axis.  Bound by the matrix units in 256 x 256 tiles: 8192
-// rows, 4096 -> 8192 in bf16 462 us with the low-rank term of rank 32, 437
+// rows, 4096 -> 8192 in bf16 450-490 us with the low-rank term of rank 32, 437
 // without it (1.27 PFLOP/s); in 128 x 128 tiles 2167 rows, 1280 -> 3840 in fp16
 // 44 and 29 us.
 template <int DT, int BM, int BN, int WM, int WN, int NS, bool Runs>
@@ -851,7 +851,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(const LoraArgs a
 // Four waves take 16 outputs each and a run of the sum's axis: x arrives in
 // LDS, W straight in registers (each of its values has one reader), all of a
 // run on its way at once.  The first `low_jobs` workgroups take the low-rank
-// values meanwhile.  64 rows, 4096 -> 4096, rank 16 in bf16: 13 us (42 MB, and x
+// values meanwhile.  64 rows, 4096 -> 4096, rank 16 in bf16: 12 us (42 MB, and x
 // from L2 for each 64 outputs).
 // Bytes of a run, at most: x of 64 rows then takes 48 KB, and three workgroups
 // share a compute unit (4096 -> 4096, 64 rows 16.7 us with the sum; runs of 1024
