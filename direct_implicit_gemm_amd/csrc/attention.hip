@@ -596,9 +596,10 @@ __device__ __forceinline__ int xcd_order(int id, int n) {
 }
 
 // Each entry's rows over its prefix and own keys.  130 queries of 2 entries, 8
-// heads of 64 over 333 + 190 keys in fp32: 17 us (bound by the fp32 matrix
-// instructions of 80 workgroups); one query of 4 entries, 20 heads of 64 over
-// 1000 keys in bf16: 11 us (the chain of a workgroup's 8 tiles).
+// heads of 64 over 333 + 190 keys in fp32: 14 us, and 3 of the join (bound by
+// the fp32 matrix instructions of 160 workgroups); one query of 4 entries, 20
+// heads of 64 over 1000 keys in bf16: 10 us (the keys that one workgroup's
+// compute unit reads, 256 KB; eight waves instead of four: 10 us).
 template <int DT, int DP, int WK>
 __global__ __launch_bounds__(kThreads, fit((Shape<DT, DP, WK>::LDS))) void attn_kernel(
     const AttnArgs a) {
@@ -803,14 +804,20 @@ long long attn_plan(AttnArgs* a, int dtype, int cus, bool allowed) {
   a->chunk = 0;
   a->waves = key_waves(per_entry, (long long)a->B * a->Hk);
   if (!allowed || all == 0) return 0;
-  // Few keys: one launch, and nothing to join.  Measured for one query of 4
-  // entries with 8 key heads, heads of 64 in 16 bits (128 bytes a key): 552 keys
-  // 8.5 us against 8.9 in two launches, 1000 keys 10.6 against 9.6, where the
-  // second launch and the workspace take the host another 4 us; 1540 keys 12.8
-  // against 9.7.  Heads of 128: 552 keys 11.2 against 11.6, 1000 keys 14.2
-  // against 12.7.
+  // Few keys: one launch, no workspace and nothing to join.  Measured, calls in
+  // a row (in a graph), one launch against two: one query of 4 entries with 20
+  // key heads of 64 in 16 bits, 520 keys 8.3 us (8.0) against 10.7 (9.7), 760
+  // keys 9.2 (9.1) against 10.2 (9.2), 1000 keys 10.4 (10.4) against 9.7 (9.3),
+  // which a workspace is not worth; 12 entries (240 workgroups), 760 keys 9.9
+  // (10.0) against 10.5 (9.6), 1000 keys 11.9 (12.3) against 10.2 (9.6); heads
+  // of 128, 552 keys 10.9 (10.6) against 13.2 (12.4), 1000 keys 14.2 (14.0)
+  // against 12.6 (11.7); fp32 of 64, 440 keys 17.3 (17.1) against 18.4 (17.4),
+  // 130 queries over 523 keys 17.4 (17.4) against 16.4 (15.6).
+  const long long keys = a->P + (long long)a->S, sets = (long long)a->B * a->Hk;
   const long long key_bytes = a->D * (dtype == LIBCONV_F32 ? 4LL : 2LL);
-  if (a->waves == 4 && ((long long)a->P + a->S) * key_bytes <= 160 * 1024) return 0;
+  if (a->waves == 4 && (keys <= (dtype == LIBCONV_F32 ? 512 : 768) ||
+                        (sets <= kPlanCus / 2 && keys * key_bytes <= 128 * 1024)))
+    return 0;
   // Splits so that `groups` workgroups become `want`, each with `least` keys
   // or more.
   auto split = [&](long long want, long long groups, long long keys, long long least) {
