@@ -36,7 +36,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLowest = -3.402823466e38f;   // the maximum of no keys: finite, so that no
                                               // difference of maxima is a NaN
-constexpr float kSlack = 8.0f;   // log2 of how far a maximum may fall behind
+// log2 of how far a maximum may fall behind (lazy), and of what the
+// probabilities are multiplied by.  fp16 ends at 2^-24: probabilities below
+// 2^-25 of the largest would vanish from the second product and still count in
+// the sum, and those below 2^-14 lose bits.  Multiplied by 2^15, less the slack,
+// the largest stays below 2^16, and 2^-36 (2^-40 where the maximum is exact) is
+// what vanishes; the sum is multiplied alike, so the quotient needs no care.
+// bfloat16 ends where fp32 does.
+template <int DT> constexpr float slack() { return DT == DT_F16 ? 4.0f : 8.0f; }
+template <int DT, bool Lazy> constexpr float lift() {
+  return DT != DT_F16 ? 0.0f : Lazy ? 15.0f - slack<DT>() : 15.0f;
+}
 
 template <int DT, int DP, int WK> struct Shape {
   static_assert(WK == 1 || WK == 4, "rows or keys split over the four waves");
@@ -160,6 +170,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
   constexpr int KS = DP * EB / 32;  // steps of the first product
   constexpr int NB = KPW / 32;      // blocks of 32 keys a wave
   constexpr int DB = DP / 32;       // blocks of 32 components
+  constexpr float LIFT = lift<DT, EB == 2 && WK == 1>();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int wr = wave / WK, wk = wave % WK;   // row block, key share
@@ -297,11 +308,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
     for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
     return swap_halves_max(top) * a.scale;
   };
-  // probabilities times 2^(their maximum - m), added to the sum
+  // probabilities times 2^(LIFT + their maximum - m), added to the sum
   auto probabilities = [&](float16_t& s) {
+    const float base = LIFT == 0.0f ? -m : LIFT - m;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale, -m));
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale, base));
       l += s[r];
     }
   };
@@ -348,11 +360,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
     float16_t s0, s1;      // scores of two blocks
     u32x4_t p0[2], p1[2];  // probabilities of two blocks
     float f;               // what a block's maximum makes of the sums so far
-    // The maximum moves only when it falls behind by 2^8, which fp16
-    // probabilities bear too: the sums are hardly ever rescaled.
+    // The maximum moves only when it falls behind by 2^slack: the sums are
+    // hardly ever rescaled.
     auto move_up = [&](const float16_t& s) {
       const float top = top_of(s);
-      const float m_new = top > m + kSlack ? top : m;
+      const float m_new = top > m + slack<DT>() ? top : m;
       f = __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
       l *= f;
@@ -552,7 +564,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
 
   if (!row_ok) return;
   const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
-  const float lse2 = l == 0.0f ? kNegInf : m + __builtin_amdgcn_logf(l);
+  const float lse2 = l == 0.0f ? kNegInf : m + (__builtin_amdgcn_logf(l) - LIFT);
   if (job.slot >= 0) {
     const long long at = ((long long)job.slot * a.Hk + job.hk) * ((long long)a.B * per_entry) + row;
     if (half == 0) a.part_lse[at] = lse2;

@@ -621,7 +621,8 @@ libconv_status libconv_qk_norm_rope(const void* q, const void* k, const void* v,
  * into any result, whatever they hold; a non-finite value in a row that a
  * causal mask hides from a query can reach that query.
  * Scores, softmax and sums are fp32; the probabilities are rounded to the
- * dtype for the second product and `out` is rounded once.
+ * dtype for the second product (fp16: scaled first, so that those down to 2^-36
+ * of a query's largest count) and `out` is rounded once.
  *   workspace  device, 256-byte aligned, at least
  *             libconv_prefix_attention_workspace bytes for the best plan,
  *             which reads the prefix once for all entries and splits long
