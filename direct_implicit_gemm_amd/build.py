@@ -5,7 +5,9 @@
 Compiles each source with hipcc for gfx950 only, in parallel, and links the
 shared library next to this file; _torch_calls.so (csrc/torch_calls.cpp) looks
 torch's tensors over for the attention-layer operators and is built with g++
-against torch's headers.  Every build recompiles.
+against torch's headers.  Every build recompiles; if either fails, build()
+raises and both stay as they were (one calls the other by address, so that they
+have to be of the same sources).
 
 --sanitize builds libconv_san.so instead: the host code (validation, output
 extents, planning, the chunk and frame-window arithmetic, the launch
@@ -89,14 +91,13 @@ def _check_stubs(lib: str) -> None:
         raise RuntimeError("kernel launch stubs missing from libconv.so:\n" + "\n".join(missing))
 
 
-def _build_calls() -> None:
+def _build_calls(out_tmp: str) -> None:
     import importlib.util
     import sysconfig
     spec = importlib.util.find_spec("torch")   # found, not imported
     if spec is None:
         raise RuntimeError("torch is not installed: _torch_calls.so is built against its headers")
     torch = list(spec.submodule_search_locations)[0]
-    out_tmp = CALLS_PATH + ".tmp"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Werror", "-I", INCLUDE,
            "-isystem", os.path.join(torch, "include"), "-I", sysconfig.get_path("include"),
            os.path.join(CSRC, "torch_calls.cpp"), "-o", out_tmp,
@@ -104,22 +105,30 @@ def _build_calls() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed for torch_calls.cpp:\n{r.stderr}")
-    os.replace(out_tmp, CALLS_PATH)
 
 
 def build(verbose: bool = True, sanitize: bool = False) -> str:
     extra = SAN_FLAGS if sanitize else []
     out = SAN_LIB_PATH if sanitize else LIB_PATH
-    with tempfile.TemporaryDirectory(prefix="libconv_build_") as tmp:
-        objs = [os.path.join(tmp, s.rsplit(".", 1)[0] + ".o") for s in SOURCES]
-        with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
-            calls = None if sanitize else ex.submit(_build_calls)
-            list(ex.map(lambda a: _compile(*a, extra), zip(SOURCES, objs)))
-        out_tmp = out + ".tmp"
-        cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *extra, "-o", out_tmp, *objs]
-        subprocess.run(cmd, check=True, capture_output=True, text=True)
-        _check_stubs(out_tmp)
+    out_tmp, calls_tmp = out + ".tmp", CALLS_PATH + ".tmp"
+    try:
+        with tempfile.TemporaryDirectory(prefix="libconv_build_") as tmp:
+            objs = [os.path.join(tmp, s.rsplit(".", 1)[0] + ".o") for s in SOURCES]
+            with concurrent.futures.ThreadPoolExecutor(max_workers=min(len(SOURCES), 8)) as ex:
+                calls = None if sanitize else ex.submit(_build_calls, calls_tmp)
+                list(ex.map(lambda a: _compile(*a, extra), zip(SOURCES, objs)))
+            if calls:
+                calls.result()   # raises what the compilation raised
+            cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *extra, "-o", out_tmp, *objs]
+            subprocess.run(cmd, check=True, capture_output=True, text=True)
+            _check_stubs(out_tmp)
         os.replace(out_tmp, out)
+        if calls:
+            os.replace(calls_tmp, CALLS_PATH)
+    finally:
+        for left in (out_tmp, calls_tmp):
+            if os.path.exists(left):
+                os.remove(left)
     if verbose:
         print(f"built {out}" + ("" if sanitize else f", {CALLS_PATH}"))
     return out
