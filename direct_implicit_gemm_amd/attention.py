@@ -5,7 +5,11 @@
     prefix_attention   attention over keys a batch shares and each entry's own
 
 They allocate outputs (and workspaces, through torch), enqueue on the current
-stream or ``stream``, and raise ``LibconvError`` on a status other than OK.
+stream or ``stream`` (a handle), and raise ``LibconvError`` on a status other than
+OK.  What they allocate for another ``stream`` than the current one is allocated
+there, as under ``torch.cuda.stream``; an output may be dropped at any time.  That
+the stream waits for the operands, and the reader for the stream, and that operands
+live until the stream is done with them, is the caller's affair.
 Tensors may be strided (slices of a fused projection, caches in any order of
 axes) as long as their last axis is dense and their rows lie on 16-byte
 boundaries.  There is no backward pass: libconv runs networks forward.
@@ -28,9 +32,8 @@ def _load():
     import direct_implicit_gemm_amd as L
     global _calls
 
-    def record(buffer, stream, device):
-        # a workspace that torch allocated: its memory is that stream's until then
-        buffer.record_stream(torch.cuda.ExternalStream(stream, device=device))
+    def stream_id(handle, device):
+        return torch.cuda.ExternalStream(handle, device=device).stream_id
 
     def fail(status, what):
         raise L.LibconvError(status, what)
@@ -47,7 +50,7 @@ def _load():
                  lib.libconv_lora_workspace)
     calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in functions),
                # as torch.cuda.current_stream() has it, without the object
-               getattr(torch._C, "_cuda_getCurrentRawStream", None), record, fail)
+               getattr(torch._C, "_cuda_getCurrentRawStream", None), stream_id, fail)
     _calls = calls
     return calls
 

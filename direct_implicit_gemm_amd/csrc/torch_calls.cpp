@@ -11,9 +11,12 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/StreamGuard.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 
 #include <cmath>
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "libconv.h"
@@ -25,9 +28,9 @@ decltype(&libconv_prefix_attention) attention_call;
 decltype(&libconv_prefix_attention_workspace) attention_workspace;
 decltype(&libconv_lora_linear) lora_call;
 decltype(&libconv_lora_workspace) lora_workspace;
-// raw_stream(device) -> handle of the current stream; record(tensor, handle,
-// device): its memory is in use on that stream; fail(status, name) raises
-PyObject *raw_stream, *record, *fail;
+// raw_stream(device) -> handle of the current stream; stream_id(handle, device)
+// -> torch's number of any stream; fail(status, name) raises
+PyObject *raw_stream, *stream_id, *fail;
 
 constexpr const char* kOperands =
     "operands must be device tensors of one device and dtype, their last axis dense";
@@ -91,27 +94,50 @@ struct Unlocked {
   ~Unlocked() { PyEval_RestoreThread(state); }
 };
 
-// The stream of a call and, where it is asked for, the workspace.
+// The stream of a call, its outputs and, where it is asked for, its workspace.
+// torch's allocator hands freed memory out again in the order of the stream it
+// was allocated on: outputs and workspaces of a call are allocated with the
+// call's stream as the current one, so that neither work still queued on the
+// caller's stream nor the call itself meets another user of the same memory.
 struct Call {
   c10::DeviceGuard guard;
   const Kind& kind;
-  PyObject* given;   // the caller's stream, or None
+  c10::OptionalStreamGuard on_stream;
+  std::optional<c10::Stream> callers;   // the caller's stream, where it is another one
   void* stream = nullptr;
   at::Tensor buffer;
   void* ws = nullptr;
   long long bytes = 0;
 
-  Call(const Kind& k, PyObject* stream_arg) : guard(k.device), kind(k), given(stream_arg) {
-    PyObject* handle = given;
-    if (given == Py_None) {
-      PyObject* index = PyLong_FromLong(k.device.index());
-      handle = index ? PyObject_CallOneArg(raw_stream, index) : nullptr;
-      Py_XDECREF(index);
-      if (!handle) throw python_error();
-    }
+  Call(const Kind& k, PyObject* given) : guard(k.device), kind(k) {
+    PyObject* index = PyLong_FromLong(k.device.index());
+    PyObject* handle = index ? PyObject_CallOneArg(raw_stream, index) : nullptr;
+    Py_XDECREF(index);
+    if (!handle) throw python_error();
     stream = PyLong_AsVoidPtr(handle);
-    if (given == Py_None) Py_DECREF(handle);
+    Py_DECREF(handle);
     if (PyErr_Occurred()) throw python_error();
+    if (given == Py_None) return;
+    void* const current = stream;
+    stream = PyLong_AsVoidPtr(given);
+    if (PyErr_Occurred()) throw python_error();
+    if (stream == current) return;
+    PyObject* id = PyObject_CallFunction(stream_id, "Oi", given, (int)k.device.index());
+    const long long number = id ? PyLong_AsLongLong(id) : -1;
+    Py_XDECREF(id);
+    if (PyErr_Occurred()) throw python_error();
+    callers = c10::impl::VirtualGuardImpl(k.device.type()).getStream(k.device);
+    on_stream.reset_stream(c10::Stream::unpack3(number, k.device.index(), k.device.type()));
+  }
+  // An output: the caller, who reads it on a stream of theirs, may drop it while
+  // that stream still does.
+  at::Tensor fresh(at::ScalarType type, std::initializer_list<int64_t> shape) {
+    at::Tensor t = at::empty(c10::IntArrayRef(shape),
+                             at::TensorOptions().dtype(type).device(kind.device));
+    if (callers)
+      c10::impl::VirtualGuardImpl(kind.device.type())
+          .recordDataPtrOnStream(t.storage().data_ptr(), *callers);
+    return t;
   }
   // workspace: True (allocate `need` bytes), None or False (none), or a tensor
   void workspace(const char* what, PyObject* o, long long need) {
@@ -134,14 +160,6 @@ struct Call {
       Unlocked other_threads_run;
       status = enqueue();
     }
-    if (buffer.defined() && given != Py_None) {
-      PyObject* t = THPVariable_Wrap(buffer);
-      PyObject* r = t ? PyObject_CallFunction(record, "OOi", t, given, (int)kind.device.index())
-                      : nullptr;
-      Py_XDECREF(t);
-      if (!r) throw python_error();
-      Py_DECREF(r);
-    }
     if (status != LIBCONV_OK) {
       PyObject* r = PyObject_CallFunction(fail, "is", (int)status, name);
       Py_XDECREF(r);
@@ -150,10 +168,6 @@ struct Call {
   }
 };
 
-at::Tensor fresh(const at::Tensor& like, std::initializer_list<int64_t> shape) {
-  return at::empty(c10::IntArrayRef(shape),
-                   at::TensorOptions().dtype(like.scalar_type()).device(like.device()));
-}
 // The caller's tensor again, or the one made for the call.
 PyObject* result(PyObject* given, const at::Tensor& t) {
   if (given == Py_None) {
@@ -233,10 +247,11 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if ((qo && bad(*qo, kind, {T, Hq, D})) || (ko && bad(*ko, kind, {rows, Hk, D})) ||
       (vo && bad(*vo, kind, {rows, Hk, D})))
     refuse(what, "bad output tensor");
+  Call call(kind, a[14]);
   at::Tensor made[3];
-  if (!qo) qo = &(made[0] = fresh(q, {T, Hq, D}));
-  if (!ko) ko = &(made[1] = fresh(q, {T, Hk, D}));
-  if (v && !vo) vo = &(made[2] = fresh(q, {T, Hk, D}));
+  if (!qo) qo = &(made[0] = call.fresh(kind.type, {T, Hq, D}));
+  if (!ko) ko = &(made[1] = call.fresh(kind.type, {T, Hk, D}));
+  if (v && !vo) vo = &(made[2] = call.fresh(kind.type, {T, Hk, D}));
   if (T > 0) {
     const at::Tensor* in[6] = {&q, &k, v, qo, ko, vo};
     long long strides[12] = {};
@@ -248,7 +263,6 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int t = as_int(what, T), hq = as_int(what, Hq), hk = as_int(what, Hk),
               d = as_int(what, D), out_rows = as_int(what, rows), interleaved = truth(a[8]);
     const float eps = (float)number(a[6]);
-    Call call(kind, a[14]);
     call.run("libconv_qk_norm_rope", [&] {
       return rope_call(q.const_data_ptr(), k.const_data_ptr(), address(v), qo->mutable_data_ptr(),
                        ko->mutable_data_ptr(), vo ? vo->mutable_data_ptr() : nullptr, address(qw),
@@ -298,11 +312,11 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (bad_array(lengths, kind, at::kInt, {B}))
     refuse(what, "lengths must be a contiguous int32 device tensor [B]");
   if (out && bad(*out, kind, {B, Sq, Hq, D})) refuse(what, "bad output tensor");
-  at::Tensor made, lse;
-  if (!out) out = &(made = fresh(q, {B, Sq, Hq, D}));
   const bool with_lse = truth(a[9]);
-  if (with_lse)
-    lse = at::empty({B, Hq, Sq}, at::TensorOptions().dtype(at::kFloat).device(kind.device));
+  Call call(kind, a[10]);
+  at::Tensor made, lse;
+  if (!out) out = &(made = call.fresh(kind.type, {B, Sq, Hq, D}));
+  if (with_lse) lse = call.fresh(at::kFloat, {B, Hq, Sq});
   if (B > 0 && Sq > 0) {
     long long strides[16] = {};
     auto put = [&](int at, const at::Tensor* t, int axes) {
@@ -318,7 +332,6 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
               hq = as_int(what, Hq), hk = as_int(what, Hk), d = as_int(what, D);
     const float scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)number(a[6]);
     const int with_causal = truth(a[7]);
-    Call call(kind, a[10]);
     call.workspace(what, a[11],
                    a[11] == Py_True ? attention_workspace(b, sq, p, s, hq, hk, d, kind.code) : 0);
     call.run("libconv_prefix_attention", [&] {
@@ -370,12 +383,12 @@ PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     refuse(what, "a, b, scales, row_starts and adapters come together");
   }
   if (out && bad(*out, kind, {T, N})) refuse(what, "bad output tensor");
+  Call call(kind, a[9]);
   at::Tensor made;
-  if (!out) out = &(made = fresh(x, {T, N}));
+  if (!out) out = &(made = call.fresh(kind.type, {T, N}));
   if (T > 0) {
     const int t = as_int(what, T), kk = as_int(what, K), nn = as_int(what, N),
               r = as_int(what, rank), c = as_int(what, count), q = as_int(what, R);
-    Call call(kind, a[9]);
     call.workspace(what, a[10],
                    a[10] == Py_True ? lora_workspace(t, kk, nn, r, c, q, kind.code) : 0);
     call.run("libconv_lora_linear", [&] {
@@ -391,8 +404,8 @@ PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The addresses of the five functions (in the order above), raw_stream, record,
-// fail.
+// The addresses of the five functions (in the order above), raw_stream,
+// stream_id, fail.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 8) refuse_type("bind", "8 arguments");
@@ -404,7 +417,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   attention_workspace = reinterpret_cast<decltype(attention_workspace)>(f[2]);
   lora_call = reinterpret_cast<decltype(lora_call)>(f[3]);
   lora_workspace = reinterpret_cast<decltype(lora_workspace)>(f[4]);
-  PyObject** keep[3] = {&raw_stream, &record, &fail};
+  PyObject** keep[3] = {&raw_stream, &stream_id, &fail};
   for (int i = 0; i < 3; ++i) {
     Py_INCREF(a[5 + i]);
     Py_XDECREF(*keep[i]);
