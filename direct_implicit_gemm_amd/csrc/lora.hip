@@ -34,15 +34,20 @@ __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-// Low-rank value r of a row, at the row's values.
+// Low-rank value r of a row, at the row's values.  The high part is always
+// finite: an infinity or a NaN is the low part beside a 0, because fp16 B's low
+// part (mostly 0) is multiplied by the high part too, and 0 times an infinity
+// would be a NaN.
 template <int DT>
 __device__ __forceinline__ void store_low(const LoraArgs& a, unsigned char* at, int r, float v) {
   if constexpr (DT == DT_F32) {
     reinterpret_cast<float*>(at)[r] = v;
   } else {
-    const uint16_t hi = Elem<DT_BF16>::from_f32(v);
-    // (an infinity has no rest)
-    const float rest = (hi & 0x7f80u) == 0x7f80u ? 0.0f : v - Elem<DT_BF16>::bits_to_f32(hi);
+    const bool finite = __builtin_isfinite(v);
+    uint16_t hi = Elem<DT_BF16>::from_f32(v);
+    // (a value that would be rounded to an infinity keeps the largest number)
+    if ((hi & 0x7f80u) == 0x7f80u) hi = finite ? hi - 1 : 0;
+    const float rest = finite ? v - Elem<DT_BF16>::bits_to_f32(hi) : v;
     reinterpret_cast<uint16_t*>(at)[r] = hi;
     reinterpret_cast<uint16_t*>(at)[a.low_width + r] = Elem<DT_BF16>::from_f32(rest);
   }
@@ -175,9 +180,11 @@ __global__ __launch_bounds__(256, NS <= 4 ? 2 : 1) void low_kernel(const LoraArg
   lds_barrier();
   for (int i = threadIdx.x; i < 32 * 32; i += THREADS) {
     const int t = i >> 5, r = i & 31;
+    // (past the rank, an infinity of x times the 0 that stands for A is no 0)
     if (rows >> t & 1)
       store_low<DT>(a, a.low + (long long)(row0 + t) * a.low_width * 4, r0 + r,
-                    red[0][t][r] + red[1][t][r] + red[2][t][r] + red[3][t][r]);
+                    r0 + r < a.rank ? red[0][t][r] + red[1][t][r] + red[2][t][r] + red[3][t][r]
+                                    : 0.0f);
   }
 }
 
@@ -269,11 +276,13 @@ __device__ __forceinline__ void low_step(const u32x4_t& bf, const u32x4_t& hi, c
   }
 }
 
-// Where tokens of several adapters share a block, the others' low-rank values
-// are 0 for an adapter's step, but 0 times an infinity or a NaN of its B would
-// reach them.  Such values take no part in the step: drop_not_finite sets them
-// to 0, and add_not_finite adds what they give their own tokens to the written
-// outputs (which are not finite then, whatever else they are).
+// An infinity or a NaN of B is not for the matrix instructions.  Where tokens of
+// several adapters share a block, the others' low-rank values are 0 for an
+// adapter's step, and 0 times it would reach them; and of a low-rank value in two
+// parts, the low one may be 0 or of the other sign.  drop_not_finite puts 1 with
+// its sign in its place (no 0: the low-rank value may itself be an infinity), and
+// add_not_finite adds what it gives its own tokens to the written outputs (which
+// are not finite then, whatever else they are).
 template <int DT>
 __device__ __forceinline__ bool drop_not_finite(u32x4_t& v) {
   bool any = false;
@@ -282,18 +291,36 @@ __device__ __forceinline__ bool drop_not_finite(u32x4_t& v) {
     uint32_t w = v[j];
     if constexpr (DT == DT_F32) {
       const bool bad = (w & 0x7f800000u) == 0x7f800000u;
-      w = bad ? 0u : w;
+      w = bad ? (w & 0x80000000u) | 0x3f800000u : w;
       any = any || bad;
     } else {
-      constexpr uint32_t E = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+      constexpr uint32_t E = DT == DT_F16 ? 0x7c00u : 0x7f80u, ONE = DT == DT_F16 ? 0x3c00u : 0x3f80u;
       const bool low = (w & E) == E, high = (w & (E << 16)) == E << 16;
-      w &= low ? 0xffff0000u : 0xffffffffu;
-      w &= high ? 0x0000ffffu : 0xffffffffu;
+      w = low ? (w & 0xffff8000u) | ONE : w;
+      w = high ? (w & 0x8000ffffu) | ONE << 16 : w;
       any = any || low || high;
     }
     v[j] = w;
   }
   return any;
+}
+// The largest magnitudes so far of a word's values, and whether they are not
+// finite: fewer instructions than dropping, which is hardly ever needed.
+template <int DT> __device__ __forceinline__ uint32_t largest(uint32_t so_far, uint32_t w) {
+  if constexpr (DT == DT_F32) {
+    w &= 0x7fffffffu;
+    return so_far > w ? so_far : w;
+  } else {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
+                                            __builtin_bit_cast(u16x2_t, so_far),
+                                            __builtin_bit_cast(u16x2_t, w & 0x7fff7fffu)));
+  }
+}
+template <int DT> __device__ __forceinline__ bool not_finite(uint32_t top) {
+  if constexpr (DT == DT_F32) return top >= 0x7f800000u;
+  constexpr uint32_t E = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+  return (top & 0xffffu) >= E || (top >> 16) >= E;
 }
 // Output n of token t, written by this lane.
 template <int DT>
@@ -311,7 +338,8 @@ __device__ __forceinline__ void add_not_finite(const LoraArgs& a, int t, int n) 
       v = reinterpret_cast<const float*>(low)[r];
     } else {
       w = Elem<DT>::bits_to_f32(reinterpret_cast<const uint16_t*>(b)[r]);
-      v = Elem<DT_BF16>::bits_to_f32(reinterpret_cast<const uint16_t*>(low)[r]);
+      v = Elem<DT_BF16>::bits_to_f32(reinterpret_cast<const uint16_t*>(low)[r]) +
+          Elem<DT_BF16>::bits_to_f32(reinterpret_cast<const uint16_t*>(low)[a.low_width + r]);
     }
     if (!__builtin_isfinite(w)) extra = fmaf(w, v, extra);
   }
@@ -592,11 +620,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LoraArgs a,
             bf[u][i] = load_b<DT>(a, rb, n0 + (wn * NB + i) * 32 + l32, off / LB);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (mixed) {
+        if (mixed || DT != DT_F32) {
+          uint32_t top = 0;
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < NB; ++i) dropped |= drop_not_finite<DT>(bf[u][i]);
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top = largest<DT>(top, bf[u][i][j]);
+          if (__any(not_finite<DT>(top))) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int i = 0; i < NB; ++i) dropped |= drop_not_finite<DT>(bf[u][i]);
+          }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)

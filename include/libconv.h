@@ -662,7 +662,7 @@ long long libconv_prefix_attention_workspace(int B, int Sq, int P, int S, int q_
  * 16 significant bits) and y is rounded once.
  * K: a multiple of 8; rank 1 to 128; x, w, a, b on 16-byte boundaries; rows of
  * x and w below 2^23 bytes, T below 2^26 - 64.  An infinity or a NaN of one
- * adapter stays with its own rows.
+ * adapter stays with its own rows, and gives there what the formula gives.
  * n_adapters or n_requests 0: the projection alone (a, b, scales, row_starts
  * and adapters may be NULL).
  *   workspace  device, 256-byte aligned, at least libconv_lora_workspace
