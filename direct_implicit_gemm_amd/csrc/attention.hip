@@ -839,14 +839,17 @@ long long attn_plan(AttnArgs* a, int dtype, int cus, bool allowed) {
   };
   const long long groups = a->B * a->Hk * row_tiles(per_entry, a->waves);
   // The prefix once for all entries: with few rows an entry, reading it for
-  // each of them would be what the call spends its time on.
-  if (a->B > 1 && per_entry <= 64 && a->P >= 128) {
+  // each of them would be what the call spends its time on.  (Its workgroups
+  // come on top of the entries', whose number is bounded by what a launch
+  // holds: the most entries read it each.)
+  const long long prefix_groups = a->Hk * row_tiles(all, all <= 64 ? 4 : 1);
+  if (a->B > 1 && per_entry <= 64 && a->P >= 128 && groups + prefix_groups < (1 << 24)) {
     a->shared = 1;
     // (a share of the prefix leaves a partial result of every row: few with
     // many rows)
     a->waves = 4;
     a->prefix_waves = all <= 64 ? 4 : 1;
-    a->prefix_splits = split(2LL * cus, a->Hk * row_tiles(all, a->prefix_waves), a->P, 256);
+    a->prefix_splits = split(2LL * cus, prefix_groups, a->P, 256);
     if (all > 64 && a->prefix_splits > 8) a->prefix_splits = 8;
     // own keys: runs of one length, so that long entries do not hold up the
     // end; about half of them will have keys
