@@ -29,6 +29,9 @@ namespace {
 constexpr int kLowRows = 32;      // rows of a workgroup of the first launch
 constexpr int kFewRows = 64;      // up to which W is read once, and bounds the call
 constexpr int kLowGroup = 4;      // rows that share their reads of A, where more
+// Workgroups of 256 lanes of a launch, which holds less than 2^32 lanes (a
+// launch's low-rank workgroups come on top).
+constexpr long long kMostGroups = (1 << 24) - 4096;
 
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, int off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
@@ -1083,7 +1086,11 @@ int pick_tile(const LoraArgs& a, int eb, int cus, int splits) {
       const long long tiles = ((a.T + b - 1) / b) * ((a.N + b - 1) / b) * splits;
       return (double)((tiles + cus - 1) / cus * b * b);
     };
-    const double w128 = work(128) * 0.85, w64 = work(64) * 0.92, w32 = work(32);
+    const double w128 = work(128) * 0.85, w64 = work(64) * 0.92;
+    // (sizes are checked for tiles of 64; four times as many may be more than a
+    // launch holds)
+    const long long n32 = ((a.T + 31LL) / 32) * ((a.N + 31LL) / 32);
+    const double w32 = n32 * splits < kMostGroups ? work(32) : 2.0 * (w128 + w64);
     return w128 <= w64 && w128 <= w32 ? 128 : w64 <= w32 ? 64 : 32;
   }
   const double c256 = tile_cost(a, cus, splits, 256, 1, 1.0);
@@ -1112,7 +1119,8 @@ void launch_dt(const LoraArgs& a, int cus, hipStream_t stream) {
     else
       hipLaunchKernelGGL((low_kernel<DT, 8>), grid, dim3(256), 0, stream, a);
   }
-  if (a.T <= kFewRows) {
+  // (workgroups of twice the lanes; more outputs are for the tiles below)
+  if (a.T <= kFewRows && (a.N + 15) / 16 < kMostGroups / 2) {
     const dim3 grid((unsigned)((a.N + 15) / 16)), threads(64 * kFewWaves);
     if (a.T <= 16) hipLaunchKernelGGL((few_kernel<DT, 1>), grid, threads, 0, stream, a);
     else if (a.T <= 32) hipLaunchKernelGGL((few_kernel<DT, 2>), grid, threads, 0, stream, a);

@@ -34,3 +34,23 @@ def test_attention_of_the_most_entries():
     want, bound, _, _ = C.attention(q[at], kp, vp, k[at], k[at], n[at], 8 ** -0.5, True)
     C.assert_within(out[at], want, bound, "entries")
     assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N,dtype", [(1, (1 << 27) + 20, "bf16"), (65, 180000000, "f32")])
+def test_projections_of_many_outputs(T, N, dtype):
+    """16 outputs a workgroup of 512 lanes, and tiles of 32 x 32, would be more than a launch
+    holds."""
+    g = torch.Generator().manual_seed(2)
+    t, K = C.TYPES[dtype], 8
+    print(f"[gpu] lora {T} rows of {N} outputs", flush=True)
+    x, w = torch.randn(T, K, generator=g).to(t).cuda(), torch.randn(N, K, dtype=t, device="cuda")
+    y = L.lora_linear(x, w, None, None, None, None, None, None)
+    torch.cuda.synchronize()
+    at = torch.cat([torch.arange(300), torch.randint(300, N - 300, (3000,), generator=g),
+                    torch.arange(N - 300, N)]).cuda()
+    want, bound = C.lora(x, w[at], None, None, None, None, None, None)
+    C.assert_within(y[:, at], want, bound, "outputs")
+    assert bool(torch.isfinite(y[:, ::97]).all())
+    del x, w, y
+    torch.cuda.empty_cache()
