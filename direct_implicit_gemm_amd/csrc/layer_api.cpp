@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <numeric>
 
 #include "internal.h"
 #include "layer.h"
@@ -48,12 +49,10 @@ struct View {
     }
     return true;
   }
-  // Bytes of one row's heads, or -1 where rows of axis 1 do not follow one
-  // another without interleaving.
-  long long in_row() const {
-    const long long used = (n[2] - 1) * s[2] + dense;
-    return s[1] > 0 && used <= s[1] && s[0] % s[1] == 0 ? used : -1;
-  }
+  // What all rows (of axes 0 and 1) are multiples of apart; 0: one row.
+  long long row_step() const { return std::gcd(s[0], s[1]); }
+  // Bytes of one row's heads.
+  long long in_row() const { return (n[2] - 1) * s[2] + dense; }
 };
 
 View view(const void* p, long long n0, long long s0, long long n1, long long s1, long long n2,
@@ -81,17 +80,15 @@ bool ranges_meet(const void* a, long long abytes, const void* b, long long bbyte
 
 // Whether two operands may share a byte.  Slices of the rows of one buffer
 // (queries, keys and values of a fused projection) lie in one another's range
-// without meeting.
+// without meeting, where each has a part of its own of the step that all their
+// rows are multiples of apart.
 bool meet(const View& a, const View& b) {
   if (!ranges_meet(a.p, a.span(), b.p, b.span())) return false;
-  const long long fa = a.in_row(), fb = b.in_row();
-  if (a.s[1] == b.s[1] && fa >= 0 && fb >= 0) {
-    const long long step = a.s[1];
-    long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % step;
-    if (d < 0) d += step;
-    if (d >= fa && d + fb <= step) return false;
-  }
-  return true;
+  const long long step = std::gcd(a.row_step(), b.row_step());
+  if (step == 0) return true;
+  long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % step;
+  if (d < 0) d += step;
+  return d < a.in_row() || d + b.in_row() > step;
 }
 
 bool good_strides(const long long* s, int n) {
