@@ -12,7 +12,8 @@ the stream waits for the operands, and the reader for the stream, and that opera
 live until the stream is done with them, is the caller's affair.
 Tensors may be strided (slices of a fused projection, caches in any order of
 axes) as long as their last axis is dense and their rows lie on 16-byte
-boundaries.  There is no backward pass: libconv runs networks forward.
+boundaries.  There is no backward pass: libconv runs networks forward, and an
+operand that requires gradients outside ``torch.no_grad()`` gets a warning.
 """
 from __future__ import annotations
 

@@ -11,6 +11,7 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/StreamGuard.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 
@@ -79,6 +80,21 @@ bool bad_array(const at::Tensor& t, const Kind& k, at::ScalarType type,
   return t.device() != k.device || t.scalar_type() != type ||
          t.sizes() != c10::IntArrayRef(shape) || !t.is_contiguous();
 }
+// There is no backward pass: a caller who may expect one is told (once an operator).
+bool wants_grad(std::initializer_list<const at::Tensor*> operands) {
+  if (!c10::GradMode::is_enabled()) return false;
+  for (const at::Tensor* t : operands)
+    if (t && t->requires_grad()) return true;
+  return false;
+}
+#define LIBCONV_FORWARD_ONLY(what, ...)                                                       \
+  do {                                                                                        \
+    if (wants_grad({__VA_ARGS__})) {                                                          \
+      TORCH_WARN_ONCE(what, ": an operand requires gradients, but the operator has no "       \
+                      "backward pass: its outputs require none (torch.no_grad() says so)");   \
+    }                                                                                         \
+  } while (0)
+
 const void* address(const at::Tensor* t) { return t ? t->const_data_ptr() : nullptr; }
 template <class T> const T* address_of(const at::Tensor& t) {
   return static_cast<const T*>(t.const_data_ptr());
@@ -247,6 +263,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if ((qo && bad(*qo, kind, {T, Hq, D})) || (ko && bad(*ko, kind, {rows, Hk, D})) ||
       (vo && bad(*vo, kind, {rows, Hk, D})))
     refuse(what, "bad output tensor");
+  LIBCONV_FORWARD_ONLY(what, &q, &k, v, qw, kw, &freqs);
   Call call(kind, a[14]);
   at::Tensor made[3];
   if (!qo) qo = &(made[0] = call.fresh(kind.type, {T, Hq, D}));
@@ -313,6 +330,7 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     refuse(what, "lengths must be a contiguous int32 device tensor [B]");
   if (out && bad(*out, kind, {B, Sq, Hq, D})) refuse(what, "bad output tensor");
   const bool with_lse = truth(a[9]);
+  LIBCONV_FORWARD_ONLY(what, &q, kp, vp, k, v);
   Call call(kind, a[10]);
   at::Tensor made, lse;
   if (!out) out = &(made = call.fresh(kind.type, {B, Sq, Hq, D}));
@@ -383,6 +401,7 @@ PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     refuse(what, "a, b, scales, row_starts and adapters come together");
   }
   if (out && bad(*out, kind, {T, N})) refuse(what, "bad output tensor");
+  LIBCONV_FORWARD_ONLY(what, &x, &w, bias, la, lb, scales);
   Call call(kind, a[9]);
   at::Tensor made;
   if (!out) out = &(made = call.fresh(kind.type, {T, N}));
