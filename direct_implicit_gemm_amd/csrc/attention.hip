@@ -614,8 +614,8 @@ __device__ __forceinline__ int xcd_order(int id, int n) {
 // Each entry's rows over its prefix and own keys.  130 queries of 2 entries, 8
 // heads of 64 over 333 + 190 keys in fp32: 14 us, and 3 of the join (bound by
 // the fp32 matrix instructions of 160 workgroups); one query of 4 entries, 20
-// heads of 64 over 1000 keys in bf16: 10 us (the keys that one workgroup's
-// compute unit reads, 256 KB; eight waves instead of four: 10 us).
+// heads of 64 over 1000 keys in bf16: 10 us (80 workgroups, whose waves take 8
+// tiles of keys one after another; eight waves instead of four: 10 us).
 template <int DT, int DP, int WK>
 __global__ __launch_bounds__(kThreads, fit((Shape<DT, DP, WK>::LDS))) void attn_kernel(
     const AttnArgs a) {

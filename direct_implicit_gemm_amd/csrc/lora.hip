@@ -892,7 +892,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void few_kernel(const LoraArgs a
 // LDS, W straight in registers (each of its values has one reader), all of a
 // run on its way at once.  The first `low_jobs` workgroups take the low-rank
 // values meanwhile.  64 rows, 4096 -> 4096, rank 16 in bf16: 12 us (42 MB, and x
-// from L2 for each 64 outputs).
+// from L2 for each 64 outputs; one round of workgroups that load, wait, compute
+// and store, so that nothing overlaps).
 // Bytes of a run, at most: x of 64 rows then takes 48 KB, and three workgroups
 // share a compute unit (4096 -> 4096, 64 rows 16.7 us with the sum; runs of 1024
 // 17.4, of 512 17.8; a row of 4160 17.1, 19.6 and 18.8).
