@@ -211,8 +211,7 @@ def run(s):
             return L.linear(s["x"], s["w"], s["bias"], act=c["act"], residual=s["residual"])
         cache = (s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"])
         if c["op"] == "cache":
-            L.kv_cache_write(s["k"], s["v"], *cache, s["starts"], s["lengths"], s["table"],
-                             max_rows=s["max_rows"])
+            L.kv_cache_write(s["k"], s["v"], *cache, s["starts"], s["lengths"], s["table"])
             L.kv_cache_read(*cache, s["lengths"], s["table"], k_out=s["k_out"], v_out=s["v_out"])
             return [s["k_out"], s["v_out"], s["k_scale"], s["v_scale"]]
         return list(L.cache_attention(s["q"], *cache, s["starts"], s["lengths"], s["table"],
