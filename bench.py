@@ -119,7 +119,8 @@ def kernel_source_sha():
     """Of what the convolution kernels are built from (the attention-layer operators are not)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "direct_implicit_gemm_amd", "csrc")
-    others = ("attention.hip", "lora.hip", "rope.hip", "layer.h")
+    others = ("attention.hip", "attention_common.h", "cache_attention.hip", "codes.h",
+              "kv_cache.hip", "layer.h", "linear.hip", "lora.hip", "rope.hip")
     for f in sorted(os.listdir(csrc)):
         if f.endswith((".hip", ".h", ".def")) and f not in others:
             with open(os.path.join(csrc, f), "rb") as fh:

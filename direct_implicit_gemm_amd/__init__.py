@@ -25,6 +25,8 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "libconv.h")
 
 F32, F16, BF16 = 0, 1, 2
 ACT_NONE, ACT_RELU = 0, 1
+ACT_GELU, ACT_GELU_TANH, ACT_SILU = 2, 3, 4     # of libconv_linear only
+CACHE_I8, CACHE_E4M3 = 0, 1
 ALGO_AUTO, ALGO_DIRECT, ALGO_IGEMM = 0, 1, 2
 
 STATUS = {
@@ -133,6 +135,18 @@ def load() -> ctypes.CDLL:
     lib.libconv_lora_linear.restype = I
     lib.libconv_lora_workspace.argtypes = [I] * 7
     lib.libconv_lora_workspace.restype = LL
+    lib.libconv_kv_cache_write.argtypes = [P] * 10 + [I] * 9 + [P]
+    lib.libconv_kv_cache_write.restype = I
+    lib.libconv_kv_cache_read.argtypes = [P] * 9 + [I] * 9 + [P]
+    lib.libconv_kv_cache_read.restype = I
+    lib.libconv_cache_attention.argtypes = [P] * 11 + [I] * 9 + [F, I, I, I, P, LL, P]
+    lib.libconv_cache_attention.restype = I
+    lib.libconv_cache_attention_workspace.argtypes = [I] * 9
+    lib.libconv_cache_attention_workspace.restype = LL
+    lib.libconv_linear.argtypes = [P] * 5 + [I] * 3 + [LL] * 3 + [I, I, P, LL, P]
+    lib.libconv_linear.restype = I
+    lib.libconv_linear_workspace.argtypes = [I] * 4
+    lib.libconv_linear_workspace.restype = LL
     _lib = lib
     return lib
 
@@ -359,6 +373,52 @@ def libconv_lora_linear(x, w, bias, a, b, scales, row_starts, adapters, y, T, K,
 
 def libconv_lora_workspace(T, K, N, rank, n_adapters, n_requests, dtype) -> int:
     return load().libconv_lora_workspace(T, K, N, rank, n_adapters, n_requests, dtype)
+
+
+def libconv_kv_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, row_starts, lengths,
+                           block_table, strides, B, T, blocks, block_size, table_width, k_heads,
+                           head_dim, format, dtype, stream) -> int:
+    """strides: ctypes array of 10 long longs (host)."""
+    return load().libconv_kv_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, row_starts,
+                                         lengths, block_table, strides, B, T, blocks, block_size,
+                                         table_width, k_heads, head_dim, format, dtype, stream)
+
+
+def libconv_kv_cache_read(k_cache, v_cache, k_scale, v_scale, lengths, block_table, k, v, strides,
+                          B, S, blocks, block_size, table_width, k_heads, head_dim, format, dtype,
+                          stream) -> int:
+    """strides: ctypes array of 12 long longs (host)."""
+    return load().libconv_kv_cache_read(k_cache, v_cache, k_scale, v_scale, lengths, block_table,
+                                        k, v, strides, B, S, blocks, block_size, table_width,
+                                        k_heads, head_dim, format, dtype, stream)
+
+
+def libconv_cache_attention(q, k_cache, v_cache, k_scale, v_scale, row_starts, lengths,
+                            block_table, out, lse, strides, B, T, max_rows, blocks, block_size,
+                            table_width, q_heads, k_heads, head_dim, scale, causal, format, dtype,
+                            workspace, workspace_bytes, stream) -> int:
+    """strides: ctypes array of 10 long longs (host)."""
+    return load().libconv_cache_attention(q, k_cache, v_cache, k_scale, v_scale, row_starts,
+                                          lengths, block_table, out, lse, strides, B, T, max_rows,
+                                          blocks, block_size, table_width, q_heads, k_heads,
+                                          head_dim, scale, causal, format, dtype, workspace,
+                                          workspace_bytes, stream)
+
+
+def libconv_cache_attention_workspace(B, T, max_rows, block_size, table_width, q_heads, k_heads,
+                                      head_dim, dtype) -> int:
+    return load().libconv_cache_attention_workspace(B, T, max_rows, block_size, table_width,
+                                                    q_heads, k_heads, head_dim, dtype)
+
+
+def libconv_linear(x, w, bias, residual, y, T, K, N, x_stride, residual_stride, y_stride, act,
+                   dtype, workspace, workspace_bytes, stream) -> int:
+    return load().libconv_linear(x, w, bias, residual, y, T, K, N, x_stride, residual_stride,
+                                 y_stride, act, dtype, workspace, workspace_bytes, stream)
+
+
+def libconv_linear_workspace(T, K, N, dtype) -> int:
+    return load().libconv_linear_workspace(T, K, N, dtype)
 
 
 def libconv_query_algo(N, C_in, T, H, W, C_out, KT, KH, KW, pad_t, pad_h, pad_w,
@@ -892,4 +952,5 @@ def conv3d(x, w, b=None, stride=1, padding=0, act="none", algo="auto", out=None,
 
 
 from .attention import (  # noqa: E402  (the helpers above are what these call)
-    lora_linear, prefix_attention, qk_norm_rope, rotary_frequencies)
+    cache_attention, kv_cache_read, kv_cache_write, linear, lora_linear, prefix_attention,
+    qk_norm_rope, rotary_frequencies)

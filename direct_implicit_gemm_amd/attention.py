@@ -3,6 +3,10 @@
     lora_linear        a projection with each request's low-rank adapter beside it
     qk_norm_rope       norms of queries and keys, position rotation, cache write
     prefix_attention   attention over keys a batch shares and each entry's own
+    kv_cache_write     keys and values of new tokens into a cache of 8-bit blocks
+    kv_cache_read      ... and back, in the activations' type
+    cache_attention    attention of a ragged batch over such a cache
+    linear             a projection with bias, activation and residual
 
 They allocate outputs (and workspaces, through torch), enqueue on the current
 stream or ``stream`` (a handle), and raise ``LibconvError`` on a status other than
@@ -48,7 +52,9 @@ def _load():
     spec.loader.exec_module(calls)
     functions = (lib.libconv_qk_norm_rope, lib.libconv_prefix_attention,
                  lib.libconv_prefix_attention_workspace, lib.libconv_lora_linear,
-                 lib.libconv_lora_workspace)
+                 lib.libconv_lora_workspace, lib.libconv_kv_cache_write, lib.libconv_kv_cache_read,
+                 lib.libconv_cache_attention, lib.libconv_cache_attention_workspace,
+                 lib.libconv_linear, lib.libconv_linear_workspace)
     calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in functions),
                # as torch.cuda.current_stream() has it, without the object
                getattr(torch._C, "_cuda_getCurrentRawStream", None), stream_id, fail)
@@ -103,3 +109,61 @@ def lora_linear(x, w, bias, a, b, scales, row_starts, adapters, out=None, stream
     a .. adapters may all be None: the projection alone."""
     return (_calls or _load()).lora_linear(
         x, w, bias, a, b, scales, row_starts, adapters, out, stream, workspace)
+
+
+def kv_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, row_starts, lengths, block_table,
+                   stream=None):
+    """Appends rows k, v [T, Hk, D] to a cache of codes (int8 or float8_e4m3fn)
+    k_cache, v_cache [blocks, block, Hk, D] with scales k_scale, v_scale (float32
+    [blocks, Hk]).  Entry b has rows row_starts[b] .. row_starts[b + 1] - 1 (int32
+    [B + 1]), which become the last of its lengths[b] (int32 [B]) tokens; position p
+    lies in block block_table[b, p // block] (int32 [B, any]).  A block's scale is the
+    least power of two that holds its largest value, and grows with new tokens.
+
+        shape = (blocks, heads, block, head_dim)     # each head's tokens side by side
+        k_cache = torch.zeros(shape, dtype=torch.int8, device="cuda").transpose(1, 2)
+        k_scale = torch.zeros(blocks, heads, device="cuda")"""
+    return (_calls or _load()).kv_cache_write(
+        k, v, k_cache, v_cache, k_scale, v_scale, row_starts, lengths, block_table, stream)
+
+
+def kv_cache_read(k_cache, v_cache, k_scale, v_scale, lengths, block_table, k_out=None, v_out=None,
+                  dtype=None, rows: Optional[int] = None, stream=None):
+    """The first lengths[b] tokens of every entry, as prefix_attention takes them:
+    (k_out, v_out) [B, S, Hk, D].  Rows from lengths[b] on are left as they were.
+    Outputs not given are made, zero where nothing is written, of `dtype` (bfloat16)
+    with S = rows (all positions of the table)."""
+    like = None
+    if k_out is None or v_out is None:
+        import torch
+        like = torch.empty(0, dtype=torch.bfloat16 if dtype is None else dtype)
+    return (_calls or _load()).kv_cache_read(
+        k_cache, v_cache, k_scale, v_scale, lengths, block_table, k_out, v_out, like, rows, stream)
+
+
+def cache_attention(q, k_cache, v_cache, k_scale, v_scale, row_starts, lengths, block_table,
+                    max_rows: Optional[int] = None, scale: Optional[float] = None,
+                    causal: bool = True, out=None, return_lse: bool = False, stream=None,
+                    workspace=True):
+    """Attention of q [T, Hq, D] over a cache (see kv_cache_write): row t of entry b
+    over the entry's lengths[b] tokens, causal: up to its own position.  max_rows: the
+    rows of the entry with the most (T will do; 1 for single tokens plans best).
+    Returns out, or (out, lse [T, Hq] float32); rows of no entry are not written.
+    workspace: True (allocate what the best plan takes), False (none), or a uint8
+    device tensor."""
+    return (_calls or _load()).cache_attention(
+        q, k_cache, v_cache, k_scale, v_scale, row_starts, lengths, block_table, max_rows, scale,
+        causal, out, return_lse, stream, workspace)
+
+
+_LINEAR_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, out=None, stream=None,
+           workspace=True):
+    """y = act(x w^T + bias) + residual for x [T, K], w [N, K], bias [N], residual
+    [T, N] (out may be the residual).  act: none, relu, gelu, gelu_tanh or silu."""
+    number = _LINEAR_ACTS.get(act)
+    if number is None:
+        raise ValueError(f"linear: act must be one of {', '.join(_LINEAR_ACTS)}")
+    return (_calls or _load()).linear(x, w, bias, number, residual, out, stream, workspace)

@@ -35,7 +35,8 @@ SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=und
              "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
 SOURCES = ["api.cpp", "direct.hip", "igemm.hip", "layout.hip",
            # the attention-layer operators
-           "layer_api.cpp", "rope.hip", "attention.hip", "lora.hip",
+           "layer_api.cpp", "rope.hip", "attention.hip", "lora.hip", "kv_cache.hip",
+           "cache_attention.hip", "linear.hip",
            # the implicit-GEMM tiles, one unit per group so that they build in parallel
            "igemm_inst_a.hip", "igemm_inst_b.hip", "igemm_inst_c.hip", "igemm_inst_d.hip",
            "igemm_inst_e.hip"]

@@ -24,7 +24,7 @@
 // 1024 that its products take, so both have to run at a time (see the loop).
 // Measured: 12 entries of 3200 queries, 20 heads of 128, 3277 keys, bf16, 1.25
 // ms (1.03 PFLOP/s; the loop with both products after one another 2.4 ms).
-#include "device_common.h"
+#include "attention_common.h"
 #include "internal.h"
 #include "layer.h"
 
@@ -32,10 +32,6 @@ namespace libconv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNegInf = -__builtin_inff();
-constexpr float kLowest = -3.402823466e38f;   // the maximum of no keys: finite, so that no
-                                              // difference of maxima is a NaN
 // log2 of how far a maximum may fall behind (lazy), and of what the
 // probabilities are multiplied by.  fp16 ends at 2^-24: probabilities below
 // 2^-25 of the largest would vanish from the second product and still count in
@@ -62,8 +58,6 @@ template <int DT, int DP, int WK> struct Shape {
 // Workgroups that a compute unit's LDS holds, at most 2 counted.
 constexpr int fit(int lds) { return 2 * lds <= 160 * 1024 ? 2 : 1; }
 
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-
 // 16-byte chunk of a row of K (V) in LDS is kept at chunk ^ swizzle(row): the
 // 16 lanes that read one chunk of 16 rows at a time then hit all banks (in
 // rows of 512 bytes, twice: a copy covers 8 rows there, and a thread's chunk
@@ -76,42 +70,6 @@ template <int CPR> __device__ __forceinline__ int k_swizzle(int row) {
 template <int EB, int CPR> __device__ __forceinline__ int v_swizzle(int row) {
   if constexpr (EB == 4) return ((row >> 2) & 1) << 3;
   return CPR >= 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
-}
-
-// The larger of v in this lane and in the lane 32 away.
-__device__ __forceinline__ float swap_halves_max(float v) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  // (through scalars: a bit cast of a vector's element takes element 0)
-  const uint32_t lower = r[0], upper = r[1];
-  return fmaxf(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
-}
-
-// 4 elements of one column of 16-bit elements: the 16 lanes of a quarter wave
-// name 8 bytes each of 4 rows.  `p` is restrict so that the read has a scope of
-// its own: without one, the compiler lets it wait for every copy to LDS that
-// is on its way, those of the next tile among them.
-__device__ __forceinline__ u32x2_t read_column(const unsigned char* __restrict p) {
-  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                         (__attribute__((address_space(3))) s16x4_t*)p));
-}
-
-// Probabilities are rounded to the 16-bit type for the second product (their sum
-// is not): an error of that one rounding beside the output's own, 0.0022 to
-// 0.0024 of the output in bf16 and 0.00029 in fp16 against 0.0017 and 0.00021 of
-// a product in fp32.  Two terms a probability would hold 16 bits, for half again
-// the matrix work of what the matrix units bound.
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  const f32x2_t v = {a, b};
-  if constexpr (DT == DT_F16) {
-    typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2_t));
-  } else {
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
-  }
 }
 
 // A walk over the tiles of K or of V: prefix, then own keys.
@@ -327,6 +285,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[d][r] *= f;
   };
+  // Probabilities are rounded to the 16-bit type for the second product (their sum
+  // is not): an error of that one rounding beside the output's own, 0.0022 to
+  // 0.0024 of the output in bf16 and 0.00029 in fp16 against 0.0017 and 0.00021 of
+  // a product in fp32.  Two terms a probability would hold 16 bits, for half again
+  // the matrix work of what the matrix units bound.
   // 16 keys a step of the second product: this lane's are 4 half + {0..3, 8..11}
   auto pack = [&](const float16_t& s, u32x4_t* pf) {
     if constexpr (EB == 2) {
@@ -601,14 +564,6 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Job& job, unsign
       else
         *reinterpret_cast<u32x2_t*>(op + comp * 2) = u32x2_t{pack2<DT>(o0, o1), pack2<DT>(o2, o3)};
     }
-}
-
-// Workgroups that read the same keys (one entry and key head) follow one
-// another on one XCD, whose L2 then holds those keys: dispatch deals
-// workgroups out to the 8 XCDs in turn.
-__device__ __forceinline__ int xcd_order(int id, int n) {
-  const int per = n >> 3, more = n & 7, x = id & 7;
-  return x * per + (x < more ? x : more) + (id >> 3);
 }
 
 // Each entry's rows over its prefix and own keys.  130 queries of 2 entries, 8

@@ -1,0 +1,645 @@
+// cache_attention.hip -- attention of a ragged batch over a cache of keys and
+// values in 8-bit codes, in blocks with a scale for each head.
+//
+//   out = sum_j p_j s_v(j) c_v(j),  p = softmax_j(scale s_k(j) <q, c_k(j)>)
+//
+// One pass over the keys with the running maximum m and sum l of a softmax, as in
+// attention.hip: S = K Q^T and O = V^T P transposed, keys and components on the
+// rows of the matrix instructions and queries on their columns, so that a lane
+// holds scores, maximum, sum and outputs of one query.  The codes enter the
+// matrix instructions as 16-bit numbers, which hold them exactly; the scale of a
+// block's keys multiplies their scores, that of its values their probabilities
+// (16 consecutive keys always have one scale).
+#include "codes.h"
+#include "internal.h"
+#include "layer.h"
+
+namespace libconv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;       // keys of a tile: 32 for each of a workgroup's waves
+constexpr int kFewRows = 32;     // rows of a key head that one set of matrix columns holds
+
+// Terms that q and the probabilities enter the matrix instructions as: bfloat16
+// holds 8 bits, fp16's 11 and fp32's 24 take two and three.  (q in fp16 meets
+// codes in fp16; the probabilities times their scale may be past its range.)
+template <int DT> struct Terms {
+  static constexpr int Q = DT == DT_F32 ? 3 : 1, P = DT == DT_F32 ? 3 : DT == DT_F16 ? 2 : 1;
+  static constexpr int KT = DT == DT_F16 ? DT_F16 : DT_BF16;   // type of the first product
+};
+
+// x as N bfloat16 terms: each the rest of the ones before, rounded.
+template <int N> __device__ __forceinline__ void split2(float a, float b, uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i] = pack2<DT_BF16>(a, b);
+    if (i + 1 < N) {
+      const float ha = Elem<DT_BF16>::bits_to_f32(w[i] & 0xffffu);
+      const float hb = Elem<DT_BF16>::bits_to_f32(w[i] >> 16);
+      a = __builtin_isfinite(ha) ? a - ha : 0.0f;
+      b = __builtin_isfinite(hb) ? b - hb : 0.0f;
+    }
+  }
+}
+
+template <int DP> struct Shape {
+  static constexpr int RB = DP <= 64 ? 64 : 128;   // bytes of a row of codes in LDS
+  static constexpr int CPR = RB / 16;              // 16-byte chunks of it
+  static constexpr int KS = DP / 16;               // steps of the first product
+  static constexpr int DB = DP / 32;               // blocks of 32 components
+  static constexpr int PART = 32 * RB;             // a wave's keys (values) of a tile
+  static constexpr int COPIES = PART / 1024;       // 16 bytes a lane each
+  static constexpr int LDS = 4 * 2 * 2 * PART;     // waves, stages, keys and values
+};
+// Chunk c of row r is kept at c ^ swizzle(r): 16 rows' reads of one chunk, and the
+// 8 rows that 16 lanes read a chunk of, hit all banks.
+template <int CPR> __device__ __forceinline__ int swizzle(int row) {
+  return CPR == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
+
+// 8 codes of one column: the 16 lanes of a quarter wave name 8 bytes each of 8
+// rows of 16.  (restrict: as for read_column)
+__device__ __forceinline__ u32x2_t read_column8(const unsigned char* __restrict p) {
+  typedef int i32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                                         (__attribute__((address_space(3))) i32x2_t*)p));
+}
+
+// An entry: its rows and its keys.
+struct Entry {
+  int row0, n, rows;   // first row, rows, rows of a key head that are computed
+  int len;
+};
+__device__ __forceinline__ Entry entry_of(const CacheAttnArgs& a, int b) {
+  Entry e;
+  int s0 = a.starts[b], s1 = a.starts[b + 1], len = a.c.lengths[b];
+  s0 = s0 < 0 ? 0 : s0;
+  s1 = s1 > a.T ? a.T : s1;
+  const int most = a.c.width << a.c.log_block;
+  e.row0 = s0;
+  e.n = s1 > s0 ? s1 - s0 : 0;
+  e.rows = (e.n < a.max_rows ? e.n : a.max_rows) * a.G;
+  e.len = len < 0 ? 0 : len > most ? most : len;
+  return e;
+}
+
+// Whether an entry's rows fit one set of columns.
+__device__ __forceinline__ bool few(const Entry& e) { return e.rows > 0 && e.rows <= kFewRows; }
+// Tiles of such an entry (one without keys still has an output to write).
+__device__ __forceinline__ int few_tiles(const Entry& e) {
+  const int t = (e.len + kTile - 1) / kTile;
+  return few(e) ? (t > 0 ? t : 1) : 0;
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int lanes_before(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    v += lane >= d ? o : 0;
+  }
+  return v;
+}
+
+// Work of all entries, `weight(b)` each.
+template <class W> __device__ __forceinline__ long long total_of(int B, W&& weight) {
+  const int lane = threadIdx.x & 63;
+  long long sum = 0;
+  for (int b0 = 0; b0 < B; b0 += 64) {
+    const int w = b0 + lane < B ? weight(b0 + lane) : 0;
+    sum += __builtin_amdgcn_readlane(lanes_before(w), 63);
+  }
+  return sum;
+}
+// The entry that holds number x of the work (B: none), and where its own begins.
+struct Found {
+  int b;
+  long long first;
+};
+template <class W> __device__ __forceinline__ Found find(int B, long long x, W&& weight) {
+  const int lane = threadIdx.x & 63;
+  long long sum = 0;
+  for (int b0 = 0; b0 < B; b0 += 64) {
+    const int w = b0 + lane < B ? weight(b0 + lane) : 0, up_to = lanes_before(w);
+    const uint64_t past = __ballot(sum + up_to > x);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      return {b0 + l, sum + __builtin_amdgcn_readlane(up_to - w, l)};
+    }
+    sum += __builtin_amdgcn_readlane(up_to, 63);
+  }
+  return {B, sum};
+}
+// Where an entry's work begins.
+template <class W> __device__ __forceinline__ long long begin_of(int b, W&& weight) {
+  return total_of(b, weight);
+}
+
+// How the few_groups workgroups share the tiles of all heads: each a run of `per`.
+__device__ __forceinline__ long long share_of(long long total, int groups) {
+  const long long per = (total + groups - 1) / groups;
+  return per < 2 ? 2 : per;   // (fewer keys are not worth a partial result)
+}
+
+// Rows `row_tile` * 32 .. of key head hk of an entry over tiles t0 .. t1 - 1 of its
+// keys, in order; slot: where the partial result goes (-1: to the output).
+struct Job {
+  Entry e;
+  int b, hk, row_tile, t0, t1;
+  long long slot;
+};
+
+template <int DT, int CF, int DP>
+__device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& job,
+                                           unsigned char* lds) {
+  using Z = Shape<DP>;
+  constexpr int RB = Z::RB, CPR = Z::CPR, KS = Z::KS, DB = Z::DB, COPIES = Z::COPIES;
+  constexpr int NQ = Terms<DT>::Q, NP = Terms<DT>::P, KT = Terms<DT>::KT;
+  constexpr int EB = Elem<DT>::bytes;
+  const CacheView& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, half = lane >> 5;
+  const int len = job.e.len, D = c.D, hk = job.hk;
+
+  // blocks and scales of the groups of 16 keys that this wave reads: lane L holds
+  // those of group L & 1 of tile first + L / 2
+  const int mask = (1 << c.log_block) - 1;
+  auto ids_of = [&](int first) {
+    const long long p = (long long)(first + (lane >> 1)) * kTile + wave * 32 + (lane & 1) * 16;
+    int id = -1;
+    if (p < len) id = c.table[(long long)job.b * c.width + (p >> c.log_block)];
+    return id >= 0 && id < c.blocks ? id : -1;
+  };
+  auto scale_of = [&](int id, int kv) {
+    return id >= 0 ? c.scale[kv][(long long)id * c.Hk + hk] : 0.0f;
+  };
+  int at = job.t0;   // first tile of the batch in hand
+  int ids = ids_of(at), ids_next = -1;
+
+  // copies: 16 bytes of a row a lane
+  constexpr int PASS = 64 / CPR;   // rows of a copy
+  const int row_in = lane / CPR;
+  int off[2][2];                   // keys and values, of even and odd copies of a group
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int chunk = (lane % CPR) ^ swizzle<CPR>(j * PASS + row_in);
+      off[kv][j] = chunk * 16 < D ? row_in * (int)c.token[kv] + chunk * 16 : kFarOffset;
+    }
+  unsigned char* const mine = lds + wave * 4 * Z::PART;
+  auto stage = [&](int t, int kv) { return mine + (((t - job.t0) & 1) * 2 + kv) * Z::PART; };
+  auto copy = [&](int t, int kv) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int in = (t - at) * 2 + g;
+      int id = __builtin_amdgcn_readlane(in < 64 ? ids : ids_next, in & 63);
+      const long long p = (long long)t * kTile + wave * 32 + g * 16;
+      const long long left = len - p;
+      const int rows = left < 16 ? (int)left : 16;
+      const bool any = t < job.t1 && rows > 0 && id >= 0;
+      id = any ? id : 0;
+      const char* base = c.codes[kv] + id * c.block[kv] + hk * c.head[kv] +
+                         (long long)((int)p & mask) * c.token[kv];
+      const __amdgpu_buffer_rsrc_t r =
+          make_rsrc(base, any ? (uint32_t)((rows - 1) * (int)c.token[kv] + D) : 0u);
+#pragma unroll
+      for (int j = 0; j < 16 / PASS; ++j)
+        copy16_to_lds(r, stage(t, kv) + (g * (16 / PASS) + j) * 1024, off[kv][j],
+                      j * PASS * (int)c.token[kv]);
+    }
+  };
+  copy(job.t0, 0);
+  copy(job.t0, 1);
+  copy(job.t0 + 1, 0);
+  copy(job.t0 + 1, 1);
+  float ks = scale_of(ids, 0), vs = scale_of(ids, 1), ks_next = 0.0f, vs_next = 0.0f;
+
+  // this lane's query
+  const int local = job.row_tile * 32 + l32;
+  const bool row_ok = local < job.e.rows;
+  const int row = row_ok ? local : 0, qi = row / a.G, qg = row - qi * a.G;
+  const char* qp =
+      a.q + (long long)(job.e.row0 + qi) * a.q_r + (long long)(hk * a.G + qg) * a.q_h;
+  u32x4_t qf[NQ][KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int el = ((s & ~1) + half) * 16 + (s & 1) * 8;
+    u32x4_t raw[EB / 2];
+#pragma unroll
+    for (int i = 0; i < EB / 2; ++i) {
+      raw[i] = u32x4_t{0, 0, 0, 0};
+      if (row_ok && el < D) raw[i] = *reinterpret_cast<const u32x4_t*>(qp + el * EB + i * 16);
+      if (a.flip) {
+        const uint32_t sign = EB == 4 ? 0x80000000u : 0x80008000u;
+        raw[i] = a.flip < 0 ? raw[i] ^ u32x4_t{sign, sign, sign, sign} : u32x4_t{0, 0, 0, 0};
+      }
+    }
+    if constexpr (DT == DT_F32) {
+      float f[8];
+      unpack<DT_F32>(raw[0], f);
+      unpack<DT_F32>(raw[1], f + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[NQ];
+        split2<NQ>(f[2 * j], f[2 * j + 1], w);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) qf[i][s][j] = w[i];
+      }
+    } else {
+      qf[0][s] = raw[0];
+    }
+  }
+  // keys that this query sees, and that every query of the tile does
+  const int first_row = job.row_tile * 32;
+  const int lim = a.causal ? len - job.e.n + qi + 1 : len;
+  const int lim_all = a.causal ? len - job.e.n + first_row / a.G + 1 : len;
+
+  float16_t acc[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) acc[d] = float16_t{};
+  float m = kLowest, l = 0.0f;
+
+  const int krow = l32 * RB, ksw = swizzle<CPR>(l32);
+  const int vrow = (((lane & 15) >> 1) & 3) + 8 * ((lane & 15) >> 3) + 4 * half;
+
+  for (int t = job.t0; t < job.t1; ++t) {
+    if (t - at == 32) {
+      at += 32;
+      ids = ids_next;
+      ks = ks_next;
+      vs = vs_next;
+    }
+    // the next batch, a little at a time: blocks, then their scales
+    if (t - at == 8 && at + 32 < job.t1) ids_next = ids_of(at + 32);
+    if (t - at == 16 && at + 32 < job.t1) {
+      ks_next = scale_of(ids_next, 0);
+      vs_next = scale_of(ids_next, 1);
+    }
+    const int in = (t - at) * 2;
+    float f[2], add[2], fv[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      f[g] = a.scale * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                                     __builtin_bit_cast(int, ks), in + g));
+      fv[g] = __builtin_bit_cast(float,
+                                 __builtin_amdgcn_readlane(__builtin_bit_cast(int, vs), in + g));
+      add[g] = __builtin_amdgcn_readlane(ids, in + g) >= 0 ? 0.0f : kNegInf;
+    }
+
+    wait_vmcnt<3 * COPIES>();
+    lds_fence();
+    float16_t s = {};
+    const unsigned char* kt = stage(t, 0);
+#pragma unroll
+    for (int j = 0; j < KS / 2; ++j) {
+      const u32x4_t w =
+          *reinterpret_cast<const u32x4_t*>(kt + krow + (((2 * j + half) ^ ksw) * 16));
+      const u32x4_t k0 = code_values16<CF, KT>(w[0], w[1]), k1 = code_values16<CF, KT>(w[2], w[3]);
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        Mma<KT>::step(k0, qf[i][2 * j], s, 0);
+        Mma<KT>::step(k1, qf[i][2 * j + 1], s, 0);
+      }
+    }
+    lds_fence();
+    copy(t + 2, 0);
+
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], f[r >> 3], add[r >> 3]);
+    const long long p0 = (long long)t * kTile + wave * 32;
+    if (p0 + 32 > lim_all) {
+      const int lane_lim = (int)(lim - p0) - 4 * half;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        s[r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[r] : kNegInf;
+    }
+    float top = s[0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+    top = swap_halves_max(top);
+    if (__any(top > m)) {
+      const float m_new = fmaxf(m, top), fall = __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= fall;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[d][r] *= fall;
+    }
+    u32x4_t pf[NP][2];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(s[r] - m);
+      l += s[r];
+      s[r] *= fv[r >> 3];
+    }
+#pragma unroll
+    for (int r = 0; r < 16; r += 2) {
+      uint32_t w[NP];
+      split2<NP>(s[r], s[r + 1], w);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) pf[i][r >> 3][(r & 7) >> 1] = w[i];
+    }
+
+    wait_vmcnt<3 * COPIES>();
+    lds_fence();
+    const unsigned char* vt = stage(t, 1);
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const int r = g * 16 + vrow, chunk = (2 * d + ((lane >> 4) & 1)) ^ swizzle<CPR>(r);
+        const u32x2_t w = read_column8(vt + r * RB + chunk * 16 + (lane & 1) * 8);
+        const u32x4_t vf = code_values16<CF, DT_BF16>(w[0], w[1]);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) Mma<DT_BF16>::step(vf, pf[i][g], acc[d], 0);
+      }
+    lds_fence();
+    copy(t + 2, 1);
+  }
+  wait_vmcnt<0>();
+
+  // join the waves: each leaves maximum, sum and outputs (32 rows, DP components,
+  // rows fastest) in LDS
+  l += __shfl_xor(l, 32);
+  constexpr int PER = 32 * (DP + 2) * 4;
+  static_assert(3 * PER <= Z::LDS, "the join fits the stages");
+  lds_barrier();   // every wave is done with its stages, no copy is on its way
+  if (wave > 0) {
+    float* room = reinterpret_cast<float*>(lds + (wave - 1) * PER);
+    if (half == 0) {
+      room[l32] = m;
+      room[32 + l32] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        room[(2 + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32] = acc[d][r];
+  }
+  lds_barrier();
+  if (wave == 0) {
+    float m_all = m;
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+      m_all = fmaxf(m_all, reinterpret_cast<const float*>(lds + w * PER)[l32]);
+    const float fall = __builtin_amdgcn_exp2f(m - m_all);
+    l *= fall;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[d][r] *= fall;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) {
+      const float* o = reinterpret_cast<const float*>(lds + w * PER);
+      const float g = __builtin_amdgcn_exp2f(o[l32] - m_all);
+      l = fmaf(o[32 + l32], g, l);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          acc[d][r] =
+              fmaf(o[(2 + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32], g, acc[d][r]);
+    }
+    if (row_ok) {
+      const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
+      const float lse2 = l == 0.0f ? kNegInf : m_all + __builtin_amdgcn_logf(l);
+      if (job.slot >= 0) {
+        const long long slot = job.slot * kFewRows + local;
+        if (half == 0) a.part_lse[slot] = lse2;
+        float* po = a.part + slot * D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int comp = d * 32 + 8 * r + 4 * half;
+            if (comp < D)
+              *reinterpret_cast<float4_t*>(po + comp) =
+                  float4_t{acc[d][4 * r] * inv, acc[d][4 * r + 1] * inv, acc[d][4 * r + 2] * inv,
+                           acc[d][4 * r + 3] * inv};
+          }
+      } else {
+        const long long t = job.e.row0 + qi;
+        const int head = hk * a.G + qg;
+        if (a.lse && half == 0) a.lse[t * (c.Hk * a.G) + head] = lse2 * kLn2;
+        char* op = a.out + t * a.o_r + head * a.o_h;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int comp = d * 32 + 8 * r + 4 * half;
+            if (comp >= D) continue;
+            const float o0 = acc[d][4 * r] * inv, o1 = acc[d][4 * r + 1] * inv,
+                        o2 = acc[d][4 * r + 2] * inv, o3 = acc[d][4 * r + 3] * inv;
+            if constexpr (EB == 4)
+              *reinterpret_cast<float4_t*>(op + comp * 4) = float4_t{o0, o1, o2, o3};
+            else
+              *reinterpret_cast<u32x2_t*>(op + comp * 2) =
+                  u32x2_t{pack2<DT>(o0, o1), pack2<DT>(o2, o3)};
+          }
+      }
+    }
+  }
+  lds_barrier();   // the joined results are read
+}
+
+// Entries of few rows: the tiles of all their key heads in a row, entry after
+// entry, each workgroup a run of them of one length (so that entries of very
+// different lengths fill the GPU to the end).  A head whose tiles lie in one run
+// is written at once, of others the runs' parts are joined (few_join_kernel).
+template <int DT, int CF, int DP>
+__global__ __launch_bounds__(kThreads, 2) void few_kernel(const CacheAttnArgs a) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
+  Job job;
+  job.row_tile = 0;
+  if (a.few_groups == 0) {
+    job.b = blockIdx.x / a.c.Hk;
+    job.hk = blockIdx.x - job.b * a.c.Hk;
+    job.e = entry_of(a, job.b);
+    job.t0 = 0;
+    job.t1 = few_tiles(job.e);
+    job.slot = -1;
+    if (job.t1 > 0) attend_few<DT, CF, DP>(a, job, lds);
+    return;
+  }
+  auto weight = [&](int b) { return few_tiles(entry_of(a, b)); };
+  const int Hk = a.c.Hk;
+  const long long total = total_of(a.c.B, weight) * Hk, per = share_of(total, a.few_groups);
+  long long x = blockIdx.x * per;
+  const long long begin = x, end = x + per < total ? x + per : total;
+  while (x < end) {
+    const Found f = find(a.c.B, x / Hk, [&](int b) { return weight(b); });
+    job.b = __builtin_amdgcn_readfirstlane(f.b);
+    job.e = entry_of(a, job.b);
+    const int tiles = few_tiles(job.e);
+    // the entry's heads one after another
+    while (x < end && x < (f.first + tiles) * Hk) {
+      const int in = (int)(x - f.first * Hk);
+      job.hk = in / tiles;
+      job.t0 = in - job.hk * tiles;
+      job.t1 = tiles - job.t0 < end - x ? tiles : job.t0 + (int)(end - x);
+      job.slot = job.t0 == 0 && job.t1 == tiles ? -1 : 2LL * blockIdx.x + (x == begin ? 0 : 1);
+      attend_few<DT, CF, DP>(a, job, lds);
+      x += job.t1 - job.t0;
+    }
+  }
+}
+
+// Joins the parts of row blockIdx.y of a key head of an entry:
+// out = sum_s 2^(lse_s - lse) o_s.  LPR lanes a part, 4 components a lane; the
+// workgroup's sets of lanes take parts in turn and meet in LDS, in order.
+template <int DT, int LPR>
+__global__ __launch_bounds__(kThreads) void few_join_kernel(const CacheAttnArgs a) {
+  constexpr int SETS = kThreads / LPR;
+  __shared__ float tops[SETS], sums[SETS];
+  __shared__ float4_t outs[SETS][LPR];
+  const int Hk = a.c.Hk, D = a.c.D;
+  const int b = blockIdx.x / Hk, hk = blockIdx.x - b * Hk, row = blockIdx.y;
+  const Entry e = entry_of(a, b);
+  const int tiles = few_tiles(e);
+  if (tiles < 2 || row >= e.rows) return;
+  auto weight = [&](int i) { return few_tiles(entry_of(a, i)); };
+  const long long total = total_of(a.c.B, weight) * Hk, per = share_of(total, a.few_groups);
+  const long long u0 = begin_of(b, weight) * Hk + (long long)hk * tiles, u1 = u0 + tiles;
+  const int g0 = (int)(u0 / per), g1 = (int)((u1 - 1) / per);
+  if (g0 == g1) return;
+  const int set = threadIdx.x / LPR, lane = threadIdx.x % LPR;
+  const bool live = 4 * lane < D;
+  float m = kLowest, sum = 0.0f;
+  float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g = g0 + set; g <= g1; g += SETS) {
+    // a run's first part is its slot 0
+    const long long slot =
+        (2LL * g + (g == g0 && u0 != g * per ? 1 : 0)) * kFewRows + row;
+    const float w = a.part_lse[slot];
+    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (live) v = *reinterpret_cast<const float4_t*>(a.part + slot * D + 4 * lane);
+    const float m_new = fmaxf(m, w), fall = __builtin_amdgcn_exp2f(m - m_new),
+                p = __builtin_amdgcn_exp2f(w - m_new);
+    m = m_new;
+    sum = fmaf(sum, fall, p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j] * fall);
+  }
+  if (lane == 0) {
+    tops[set] = m;
+    sums[set] = sum;
+  }
+  outs[set][lane] = o;
+  __syncthreads();
+  if (set > 0) return;
+  float m_all = m;
+#pragma unroll
+  for (int s = 1; s < SETS; ++s) m_all = fmaxf(m_all, tops[s]);
+  sum = 0.0f;
+  o = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < SETS; ++s) {
+    const float p = __builtin_amdgcn_exp2f(tops[s] - m_all);
+    sum = fmaf(sums[s], p, sum);
+    const float4_t v = outs[s][lane];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j]);
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : sum;
+  const int qi = row / a.G, head = hk * a.G + row - qi * a.G;
+  const long long t = e.row0 + qi;
+  if (a.lse && lane == 0)
+    a.lse[t * (Hk * a.G) + head] =
+        sum == 0.0f ? kNegInf : (m_all + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (!live) return;
+  char* op = a.out + t * a.o_r + head * a.o_h;
+  if constexpr (DT == DT_F32)
+    *reinterpret_cast<float4_t*>(op + 16 * lane) = o * inv;
+  else
+    *reinterpret_cast<u32x2_t*>(op + 8 * lane) =
+        u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+}
+
+// Entries of more rows (with `all`, of any): 32 rows of a key head a workgroup.
+template <int DT, int CF, int DP>
+__global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a, int all) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
+  Job job;
+  const int x = blockIdx.x / a.c.Hk;
+  job.hk = blockIdx.x - x * a.c.Hk;
+  const Found f = find(a.c.B, x, [&](int b) {
+    const Entry e = entry_of(a, b);
+    return all || !few(e) ? (e.rows + 31) / 32 : 0;
+  });
+  if (f.b >= a.c.B) return;
+  job.b = __builtin_amdgcn_readfirstlane(f.b);
+  job.e = entry_of(a, job.b);
+  job.row_tile = x - (int)f.first;
+  const int last = (job.row_tile * 32 + 31 < job.e.rows ? job.row_tile * 32 + 31 : job.e.rows - 1);
+  int keys = a.causal ? job.e.len - job.e.n + last / a.G + 1 : job.e.len;
+  job.t0 = 0;
+  job.t1 = keys > 0 ? (keys + kTile - 1) / kTile : 0;
+  job.slot = -1;
+  attend_few<DT, CF, DP>(a, job, lds);
+}
+
+// Sets of 32 rows of a key head that a batch of T rows may have.
+long long row_sets(const CacheAttnArgs& a, long long set) {
+  const long long each = ((long long)a.max_rows * a.G + set - 1) / set * a.c.B;
+  const long long all = (long long)a.T * a.G / set + a.c.B;
+  return each < all ? each : all;
+}
+
+template <int DT, int CF, int DP>
+void launch(const CacheAttnArgs& a, hipStream_t stream) {
+  const dim3 threads(kThreads);
+  // all entries have the most rows, or (rows of no entry) none does
+  const int all = (long long)a.max_rows * a.G > kFewRows && (long long)a.T == (long long)a.max_rows * a.c.B;
+  if (!all && a.G <= kFewRows) {
+    const int groups = a.few_groups > 0 ? a.few_groups : a.c.B * a.c.Hk;
+    hipLaunchKernelGGL((few_kernel<DT, CF, DP>), dim3((unsigned)groups), threads, 0, stream, a);
+    if (a.few_groups > 0) {
+      constexpr int LPR = DP <= 64 ? 16 : 32;
+      const long long most = (long long)a.max_rows * a.G;
+      hipLaunchKernelGGL((few_join_kernel<DT, LPR>),
+                         dim3((unsigned)(a.c.B * a.c.Hk), (unsigned)(most < 32 ? most : 32)), threads,
+                         0, stream, a);
+    }
+  }
+  if ((long long)a.max_rows * a.G > kFewRows)
+    hipLaunchKernelGGL((many_kernel<DT, CF, DP>), dim3((unsigned)(row_sets(a, 32) * a.c.Hk)),
+                       threads, 0, stream, a, all);
+}
+
+template <int DT, int CF> void launch_cf(const CacheAttnArgs& a, hipStream_t stream) {
+  if (a.c.D <= 64) launch<DT, CF, 64>(a, stream);
+  else if (a.c.D <= 96) launch<DT, CF, 96>(a, stream);
+  else launch<DT, CF, 128>(a, stream);
+}
+template <int DT> void launch_dt(const CacheAttnArgs& a, int format, hipStream_t stream) {
+  if (format == LIBCONV_CACHE_I8) launch_cf<DT, LIBCONV_CACHE_I8>(a, stream);
+  else launch_cf<DT, LIBCONV_CACHE_E4M3>(a, stream);
+}
+
+}  // namespace
+
+long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
+  a->few_groups = 0;
+  a->splits = 1;
+  if (!allowed || a->T == 0 || a->c.B == 0) return 0;
+  if (a->G <= kFewRows && (long long)a->c.width << a->c.log_block > 512) a->few_groups = 2 * cus;
+  return 2LL * a->few_groups * kFewRows * (a->c.D + 1) * 4;
+}
+
+void cache_attn_place(CacheAttnArgs* a, char* workspace) {
+  a->part = reinterpret_cast<float*>(workspace);
+  a->part_lse = a->part + 2LL * a->few_groups * kFewRows * a->c.D;
+}
+
+libconv_status cache_attn_launch(CacheAttnArgs a, int format, int dtype, hipStream_t stream) {
+  if (dtype == LIBCONV_F32) launch_dt<DT_F32>(a, format, stream);
+  else if (dtype == LIBCONV_F16) launch_dt<DT_F16>(a, format, stream);
+  else launch_dt<DT_BF16>(a, format, stream);
+  return hipGetLastError() == hipSuccess ? LIBCONV_OK : LIBCONV_ERR_LAUNCH;
+}
+
+}  // namespace libconv

@@ -1,6 +1,6 @@
 // layer.h -- the attention-layer operators' launches, shared by their entry
 // points (layer_api.cpp) and their kernels (rope.hip, attention.hip,
-// lora.hip).  Not part of the public ABI.
+// lora.hip, kv_cache.hip, cache_attention.hip, linear.hip).  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -73,5 +73,69 @@ struct LoraArgs {
 // Fills the plan, and returns the workspace bytes it takes.
 long long lora_plan(LoraArgs* a, int dtype, int cus);
 libconv_status lora_launch(LoraArgs a, int dtype, int cus, hipStream_t stream);
+
+// The cache in 8 bits; strides in bytes.
+struct CacheView {
+  char* codes[2];           // keys, values
+  float* scale[2];          // [blocks][Hk]
+  long long block[2], token[2], head[2];
+  const int* lengths;
+  const int* table;         // [B][width]
+  int B, blocks, log_block, width, Hk, D;
+};
+// libconv_kv_cache_write (rows of k and v) and _read (entries' rows).
+struct CacheCopyArgs {
+  CacheView c;
+  char* x[2];               // k, v
+  long long entry[2], row[2], head[2];
+  const int* starts;        // write
+  int T;                    // rows of k and v, or (read) of an entry
+};
+libconv_status cache_write_launch(const CacheCopyArgs& a, int format, int dtype,
+                                  hipStream_t stream);
+libconv_status cache_read_launch(const CacheCopyArgs& a, int format, int dtype,
+                                 hipStream_t stream);
+
+// libconv_cache_attention; strides in bytes.
+struct CacheAttnArgs {
+  CacheView c;
+  const char* q;
+  char* out;
+  float* lse;
+  const int* starts;
+  long long q_r, q_h, o_r, o_h;
+  int T, max_rows, G;
+  float scale;              // |scale| log2(e), never 0
+  int flip;                 // -1: q changes sign (scale < 0), 1: q counts as 0 (scale 0)
+  int causal;
+  // plan
+  int few_groups;           // workgroups that share the keys of entries of few rows;
+                            // 0: one to an entry and key head
+  int splits;               // of the keys of entries of many rows
+  float* few;               // partial results of the former: [2 few_groups][32][D + 1]
+  float* part;              // of the latter: [splits][Hk][T * G][D]
+  float* part_lse;          // [splits][Hk][T * G], log2
+};
+// Fills the plan for `cus` compute units and returns the workspace bytes it
+// takes; with a smaller workspace the plan has to be made with allowed = false.
+long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed);
+// Puts the partial results into a workspace of that many bytes.
+void cache_attn_place(CacheAttnArgs* a, char* workspace);
+libconv_status cache_attn_launch(CacheAttnArgs a, int format, int dtype, hipStream_t stream);
+
+// libconv_linear; strides in bytes.
+struct LinearArgs {
+  const char *x, *w;
+  const void* bias;
+  const char* residual;
+  char* y;
+  int T, K, N, act;
+  long long x_row, r_row, y_row;
+  // plan: sums of runs of the sum's axis [splits][T][N up to 64s], the runs' bytes
+  float* part;
+  int splits, run, tile;
+};
+long long linear_plan(LinearArgs* a, int dtype, int cus, bool allowed);
+libconv_status linear_launch(LinearArgs a, int dtype, hipStream_t stream);
 
 }  // namespace libconv

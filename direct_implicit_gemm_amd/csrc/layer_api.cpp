@@ -51,8 +51,9 @@ struct View {
   }
   // What all rows (of axes 0 and 1) are multiples of apart; 0: one row.
   long long row_step() const { return std::gcd(s[0], s[1]); }
-  // Bytes of one row's heads.
+  // Bytes of one row's heads, and of one entry's (or block's) rows.
   long long in_row() const { return (n[2] - 1) * s[2] + dense; }
+  long long in_entry() const { return (n[1] - 1) * s[1] + in_row(); }
 };
 
 View view(const void* p, long long n0, long long s0, long long n1, long long s1, long long n2,
@@ -81,14 +82,18 @@ bool ranges_meet(const void* a, long long abytes, const void* b, long long bbyte
 // Whether two operands may share a byte.  Slices of the rows of one buffer
 // (queries, keys and values of a fused projection) lie in one another's range
 // without meeting, where each has a part of its own of the step that all their
-// rows are multiples of apart.
+// rows are multiples of apart; so do slices of its entries (the keys and the
+// values of a cache's blocks).
 bool meet(const View& a, const View& b) {
   if (!ranges_meet(a.p, a.span(), b.p, b.span())) return false;
-  const long long step = std::gcd(a.row_step(), b.row_step());
-  if (step == 0) return true;
-  long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % step;
-  if (d < 0) d += step;
-  return d < a.in_row() || d + b.in_row() > step;
+  auto apart = [&](long long step, long long in_a, long long in_b) {
+    if (step == 0) return false;
+    long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % step;
+    if (d < 0) d += step;
+    return d >= in_a && d + in_b <= step;
+  };
+  return !apart(std::gcd(a.row_step(), b.row_step()), a.in_row(), b.in_row()) &&
+         !apart(std::gcd(a.s[0], b.s[0]), a.in_entry(), b.in_entry());
 }
 
 bool good_strides(const long long* s, int n) {
@@ -137,6 +142,94 @@ libconv_status lora_shape(int T, int K, int N, int rank, int n_adapters, int n_r
       ((double)T / 64 + 1) * ((double)N / 64 + 1) > (double)(1 << 24))
     return LIBCONV_ERR_TOO_LARGE;
   return LIBCONV_OK;
+}
+
+// ---------------------------------------------------------- the 8-bit cache
+libconv_status cache_shape(int B, int blocks, int block_size, int width, int k_heads,
+                           int head_dim, int format, int dtype) {
+  if (!good_dtype(dtype) || (format != LIBCONV_CACHE_I8 && format != LIBCONV_CACHE_E4M3))
+    return LIBCONV_ERR_BAD_DTYPE;
+  if (B < 0 || blocks < 0 || width < 0 || k_heads < 1 || head_dim < 1 || block_size < 1)
+    return LIBCONV_ERR_BAD_SHAPE;
+  if (head_dim > 128 || head_dim % 16 != 0 || block_size < 16 || block_size > 256 ||
+      (block_size & (block_size - 1)) != 0)
+    return LIBCONV_ERR_UNSUPPORTED;
+  // positions and heads are counted in 31 bits
+  if ((long long)width * block_size > kMaxInt - 1024 || k_heads > (1 << 20) || B > (1 << 24) - 4096)
+    return LIBCONV_ERR_TOO_LARGE;
+  return LIBCONV_OK;
+}
+
+// The cache's operands and the views of its codes; strides: those of the keys'
+// codes, then of the values', in bytes.
+struct CacheOperands {
+  View codes[2];
+  const void* read[4];        // scales, lengths, table
+  long long bytes[4];
+};
+libconv_status cache_operands(CacheView* c, CacheOperands* o, const void* k_cache,
+                              const void* v_cache, const float* k_scale, const float* v_scale,
+                              const int* lengths, const int* table, const long long* strides,
+                              int B, int blocks, int block_size, int width, int k_heads,
+                              int head_dim) {
+  const bool any = (long long)blocks * width > 0;   // else the cache holds nothing
+  if ((any && (!k_cache || !v_cache || !k_scale || !v_scale)) ||
+      (B > 0 && (!lengths || (width > 0 && !table))))
+    return LIBCONV_ERR_NULL_POINTER;
+  if (!good_strides(strides, 6)) return LIBCONV_ERR_BAD_SHAPE;
+  std::memset(c, 0, sizeof(*c));
+  const void* codes[2] = {k_cache, v_cache};
+  const float* scale[2] = {k_scale, v_scale};
+  for (int i = 0; i < 2; ++i) {
+    o->codes[i] = view(codes[i], blocks, strides[3 * i], block_size, strides[3 * i + 1], k_heads,
+                       strides[3 * i + 2], head_dim, 1);
+    if (!aligned16(o->codes[i]) || ((uintptr_t)scale[i] & 3) != 0) return LIBCONV_ERR_MISALIGNED;
+    if (o->codes[i].s[1] > kMaxRowBytes) return LIBCONV_ERR_TOO_LARGE;
+    c->codes[i] = const_cast<char*>(o->codes[i].p);
+    c->scale[i] = const_cast<float*>(scale[i]);
+    c->block[i] = o->codes[i].s[0];
+    c->token[i] = o->codes[i].s[1];
+    c->head[i] = o->codes[i].s[2];
+    o->read[i] = scale[i];
+    o->bytes[i] = 4LL * blocks * k_heads;
+  }
+  if ((((uintptr_t)lengths | (uintptr_t)table) & 3) != 0) return LIBCONV_ERR_MISALIGNED;
+  o->read[2] = lengths;
+  o->bytes[2] = 4LL * B;
+  o->read[3] = table;
+  o->bytes[3] = 4LL * B * width;
+  c->lengths = lengths;
+  c->table = table;
+  c->B = B;
+  c->blocks = blocks;
+  while ((1 << c->log_block) < block_size) ++c->log_block;
+  c->width = width;
+  c->Hk = k_heads;
+  c->D = head_dim;
+  return LIBCONV_OK;
+}
+
+libconv_status cache_attn_shape(int B, int T, int max_rows, int block_size, int width, int q_heads,
+                                int k_heads, int head_dim, int format, int dtype) {
+  const libconv_status st =
+      cache_shape(B, 0, block_size, width, k_heads, head_dim, format, dtype);
+  if (st != LIBCONV_OK) return st;
+  if (T < 0 || max_rows < 0 || q_heads < 1 || q_heads % k_heads != 0) return LIBCONV_ERR_BAD_SHAPE;
+  // rows are counted in 31 bits, the lanes of a launch (256 to 128 rows of a key
+  // head, one set at least for each entry) in 32
+  const double rows = (double)T * q_heads;
+  const double groups =
+      k_heads * ((double)T * (q_heads / k_heads) / 128 + 2.0 * B) * (T > 0 ? 1 : 0);
+  const double keys = (double)k_heads * ((double)width * block_size + 128);
+  if (T > kMaxRows || rows > (double)(kMaxInt / 64) || groups > (double)((1 << 24) - 4096) ||
+      keys > 64.0 * kMaxInt)
+    return LIBCONV_ERR_TOO_LARGE;
+  return LIBCONV_OK;
+}
+
+// ------------------------------------------------------------------ linear
+libconv_status linear_shape(int T, int K, int N, int dtype) {
+  return lora_shape(T, K, N, 0, 0, 0, dtype);
 }
 
 }  // namespace
@@ -391,6 +484,267 @@ libconv_status libconv_lora_linear(const void* x, const void* w, const void* bia
   int cus = 0;
   if (!current_device(&cus)) return LIBCONV_ERR_NO_DEVICE;
   return lora_launch(l, dtype, cus, reinterpret_cast<hipStream_t>(stream));
+}
+
+libconv_status libconv_kv_cache_write(const void* k, const void* v, void* k_cache, void* v_cache,
+                                      float* k_scale, float* v_scale, const int* row_starts,
+                                      const int* lengths, const int* block_table,
+                                      const long long* strides, int B, int T, int blocks,
+                                      int block_size, int table_width, int k_heads, int head_dim,
+                                      int format, int dtype, void* stream) {
+  const libconv_status st =
+      cache_shape(B, blocks, block_size, table_width, k_heads, head_dim, format, dtype);
+  if (st != LIBCONV_OK) return st;
+  if (T < 0) return LIBCONV_ERR_BAD_SHAPE;
+  if (T > kMaxRows) return LIBCONV_ERR_TOO_LARGE;
+  if (!strides || (T > 0 && (!k || !v)) || (B > 0 && !row_starts)) return LIBCONV_ERR_NULL_POINTER;
+  if (!good_strides(strides, 4)) return LIBCONV_ERR_BAD_SHAPE;
+  CacheCopyArgs a;
+  std::memset(&a, 0, sizeof(a));
+  CacheOperands o;
+  const libconv_status so =
+      cache_operands(&a.c, &o, k_cache, v_cache, k_scale, v_scale, lengths, block_table,
+                     strides + 4, B, blocks, block_size, table_width, k_heads, head_dim);
+  if (so != LIBCONV_OK) return so;
+  const int eb = dtype_bytes(dtype);
+  const void* x[2] = {k, v};
+  View vx[2];
+  for (int i = 0; i < 2; ++i) {
+    vx[i] = view(x[i], 1, 0, T, strides[2 * i], k_heads, strides[2 * i + 1], head_dim, eb);
+    if (!aligned16(vx[i])) return LIBCONV_ERR_MISALIGNED;
+    a.x[i] = const_cast<char*>(vx[i].p);
+    a.row[i] = vx[i].s[1];
+    a.head[i] = vx[i].s[2];
+  }
+  if (((uintptr_t)row_starts & 3) != 0) return LIBCONV_ERR_MISALIGNED;
+  // what is written: codes and scales
+  const long long starts_bytes = 4LL * (B + 1LL);
+  for (int i = 0; i < 2; ++i) {
+    const View& w = o.codes[i];
+    if (!w.distinct() || meet(w, vx[0]) || meet(w, vx[1]) || (i == 0 && meet(w, o.codes[1])) ||
+        ranges_meet(w.p, w.span(), row_starts, starts_bytes) ||
+        ranges_meet(o.read[i], o.bytes[i], row_starts, starts_bytes) ||
+        ranges_meet(o.read[i], o.bytes[i], vx[0].p, vx[0].span()) ||
+        ranges_meet(o.read[i], o.bytes[i], vx[1].p, vx[1].span()))
+      return LIBCONV_ERR_ALIAS;
+    for (int j = 0; j < 4; ++j)
+      if (ranges_meet(w.p, w.span(), o.read[j], o.bytes[j]) ||
+          (j > i && ranges_meet(o.read[i], o.bytes[i], o.read[j], o.bytes[j])))
+        return LIBCONV_ERR_ALIAS;
+  }
+  if (T == 0 || B == 0 || blocks == 0 || table_width == 0) return LIBCONV_OK;
+  int cus = 0;
+  if (!current_device(&cus)) return LIBCONV_ERR_NO_DEVICE;
+  a.starts = row_starts;
+  a.T = T;
+  return cache_write_launch(a, format, dtype, reinterpret_cast<hipStream_t>(stream));
+}
+
+libconv_status libconv_kv_cache_read(const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int* lengths, const int* block_table, void* k, void* v,
+                                     const long long* strides, int B, int S, int blocks,
+                                     int block_size, int table_width, int k_heads, int head_dim,
+                                     int format, int dtype, void* stream) {
+  const libconv_status st =
+      cache_shape(B, blocks, block_size, table_width, k_heads, head_dim, format, dtype);
+  if (st != LIBCONV_OK) return st;
+  if (S < 0) return LIBCONV_ERR_BAD_SHAPE;
+  if (!strides || ((long long)B * S > 0 && (!k || !v))) return LIBCONV_ERR_NULL_POINTER;
+  if (!good_strides(strides + 6, 6)) return LIBCONV_ERR_BAD_SHAPE;
+  CacheCopyArgs a;
+  std::memset(&a, 0, sizeof(a));
+  CacheOperands o;
+  const libconv_status so =
+      cache_operands(&a.c, &o, k_cache, v_cache, k_scale, v_scale, lengths, block_table, strides, B,
+                     blocks, block_size, table_width, k_heads, head_dim);
+  if (so != LIBCONV_OK) return so;
+  // no more rows than the table has positions
+  const long long most = (long long)table_width * block_size;
+  const int rows = S < most ? S : (int)most;
+  if ((double)B * ((rows + block_size - 1) / block_size) > (double)((1 << 24) - 4096))
+    return LIBCONV_ERR_TOO_LARGE;
+  const int eb = dtype_bytes(dtype);
+  void* x[2] = {k, v};
+  View vx[2];
+  for (int i = 0; i < 2; ++i) {
+    vx[i] = view(x[i], B, strides[6 + 3 * i], S, strides[7 + 3 * i], k_heads, strides[8 + 3 * i],
+                 head_dim, eb);
+    if (!aligned16(vx[i])) return LIBCONV_ERR_MISALIGNED;
+    a.x[i] = static_cast<char*>(x[i]);
+    a.entry[i] = vx[i].s[0];
+    a.row[i] = vx[i].s[1];
+    a.head[i] = vx[i].s[2];
+  }
+  for (int i = 0; i < 2; ++i) {
+    const View& w = vx[i];
+    if (!w.distinct() || meet(w, o.codes[0]) || meet(w, o.codes[1]) || (i == 0 && meet(w, vx[1])))
+      return LIBCONV_ERR_ALIAS;
+    for (int j = 0; j < 4; ++j)
+      if (ranges_meet(w.p, w.span(), o.read[j], o.bytes[j])) return LIBCONV_ERR_ALIAS;
+  }
+  if (B == 0 || rows == 0 || blocks == 0) return LIBCONV_OK;
+  int cus = 0;
+  if (!current_device(&cus)) return LIBCONV_ERR_NO_DEVICE;
+  a.T = rows;
+  return cache_read_launch(a, format, dtype, reinterpret_cast<hipStream_t>(stream));
+}
+
+long long libconv_cache_attention_workspace(int B, int T, int max_rows, int block_size,
+                                            int table_width, int q_heads, int k_heads,
+                                            int head_dim, int dtype) {
+  if (cache_attn_shape(B, T, max_rows, block_size, table_width, q_heads, k_heads, head_dim,
+                       LIBCONV_CACHE_I8, dtype) != LIBCONV_OK)
+    return -1;
+  CacheAttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.c.B = B;
+  a.c.width = table_width;
+  while ((1 << a.c.log_block) < block_size) ++a.c.log_block;
+  a.c.Hk = k_heads;
+  a.c.D = head_dim;
+  a.T = T;
+  a.max_rows = max_rows < T ? max_rows : T;
+  a.G = q_heads / k_heads;
+  return cache_attn_plan(&a, dtype, kPlanCus, true);
+}
+
+libconv_status libconv_cache_attention(const void* q, const void* k_cache, const void* v_cache,
+                                       const float* k_scale, const float* v_scale,
+                                       const int* row_starts, const int* lengths,
+                                       const int* block_table, void* out, float* lse,
+                                       const long long* strides, int B, int T, int max_rows,
+                                       int blocks, int block_size, int table_width, int q_heads,
+                                       int k_heads, int head_dim, float scale, int causal,
+                                       int format, int dtype, void* workspace,
+                                       long long workspace_bytes, void* stream) {
+  const libconv_status sc =
+      cache_shape(B, blocks, block_size, table_width, k_heads, head_dim, format, dtype);
+  if (sc != LIBCONV_OK) return sc;
+  const libconv_status st = cache_attn_shape(B, T, max_rows, block_size, table_width, q_heads,
+                                             k_heads, head_dim, format, dtype);
+  if (st != LIBCONV_OK) return st;
+  if (!std::isfinite(scale) || workspace_bytes < 0) return LIBCONV_ERR_BAD_SHAPE;
+  if (!strides || (T > 0 && (!q || !out)) || (B > 0 && !row_starts))
+    return LIBCONV_ERR_NULL_POINTER;
+  if (!good_strides(strides, 4)) return LIBCONV_ERR_BAD_SHAPE;
+  CacheAttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  CacheOperands o;
+  const libconv_status so =
+      cache_operands(&a.c, &o, k_cache, v_cache, k_scale, v_scale, lengths, block_table,
+                     strides + 4, B, blocks, block_size, table_width, k_heads, head_dim);
+  if (so != LIBCONV_OK) return so;
+  const int eb = dtype_bytes(dtype);
+  const View vq = view(q, 1, 0, T, strides[0], q_heads, strides[1], head_dim, eb);
+  const View vo = view(out, 1, 0, T, strides[2], q_heads, strides[3], head_dim, eb);
+  if (!aligned16(vq) || !aligned16(vo) || (((uintptr_t)row_starts | (uintptr_t)lse) & 3) != 0 ||
+      ((uintptr_t)workspace & 255) != 0)
+    return LIBCONV_ERR_MISALIGNED;
+  const long long lse_bytes = 4LL * T * q_heads;
+  if (!vo.distinct() || meet(vo, vq) || meet(vo, o.codes[0]) || meet(vo, o.codes[1]) ||
+      ranges_meet(out, vo.span(), lse, lse_bytes) ||
+      ranges_meet(out, vo.span(), workspace, workspace_bytes) ||
+      ranges_meet(lse, lse_bytes, workspace, workspace_bytes))
+    return LIBCONV_ERR_ALIAS;
+  const void* read[8] = {q, o.codes[0].p, o.codes[1].p, row_starts, o.read[0], o.read[1],
+                         o.read[2], o.read[3]};
+  const long long bytes[8] = {vq.span(), o.codes[0].span(), o.codes[1].span(), 4LL * (B + 1LL),
+                              o.bytes[0], o.bytes[1], o.bytes[2], o.bytes[3]};
+  for (int i = 0; i < 8; ++i)
+    if ((i >= 3 && ranges_meet(out, vo.span(), read[i], bytes[i])) ||
+        ranges_meet(lse, lse_bytes, read[i], bytes[i]) ||
+        ranges_meet(workspace, workspace_bytes, read[i], bytes[i]))
+      return LIBCONV_ERR_ALIAS;
+  if (B == 0 || T == 0 || max_rows == 0) return LIBCONV_OK;
+  int cus = 0;
+  if (!current_device(&cus)) return LIBCONV_ERR_NO_DEVICE;
+  a.q = vq.p;
+  a.out = static_cast<char*>(out);
+  a.lse = lse;
+  a.starts = row_starts;
+  a.q_r = vq.s[1];
+  a.q_h = vq.s[2];
+  a.o_r = vo.s[1];
+  a.o_h = vo.s[2];
+  a.T = T;
+  a.max_rows = max_rows < T ? max_rows : T;
+  a.G = q_heads / k_heads;
+  a.scale = scale == 0.0f ? 1.0f : std::fabs(scale) * 1.4426950408889634f;
+  a.flip = scale == 0.0f ? 1 : scale < 0.0f ? -1 : 0;
+  a.causal = causal != 0;
+  const long long need = cache_attn_plan(&a, dtype, kPlanCus, true);
+  if (need > 0) {
+    if (workspace && workspace_bytes >= need)
+      cache_attn_place(&a, static_cast<char*>(workspace));
+    else
+      cache_attn_plan(&a, dtype, kPlanCus, false);
+  }
+  return cache_attn_launch(a, format, dtype, reinterpret_cast<hipStream_t>(stream));
+}
+
+long long libconv_linear_workspace(int T, int K, int N, int dtype) {
+  if (linear_shape(T, K, N, dtype) != LIBCONV_OK) return -1;
+  LinearArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.T = T; a.K = K; a.N = N;
+  return linear_plan(&a, dtype, kPlanCus, true);
+}
+
+libconv_status libconv_linear(const void* x, const void* w, const void* bias,
+                              const void* residual, void* y, int T, int K, int N,
+                              long long x_stride, long long residual_stride, long long y_stride,
+                              int act, int dtype, void* workspace, long long workspace_bytes,
+                              void* stream) {
+  const libconv_status st = linear_shape(T, K, N, dtype);
+  if (st != LIBCONV_OK) return st;
+  if (act < LIBCONV_ACT_NONE || act > LIBCONV_ACT_SILU) return LIBCONV_ERR_BAD_ACTIVATION;
+  if (!w || (T > 0 && (!x || !y))) return LIBCONV_ERR_NULL_POINTER;
+  const long long strides[3] = {x_stride, residual_stride, y_stride};
+  if (workspace_bytes < 0 || !good_strides(strides, 3) || (T > 1 && y_stride < N))
+    return LIBCONV_ERR_BAD_SHAPE;
+  const int eb = dtype_bytes(dtype);
+  const View vx = view(x, 1, 0, T, x_stride, 1, 0, K, eb);
+  const View vr = view(residual, 1, 0, T, residual_stride, 1, 0, N, eb);
+  const View vy = view(y, 1, 0, T, y_stride, 1, 0, N, eb);
+  if (vx.s[1] > kMaxRowBytes) return LIBCONV_ERR_TOO_LARGE;
+  if (!aligned16(vx) || ((uintptr_t)w & 15) != 0 || ((uintptr_t)workspace & 255) != 0 ||
+      (((uintptr_t)y | (uintptr_t)bias | (uintptr_t)residual) & (eb - 1)) != 0)
+    return LIBCONV_ERR_MISALIGNED;
+  // an output is written by the lane that has read its residual
+  const bool in_place = residual == y && vr.s[1] == vy.s[1];
+  const void* read[4] = {x, w, bias, residual};
+  const long long bytes[4] = {vx.span(), (long long)N * K * eb, (long long)N * eb,
+                              residual ? vr.span() : 0};
+  if (meet(vy, vx) || (residual && !in_place && meet(vy, vr)) ||
+      ranges_meet(workspace, workspace_bytes, y, vy.span()))
+    return LIBCONV_ERR_ALIAS;
+  for (int i = 0; i < 4; ++i)
+    if (((i == 1 || i == 2) && ranges_meet(y, vy.span(), read[i], bytes[i])) ||
+        ranges_meet(workspace, workspace_bytes, read[i], bytes[i]))
+      return LIBCONV_ERR_ALIAS;
+  if (T == 0) return LIBCONV_OK;
+  int cus = 0;
+  if (!current_device(&cus)) return LIBCONV_ERR_NO_DEVICE;
+  LinearArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = vx.p;
+  a.w = static_cast<const char*>(w);
+  a.bias = bias;
+  a.residual = static_cast<const char*>(residual);
+  a.y = static_cast<char*>(y);
+  a.T = T; a.K = K; a.N = N; a.act = act;
+  a.x_row = vx.s[1];
+  a.r_row = vr.s[1];
+  a.y_row = vy.s[1];
+  const long long need = linear_plan(&a, dtype, kPlanCus, true);
+  if (need > 0) {
+    if (workspace && workspace_bytes >= need)
+      a.part = static_cast<float*>(workspace);
+    else
+      linear_plan(&a, dtype, kPlanCus, false);
+  }
+  return linear_launch(a, dtype, reinterpret_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/StreamGuard.h>
@@ -29,6 +30,12 @@ decltype(&libconv_prefix_attention) attention_call;
 decltype(&libconv_prefix_attention_workspace) attention_workspace;
 decltype(&libconv_lora_linear) lora_call;
 decltype(&libconv_lora_workspace) lora_workspace;
+decltype(&libconv_kv_cache_write) cache_write_call;
+decltype(&libconv_kv_cache_read) cache_read_call;
+decltype(&libconv_cache_attention) cache_attention_call;
+decltype(&libconv_cache_attention_workspace) cache_attention_workspace;
+decltype(&libconv_linear) linear_call;
+decltype(&libconv_linear_workspace) linear_workspace;
 // raw_stream(device) -> handle of the current stream; stream_id(handle, device)
 // -> torch's number of any stream; fail(status, name) raises
 PyObject *raw_stream, *stream_id, *fail;
@@ -61,10 +68,13 @@ struct Kind {
   at::ScalarType type;
   int code;
 };
+int code_of(at::ScalarType s) {
+  return s == at::kFloat ? LIBCONV_F32 : s == at::kHalf ? LIBCONV_F16
+         : s == at::kBFloat16 ? LIBCONV_BF16 : -1;
+}
 Kind kind_of(const char* what, const at::Tensor& t, int64_t dims) {
   const at::ScalarType s = t.scalar_type();
-  const int code = s == at::kFloat ? LIBCONV_F32 : s == at::kHalf ? LIBCONV_F16
-                   : s == at::kBFloat16 ? LIBCONV_BF16 : -1;
+  const int code = code_of(s);
   if (!t.is_cuda() || code < 0 || t.dim() != dims ||
       (t.size(dims - 1) > 1 && t.stride(dims - 1) != 1))
     refuse(what, kOperands);
@@ -147,9 +157,10 @@ struct Call {
   }
   // An output: the caller, who reads it on a stream of theirs, may drop it while
   // that stream still does.
-  at::Tensor fresh(at::ScalarType type, std::initializer_list<int64_t> shape) {
-    at::Tensor t = at::empty(c10::IntArrayRef(shape),
-                             at::TensorOptions().dtype(type).device(kind.device));
+  at::Tensor fresh(at::ScalarType type, std::initializer_list<int64_t> shape, bool zeros = false) {
+    const at::TensorOptions options = at::TensorOptions().dtype(type).device(kind.device);
+    at::Tensor t = zeros ? at::zeros(c10::IntArrayRef(shape), options)
+                         : at::empty(c10::IntArrayRef(shape), options);
     if (callers)
       c10::impl::VirtualGuardImpl(kind.device.type())
           .recordDataPtrOnStream(t.storage().data_ptr(), *callers);
@@ -423,24 +434,256 @@ PyObject* lora_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// The addresses of the five functions (in the order above), raw_stream,
-// stream_id, fail.
+// A cache in 8 bits: k_cache, v_cache, k_scale, v_scale from a[at] on, and
+// lengths and block_table.
+struct Cache {
+  const at::Tensor &k, &v, &ks, &vs, &lengths, &table;
+  int64_t blocks, size, heads, dim, width, entries;
+  int format;
+
+  Cache(const char* what, PyObject* const* a, PyObject* lengths_, PyObject* table_)
+      : k(needed(what, a[0])), v(needed(what, a[1])), ks(needed(what, a[2])),
+        vs(needed(what, a[3])), lengths(needed(what, lengths_)), table(needed(what, table_)) {
+    const at::ScalarType t = k.scalar_type();
+    format = t == at::kChar ? LIBCONV_CACHE_I8 : t == at::kFloat8_e4m3fn ? LIBCONV_CACHE_E4M3 : -1;
+    if (!k.is_cuda() || format < 0 || k.dim() != 4 || (k.size(3) > 1 && k.stride(3) != 1))
+      refuse(what, "k_cache [blocks, block, Hk, D] must be an int8 or float8_e4m3fn device tensor, "
+                   "its last axis dense");
+    blocks = k.size(0);
+    size = k.size(1);
+    heads = k.size(2);
+    dim = k.size(3);
+    const Kind of_codes = {k.device(), t, format}, of_scales = {k.device(), at::kFloat, 0};
+    if (bad(v, of_codes, {blocks, size, heads, dim})) refuse(what, "v_cache must be as k_cache");
+    if (bad_array(ks, of_scales, at::kFloat, {blocks, heads}) ||
+        bad_array(vs, of_scales, at::kFloat, {blocks, heads}))
+      refuse(what, "k_scale, v_scale must be contiguous float32 device tensors [blocks, Hk]");
+    if (lengths.dim() != 1 || table.dim() != 2) refuse(what, "lengths [B], block_table [B, blocks]");
+    entries = lengths.size(0);
+    width = table.size(1);
+    if (bad_array(lengths, of_codes, at::kInt, {entries}) ||
+        bad_array(table, of_codes, at::kInt, {entries, width}))
+      refuse(what, "lengths [B] and block_table [B, blocks] must be contiguous int32 device tensors");
+  }
+  void check_starts(const char* what, const at::Tensor& starts) const {
+    const Kind any = {k.device(), at::kInt, 0};
+    if (bad_array(starts, any, at::kInt, {entries + 1}))
+      refuse(what, "row_starts must be a contiguous int32 device tensor [B + 1]");
+  }
+  void put_strides(long long* s) const {
+    for (int i = 0; i < 3; ++i) {
+      s[i] = k.stride(i);
+      s[3 + i] = v.stride(i);
+    }
+  }
+};
+
+// k, v, k_cache, v_cache, k_scale, v_scale, row_starts, lengths, block_table, stream
+PyObject* kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char* what = "kv_cache_write";
+  if (n != 10) refuse_type(what, "10 arguments");
+  const at::Tensor &k = needed(what, a[0]), &v = needed(what, a[1]), &starts = needed(what, a[6]);
+  const Kind kind = kind_of(what, k, 3);
+  const Cache c(what, a + 2, a[7], a[8]);
+  const int64_t T = k.size(0);
+  if (c.k.device() != kind.device) refuse(what, kOperands);
+  if (bad(k, kind, {T, c.heads, c.dim}) || bad(v, kind, {T, c.heads, c.dim}))
+    refuse(what, "k, v [T, Hk, D] with the cache's heads");
+  c.check_starts(what, starts);
+  LIBCONV_FORWARD_ONLY(what, &k, &v);
+  Call call(kind, a[9]);
+  if (T > 0 && c.entries > 0) {
+    long long strides[10] = {k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+    c.put_strides(strides + 4);
+    const int t = as_int(what, T), b = as_int(what, c.entries), blocks = as_int(what, c.blocks),
+              size = as_int(what, c.size), width = as_int(what, c.width),
+              heads = as_int(what, c.heads), dim = as_int(what, c.dim);
+    call.run("libconv_kv_cache_write", [&] {
+      return cache_write_call(k.const_data_ptr(), v.const_data_ptr(), c.k.mutable_data_ptr(),
+                              c.v.mutable_data_ptr(), static_cast<float*>(c.ks.mutable_data_ptr()),
+                              static_cast<float*>(c.vs.mutable_data_ptr()),
+                              address_of<int>(starts), address_of<int>(c.lengths),
+                              address_of<int>(c.table), strides, b, t, blocks, size, width, heads,
+                              dim, c.format, kind.code, call.stream);
+    });
+  }
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// k_cache, v_cache, k_scale, v_scale, lengths, block_table, k_out, v_out, like (an
+// empty tensor of the type of outputs made here), rows, stream
+PyObject* kv_cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char* what = "kv_cache_read";
+  if (n != 11) refuse_type(what, "11 arguments");
+  const Cache c(what, a, a[4], a[5]);
+  const at::Tensor *ko = tensor(what, a[6]), *vo = tensor(what, a[7]);
+  const at::ScalarType type = ko ? ko->scalar_type() : vo ? vo->scalar_type()
+                                                          : needed(what, a[8]).scalar_type();
+  const Kind kind = {c.k.device(), type, code_of(type)};
+  if (kind.code < 0) refuse(what, "outputs are float32, float16 or bfloat16");
+  int64_t S = ko && ko->dim() == 4 ? ko->size(1) : vo && vo->dim() == 4 ? vo->size(1) : -1;
+  if (S < 0) {
+    S = c.width * c.size;
+    if (a[9] != Py_None) {
+      const long long rows = PyLong_AsLongLong(a[9]);
+      if (rows == -1 && PyErr_Occurred()) throw python_error();
+      S = as_int(what, rows);
+    }
+  }
+  if ((ko && bad(*ko, kind, {c.entries, S, c.heads, c.dim})) ||
+      (vo && bad(*vo, kind, {c.entries, S, c.heads, c.dim})))
+    refuse(what, "bad output tensor");
+  Call call(kind, a[10]);
+  at::Tensor made[2];
+  if (!ko) ko = &(made[0] = call.fresh(type, {c.entries, S, c.heads, c.dim}, true));
+  if (!vo) vo = &(made[1] = call.fresh(type, {c.entries, S, c.heads, c.dim}, true));
+  if (c.entries > 0 && S > 0) {
+    long long strides[12] = {};
+    c.put_strides(strides);
+    for (int i = 0; i < 3; ++i) {
+      strides[6 + i] = ko->stride(i);
+      strides[9 + i] = vo->stride(i);
+    }
+    const int s = as_int(what, S), b = as_int(what, c.entries), blocks = as_int(what, c.blocks),
+              size = as_int(what, c.size), width = as_int(what, c.width),
+              heads = as_int(what, c.heads), dim = as_int(what, c.dim);
+    call.run("libconv_kv_cache_read", [&] {
+      return cache_read_call(c.k.const_data_ptr(), c.v.const_data_ptr(), address_of<float>(c.ks),
+                             address_of<float>(c.vs), address_of<int>(c.lengths),
+                             address_of<int>(c.table), ko->mutable_data_ptr(),
+                             vo->mutable_data_ptr(), strides, b, s, blocks, size, width, heads, dim,
+                             c.format, kind.code, call.stream);
+    });
+  }
+  PyObject* pair = PyTuple_New(2);
+  if (!pair) throw python_error();
+  PyTuple_SET_ITEM(pair, 0, result(a[6], *ko));
+  PyTuple_SET_ITEM(pair, 1, result(a[7], *vo));
+  return pair;
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k_cache, v_cache, k_scale, v_scale, row_starts, lengths, block_table, max_rows,
+// scale, causal, out, return_lse, stream, workspace
+PyObject* cache_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char* what = "cache_attention";
+  if (n != 15) refuse_type(what, "15 arguments");
+  const at::Tensor &q = needed(what, a[0]), &starts = needed(what, a[5]);
+  const Kind kind = kind_of(what, q, 3);
+  const Cache c(what, a + 1, a[6], a[7]);
+  const int64_t T = q.size(0), Hq = q.size(1);
+  if (c.k.device() != kind.device) refuse(what, kOperands);
+  if (q.size(2) != c.dim) refuse(what, "q [T, Hq, D] with the cache's head size");
+  c.check_starts(what, starts);
+  const at::Tensor* out = tensor(what, a[11]);
+  if (out && bad(*out, kind, {T, Hq, c.dim})) refuse(what, "bad output tensor");
+  long long most = T;
+  if (a[8] != Py_None) {
+    most = PyLong_AsLongLong(a[8]);
+    if (most == -1 && PyErr_Occurred()) throw python_error();
+    if (most < 0) refuse(what, "max_rows: the largest number of rows of an entry");
+  }
+  const bool with_lse = truth(a[12]);
+  LIBCONV_FORWARD_ONLY(what, &q);
+  Call call(kind, a[13]);
+  at::Tensor made, lse;
+  if (!out) out = &(made = call.fresh(kind.type, {T, Hq, c.dim}));
+  if (with_lse) lse = call.fresh(at::kFloat, {T, Hq});
+  if (T > 0 && c.entries > 0) {
+    long long strides[10] = {q.stride(0), q.stride(1), out->stride(0), out->stride(1)};
+    c.put_strides(strides + 4);
+    const int t = as_int(what, T), hq = as_int(what, Hq), rows = as_int(what, most),
+              b = as_int(what, c.entries), blocks = as_int(what, c.blocks),
+              size = as_int(what, c.size), width = as_int(what, c.width),
+              heads = as_int(what, c.heads), dim = as_int(what, c.dim);
+    const float scale =
+        a[9] == Py_None ? (float)(1.0 / std::sqrt((double)dim)) : (float)number(a[9]);
+    const int causal = truth(a[10]);
+    call.workspace(what, a[14],
+                   a[14] == Py_True ? cache_attention_workspace(b, t, rows, size, width, hq, heads,
+                                                                dim, kind.code)
+                                    : 0);
+    call.run("libconv_cache_attention", [&] {
+      return cache_attention_call(
+          q.const_data_ptr(), c.k.const_data_ptr(), c.v.const_data_ptr(),
+          address_of<float>(c.ks), address_of<float>(c.vs), address_of<int>(starts),
+          address_of<int>(c.lengths), address_of<int>(c.table), out->mutable_data_ptr(),
+          with_lse ? static_cast<float*>(lse.mutable_data_ptr()) : nullptr, strides, b, t, rows,
+          blocks, size, width, hq, heads, dim, scale, causal, c.format, kind.code, call.ws,
+          call.bytes, call.stream);
+    });
+  }
+  if (!with_lse) return result(a[11], *out);
+  PyObject* pair = PyTuple_New(2);
+  if (!pair) throw python_error();
+  PyTuple_SET_ITEM(pair, 0, result(a[11], *out));
+  PyTuple_SET_ITEM(pair, 1, result(Py_None, lse));
+  return pair;
+  END_HANDLE_TH_ERRORS
+}
+
+// x, w, bias, act (a number), residual, out, stream, workspace
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const char* what = "linear";
+  if (n != 8) refuse_type(what, "8 arguments");
+  const at::Tensor &x = needed(what, a[0]), &w = needed(what, a[1]);
+  const at::Tensor *bias = tensor(what, a[2]), *residual = tensor(what, a[4]),
+                   *out = tensor(what, a[5]);
+  const Kind kind = kind_of(what, x, 2);
+  const int64_t T = x.size(0), K = x.size(1);
+  const int64_t N = w.dim() == 2 ? w.size(0) : -1;
+  if (N < 0 || bad(w, kind, {N, K}) || !w.is_contiguous())
+    refuse(what, "w must be a contiguous [N, K] as x");
+  if (bias && bad(*bias, kind, {N})) refuse(what, "bias must be [N] as x");
+  if (residual && bad(*residual, kind, {T, N})) refuse(what, "residual must be [T, N] as x");
+  if (out && bad(*out, kind, {T, N})) refuse(what, "bad output tensor");
+  const long long act = PyLong_AsLongLong(a[3]);
+  if (act == -1 && PyErr_Occurred()) throw python_error();
+  LIBCONV_FORWARD_ONLY(what, &x, &w, bias, residual);
+  Call call(kind, a[6]);
+  at::Tensor made;
+  if (!out) out = &(made = call.fresh(kind.type, {T, N}));
+  if (T > 0) {
+    const int t = as_int(what, T), kk = as_int(what, K), nn = as_int(what, N);
+    call.workspace(what, a[7], a[7] == Py_True ? linear_workspace(t, kk, nn, kind.code) : 0);
+    call.run("libconv_linear", [&] {
+      return linear_call(x.const_data_ptr(), w.const_data_ptr(), address(bias), address(residual),
+                         out->mutable_data_ptr(), t, kk, nn, x.stride(0),
+                         residual ? residual->stride(0) : 0, out->stride(0), (int)act, kind.code,
+                         call.ws, call.bytes, call.stream);
+    });
+  }
+  return result(a[5], *out);
+  END_HANDLE_TH_ERRORS
+}
+
+// The addresses of the functions, in the order of `calls`, raw_stream, stream_id,
+// fail.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 8) refuse_type("bind", "8 arguments");
-  void* f[5];
-  for (int i = 0; i < 5; ++i) f[i] = PyLong_AsVoidPtr(a[i]);
+  void** const calls[] = {
+      reinterpret_cast<void**>(&rope_call), reinterpret_cast<void**>(&attention_call),
+      reinterpret_cast<void**>(&attention_workspace), reinterpret_cast<void**>(&lora_call),
+      reinterpret_cast<void**>(&lora_workspace), reinterpret_cast<void**>(&cache_write_call),
+      reinterpret_cast<void**>(&cache_read_call), reinterpret_cast<void**>(&cache_attention_call),
+      reinterpret_cast<void**>(&cache_attention_workspace), reinterpret_cast<void**>(&linear_call),
+      reinterpret_cast<void**>(&linear_workspace)};
+  constexpr int count = sizeof(calls) / sizeof(*calls);
+  if (n != count + 3) refuse_type("bind", "another number of functions");
+  void* f[count];
+  for (int i = 0; i < count; ++i) f[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) throw python_error();
-  rope_call = reinterpret_cast<decltype(rope_call)>(f[0]);
-  attention_call = reinterpret_cast<decltype(attention_call)>(f[1]);
-  attention_workspace = reinterpret_cast<decltype(attention_workspace)>(f[2]);
-  lora_call = reinterpret_cast<decltype(lora_call)>(f[3]);
-  lora_workspace = reinterpret_cast<decltype(lora_workspace)>(f[4]);
+  for (int i = 0; i < count; ++i) *calls[i] = f[i];
   PyObject** keep[3] = {&raw_stream, &stream_id, &fail};
   for (int i = 0; i < 3; ++i) {
-    Py_INCREF(a[5 + i]);
+    Py_INCREF(a[count + i]);
     Py_XDECREF(*keep[i]);
-    *keep[i] = a[5 + i];
+    *keep[i] = a[count + i];
   }
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
@@ -449,7 +692,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define LIBCONV_METHOD(f) \
   {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {LIBCONV_METHOD(qk_norm_rope), LIBCONV_METHOD(prefix_attention),
-                         LIBCONV_METHOD(lora_linear), LIBCONV_METHOD(bind),
+                         LIBCONV_METHOD(lora_linear), LIBCONV_METHOD(kv_cache_write),
+                         LIBCONV_METHOD(kv_cache_read), LIBCONV_METHOD(cache_attention),
+                         LIBCONV_METHOD(linear), LIBCONV_METHOD(bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

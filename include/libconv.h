@@ -74,7 +74,11 @@ typedef enum {
 
 typedef enum {
   LIBCONV_ACT_NONE = 0,
-  LIBCONV_ACT_RELU = 1
+  LIBCONV_ACT_RELU = 1,
+  /* of libconv_linear only */
+  LIBCONV_ACT_GELU = 2,           /* v (1 + erf(v / sqrt 2)) / 2 */
+  LIBCONV_ACT_GELU_TANH = 3,      /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+  LIBCONV_ACT_SILU = 4            /* v / (1 + exp(-v)) */
 } libconv_act;
 
 /* Kernel families the dispatcher chooses between. */
@@ -679,6 +683,133 @@ libconv_status libconv_lora_linear(const void* x, const void* w, const void* bia
  * or -1 for invalid arguments.  Pure host arithmetic. */
 long long libconv_lora_workspace(int T, int K, int N, int rank, int n_adapters, int n_requests,
                                  int dtype);
+
+/* ------------------------------------------------------------------------
+ * A cache of keys and values in 8 bits, in blocks, for many requests at once:
+ * libconv_kv_cache_write appends new tokens (after libconv_qk_norm_rope),
+ * libconv_cache_attention attends over it, libconv_kv_cache_read gives it back
+ * in the activations' type (for libconv_prefix_attention, or to keep).
+ *
+ * k_cache, v_cache  [blocks][block_size][k_heads][head_dim] codes of one byte (strides in
+ *     bytes, as codes are one byte each; a layout with each head's tokens of a
+ *     block one after another reads best), and
+ * k_scale, v_scale  [blocks][k_heads] fp32, dense: a code c stands for c * scale.
+ * block_size: 16, 32, 64, 128 or 256 tokens.  head_dim: a multiple of 16 up to
+ * 128 (else LIBCONV_ERR_UNSUPPORTED).
+ *
+ * B entries (requests), whose rows lie one after another in T rows:
+ * row_starts   [B + 1] ints, ascending: entry b has rows row_starts[b] <= t <
+ *              row_starts[b + 1] (clamped to [0, T]), n of them, maybe none.
+ * lengths      [B] ints: the entry's tokens in the cache with those of this call,
+ *              which are the last n of them: row t is at position lengths[b] -
+ *              row_starts[b + 1] + t.  Clamped to [0, table_width * block_size].
+ * block_table  [B][table_width] ints, dense: position p lies in block
+ *              block_table[b][p / block_size], at its token p % block_size.  A
+ *              number outside [0, blocks) is no block: nothing is written to
+ *              it, and its positions are skipped (a window that has moved on).
+ * All three lie on the device.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  LIBCONV_CACHE_I8 = 0,     /* -127 .. 127 */
+  LIBCONV_CACHE_E4M3 = 1    /* 8-bit floats: 4 bits of exponent, 3 of fraction, up to 448 */
+} libconv_cache_format;
+
+/*
+ * Appends rows k, v [T][k_heads][head_dim] to the cache.  The new tokens of a
+ * block, one head's keys or values, are written with one scale
+ *   s = the least power of two >= 2^-126 with max |x| / s <= 127 (448)
+ * over their finite values, or the block's scale so far where that is larger and
+ * the block holds earlier tokens of the entry; those are rounded again where the
+ * scale grows: c -> c * old / s.  Codes are rounded to nearest even.  With
+ * powers of two nothing else is rounded, a block's scale grows a few times at
+ * most, and the roundings again add up to less than one step of the last
+ * scale; the price is up to one bit of I8's seven.  An infinity is written as the
+ * largest code, a NaN as NaN (E4M3) or 0 (I8).  Positions below 0 are not
+ * written, nor is anything else in the cache.
+ *   strides  host array of 10: k (row, head), v (row, head) in elements, k_cache
+ *            (block, token, head), v_cache (block, token, head)
+ * No block may be written by two entries in one call.  T and B may be 0.
+ */
+libconv_status libconv_kv_cache_write(const void* k, const void* v, void* k_cache, void* v_cache,
+                                      float* k_scale, float* v_scale, const int* row_starts,
+                                      const int* lengths, const int* block_table,
+                                      const long long* strides, int B, int T, int blocks,
+                                      int block_size, int table_width, int k_heads, int head_dim,
+                                      int format, int dtype, void* stream);
+
+/*
+ * k[b][p], v[b][p] = code * scale of position p of entry b, rounded to dtype,
+ * for p < min(lengths[b], S); k, v [B][S][k_heads][head_dim].  Rows from there
+ * on, and those of positions in no block, are left as they were.
+ *   strides  host array of 12: k_cache (block, token, head), v_cache (block,
+ *            token, head), k (batch, row, head), v (batch, row, head) in elements
+ */
+libconv_status libconv_kv_cache_read(const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int* lengths, const int* block_table, void* k, void* v,
+                                     const long long* strides, int B, int S, int blocks,
+                                     int block_size, int table_width, int k_heads, int head_dim,
+                                     int format, int dtype, void* stream);
+
+/*
+ * Attention of a ragged batch over the cache:
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * <q[t][h], k_j>)
+ * for row t of entry b, over the entry's positions 0 <= j < lengths[b] (causal:
+ * and j <= the row's own position) that lie in a block.  A query with no key to
+ * see gives 0 (and lse -inf).  Rows of no entry are left as they were.
+ *   q, out   [T][q_heads][head_dim]    lse [T][q_heads] fp32 or NULL
+ *   max_rows at least the rows of any entry (a row past it in its entry is left as
+ *            it was); T will do, the largest number of rows makes a better plan
+ *   strides  host array of 10: q (row, head), out (row, head) in elements,
+ *            k_cache (block, token, head), v_cache (block, token, head)
+ * q_heads is a multiple of k_heads: query head h reads key head
+ * h / (q_heads / k_heads).  Scores, softmax and sums are fp32; codes are exact in
+ * the matrix instructions, q too (fp32 as three bfloat16 terms), and the
+ * probabilities times their values' scale are rounded to 8 bits (bf16), 16
+ * (fp16) or 24 (fp32) for the second product; `out` is rounded once.  Tokens past
+ * an entry's length are not read into any result, whatever their codes and
+ * scales; a NaN that a causal mask hides from a query can reach that query.
+ *   workspace  device, 256-byte aligned, at least
+ *              libconv_cache_attention_workspace bytes for the best plan, which
+ *              splits the keys over workgroups; NULL or smaller: a plan without.
+ */
+libconv_status libconv_cache_attention(const void* q, const void* k_cache, const void* v_cache,
+                                       const float* k_scale, const float* v_scale,
+                                       const int* row_starts, const int* lengths,
+                                       const int* block_table, void* out, float* lse,
+                                       const long long* strides, int B, int T, int max_rows,
+                                       int blocks, int block_size, int table_width, int q_heads,
+                                       int k_heads, int head_dim, float scale, int causal,
+                                       int format, int dtype, void* workspace,
+                                       long long workspace_bytes, void* stream);
+
+/* Workspace bytes of the best plan (0: none), or -1 for invalid arguments.
+ * Pure host arithmetic. */
+long long libconv_cache_attention_workspace(int B, int T, int max_rows, int block_size,
+                                            int table_width, int q_heads, int k_heads,
+                                            int head_dim, int dtype);
+
+/*
+ * y[t][n] = act(sum_k x[t][k] w[n][k] + bias[n]) + residual[t][n]
+ *   x [T][K], residual [T][N] (or NULL), y [T][N]: rows their strides apart
+ *   w [N][K] dense     bias [N] or NULL     act: a libconv_act
+ * Sums, bias, activation and residual are fp32, y is rounded once.  y may be the
+ * residual (the same pointer and stride).  A NaN stays one through every
+ * activation but ReLU, which gives 0 for it, as for the convolutions.
+ * K: a multiple of 8; x and w on 16-byte boundaries; rows of x and w below 2^23
+ * bytes, T below 2^26 - 64.
+ *   workspace  device, 256-byte aligned, at least libconv_linear_workspace bytes
+ *              for the best plan, which splits the sums of few rows over
+ *              workgroups; NULL or smaller: a plan without.
+ */
+libconv_status libconv_linear(const void* x, const void* w, const void* bias,
+                              const void* residual, void* y, int T, int K, int N,
+                              long long x_stride, long long residual_stride, long long y_stride,
+                              int act, int dtype, void* workspace, long long workspace_bytes,
+                              void* stream);
+
+/* Workspace bytes of the best plan (0: none), or -1 for invalid arguments. */
+long long libconv_linear_workspace(int T, int K, int N, int dtype);
 
 /* Static description of a status code; never NULL.  Failures are reported,
  * never turned into an abort (the fault-tolerant backend bring-up of
