@@ -15,18 +15,47 @@ namespace {
 // The activation of a sum in fp32.  The exponentials and the quotient are the
 // hardware's (about one step each); what is left is far below a 16-bit output's
 // step, and a few steps of a 32-bit one.
-__device__ __forceinline__ float activated(float v, int act) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  if (act == LIBCONV_ACT_RELU) return v > 0.0f ? v : 0.0f;
-  if (act == LIBCONV_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  if (act == LIBCONV_ACT_GELU_TANH) {
+template <int DT, int ACT> __device__ __forceinline__ float activated(float v) {
+  constexpr float kLog2e = 1.4426950408889634f, kTwoC = 2.0f * 0.7978845608028654f;   // sqrt(2 / pi)
+  if constexpr (ACT == LIBCONV_ACT_RELU) return v > 0.0f ? v : 0.0f;
+  if constexpr (ACT == LIBCONV_ACT_GELU) {
+    if constexpr (DT == DT_F32) {
+      return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    } else {
+      // Abramowitz and Stegun, 7.1.26: erfc(z) = poly(1 / (1 + p z)) exp(-z^2), z >= 0,
+      // to 1.5e-7.  2167 x 3840 outputs in fp16: the call takes 30 us, with erff 36.
+      const float z = __builtin_fabsf(v) * 0.70710678118654752f;
+      const float t = __builtin_amdgcn_rcpf(fmaf(z, 0.3275911f, 1.0f));
+      float c = fmaf(t, 1.061405429f, -1.453152027f);
+      c = fmaf(t, c, 1.421413741f);
+      c = fmaf(t, c, -0.284496736f);
+      c = fmaf(t, c, 0.254829592f);
+      c *= 0.5f * t * __builtin_amdgcn_exp2f(-kLog2e * z * z);
+      return v * (v > 0.0f ? 1.0f - c : c);
+    }
+  }
+  if constexpr (ACT == LIBCONV_ACT_GELU_TANH) {
     // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u))
-    const float u2 = v * fmaf(v * v, 2.0f * 0.7978845608028654f * 0.044715f, 2.0f * 0.7978845608028654f);
+    const float u2 = v * fmaf(v * v, kTwoC * 0.044715f, kTwoC);
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * u2));
   }
-  if (act == LIBCONV_ACT_SILU)
+  if constexpr (ACT == LIBCONV_ACT_SILU)
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v));
   return v;
+}
+template <int DT, int ACT>
+__device__ __forceinline__ void activate_by(float* v, const float* bias, const float* r) {
+#pragma unroll
+  for (int j = 0; j < 16 / Elem<DT>::bytes; ++j)
+    v[j] = activated<DT, ACT>(v[j] + bias[j]) + r[j];
+}
+template <int DT>
+__device__ __forceinline__ void activate(float* v, const float* bias, const float* r, int act) {
+  if (act == LIBCONV_ACT_NONE) activate_by<DT, LIBCONV_ACT_NONE>(v, bias, r);
+  else if (act == LIBCONV_ACT_RELU) activate_by<DT, LIBCONV_ACT_RELU>(v, bias, r);
+  else if (act == LIBCONV_ACT_GELU) activate_by<DT, LIBCONV_ACT_GELU>(v, bias, r);
+  else if (act == LIBCONV_ACT_GELU_TANH) activate_by<DT, LIBCONV_ACT_GELU_TANH>(v, bias, r);
+  else activate_by<DT, LIBCONV_ACT_SILU>(v, bias, r);
 }
 
 template <int DT> __device__ __forceinline__ float load1(const void* p, long long i) {
@@ -34,70 +63,85 @@ template <int DT> __device__ __forceinline__ float load1(const void* p, long lon
   else return Elem<DT>::bits_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
-// 4 consecutive outputs of a token from their sums; those past N are not there.
-template <int DT>
-__device__ __forceinline__ void finish4(const LinearArgs& a, int t, int n, const float* v) {
-  constexpr int EB = Elem<DT>::bytes;
-  char* at = a.y + t * a.y_row + (long long)n * EB;
-  const char* rt = a.residual ? a.residual + t * a.r_row + (long long)n * EB : nullptr;
-  const bool whole = n + 4 <= a.N;
-  float o[4], r[4] = {0, 0, 0, 0};
-  if (rt) {
-    if (whole && (reinterpret_cast<uintptr_t>(rt) & (4 * EB - 1)) == 0) {
-      if constexpr (EB == 4) {
-        const float4_t f = *reinterpret_cast<const float4_t*>(rt);
+// 16 bytes of a token's outputs, from n on, with bias, activation and residual.
+// Where they do not lie on 16-byte boundaries or reach past N, one by one.
+template <int DT> struct Outputs {
+  static constexpr int EB = Elem<DT>::bytes, E = 16 / EB;
+  int n;
+  bool whole, whole_r;
+  float bias[E];
+
+  __device__ __forceinline__ Outputs(const LinearArgs& a, int first) : n(first) {
+    whole = n + E <= a.N && ((reinterpret_cast<uintptr_t>(a.y) + n * EB | a.y_row) & 15) == 0;
+    whole_r = a.residual && n + E <= a.N &&
+              ((reinterpret_cast<uintptr_t>(a.residual) + n * EB | a.r_row) & 15) == 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = f[j];
-      } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(rt);
+    for (int j = 0; j < E; ++j)
+      bias[j] = a.bias && n + j < a.N ? load1<DT>(a.bias, n + j) : 0.0f;
+  }
+  // What can be read ahead of a token's residual.
+  __device__ __forceinline__ u32x4_t residual(const LinearArgs& a, int t) const {
+    u32x4_t v = {0, 0, 0, 0};
+    if (whole_r && t < a.T)
+      v = *reinterpret_cast<const u32x4_t*>(a.residual + t * a.r_row + (long long)n * EB);
+    return v;
+  }
+  __device__ __forceinline__ void finish(const LinearArgs& a, int t, float* v,
+                                         const u32x4_t& ahead) const {
+    if (t >= a.T || n >= a.N) return;
+    float r[E];
+    unpack<DT>(ahead, r);
+    if (a.residual && !whole_r) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = Elem<DT>::bits_to_f32((w[j / 2] >> (16 * (j & 1))) & 0xffffu);
+      for (int j = 0; j < E; ++j)
+        if (n + j < a.N) r[j] = load1<DT>(a.residual + t * a.r_row, n + j);
+    }
+    activate<DT>(v, bias, r, a.act);
+    char* at = a.y + t * a.y_row + (long long)n * EB;
+    const u32x4_t w = pack<DT>(v);
+    if (whole) {
+      store_out16(at, w);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (n + j < a.N) {
+        if constexpr (EB == 4) reinterpret_cast<uint32_t*>(at)[j] = w[j];
+        else reinterpret_cast<uint16_t*>(at)[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (n + j < a.N) r[j] = load1<DT>(rt, j);
-    }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float b = a.bias && n + j < a.N ? load1<DT>(a.bias, n + j) : 0.0f;
-    o[j] = activated(v[j] + b, a.act) + r[j];
-  }
-  if (whole && (reinterpret_cast<uintptr_t>(at) & (4 * EB - 1)) == 0) {
-    if constexpr (EB == 4)
-      *reinterpret_cast<float4_t*>(at) = float4_t{o[0], o[1], o[2], o[3]};
-    else
-      *reinterpret_cast<u32x2_t*>(at) =
-          u32x2_t{(uint32_t)Elem<DT>::from_f32(o[0]) | ((uint32_t)Elem<DT>::from_f32(o[1]) << 16),
-                  (uint32_t)Elem<DT>::from_f32(o[2]) | ((uint32_t)Elem<DT>::from_f32(o[3]) << 16)};
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (n + j < a.N) {
-      if constexpr (EB == 4) reinterpret_cast<float*>(at)[j] = o[j];
-      else reinterpret_cast<uint16_t*>(at)[j] = Elem<DT>::from_f32(o[j]);
-    }
-}
+};
 
 // Position of the 16-byte chunk c of a 128-byte row in LDS: the 16 lanes that
 // read one chunk of 16 rows at a time hit all banks.
 __device__ __forceinline__ int chunk_at(int row, int c) { return c ^ ((row >> 1) & 7); }
 
-// BM tokens x BN outputs, WM x WN waves, NS stages in LDS or on their way.
-template <int DT, int BM, int BN, int WM, int WN, int NS>
+// BM tokens x BN outputs, WM x WN waves; stages of 128 bytes of the sums' axis, NS
+// of them in LDS or on their way.  Runs: the sums of a run of the sum's axis.
+template <int DT, int BM, int BN, int WM, int WN, int NS, int SPREAD, bool Runs>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LinearArgs a, int tiles_m,
                                                                int tiles_n) {
+  constexpr int SB = 128;
   constexpr int EB = Elem<DT>::bytes;
   constexpr int THREADS = 64 * WM * WN;
   constexpr int MB = BM / WM / 32, NB = BN / WN / 32;   // 32 x 32 blocks of a wave
-  constexpr int STAGE = (BM + BN) * 128;
+  constexpr int STAGE = (BM + BN) * SB, CPR = SB / 16, STEPS = SB / 32;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[NS * STAGE];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int wm = wave % WM, wn = wave / WM;
-  const int m0 = blockIdx.x / tiles_n * BM, n0 = blockIdx.x % tiles_n * BN;
+
+  // workgroups of one XCD follow one another over a band of 4 tiles of
+  // outputs, so that its L2 holds the x and W tiles they share
+  const int n_tiles = tiles_m * tiles_n;
+  const int split = Runs ? blockIdx.x / n_tiles : 0, block = blockIdx.x - split * n_tiles;
+  const int per = n_tiles >> 3, more = n_tiles & 7, xcd = block & 7;
+  const int id = xcd * per + (xcd < more ? xcd : more) + (block >> 3);
+  constexpr int BAND = 4;
+  const int band = id / (BAND * tiles_m), in_band = id - band * BAND * tiles_m;
+  const int width_n = tiles_n - band * BAND < BAND ? tiles_n - band * BAND : BAND;
+  const int m0 = in_band / width_n * BM;
+  const int n0 = (band * BAND + in_band % width_n) * BN;
 
   float16_t acc[NB][MB];
 #pragma unroll
@@ -106,88 +150,270 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LinearArgs 
     for (int j = 0; j < MB; ++j) acc[i][j] = float16_t{};
 
   const int row = a.K * EB;   // bytes of a row of W
-  const int stages = (row + 127) / 128;
-  constexpr int PASS = THREADS / 8;
+  const int from = Runs ? split * a.run : 0;
+  const int run = Runs && from + a.run < row ? a.run : row - from;   // of this run
+  const int stages = (run + SB - 1) / SB;
+  // a thread copies one 16-byte chunk of rows PASS apart: its place in them is
+  // the same, and the rows are told apart by a scalar offset.  Rows that do not
+  // exist lie past the resource's end.
+  constexpr int PASS = THREADS / CPR;
   static_assert(PASS % 16 == 0, "one chunk for a thread's rows");
   const int rows_x = a.T - m0 < BM ? a.T - m0 : BM, rows_w = a.N - n0 < BN ? a.N - n0 : BN;
   const int x_row = (int)a.x_row;
   const __amdgpu_buffer_rsrc_t rx =
-      make_rsrc(a.x + (long long)m0 * a.x_row, (uint32_t)((rows_x - 1) * x_row + row));
+      make_rsrc(a.x + (long long)m0 * a.x_row + from, (uint32_t)((rows_x - 1) * x_row + run));
   const __amdgpu_buffer_rsrc_t rw =
-      make_rsrc(a.w + (long long)n0 * row, (uint32_t)((rows_w - 1) * row + row));
-  const int chunk = chunk_at(threadIdx.x >> 3, threadIdx.x & 7) * 16;
-  const int x_off = (int)(threadIdx.x >> 3) * x_row + chunk;
-  const int w_off = (int)(threadIdx.x >> 3) * row + chunk;
+      make_rsrc(a.w + (long long)n0 * row + from, (uint32_t)((rows_w - 1) * row + run));
+  const int chunk = chunk_at(threadIdx.x / CPR, threadIdx.x % CPR) * 16;
+  const int x_off = (int)(threadIdx.x / CPR) * x_row + chunk;
+  const int w_off = (int)(threadIdx.x / CPR) * row + chunk;
   constexpr int CX = BM / PASS, CW = BN / PASS;   // copies a thread
-  auto copy_stage = [&](int st, int at) {
-    unsigned char* to = lds + at * STAGE + wave * 1024;
-    const int k = st * 128;
-    const bool in = k + chunk < row;
-    const int xo = in ? x_off + k : kFarOffset, wo = in ? w_off + k : kFarOffset;
+  // 32 bytes of the sums' axis a step.  Its operands are read a step ahead, in the
+  // order in which they are taken, and a stage's copies are spread over SPREAD
+  // steps, the last of a stage (which frees its place) and those of the next: one
+  // read or copy after a matrix instruction, which runs meanwhile.
+  constexpr int MMA = NB * MB, READS = NB + MB, COPIES = CX + CW, PARTS = COPIES / SPREAD;
+  static_assert(COPIES % SPREAD == 0, "the same number of copies a step");
+  // bytes from the stage's first that a thread copies, past the end where the row
+  // has ended
+  auto begin_of = [&](int st) { return st * SB + chunk < run ? st * SB : kFarOffset; };
+  // copy c (first x's, then W's) into stage `at`
+  auto copy = [&](int begin, int at, int c) __attribute__((always_inline)) {
+    unsigned char* to = lds + at * STAGE + wave * 1024 + c * THREADS * 16;
+    if (c < CX) copy16_to_lds(rx, to, x_off + begin, c * PASS * x_row);
+    else copy16_to_lds(rw, to, w_off + begin, (c - CX) * PASS * row);
+  };
+  u32x4_t wf[2][NB], xf[2][MB];
+  // this lane's place in a block of 32 rows of x and of W, for each step (the same in
+  // all blocks)
+  int at_x[STEPS], at_w[STEPS];
 #pragma unroll
-    for (int c = 0; c < CX; ++c) copy16_to_lds(rx, to + c * THREADS * 16, xo, c * PASS * x_row);
-#pragma unroll
-    for (int c = 0; c < CW; ++c)
-      copy16_to_lds(rw, to + BM * 128 + c * THREADS * 16, wo, c * PASS * row);
+  for (int k = 0; k < STEPS; ++k) {
+    const int in = l32 * SB + chunk_at(l32, 2 * k + half) * 16;
+    at_x[k] = in + wm * MB * 32 * SB;
+    at_w[k] = in + (BM + wn * NB * 32) * SB;
+  }
+  auto read = [&](int at, int k, int n, u32x4_t* w, u32x4_t* x) __attribute__((always_inline)) {
+    if (n >= 1 && n <= MB) {
+      x[n - 1] = *reinterpret_cast<const u32x4_t*>(lds + at_x[k] + (at * STAGE + (n - 1) * 32 * SB));
+    } else {
+      const int i = n == 0 ? 0 : n - MB;
+      w[i] = *reinterpret_cast<const u32x4_t*>(lds + at_w[k] + (at * STAGE + i * 32 * SB));
+    }
   };
 #pragma unroll
-  for (int st = 0; st < NS - 1; ++st) copy_stage(st, st);
-  for (int st = 0; st < stages; ++st) {
-    wait_vmcnt<(NS - 2) * (CX + CW)>();
-    lds_barrier();   // this stage has arrived for all, nobody reads the one before
-    copy_stage(st + NS - 1, (st + NS - 1) % NS);
-    const unsigned char* xs = lds + st % NS * STAGE;
+  for (int st = 0; st < NS; ++st)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      u32x4_t wf[NB], xf[MB];
+    for (int c = 0; c < (st < NS - 1 ? COPIES : PARTS); ++c) copy(begin_of(st), st, c);
+  wait_vmcnt<(NS - 2) * COPIES + PARTS>();
+  lds_barrier();
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int r = (wn * NB + i) * 32 + l32;
-        wf[i] = *reinterpret_cast<const u32x4_t*>(xs + (BM + r) * 128 +
-                                                  chunk_at(r, 2 * k + half) * 16);
+  for (int n = 0; n < READS; ++n) read(0, 0, n, wf[0], xf[0]);
+  // Stage st, which lies at place `at` (a constant where it is called, so that the
+  // addresses are).
+  auto stage = [&](int st, int at) __attribute__((always_inline)) {
+    const int next = at + 1 < NS ? at + 1 : 0, before = at > 0 ? at - 1 : NS - 1;
+    const int begin = begin_of(st + NS - 1), begin_next = begin_of(st + NS);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const bool last = k == STEPS - 1;
+      // matrix instructions before the barrier of a stage's last step
+      constexpr int EARLY = MMA / 4;
+      const int first = last ? EARLY : 0, left = MMA - first;
+#pragma unroll
+      for (int n = 0; n < MMA; ++n) {
+        if (last && n == EARLY) {
+          // nobody reads this stage any more, the next one has arrived
+          __builtin_amdgcn_sched_barrier(0);
+          wait_vmcnt<(NS - 2) * COPIES>();
+          lds_barrier();
+        }
+#pragma unroll
+        for (int e = 0; e < Mma<DT>::KSUB; ++e)
+          Mma<DT>::step(wf[k & 1][n / MB], xf[k & 1][n % MB], acc[n / MB][n % MB], e);
+        // this instruction's share of the reads and of the copies
+        const int i = n - first;
+        if (i >= 0) {
+#pragma unroll
+          for (int q = 0; q < READS; ++q)
+            if (q * (left > READS ? 1 : left) / (left > READS ? 1 : READS) == i)
+              read(last ? next : at, last ? 0 : k + 1, q, wf[(k + 1) & 1], xf[(k + 1) & 1]);
+#pragma unroll
+          for (int c = 0; c < PARTS; ++c)
+            if ((2 * c + 1) * left / (2 * PARTS) == i) {
+              if (last) copy(begin_next, at, c);
+              else if (k + 1 < SPREAD) copy(begin, before, (k + 1) * PARTS + c);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
+    }
+  };
+  int st = 0;
+  for (; st + NS <= stages; st += NS) {
 #pragma unroll
-      for (int j = 0; j < MB; ++j) {
-        const int r = (wm * MB + j) * 32 + l32;
-        xf[j] = *reinterpret_cast<const u32x4_t*>(xs + r * 128 + chunk_at(r, 2 * k + half) * 16);
-      }
+    for (int i = 0; i < NS; ++i) stage(st + i, i);
+  }
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i)
+    if (st + i < stages) stage(st + i, i);
+  wait_vmcnt<0>();
+
+  if constexpr (Runs) {
+    const long long n_pad = (a.N + 63) / 64 * 64;
+#pragma unroll
+    for (int j = 0; j < MB; ++j) {
+      const int t = m0 + (wm * MB + j) * 32 + l32;
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < MB; ++j)
-#pragma unroll
-          for (int e = 0; e < Mma<DT>::KSUB; ++e) Mma<DT>::step(wf[i], xf[j], acc[i][j], e);
+        for (int r = 0; r < 4; ++r) {
+          const int n = n0 + (wn * NB + i) * 32 + 8 * r + 4 * half;
+          if (t < a.T && n < n_pad)
+            *reinterpret_cast<float4_t*>(a.part + ((long long)split * a.T + t) * n_pad + n) =
+                float4_t{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
+                         acc[i][j][4 * r + 3]};
+        }
     }
+    return;
   }
-  wait_vmcnt<0>();
-
+  lds_barrier();   // the stages are read: each wave has a part of them for its sums
+  // 32 tokens at a time, through LDS: a lane then has 16 bytes of a token's outputs,
+  // and neighbouring lanes neighbouring ones.  The residual of the next 32 tokens
+  // is on its way meanwhile.
+  constexpr int E = 16 / EB, COLS = NB * 32, LPT = COLS / E, TPI = 64 / LPT;   // lanes of a token
+  constexpr int PAD = COLS + 4, TURNS = 32 / TPI;   // floats of a token in LDS
+  constexpr bool AHEAD = EB == 2;   // (fp32: twice the room, for a call that is far slower)
+  constexpr int ROOM = 32 * PAD * 4 + (AHEAD ? TURNS * 1024 : 0);
+  static_assert(Runs || ROOM * WM * WN <= NS * STAGE,
+                "32 tokens' sums and residual fit a wave's part");
+  float* const sums = reinterpret_cast<float*>(lds + wave * ROOM);
+  u32x4_t* const ahead = reinterpret_cast<u32x4_t*>(lds + wave * ROOM + 32 * PAD * 4) + lane;
+  const Outputs<DT> out(a, n0 + wn * COLS + lane % LPT * E);
+  const int t_first = m0 + wm * MB * 32 + lane / LPT;
+  u32x4_t res[TURNS];
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) res[i] = out.residual(a, t_first + i * TPI);
+  }
 #pragma unroll
   for (int j = 0; j < MB; ++j) {
-    const int t = m0 + (wm * MB + j) * 32 + l32;
-    if (t >= a.T) continue;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = n0 + (wn * NB + i) * 32 + 8 * r + 4 * half;
-        const float v[4] = {acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
-                            acc[i][j][4 * r + 3]};
-        if (n < a.N) finish4<DT>(a, t, n, v);
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4_t*>(sums + l32 * PAD + i * 32 + 8 * r + 4 * half) =
+            float4_t{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
+                     acc[i][j][4 * r + 3]};
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < TURNS; ++i) ahead[i * 64] = res[i];
+      if (j + 1 < MB) {
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i) res[i] = out.residual(a, t_first + (j + 1) * 32 + i * TPI);
       }
+    }
+    lds_fence();
+#pragma unroll 1
+    for (int i = 0; i < TURNS; ++i) {
+      const float* from = sums + (lane / LPT + i * TPI) * PAD + lane % LPT * E;
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4_t f = *reinterpret_cast<const float4_t*>(from + e);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[e + q] = f[q];
+      }
+      const int t = t_first + j * 32 + i * TPI;
+      out.finish(a, t, v, AHEAD ? ahead[i * 64] : out.residual(a, t));
+    }
+    lds_fence();
   }
 }
 
-template <int DT> void launch_dt(const LinearArgs& a, hipStream_t stream) {
-  const int tm = (a.T + 63) / 64, tn = (a.N + 63) / 64;
-  hipLaunchKernelGGL((tile_kernel<DT, 64, 64, 2, 2, 4>), dim3((unsigned)(tm * tn)), dim3(256), 0,
+// y from the sums of its runs, in their order; a thread 16 bytes of a token.
+template <int DT> __global__ __launch_bounds__(256) void sum_kernel(const LinearArgs a) {
+  constexpr int E = 16 / Elem<DT>::bytes, U = 8;
+  const int n = (blockIdx.x * 256 + threadIdx.x) * E, t = blockIdx.y;
+  if (n >= a.N) return;
+  const long long n_pad = (a.N + 63) / 64 * 64;
+  const Outputs<DT> out(a, n);
+  const u32x4_t res = out.residual(a, t);
+  const float* part = a.part + t * n_pad + n;
+  float v[E] = {};
+  for (int s = 0; s < a.splits; s += U) {
+    float4_t p[U][E / 4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E / 4; ++e) {
+        p[u][e] = float4_t{0, 0, 0, 0};
+        if (s + u < a.splits)
+          p[u][e] = *reinterpret_cast<const float4_t*>(part + (long long)(s + u) * a.T * n_pad + 4 * e);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += p[u][e / 4][e % 4];
+  }
+  out.finish(a, t, v, res);
+}
+
+template <int DT, int BM, int BN, int WM, int WN, int NS, int SPREAD, bool Runs = false>
+void launch_tile(const LinearArgs& a, hipStream_t stream) {
+  const int tm = (a.T + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  hipLaunchKernelGGL((tile_kernel<DT, BM, BN, WM, WN, NS, SPREAD, Runs>),
+                     dim3((unsigned)(tm * tn * (Runs ? a.splits : 1))), dim3(64 * WM * WN), 0,
                      stream, a, tm, tn);
+}
+
+template <int DT> void launch_dt(const LinearArgs& a, hipStream_t stream) {
+  if (a.part) {
+    launch_tile<DT, 64, 64, 2, 2, 4, 1, true>(a, stream);
+    constexpr int E = 16 / Elem<DT>::bytes;
+    hipLaunchKernelGGL((sum_kernel<DT>),
+                       dim3((unsigned)((a.N + 256 * E - 1) / (256 * E)), (unsigned)a.T), dim3(256),
+                       0, stream, a);
+    return;
+  }
+  if constexpr (DT != DT_F32) {
+    if (a.tile == 256) {
+      launch_tile<DT, 256, 256, 2, 4, 2, 2>(a, stream);
+      return;
+    }
+  }
+  if (a.tile >= 128) launch_tile<DT, 128, 128, 2, 2, 2, 4>(a, stream);
+  else launch_tile<DT, 64, 64, 2, 2, 4, 1>(a, stream);
+}
+
+// Time of a launch in units of one 256 x 256 tile: rounds of workgroups over
+// the compute units, each as long as its workgroups together on one unit.
+double tile_cost(const LinearArgs& a, int cus, int b, int per_cu, double speed) {
+  const double tiles = (double)((a.T + b - 1) / b) * ((a.N + b - 1) / b);
+  const double rounds = (double)(long long)((tiles + (double)cus * per_cu - 1) / (cus * per_cu));
+  const double share = tiles < (double)cus * per_cu ? (tiles > cus ? tiles / cus : 1.0) : per_cu;
+  return rounds * share * b * b / speed;
 }
 
 }  // namespace
 
-long long linear_plan(LinearArgs* a, int, int, bool) {
-  a->splits = a->run = a->tile = 0;
-  return 0;
+long long linear_plan(LinearArgs* a, int dtype, int cus, bool allowed) {
+  a->splits = a->run = 0;
+  const bool f32 = dtype == LIBCONV_F32;
+  const double c256 = tile_cost(*a, cus, 256, 1, 1.0), c128 = tile_cost(*a, cus, 128, 2, 0.75),
+               c64 = tile_cost(*a, cus, 64, 4, 0.4);
+  a->tile = !f32 && c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+  if (!allowed || a->T == 0) return 0;
+  const long long row = (long long)a->K * (f32 ? 4 : 2), n_pad = (a->N + 63) / 64 * 64;
+  const long long tiles = ((a->T + 63LL) / 64) * (n_pad / 64);
+  long long splits = cus / tiles;
+  if (splits > row / 512) splits = row / 512;
+  if (splits > 16) splits = 16;
+  if (splits < 2) return 0;
+  a->tile = 64;
+  a->run = (int)((row + splits - 1) / splits + 127) / 128 * 128;
+  a->splits = (int)((row + a->run - 1) / a->run);
+  return 4LL * a->splits * a->T * n_pad;
 }
 
 libconv_status linear_launch(LinearArgs a, int dtype, hipStream_t stream) {
