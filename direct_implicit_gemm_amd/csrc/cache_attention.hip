@@ -50,7 +50,9 @@ template <int DP> struct Shape {
   static constexpr int DB = DP / 32;               // blocks of 32 components
   static constexpr int PART = 32 * RB;             // a wave's keys (values) of a tile
   static constexpr int COPIES = PART / 1024;       // 16 bytes a lane each
-  static constexpr int LDS = 4 * 2 * 2 * PART;     // waves, stages, keys and values
+  static constexpr int WAVE = 2 * 2 * PART + 256 + 1024;   // stages of keys and values, blocks,
+                                                           // scales
+  static constexpr int LDS = 4 * WAVE;
 };
 // Chunk c of row r is kept at c ^ swizzle(r): 16 rows' reads of one chunk, and the
 // 8 rows that 16 lanes read a chunk of, hit all banks.
@@ -64,6 +66,13 @@ __device__ __forceinline__ u32x2_t read_column8(const unsigned char* __restrict 
   typedef int i32x2_t __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
                                          (__attribute__((address_space(3))) i32x2_t*)p));
+}
+
+// One 4-byte read a lane straight into LDS, lane l's at dst + 4 l.
+__device__ __forceinline__ void copy4_to_lds(__amdgpu_buffer_rsrc_t r, unsigned char* dst,
+                                             int off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4, off,
+                                           0, 0, 0);
 }
 
 // An entry: its rows and its keys.
@@ -103,39 +112,70 @@ __device__ __forceinline__ int lanes_before(int v) {
   return v;
 }
 
-// Work of all entries, `weight(b)` each.
-template <class W> __device__ __forceinline__ long long total_of(int B, W&& weight) {
-  const int lane = threadIdx.x & 63;
-  long long sum = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) {
-    const int w = b0 + lane < B ? weight(b0 + lane) : 0;
-    sum += __builtin_amdgcn_readlane(lanes_before(w), 63);
+// The entries' work, `weight(entry)` each, side by side.  64 entries at a time are
+// in the wave's lanes; up to 64 are read once.
+template <class W> struct Entries {
+  const CacheAttnArgs& a;
+  W weight;
+  Entry mine;      // this lane's entry of those from b0 on
+  int b0 = 0, w, up_to;
+
+  __device__ __forceinline__ Entries(const CacheAttnArgs& args, W f) : a(args), weight(f) { load(0); }
+  __device__ __forceinline__ void load(int first) {
+    const int b = first + (int)(threadIdx.x & 63);
+    b0 = first;
+    mine = Entry{0, 0, 0, 0};
+    if (b < a.c.B) mine = entry_of(a, b);
+    w = b < a.c.B ? weight(mine) : 0;
+    up_to = lanes_before(w);
   }
-  return sum;
-}
-// The entry that holds number x of the work (B: none), and where its own begins.
-struct Found {
-  int b;
-  long long first;
-};
-template <class W> __device__ __forceinline__ Found find(int B, long long x, W&& weight) {
-  const int lane = threadIdx.x & 63;
-  long long sum = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) {
-    const int w = b0 + lane < B ? weight(b0 + lane) : 0, up_to = lanes_before(w);
-    const uint64_t past = __ballot(sum + up_to > x);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      return {b0 + l, sum + __builtin_amdgcn_readlane(up_to - w, l)};
+  // Work of all entries.
+  __device__ __forceinline__ long long total() {
+    long long sum = __builtin_amdgcn_readlane(up_to, 63);
+    for (int first = 64; first < a.c.B; first += 64) {
+      load(first);
+      sum += __builtin_amdgcn_readlane(up_to, 63);
     }
-    sum += __builtin_amdgcn_readlane(up_to, 63);
+    return sum;
   }
-  return {B, sum};
-}
-// Where an entry's work begins.
-template <class W> __device__ __forceinline__ long long begin_of(int b, W&& weight) {
-  return total_of(b, weight);
-}
+  // Where an entry's work begins.
+  __device__ __forceinline__ long long begin_of(int b) {
+    long long sum = 0;
+    for (int first = 0; first < a.c.B; first += 64) {
+      if (first != b0) load(first);
+      if (b < first + 64) return sum + __builtin_amdgcn_readlane(up_to - w, b - first);
+      sum += __builtin_amdgcn_readlane(up_to, 63);
+    }
+    return sum;
+  }
+  // The entry that holds number x of the work, and where its own begins; b = B: none.
+  struct Found {
+    Entry e;
+    int b, weight;
+    long long first;
+  };
+  __device__ __forceinline__ Found find(long long x) {
+    long long sum = 0;
+    for (int first = 0; first < a.c.B; first += 64) {
+      if (first != b0) load(first);
+      const uint64_t past = __ballot(sum + up_to > x);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        Found f;
+        f.e.row0 = __builtin_amdgcn_readlane(mine.row0, l);
+        f.e.n = __builtin_amdgcn_readlane(mine.n, l);
+        f.e.rows = __builtin_amdgcn_readlane(mine.rows, l);
+        f.e.len = __builtin_amdgcn_readlane(mine.len, l);
+        f.b = first + l;
+        f.weight = __builtin_amdgcn_readlane(w, l);
+        f.first = sum + __builtin_amdgcn_readlane(up_to, l) - f.weight;
+        return f;
+      }
+      sum += __builtin_amdgcn_readlane(up_to, 63);
+    }
+    return {Entry{0, 0, 0, 0}, a.c.B, 0, sum};
+  }
+};
 
 // How the few_groups workgroups share the tiles of all heads: each a run of `per`.
 __device__ __forceinline__ long long share_of(long long total, int groups) {
@@ -162,60 +202,6 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int len = job.e.len, D = c.D, hk = job.hk;
-
-  // blocks and scales of the groups of 16 keys that this wave reads: lane L holds
-  // those of group L & 1 of tile first + L / 2
-  const int mask = (1 << c.log_block) - 1;
-  auto ids_of = [&](int first) {
-    const long long p = (long long)(first + (lane >> 1)) * kTile + wave * 32 + (lane & 1) * 16;
-    int id = -1;
-    if (p < len) id = c.table[(long long)job.b * c.width + (p >> c.log_block)];
-    return id >= 0 && id < c.blocks ? id : -1;
-  };
-  auto scale_of = [&](int id, int kv) {
-    return id >= 0 ? c.scale[kv][(long long)id * c.Hk + hk] : 0.0f;
-  };
-  int at = job.t0;   // first tile of the batch in hand
-  int ids = ids_of(at), ids_next = -1;
-
-  // copies: 16 bytes of a row a lane
-  constexpr int PASS = 64 / CPR;   // rows of a copy
-  const int row_in = lane / CPR;
-  int off[2][2];                   // keys and values, of even and odd copies of a group
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int chunk = (lane % CPR) ^ swizzle<CPR>(j * PASS + row_in);
-      off[kv][j] = chunk * 16 < D ? row_in * (int)c.token[kv] + chunk * 16 : kFarOffset;
-    }
-  unsigned char* const mine = lds + wave * 4 * Z::PART;
-  auto stage = [&](int t, int kv) { return mine + (((t - job.t0) & 1) * 2 + kv) * Z::PART; };
-  auto copy = [&](int t, int kv) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int in = (t - at) * 2 + g;
-      int id = __builtin_amdgcn_readlane(in < 64 ? ids : ids_next, in & 63);
-      const long long p = (long long)t * kTile + wave * 32 + g * 16;
-      const long long left = len - p;
-      const int rows = left < 16 ? (int)left : 16;
-      const bool any = t < job.t1 && rows > 0 && id >= 0;
-      id = any ? id : 0;
-      const char* base = c.codes[kv] + id * c.block[kv] + hk * c.head[kv] +
-                         (long long)((int)p & mask) * c.token[kv];
-      const __amdgpu_buffer_rsrc_t r =
-          make_rsrc(base, any ? (uint32_t)((rows - 1) * (int)c.token[kv] + D) : 0u);
-#pragma unroll
-      for (int j = 0; j < 16 / PASS; ++j)
-        copy16_to_lds(r, stage(t, kv) + (g * (16 / PASS) + j) * 1024, off[kv][j],
-                      j * PASS * (int)c.token[kv]);
-    }
-  };
-  copy(job.t0, 0);
-  copy(job.t0, 1);
-  copy(job.t0 + 1, 0);
-  copy(job.t0 + 1, 1);
-  float ks = scale_of(ids, 0), vs = scale_of(ids, 1), ks_next = 0.0f, vs_next = 0.0f;
 
   // this lane's query
   const int local = job.row_tile * 32 + l32;
@@ -252,10 +238,106 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
       qf[0][s] = raw[0];
     }
   }
+
+  // The groups of 16 keys that this wave reads, 64 (32 tiles) at a time: lane L holds
+  // where the codes of group L & 1 of tile first + L / 2 lie, and how many there
+  // are; their scales are in LDS.  The blocks of the next 32 tiles, and then
+  // their scales, arrive in LDS too: what arrives in a register would have to be
+  // waited for with everything else that is on its way.
+  unsigned char* const mine = lds + wave * Z::WAVE;
+  int* const blocks_in = reinterpret_cast<int*>(mine + 4 * Z::PART);
+  float* const scales_in = reinterpret_cast<float*>(mine + 4 * Z::PART + 256);   // [2][2][64]
+  const int mask = (1 << c.log_block) - 1;
+  struct Groups {
+    int at[2][2];   // offset of the codes from the caches' first: low and high word
+    int rows;       // 0: none
+  };
+  auto position = [&](int first) { return (first + (lane >> 1)) * kTile + wave * 32 + (lane & 1) * 16; };
+  const int* const table = c.table + (long long)job.b * c.width;
+  const int last = len - 1;   // (tiles are counted so that positions fit 31 bits)
+  auto locate = [&](int first, int id) {
+    Groups g;
+    const int p = position(first), left = len - p;
+    const bool any = p <= last && id >= 0 && id < c.blocks;
+    g.rows = !any ? 0 : left < 16 ? left : 16;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const long long off = any ? id * c.block[kv] + (p & mask) * c.token[kv] : 0;
+      g.at[kv][0] = (int)off;
+      g.at[kv][1] = (int)(off >> 32);
+    }
+    return g;
+  };
+  // copies of 4 bytes a lane
+  const __amdgpu_buffer_rsrc_t scale_rsrc[2] = {
+      make_rsrc(c.scale[0], (uint32_t)c.blocks * (uint32_t)c.Hk * 4u),
+      make_rsrc(c.scale[1], (uint32_t)c.blocks * (uint32_t)c.Hk * 4u)};
+  auto fetch_scales = [&](int id, bool any, int to) {
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      copy4_to_lds(scale_rsrc[kv], reinterpret_cast<unsigned char*>(scales_in + (to * 2 + kv) * 64),
+                   any ? (id * c.Hk + hk) * 4 : kFarOffset);
+  };
+  const __amdgpu_buffer_rsrc_t table_rsrc = make_rsrc(table, (uint32_t)c.width * 4u);
+  auto fetch_blocks = [&](int first) {
+    const int p = position(first);
+    copy4_to_lds(table_rsrc, reinterpret_cast<unsigned char*>(blocks_in),
+                 p <= last ? (p >> c.log_block) * 4 : kFarOffset);
+  };
+  int at = job.t0;   // first tile of the batch in hand
+  Groups now, next;
+  {
+    int id = -1;
+    if (position(at) <= last) id = table[position(at) >> c.log_block];
+    now = next = locate(at, id);
+    fetch_scales(id, now.rows > 0, 0);
+  }
+
+  // copies: 16 bytes of a row a lane
+  constexpr int PASS = 64 / CPR;   // rows of a copy
+  const int row_in = lane / CPR;
+  int off[2][2];                   // keys and values, of even and odd copies of a group
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int chunk = (lane % CPR) ^ swizzle<CPR>(j * PASS + row_in);
+      off[kv][j] = chunk * 16 < D ? row_in * (int)c.token[kv] + chunk * 16 : kFarOffset;
+    }
+  auto stage = [&](int t, int kv) { return mine + (((t - job.t0) & 1) * 2 + kv) * Z::PART; };
+  auto copy = [&](int t, int kv) {
+    const char* const codes = c.codes[kv] + hk * c.head[kv];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int in = ((t - at) * 2 + g) & 63;
+      const bool ahead = t - at >= 32;
+      const int rows = __builtin_amdgcn_readlane(ahead ? next.rows : now.rows, in);
+      const uint32_t lo = __builtin_amdgcn_readlane(ahead ? next.at[kv][0] : now.at[kv][0], in);
+      const int hi = __builtin_amdgcn_readlane(ahead ? next.at[kv][1] : now.at[kv][1], in);
+      const bool any = t < job.t1 && rows > 0;
+      const __amdgpu_buffer_rsrc_t r =
+          make_rsrc(codes + (((long long)hi << 32) | lo),
+                    any ? (uint32_t)((rows - 1) * (int)c.token[kv] + D) : 0u);
+#pragma unroll
+      for (int j = 0; j < 16 / PASS; ++j)
+        copy16_to_lds(r, stage(t, kv) + (g * (16 / PASS) + j) * 1024, off[kv][j],
+                      j * PASS * (int)c.token[kv]);
+    }
+  };
+  copy(job.t0, 0);
+  copy(job.t0, 1);
+  copy(job.t0 + 1, 0);
+  copy(job.t0 + 1, 1);
   // keys that this query sees, and that every query of the tile does
   const int first_row = job.row_tile * 32;
   const int lim = a.causal ? len - job.e.n + qi + 1 : len;
   const int lim_all = a.causal ? len - job.e.n + first_row / a.G + 1 : len;
+  // the queries have arrived (they were asked for before the blocks): the loop's
+  // first use would wait for them again and again
+#pragma unroll
+  for (int i = 0; i < NQ; ++i)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) asm volatile("" : "+v"(qf[i][s]));
 
   float16_t acc[DB];
 #pragma unroll
@@ -265,32 +347,32 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
   const int krow = l32 * RB, ksw = swizzle<CPR>(l32);
   const int vrow = (((lane & 15) >> 1) & 3) + 8 * ((lane & 15) >> 3) + 4 * half;
 
+  int buffer = 0;   // of the scales
   for (int t = job.t0; t < job.t1; ++t) {
     if (t - at == 32) {
       at += 32;
-      ids = ids_next;
-      ks = ks_next;
-      vs = vs_next;
+      now = next;
+      buffer ^= 1;
     }
-    // the next batch, a little at a time: blocks, then their scales
-    if (t - at == 8 && at + 32 < job.t1) ids_next = ids_of(at + 32);
-    if (t - at == 16 && at + 32 < job.t1) {
-      ks_next = scale_of(ids_next, 0);
-      vs_next = scale_of(ids_next, 1);
+    // (the waits of two tiles cover a copy that was issued before them)
+    if (t - at == 8 && at + 32 < job.t1) fetch_blocks(at + 32);
+    if (t - at == 12 && at + 32 < job.t1) {
+      const int id = blocks_in[lane];
+      next = locate(at + 32, id);
+      fetch_scales(id, next.rows > 0, buffer ^ 1);
     }
     const int in = (t - at) * 2;
-    float f[2], add[2], fv[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      f[g] = a.scale * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
-                                                     __builtin_bit_cast(int, ks), in + g));
-      fv[g] = __builtin_bit_cast(float,
-                                 __builtin_amdgcn_readlane(__builtin_bit_cast(int, vs), in + g));
-      add[g] = __builtin_amdgcn_readlane(ids, in + g) >= 0 ? 0.0f : kNegInf;
-    }
 
     wait_vmcnt<3 * COPIES>();
     lds_fence();
+    const float* const of = scales_in + buffer * 128 + in;
+    float f[2], add[2], fv[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      f[g] = of[g] * a.scale;
+      fv[g] = of[64 + g];
+      add[g] = __builtin_amdgcn_readlane(now.rows, in + g) > 0 ? 0.0f : kNegInf;
+    }
     float16_t s = {};
     const unsigned char* kt = stage(t, 0);
 #pragma unroll
@@ -309,9 +391,9 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
 
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[r] = fmaf(s[r], f[r >> 3], add[r >> 3]);
-    const long long p0 = (long long)t * kTile + wave * 32;
+    const int p0 = t * kTile + wave * 32;
     if (p0 + 32 > lim_all) {
-      const int lane_lim = (int)(lim - p0) - 4 * half;
+      const int lane_lim = lim - p0 - 4 * half;
 #pragma unroll
       for (int r = 0; r < 16; ++r)
         s[r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[r] : kNegInf;
@@ -362,84 +444,71 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
   }
   wait_vmcnt<0>();
 
-  // join the waves: each leaves maximum, sum and outputs (32 rows, DP components,
-  // rows fastest) in LDS
+  // join the waves: each leaves maximum, sum and outputs (DP components, 32 rows
+  // fastest) in LDS and sums 32 components of all
   l += __shfl_xor(l, 32);
-  constexpr int PER = 32 * (DP + 2) * 4;
-  static_assert(3 * PER <= Z::LDS, "the join fits the stages");
+  static_assert(4 * 32 * DP * 4 <= Z::LDS - 1024, "the join fits the stages");
+  float* const tops = reinterpret_cast<float*>(lds + Z::LDS - 1024);   // [4][32], then the sums
   lds_barrier();   // every wave is done with its stages, no copy is on its way
-  if (wave > 0) {
-    float* room = reinterpret_cast<float*>(lds + (wave - 1) * PER);
-    if (half == 0) {
-      room[l32] = m;
-      room[32 + l32] = l;
-    }
+  float* const rooms = reinterpret_cast<float*>(lds);
+  if (half == 0) {
+    tops[wave * 32 + l32] = m;
+    tops[128 + wave * 32 + l32] = l;
+  }
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      rooms[(wave * DP + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32] = acc[d][r];
+  lds_barrier();
+  if (wave < DB) {
+    float m_all = tops[l32];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) m_all = fmaxf(m_all, tops[w * 32 + l32]);
+    float o[16] = {};
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float g = __builtin_amdgcn_exp2f(tops[w * 32 + l32] - m_all);
+      l = fmaf(tops[128 + w * 32 + l32], g, l);
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        room[(2 + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32] = acc[d][r];
-  }
-  lds_barrier();
-  if (wave == 0) {
-    float m_all = m;
-#pragma unroll
-    for (int w = 0; w < 3; ++w)
-      m_all = fmaxf(m_all, reinterpret_cast<const float*>(lds + w * PER)[l32]);
-    const float fall = __builtin_amdgcn_exp2f(m - m_all);
-    l *= fall;
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[d][r] *= fall;
-#pragma unroll
-    for (int w = 0; w < 3; ++w) {
-      const float* o = reinterpret_cast<const float*>(lds + w * PER);
-      const float g = __builtin_amdgcn_exp2f(o[l32] - m_all);
-      l = fmaf(o[32 + l32], g, l);
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          acc[d][r] =
-              fmaf(o[(2 + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32], g, acc[d][r]);
+        o[r] = fmaf(rooms[(w * DP + wave * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32], g,
+                    o[r]);
     }
     if (row_ok) {
       const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
       const float lse2 = l == 0.0f ? kNegInf : m_all + __builtin_amdgcn_logf(l);
+      const bool first = wave == 0 && half == 0;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[r] *= inv;
       if (job.slot >= 0) {
         const long long slot = job.slot * kFewRows + local;
-        if (half == 0) a.part_lse[slot] = lse2;
+        if (first) a.part_lse[slot] = lse2;
         float* po = a.part + slot * D;
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int comp = d * 32 + 8 * r + 4 * half;
-            if (comp < D)
-              *reinterpret_cast<float4_t*>(po + comp) =
-                  float4_t{acc[d][4 * r] * inv, acc[d][4 * r + 1] * inv, acc[d][4 * r + 2] * inv,
-                           acc[d][4 * r + 3] * inv};
-          }
+        for (int r = 0; r < 4; ++r) {
+          const int comp = wave * 32 + 8 * r + 4 * half;
+          if (comp < D)
+            *reinterpret_cast<float4_t*>(po + comp) =
+                float4_t{o[4 * r], o[4 * r + 1], o[4 * r + 2], o[4 * r + 3]};
+        }
       } else {
         const long long t = job.e.row0 + qi;
         const int head = hk * a.G + qg;
-        if (a.lse && half == 0) a.lse[t * (c.Hk * a.G) + head] = lse2 * kLn2;
+        if (a.lse && first) a.lse[t * (c.Hk * a.G) + head] = lse2 * kLn2;
         char* op = a.out + t * a.o_r + head * a.o_h;
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int comp = d * 32 + 8 * r + 4 * half;
-            if (comp >= D) continue;
-            const float o0 = acc[d][4 * r] * inv, o1 = acc[d][4 * r + 1] * inv,
-                        o2 = acc[d][4 * r + 2] * inv, o3 = acc[d][4 * r + 3] * inv;
-            if constexpr (EB == 4)
-              *reinterpret_cast<float4_t*>(op + comp * 4) = float4_t{o0, o1, o2, o3};
-            else
-              *reinterpret_cast<u32x2_t*>(op + comp * 2) =
-                  u32x2_t{pack2<DT>(o0, o1), pack2<DT>(o2, o3)};
-          }
+        for (int r = 0; r < 4; ++r) {
+          const int comp = wave * 32 + 8 * r + 4 * half;
+          if (comp >= D) continue;
+          if constexpr (EB == 4)
+            *reinterpret_cast<float4_t*>(op + comp * 4) =
+                float4_t{o[4 * r], o[4 * r + 1], o[4 * r + 2], o[4 * r + 3]};
+          else
+            *reinterpret_cast<u32x2_t*>(op + comp * 2) =
+                u32x2_t{pack2<DT>(o[4 * r], o[4 * r + 1]), pack2<DT>(o[4 * r + 2], o[4 * r + 3])};
+        }
       }
     }
   }
@@ -465,23 +534,23 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const CacheAttnArgs a)
     if (job.t1 > 0) attend_few<DT, CF, DP>(a, job, lds);
     return;
   }
-  auto weight = [&](int b) { return few_tiles(entry_of(a, b)); };
+  auto weight = [](const Entry& e) { return few_tiles(e); };
+  Entries<decltype(weight)> entries(a, weight);
   const int Hk = a.c.Hk;
-  const long long total = total_of(a.c.B, weight) * Hk, per = share_of(total, a.few_groups);
+  const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
   long long x = blockIdx.x * per;
   const long long begin = x, end = x + per < total ? x + per : total;
   while (x < end) {
-    const Found f = find(a.c.B, x / Hk, [&](int b) { return weight(b); });
-    job.b = __builtin_amdgcn_readfirstlane(f.b);
-    job.e = entry_of(a, job.b);
-    const int tiles = few_tiles(job.e);
+    const auto f = entries.find(x / Hk);
+    job.b = f.b;
+    job.e = f.e;
     // the entry's heads one after another
-    while (x < end && x < (f.first + tiles) * Hk) {
+    while (x < end && x < (f.first + f.weight) * Hk) {
       const int in = (int)(x - f.first * Hk);
-      job.hk = in / tiles;
-      job.t0 = in - job.hk * tiles;
-      job.t1 = tiles - job.t0 < end - x ? tiles : job.t0 + (int)(end - x);
-      job.slot = job.t0 == 0 && job.t1 == tiles ? -1 : 2LL * blockIdx.x + (x == begin ? 0 : 1);
+      job.hk = in / f.weight;
+      job.t0 = in - job.hk * f.weight;
+      job.t1 = f.weight - job.t0 < end - x ? f.weight : job.t0 + (int)(end - x);
+      job.slot = job.t0 == 0 && job.t1 == f.weight ? -1 : 2LL * blockIdx.x + (x == begin ? 0 : 1);
       attend_few<DT, CF, DP>(a, job, lds);
       x += job.t1 - job.t0;
     }
@@ -501,9 +570,10 @@ __global__ __launch_bounds__(kThreads) void few_join_kernel(const CacheAttnArgs 
   const Entry e = entry_of(a, b);
   const int tiles = few_tiles(e);
   if (tiles < 2 || row >= e.rows) return;
-  auto weight = [&](int i) { return few_tiles(entry_of(a, i)); };
-  const long long total = total_of(a.c.B, weight) * Hk, per = share_of(total, a.few_groups);
-  const long long u0 = begin_of(b, weight) * Hk + (long long)hk * tiles, u1 = u0 + tiles;
+  auto weight = [](const Entry& x) { return few_tiles(x); };
+  Entries<decltype(weight)> entries(a, weight);
+  const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
+  const long long u0 = entries.begin_of(b) * Hk + (long long)hk * tiles, u1 = u0 + tiles;
   const int g0 = (int)(u0 / per), g1 = (int)((u1 - 1) / per);
   if (g0 == g1) return;
   const int set = threadIdx.x / LPR, lane = threadIdx.x % LPR;
@@ -566,13 +636,12 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a
   Job job;
   const int x = blockIdx.x / a.c.Hk;
   job.hk = blockIdx.x - x * a.c.Hk;
-  const Found f = find(a.c.B, x, [&](int b) {
-    const Entry e = entry_of(a, b);
-    return all || !few(e) ? (e.rows + 31) / 32 : 0;
-  });
+  auto weight = [all](const Entry& e) { return all || !few(e) ? (e.rows + 31) / 32 : 0; };
+  Entries<decltype(weight)> entries(a, weight);
+  const auto f = entries.find(x);
   if (f.b >= a.c.B) return;
-  job.b = __builtin_amdgcn_readfirstlane(f.b);
-  job.e = entry_of(a, job.b);
+  job.b = f.b;
+  job.e = f.e;
   job.row_tile = x - (int)f.first;
   const int last = (job.row_tile * 32 + 31 < job.e.rows ? job.row_tile * 32 + 31 : job.e.rows - 1);
   int keys = a.causal ? job.e.len - job.e.n + last / a.G + 1 : job.e.len;

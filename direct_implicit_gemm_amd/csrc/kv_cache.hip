@@ -15,8 +15,8 @@ namespace libconv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWindow = 16;    // rows that a workgroup of the write looks over: no two
-                               // of them begin a block of the same entry
+constexpr int kWindow = 256;   // rows that a workgroup of the write looks over, at most: a
+                               // block's, so that no two begin a block of the same entry
 constexpr int kHeld = 8;       // reads of a lane that stay in registers between the
                                // largest magnitude and the rounding
 
@@ -113,16 +113,16 @@ __device__ __forceinline__ void write_block(const char* x, long long x_row, char
   if (lane == 0 && s != old_as_is) *scale = s;
 }
 
-// A workgroup looks over kWindow rows for those that are their entry's first in
-// a block, and its waves take the blocks' heads, keys and values, in turn (with
+// A workgroup looks over a block's number of rows for those that are their entry's
+// first in a block, and its waves take the blocks' heads, keys and values, in turn (with
 // the gridDim.y workgroups of the same rows).
 template <int DT, int CF>
 __global__ __launch_bounds__(kThreads) void write_kernel(const CacheCopyArgs a) {
   __shared__ int count, first[kWindow], rows[kWindow], held[kWindow], block[kWindow];
   const CacheView& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r0 = blockIdx.x * kWindow, r1 = r0 + kWindow < a.T ? r0 + kWindow : a.T;
   const int size = 1 << c.log_block;
+  const int r0 = blockIdx.x << c.log_block, r1 = r0 + size < a.T ? r0 + size : a.T;
   if (threadIdx.x == 0) count = 0;
   lds_barrier();
   for (int b = threadIdx.x; b < c.B; b += kThreads) {
@@ -240,11 +240,12 @@ struct Write {
   const CacheCopyArgs& a;
   hipStream_t stream;
   template <int DT, int CF> void run() {
-    const int x = (a.T + kWindow - 1) / kWindow;
-    // single tokens: up to a block's work for each row
-    const long long jobs = 2LL * a.c.Hk * kWindow;
-    hipLaunchKernelGGL((write_kernel<DT, CF>), dim3((unsigned)x, turns(x, jobs)), dim3(kThreads),
-                       0, stream, a);
+    const int size = 1 << a.c.log_block, x = (a.T + size - 1) / size;
+    // rows of one entry: a block's heads; single tokens: those of each row
+    const unsigned block = (2u * a.c.Hk + 3) / 4;
+    const unsigned rows = turns(x, 2LL * a.c.Hk * (a.T < size ? a.T : size));
+    hipLaunchKernelGGL((write_kernel<DT, CF>), dim3((unsigned)x, block > rows ? block : rows),
+                       dim3(kThreads), 0, stream, a);
   }
 };
 struct Read {

@@ -154,8 +154,9 @@ libconv_status cache_shape(int B, int blocks, int block_size, int width, int k_h
   if (head_dim > 128 || head_dim % 16 != 0 || block_size < 16 || block_size > 256 ||
       (block_size & (block_size - 1)) != 0)
     return LIBCONV_ERR_UNSUPPORTED;
-  // positions and heads are counted in 31 bits
-  if ((long long)width * block_size > kMaxInt - 1024 || k_heads > (1 << 20) || B > (1 << 24) - 4096)
+  // positions and heads are counted in 31 bits, bytes of scales too
+  if ((long long)width * block_size > kMaxInt - 8192 || k_heads > (1 << 20) ||
+      (double)blocks * k_heads * 4 > (double)(kMaxInt - 8192) || B > (1 << 24) - 4096)
     return LIBCONV_ERR_TOO_LARGE;
   return LIBCONV_OK;
 }
