@@ -14,6 +14,9 @@
 #include "internal.h"
 #include "layer.h"
 
+#ifndef MANYMIN
+#define MANYMIN 32
+#endif
 namespace libconv {
 namespace {
 
@@ -629,54 +632,549 @@ __global__ __launch_bounds__(kThreads) void few_join_kernel(const CacheAttnArgs 
         u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
 }
 
-// Entries of more rows (with `all`, of any): 32 rows of a key head a workgroup.
-template <int DT, int CF, int DP>
-__global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a, int all) {
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
-  Job job;
-  const int x = blockIdx.x / a.c.Hk;
-  job.hk = blockIdx.x - x * a.c.Hk;
-  auto weight = [all](const Entry& e) { return all || !few(e) ? (e.rows + 31) / 32 : 0; };
+// Many rows: four waves of 32 rows share tiles of 64 keys, widened to 16 bits once
+// for all of them.  A wave reads the codes of 16 rows of keys and of values a tile
+// ahead into registers, and widens them into LDS a tile (keys: two) before they
+// are used.  A power of two is taken into the widened numbers, which hold the
+// product exactly.  `General`, where a block that the workgroup reads is not there
+// or has another scale: scores and probabilities are multiplied instead.
+constexpr int kManyRows = 128;
+template <int DP> struct Wide {
+  static constexpr int RAW = DP <= 64 ? 64 : 128;   // bytes of a row of codes
+  static constexpr int RB = 2 * RAW, CPR = RB / 16;  // of a row of 16-bit numbers
+  static constexpr int BN = 64, TILE = BN * RB;
+  static constexpr int LOADS = 16 * RAW / 1024;      // 16 bytes a lane, of 16 rows
+  static constexpr int LDS = 4 * TILE;
+};
+template <int CPR> __device__ __forceinline__ int k_swizzle16(int row) {
+  return CPR == 16 ? row & 15 : (row >> 1) & 7;
+}
+template <int CPR> __device__ __forceinline__ int v_swizzle16(int row) {
+  return CPR == 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+}
+// Whether a scale is a power of two.
+__device__ __forceinline__ bool is_power(float s) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, s);
+  return (b & 0x807fffffu) == 0 && b - 0x00800000u < 0x7f000000u;
+}
+
+template <int DT, int CF, int DP, bool General>
+__device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& job,
+                                            unsigned char* lds) {
+  using Z = Wide<DP>;
+  constexpr int EB = Elem<DT>::bytes, RAW = Z::RAW, RB = Z::RB, CPR = Z::CPR, BN = Z::BN;
+  constexpr int KS = DP / 16, DB = DP / 32, LOADS = Z::LOADS;
+  constexpr int NQ = Terms<DT>::Q, NP = Terms<DT>::P, KT = Terms<DT>::KT;
+  constexpr bool RestK = General || KT == DT_F16;   // (fp16 might not hold the product)
+  constexpr float SLACK = 8.0f;   // log2 of how far a maximum may fall behind
+  const CacheView& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, half = lane >> 5;
+  const int D = c.D, hk = job.hk, len = job.e.len, t0 = job.t0, t1 = job.t1, n = t1 - t0;
+  const int mask = (1 << c.log_block) - 1;
+
+  // this lane's query
+  const int first_row = job.row_tile * kManyRows + wave * 32, local = first_row + l32;
+  const bool row_ok = local < job.e.rows;
+  const int row = row_ok ? local : 0, qi = row / a.G, head = hk * a.G + row - qi * a.G;
+  const int lim = a.causal ? len - job.e.n + qi + 1 : len;
+  // every row of the wave sees the keys below this
+  const int all = a.causal ? len - job.e.n + (first_row < job.e.rows ? first_row / a.G : 0) + 1 : len;
+  const int whole = __builtin_amdgcn_readfirstlane(all < 0 ? 0 : all & ~31);
+  const char* qp = a.q + (long long)(job.e.row0 + qi) * a.q_r + (long long)head * a.q_h;
+  u32x4_t qf[NQ][KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int el = (2 * s + half) * 8;
+    u32x4_t raw[EB / 2];
+#pragma unroll
+    for (int i = 0; i < EB / 2; ++i) {
+      raw[i] = u32x4_t{0, 0, 0, 0};
+      if (row_ok && el < D) raw[i] = *reinterpret_cast<const u32x4_t*>(qp + el * EB + i * 16);
+      if (a.flip) {
+        const uint32_t sign = EB == 4 ? 0x80000000u : 0x80008000u;
+        raw[i] = a.flip < 0 ? raw[i] ^ u32x4_t{sign, sign, sign, sign} : u32x4_t{0, 0, 0, 0};
+      }
+    }
+    if constexpr (DT == DT_F32) {
+      float f[8];
+      unpack<DT_F32>(raw[0], f);
+      unpack<DT_F32>(raw[1], f + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[NQ];
+        split2<NQ>(f[2 * j], f[2 * j + 1], w);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) qf[i][s][j] = w[i];
+      }
+    } else {
+      qf[0][s] = raw[0];
+    }
+  }
+
+  // This wave's rows of a tile: 16 from wave * 16 on, of one block.  Lane L holds
+  // where those of tile i = L (mod 64) lie and their scales; half of the lanes are
+  // filled again when their tiles are done.
+  int rows = 0, where[2][2];
+  float scales[2];
+  const int* const table = c.table + (long long)job.b * c.width;
+  auto locate = [&](int i) {
+    const int p = (t0 + i) * BN + wave * 16, left = len - p;
+    int id = -1;
+    if (left > 0) id = table[p >> c.log_block];
+    const bool any = id >= 0 && id < c.blocks;
+    rows = !any ? 0 : left < 16 ? left : 16;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const long long off = any ? id * c.block[kv] + (p & mask) * c.token[kv] : 0;
+      where[kv][0] = (int)off;
+      where[kv][1] = (int)(off >> 32);
+      scales[kv] = any ? c.scale[kv][(long long)id * c.Hk + hk] : 1.0f;
+    }
+  };
+  locate(lane);
+  auto scale_of = [&](int i, int kv) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, scales[kv]), i & 63));
+  };
+  // Of the general form: scales and addend of group L & 3 of tile i = L / 4 (mod 16).
+  float by_k = 0.0f, by_v = 0.0f, addend = 0.0f;
+  auto look = [&](int i) {
+    const int p = (t0 + i + (lane >> 2)) * BN + (lane & 3) * 16;
+    int id = -1;
+    if (p < len) id = table[p >> c.log_block];
+    const bool any = id >= 0 && id < c.blocks;
+    by_k = any ? c.scale[0][(long long)id * c.Hk + hk] : 1.0f;
+    by_v = any ? c.scale[1][(long long)id * c.Hk + hk] : 1.0f;
+    addend = any || p >= len ? 0.0f : kNegInf;
+  };
+  auto group = [&](float v, int i, int g) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), (i & 15) * 4 + g));
+  };
+
+  // tile i's codes: 16 bytes of a row a lane; rows past the end and components from D
+  // on arrive as zeros
+  constexpr int LPR = RAW / 16, PASS = 64 / LPR;
+  const int row_in = lane / LPR, chunk_in = lane % LPR;
+  int off[2];
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+    off[kv] = chunk_in * 16 < D ? row_in * (int)c.token[kv] + chunk_in * 16 : kFarOffset;
+  struct Part {
+    u32x4_t codes[LOADS];
+  };
+  auto fetch = [&](int i, int kv) __attribute__((always_inline)) {
+    const int have = __builtin_amdgcn_readlane(rows, i & 63);
+    const uint32_t lo = __builtin_amdgcn_readlane(where[kv][0], i & 63);
+    const int hi = __builtin_amdgcn_readlane(where[kv][1], i & 63);
+    const __amdgpu_buffer_rsrc_t r =
+        make_rsrc(c.codes[kv] + hk * c.head[kv] + (((long long)hi << 32) | lo),
+                  i < n && have > 0 ? (uint32_t)((have - 1) * (int)c.token[kv] + D) : 0u);
+    Part x;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      x.codes[j] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off[kv], j * PASS * (int)c.token[kv], 0));
+    return x;
+  };
+  // where a lane's 16 codes go, of even and odd chunks
+  int to[2][LOADS][2];
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = wave * 16 + j * PASS + row_in;
+        to[kv][j][e] = kv * 2 * Z::TILE + row * RB +
+                       ((2 * chunk_in + e) ^
+                        (kv == 0 ? k_swizzle16<CPR>(row) : v_swizzle16<CPR>(row))) * 16;
+      }
+  // Widens tile i's; odd: i & 1, a constant where it is called.
+  auto widen = [&](const Part& x, int i, int odd, int kv) __attribute__((always_inline)) {
+    const float scale = scale_of(i, kv);
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t w0 = x.codes[j][2 * e], w1 = x.codes[j][2 * e + 1];
+        *reinterpret_cast<u32x4_t*>(lds + to[kv][j][e] + odd * Z::TILE) =
+            kv == 0 && KT == DT_F16 ? code_values16<CF, DT_F16>(w0, w1)
+            : General               ? code_values16<CF, DT_BF16>(w0, w1)
+                                    : code_values16<CF>(w0, w1, scale);
+      }
+  };
+
+  float16_t acc[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) acc[d] = float16_t{};
+  float m = kLowest, l = 0.0f, fall = 1.0f;
+  // LDS offsets that do not change from tile to tile
+  const int krow = l32 * RB, ksw = (half ^ k_swizzle16<CPR>(l32)) * 16;
+  const int i16 = lane & 15, vrow = 4 * half + (i16 >> 2);
+  const int vchunk = ((lane >> 4) & 1) * 2 + ((i16 & 3) >> 1);
+
+  auto score = [&](const unsigned char* kt, int b, float16_t& s) __attribute__((always_inline)) {
+    s = float16_t{};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const u32x4_t kf =
+          *reinterpret_cast<const u32x4_t*>(kt + krow + b * 32 * RB + (ksw ^ (ks * 32)));
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) Mma<KT>::step(kf, qf[i][ks], s, 0);
+    }
+  };
+  // scores of block b of tile i as they count
+  auto settle = [&](int i, int b, float16_t& s) __attribute__((always_inline)) {
+    if constexpr (RestK) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float by = group(by_k, i, 2 * b + g), add = General ? group(addend, i, 2 * b + g) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s[8 * g + r] = fmaf(s[8 * g + r], by, add);
+      }
+    }
+    const int key0 = (t0 + i) * BN + b * 32;
+    if (key0 + 32 > whole) {
+      const int lane_lim = lim - key0 - 4 * half;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[r] : kNegInf;
+    }
+  };
+  // The maximum moves only when it falls behind by 2^SLACK: the sums are hardly
+  // ever rescaled.
+  auto move_up = [&](const float16_t& s) __attribute__((always_inline)) {
+    float top = s[0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+    top = swap_halves_max(top) * a.scale;
+    const float m_new = top > m + SLACK ? top : m;
+    fall = __builtin_amdgcn_exp2f(m - m_new);
+    m = m_new;
+    l *= fall;
+  };
+  auto probabilities = [&](int i, int b, float16_t& s, u32x4_t (*p)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale, -m));
+      l += s[r];
+    }
+    if constexpr (General) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float by = group(by_v, i, 2 * b + g);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s[8 * g + r] *= by;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 16; r += 2) {
+      uint32_t w[NP];
+      split2<NP>(s[r], s[r + 1], w);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) p[j][r >> 3][(r & 7) >> 1] = w[j];
+    }
+  };
+  auto add_values = [&](const unsigned char* vt, int b, const u32x4_t (*p)[2])
+      __attribute__((always_inline)) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const int chunk = (d * 4 + vchunk) ^ v_swizzle16<CPR>(vrow);
+        const unsigned char* from = vt + (b * 32 + g * 16 + vrow) * RB + chunk * 16 + (i16 & 1) * 8;
+        const u32x2_t lo = read_column(from), hi = read_column(from + 8 * RB);
+        const u32x4_t vf = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+        for (int j = 0; j < NP; ++j) Mma<DT_BF16>::step(vf, p[j][g], acc[d], 0);
+      }
+  };
+  // (p is formed up to here: its first use is past a branch, where the compiler
+  // would take its computation, away from the matrix instructions)
+  auto follow = [&](u32x4_t (*p)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) asm volatile("" : "+v"(p[j][0]), "+v"(p[j][1]), "+v"(l));
+    if (__any(fall != 1.0f)) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[d][r] *= fall;
+    }
+  };
+
+  // Pipelined over blocks of 32 keys: while the vector units form a block's
+  // probabilities, the matrix units form the scores of the next block and add the
+  // values of the block before, in the same wave.  Keys are therefore a tile ahead
+  // of values.
+  unsigned char* const kt = lds;
+  unsigned char* const vt = lds + 2 * Z::TILE;
+  if (n > 0) {
+    float16_t s0, s1;           // scores of two blocks
+    u32x4_t p0[NP][2], p1[NP][2];   // probabilities of two blocks
+    Part xk = fetch(0, 0), xv = fetch(0, 1);
+    {
+      const Part x = fetch(1, 0);
+      if (RestK) look(0);
+      widen(xk, 0, 0, 0);
+      widen(xv, 0, 0, 1);
+      widen(x, 1, 1, 0);
+    }
+    xk = fetch(2, 0);
+    xv = fetch(1, 1);
+    lds_barrier();
+    score(kt, 0, s0);
+    score(kt, 1, s1);
+    settle(0, 0, s0);
+    move_up(s0);                // nothing to rescale yet
+    probabilities(0, 0, s0, p0);
+    // Tile i's second block and tile i + 1's first.  odd is i & 1, a constant where it
+    // is called, so that the places' addresses are.
+    auto two_blocks = [&](int i, int odd) __attribute__((always_inline)) {
+      const unsigned char* k1 = kt + (1 - odd) * Z::TILE;
+      const unsigned char* v0 = vt + odd * Z::TILE;
+      // (waited for here, not where they are used in every tile)
+      if ((i & 31) == 16 && i > 32 && i + 16 < n) {
+        if ((lane >> 5) == ((i >> 5) - 1 & 1)) locate((i & ~31) + 32 + (lane & 31));
+        asm volatile("" : "+v"(scales[0]), "+v"(scales[1]));
+      }
+      // keys of tile i + 1 and values of tile i lie there for all, and nobody reads
+      // keys of tile i and values of tile i - 1 any more
+      lds_barrier();
+      settle(i, 1, s1);
+      move_up(s1);
+      score(k1, 0, s0);
+      // behind the first matrix instructions
+      widen(xk, i + 2, odd, 0);
+      widen(xv, i + 1, 1 - odd, 1);
+      xk = fetch(i + 3, 0);
+      xv = fetch(i + 2, 1);
+      probabilities(i, 1, s1, p1);
+      add_values(v0, 0, p0);
+      follow(p1);
+      if (RestK && (i & 15) == 15) {
+        look(i + 1);
+        asm volatile("" : "+v"(by_k), "+v"(by_v), "+v"(addend));
+      }
+      settle(i + 1, 0, s0);
+      move_up(s0);
+      score(k1, 1, s1);
+      probabilities(i + 1, 0, s0, p0);
+      add_values(v0, 1, p1);
+      follow(p0);
+    };
+    int i = 0;
+    for (; i + 2 < n; i += 2) {
+      two_blocks(i, 0);
+      two_blocks(i + 1, 1);
+    }
+    if (i + 1 < n) two_blocks(i, 0);
+    const unsigned char* v0 = vt + ((n - 1) & 1) * Z::TILE;
+    lds_barrier();
+    settle(n - 1, 1, s1);
+    move_up(s1);
+    probabilities(n - 1, 1, s1, p1);
+    add_values(v0, 0, p0);
+    follow(p1);
+    add_values(v0, 1, p1);
+  }
+
+  l += __shfl_xor(l, 32);
+  if (!row_ok) return;
+  const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
+  const float lse2 = l == 0.0f ? kNegInf : m + __builtin_amdgcn_logf(l);
+  const long long t = job.e.row0 + qi;
+  const int heads = c.Hk * a.G;
+  if (job.slot >= 0) {
+    const long long to = (job.slot * a.T + t) * heads + head;
+    if (half == 0) a.many_lse[to] = lse2;
+    float* po = a.many + to * D;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int comp = d * 32 + 8 * r + 4 * half;
+        if (comp < D)
+          *reinterpret_cast<float4_t*>(po + comp) =
+              float4_t{acc[d][4 * r] * inv, acc[d][4 * r + 1] * inv, acc[d][4 * r + 2] * inv,
+                       acc[d][4 * r + 3] * inv};
+      }
+    return;
+  }
+  if (a.lse && half == 0) a.lse[t * heads + head] = lse2 * kLn2;
+  char* op = a.out + t * a.o_r + head * a.o_h;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int comp = d * 32 + 8 * r + 4 * half;
+      if (comp >= D) continue;
+      const float o0 = acc[d][4 * r] * inv, o1 = acc[d][4 * r + 1] * inv,
+                  o2 = acc[d][4 * r + 2] * inv, o3 = acc[d][4 * r + 3] * inv;
+      if constexpr (EB == 4)
+        *reinterpret_cast<float4_t*>(op + comp * 4) = float4_t{o0, o1, o2, o3};
+      else
+        *reinterpret_cast<u32x2_t*>(op + comp * 2) = u32x2_t{pack2<DT>(o0, o1), pack2<DT>(o2, o3)};
+    }
+}
+
+// The unit of number x of the sets of `size` rows of the entries with more than a
+// few (with `all`, of any), and of a key head.
+struct Unit {
+  Entry e;
+  int b, hk, set, keys;   // keys: those that its last row sees
+};
+__device__ __forceinline__ bool unit_of(const CacheAttnArgs& a, int number, int size, int all,
+                                        Unit* u) {
+  const int x = number / a.c.Hk;
+  u->hk = number - x * a.c.Hk;
+  auto weight = [=](const Entry& e) { return all || !few(e) ? (e.rows + size - 1) / size : 0; };
   Entries<decltype(weight)> entries(a, weight);
   const auto f = entries.find(x);
-  if (f.b >= a.c.B) return;
-  job.b = f.b;
-  job.e = f.e;
-  job.row_tile = x - (int)f.first;
-  const int last = (job.row_tile * 32 + 31 < job.e.rows ? job.row_tile * 32 + 31 : job.e.rows - 1);
-  int keys = a.causal ? job.e.len - job.e.n + last / a.G + 1 : job.e.len;
-  job.t0 = 0;
-  job.t1 = keys > 0 ? (keys + kTile - 1) / kTile : 0;
-  job.slot = -1;
+  if (f.b >= a.c.B) return false;
+  u->b = f.b;
+  u->e = f.e;
+  u->set = f.weight - 1 - (x - (int)f.first);   // causal: the longest first
+  const int end = (u->set + 1) * size, last = (end < f.e.rows ? end : f.e.rows) - 1;
+  const int keys = a.causal ? f.e.len - f.e.n + last / a.G + 1 : f.e.len;
+  u->keys = keys > 0 ? keys : 0;
+  return true;
+}
+
+// 32 rows of a key head a workgroup, for calls that have few such sets.
+template <int DT, int CF, int DP>
+__global__ __launch_bounds__(kThreads, 2) void some_kernel(const CacheAttnArgs a, int all) {
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
+  Unit u;
+  if (!unit_of(a, blockIdx.x, 32, all, &u)) return;
+  const Job job = {u.e, u.b, u.hk, u.set, 0, (u.keys + kTile - 1) / kTile, -1};
   attend_few<DT, CF, DP>(a, job, lds);
 }
 
-// Sets of 32 rows of a key head that a batch of T rows may have.
-long long row_sets(const CacheAttnArgs& a, long long set) {
-  const long long each = ((long long)a.max_rows * a.G + set - 1) / set * a.c.B;
-  const long long all = (long long)a.T * a.G / set + a.c.B;
+// 128 rows of a key head a workgroup; the keys in a.splits shares.
+template <int DT, int CF, int DP>
+__global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a, int all) {
+  using Z = Wide<DP>;
+  __shared__ __attribute__((aligned(1024))) unsigned char lds[Z::LDS];
+  const int per = gridDim.x / a.splits, split = blockIdx.x / per;
+  Unit u;
+  if (!unit_of(a, xcd_order(blockIdx.x - split * per, per), kManyRows, all, &u)) return;
+  const CacheView& c = a.c;
+  const int tiles = (u.keys + Z::BN - 1) / Z::BN;
+  const Job job = {u.e,
+                   u.b,
+                   u.hk,
+                   u.set,
+                   (int)((long long)tiles * split / a.splits),
+                   (int)((long long)tiles * (split + 1) / a.splits),
+                   a.splits > 1 ? split : -1};
+  // whether all blocks are there, with powers of two
+  bool plain = true;
+  const int last = job.t1 * Z::BN < u.e.len ? job.t1 * Z::BN : u.e.len;
+  const int b0 = (job.t0 * Z::BN) >> c.log_block, b1 = (last + (1 << c.log_block) - 1) >> c.log_block;
+  for (int i = b0 + threadIdx.x; i < b1; i += kThreads) {
+    const int id = c.table[(long long)u.b * c.width + i];
+    if (id < 0 || id >= c.blocks) {
+      plain = false;
+    } else {
+      const long long at = (long long)id * c.Hk + u.hk;
+      plain = plain && is_power(c.scale[0][at]) && is_power(c.scale[1][at]);
+    }
+  }
+  if (__syncthreads_and(plain)) attend_many<DT, CF, DP, false>(a, job, lds);
+  else attend_many<DT, CF, DP, true>(a, job, lds);
+}
+
+// Joins the splits of a row of a set: LPR lanes a row, 4 components a lane.
+template <int DT, int LPR>
+__global__ __launch_bounds__(kThreads) void many_join_kernel(const CacheAttnArgs a, int size,
+                                                             int all) {
+  Unit u;
+  if (!unit_of(a, blockIdx.x, size, all, &u)) return;
+  const int lane = threadIdx.x % LPR, D = a.c.D, heads = a.c.Hk * a.G;
+  const bool live = 4 * lane < D;
+  for (int r = threadIdx.x / LPR + blockIdx.y * (kThreads / LPR); r < size;
+       r += gridDim.y * (kThreads / LPR)) {
+    const int row = u.set * size + r;
+    if (row >= u.e.rows) return;
+    const int qi = row / a.G, head = u.hk * a.G + row - qi * a.G;
+    const long long t = u.e.row0 + qi, step = (long long)a.T * heads, at = t * heads + head;
+    float m = kLowest, sum = 0.0f;
+    float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int U = 4;
+    for (int s = 0; s < a.splits; s += U) {
+      float w[U];
+      float4_t v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        w[i] = kNegInf;
+        v[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (s + i < a.splits) {
+          w[i] = a.many_lse[(s + i) * step + at];
+          if (live)
+            v[i] = *reinterpret_cast<const float4_t*>(a.many + ((s + i) * step + at) * D + 4 * lane);
+        }
+      }
+      float m_new = m;
+#pragma unroll
+      for (int i = 0; i < U; ++i) m_new = fmaxf(m_new, w[i]);
+      const float fall = __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      sum *= fall;
+      o *= fall;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const float p = __builtin_amdgcn_exp2f(w[i] - m);
+        sum += p;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[i][j], o[j]);
+      }
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : sum;
+    if (a.lse && lane == 0)
+      a.lse[at] = sum == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (!live) continue;
+    char* op = a.out + t * a.o_r + head * a.o_h;
+    if constexpr (DT == DT_F32)
+      *reinterpret_cast<float4_t*>(op + 16 * lane) = o * inv;
+    else
+      *reinterpret_cast<u32x2_t*>(op + 8 * lane) =
+          u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+  }
+}
+
+// Sets of `size` rows of a key head that a batch may have.
+long long row_sets(const CacheAttnArgs& a, long long size) {
+  const long long each = ((long long)a.max_rows * a.G + size - 1) / size * a.c.B;
+  const long long all = (long long)a.T * a.G / size + a.c.B;
   return each < all ? each : all;
 }
 
 template <int DT, int CF, int DP>
 void launch(const CacheAttnArgs& a, hipStream_t stream) {
   const dim3 threads(kThreads);
+  constexpr int LPR = DP <= 64 ? 16 : 32;
+  const long long most = (long long)a.max_rows * a.G;
   // all entries have the most rows, or (rows of no entry) none does
-  const int all = (long long)a.max_rows * a.G > kFewRows && (long long)a.T == (long long)a.max_rows * a.c.B;
+  const int all = most > kFewRows && (long long)a.T == (long long)a.max_rows * a.c.B;
   if (!all && a.G <= kFewRows) {
     const int groups = a.few_groups > 0 ? a.few_groups : a.c.B * a.c.Hk;
     hipLaunchKernelGGL((few_kernel<DT, CF, DP>), dim3((unsigned)groups), threads, 0, stream, a);
-    if (a.few_groups > 0) {
-      constexpr int LPR = DP <= 64 ? 16 : 32;
-      const long long most = (long long)a.max_rows * a.G;
+    if (a.few_groups > 0)
       hipLaunchKernelGGL((few_join_kernel<DT, LPR>),
-                         dim3((unsigned)(a.c.B * a.c.Hk), (unsigned)(most < 32 ? most : 32)), threads,
-                         0, stream, a);
-    }
+                         dim3((unsigned)(a.c.B * a.c.Hk), (unsigned)(most < 32 ? most : 32)),
+                         threads, 0, stream, a);
   }
-  if ((long long)a.max_rows * a.G > kFewRows)
-    hipLaunchKernelGGL((many_kernel<DT, CF, DP>), dim3((unsigned)(row_sets(a, 32) * a.c.Hk)),
-                       threads, 0, stream, a, all);
+  if (most <= kFewRows) return;
+  const unsigned units = (unsigned)(row_sets(a, a.set) * a.c.Hk);
+  if (a.set == 32)
+    hipLaunchKernelGGL((some_kernel<DT, CF, DP>), dim3(units), threads, 0, stream, a, all);
+  else
+    hipLaunchKernelGGL((many_kernel<DT, CF, DP>), dim3(units * a.splits), dim3(kThreads), 0,
+                       stream, a, all);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((many_join_kernel<DT, LPR>), dim3(units, 4), threads, 0, stream, a, a.set,
+                       all);
 }
 
 template <int DT, int CF> void launch_cf(const CacheAttnArgs& a, hipStream_t stream) {
@@ -694,14 +1192,32 @@ template <int DT> void launch_dt(const CacheAttnArgs& a, int format, hipStream_t
 long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   a->few_groups = 0;
   a->splits = 1;
-  if (!allowed || a->T == 0 || a->c.B == 0) return 0;
-  if (a->G <= kFewRows && (long long)a->c.width << a->c.log_block > 512) a->few_groups = 2 * cus;
-  return 2LL * a->few_groups * kFewRows * (a->c.D + 1) * 4;
+  a->set = 32;
+  if (a->T == 0 || a->c.B == 0) return 0;
+  const long long keys = (long long)a->c.width << a->c.log_block;
+  const bool many = (long long)a->max_rows * a->G > kFewRows;
+  if (many) {
+    const long long n = row_sets(*a, kManyRows) * a->c.Hk;
+    if (n >= MANYMIN) a->set = kManyRows;
+    if (allowed && a->set == kManyRows) {
+      long long s = 2LL * cus / n;
+      if (s > keys / 512) s = keys / 512;
+      a->splits = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+    }
+  }
+  if (!allowed) return 0;
+  if (a->G <= kFewRows && keys > 1024 && a->c.B <= 1024) a->few_groups = 2 * cus;
+  const long long rows = a->splits > 1 ? (long long)a->T * a->G * a->c.Hk * a->splits : 0;
+  return (2LL * a->few_groups * kFewRows + rows) * (a->c.D + 1) * 4;
 }
 
 void cache_attn_place(CacheAttnArgs* a, char* workspace) {
+  const long long few = 2LL * a->few_groups * kFewRows;
+  const long long rows = (long long)a->T * a->G * a->c.Hk * a->splits;
   a->part = reinterpret_cast<float*>(workspace);
-  a->part_lse = a->part + 2LL * a->few_groups * kFewRows * a->c.D;
+  a->many = a->part + few * a->c.D;
+  a->part_lse = a->many + (a->splits > 1 ? rows * a->c.D : 0);
+  a->many_lse = a->part_lse + few;
 }
 
 libconv_status cache_attn_launch(CacheAttnArgs a, int format, int dtype, hipStream_t stream) {

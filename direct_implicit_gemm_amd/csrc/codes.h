@@ -44,6 +44,31 @@ template <int CF, int DT> __device__ __forceinline__ u32x4_t code_values16(uint3
   return u32x4_t{a[0], a[1], b[0], b[1]};
 }
 
+// 8 codes times a power of two, in bfloat16.
+template <int CF>
+__device__ __forceinline__ u32x4_t code_values16(uint32_t w0, uint32_t w1, float power) {
+  u32x4_t v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i == 0 ? w0 : w1;
+    if constexpr (CF == LIBCONV_CACHE_I8) {
+      float f[4];
+      code_values<CF>(w, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] *= power;
+      v[2 * i] = pack2<DT_BF16>(f[0], f[1]);
+      v[2 * i + 1] = pack2<DT_BF16>(f[2], f[3]);
+    } else {
+      // (the conversion multiplies by the power of two)
+      v[2 * i] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, false));
+      v[2 * i + 1] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, true));
+    }
+  }
+  return v;
+}
+
 // The codes of 4 values, given in units of the scale: to nearest even, an
 // infinity as the largest code (the conversion to 8-bit floats would make a NaN
 // of it), a NaN as NaN or 0.

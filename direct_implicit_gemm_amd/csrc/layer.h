@@ -111,10 +111,11 @@ struct CacheAttnArgs {
   // plan
   int few_groups;           // workgroups that share the keys of entries of few rows;
                             // 0: one to an entry and key head
-  int splits;               // of the keys of entries of many rows
-  float* few;               // partial results of the former: [2 few_groups][32][D + 1]
-  float* part;              // of the latter: [splits][Hk][T * G][D]
-  float* part_lse;          // [splits][Hk][T * G], log2
+  int set;                  // rows of a key head of entries of more rows to a workgroup
+  int splits;               // and shares of their keys
+  // partial results of the former [2 few_groups][32] and of the latter [splits][T]
+  // [q heads], normed: D outputs and the log2 of their sum, each
+  float *part, *part_lse, *many, *many_lse;
 };
 // Fills the plan for `cus` compute units and returns the workspace bytes it
 // takes; with a smaller workspace the plan has to be made with allowed = false.
