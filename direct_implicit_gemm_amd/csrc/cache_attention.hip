@@ -14,9 +14,6 @@
 #include "internal.h"
 #include "layer.h"
 
-#ifndef MANYMIN
-#define MANYMIN 32
-#endif
 namespace libconv {
 namespace {
 
@@ -650,7 +647,8 @@ template <int CPR> __device__ __forceinline__ int k_swizzle16(int row) {
   return CPR == 16 ? row & 15 : (row >> 1) & 7;
 }
 template <int CPR> __device__ __forceinline__ int v_swizzle16(int row) {
-  return CPR == 16 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+  // (the lowest bit for the writes, of every second chunk of two or four rows at a time)
+  return CPR == 16 ? (row & 3) << 2 | (row & 1) : ((row >> 1) & 1) * 5;
 }
 // Whether a scale is a power of two.
 __device__ __forceinline__ bool is_power(float s) {
@@ -658,7 +656,7 @@ __device__ __forceinline__ bool is_power(float s) {
   return (b & 0x807fffffu) == 0 && b - 0x00800000u < 0x7f000000u;
 }
 
-template <int DT, int CF, int DP, bool General>
+template <int DT, int CF, int DP, int NR, bool General>
 __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& job,
                                             unsigned char* lds) {
   using Z = Wide<DP>;
@@ -673,42 +671,50 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
   const int D = c.D, hk = job.hk, len = job.e.len, t0 = job.t0, t1 = job.t1, n = t1 - t0;
   const int mask = (1 << c.log_block) - 1;
 
-  // this lane's query
-  const int first_row = job.row_tile * kManyRows + wave * 32, local = first_row + l32;
-  const bool row_ok = local < job.e.rows;
-  const int row = row_ok ? local : 0, qi = row / a.G, head = hk * a.G + row - qi * a.G;
-  const int lim = a.causal ? len - job.e.n + qi + 1 : len;
-  // every row of the wave sees the keys below this
-  const int all = a.causal ? len - job.e.n + (first_row < job.e.rows ? first_row / a.G : 0) + 1 : len;
-  const int whole = __builtin_amdgcn_readfirstlane(all < 0 ? 0 : all & ~31);
-  const char* qp = a.q + (long long)(job.e.row0 + qi) * a.q_r + (long long)head * a.q_h;
-  u32x4_t qf[NQ][KS];
+  // this lane's queries, one of each of NR sets of 32 rows
+  bool row_ok[NR];
+  int qi[NR], head[NR], lim[NR], whole[NR];
+  u32x4_t qf[NR][NQ][KS];
 #pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    const int el = (2 * s + half) * 8;
-    u32x4_t raw[EB / 2];
+  for (int h = 0; h < NR; ++h) {
+    const int first = (job.row_tile * 4 + wave) * (32 * NR) + h * 32, local = first + l32;
+    row_ok[h] = local < job.e.rows;
+    const int row = row_ok[h] ? local : 0;
+    qi[h] = row / a.G;
+    head[h] = hk * a.G + row - qi[h] * a.G;
+    lim[h] = a.causal ? len - job.e.n + qi[h] + 1 : len;
+    // every row of the set sees the keys below this
+    const int all = a.causal ? len - job.e.n + (first < job.e.rows ? first / a.G : 0) + 1 : len;
+    whole[h] = __builtin_amdgcn_readfirstlane(all < 0 ? 0 : all & ~31);
+    const char* qp = a.q + (long long)(job.e.row0 + qi[h]) * a.q_r + (long long)head[h] * a.q_h;
 #pragma unroll
-    for (int i = 0; i < EB / 2; ++i) {
-      raw[i] = u32x4_t{0, 0, 0, 0};
-      if (row_ok && el < D) raw[i] = *reinterpret_cast<const u32x4_t*>(qp + el * EB + i * 16);
-      if (a.flip) {
-        const uint32_t sign = EB == 4 ? 0x80000000u : 0x80008000u;
-        raw[i] = a.flip < 0 ? raw[i] ^ u32x4_t{sign, sign, sign, sign} : u32x4_t{0, 0, 0, 0};
+    for (int s = 0; s < KS; ++s) {
+      const int el = (2 * s + half) * 8;
+      u32x4_t raw[EB / 2];
+#pragma unroll
+      for (int i = 0; i < EB / 2; ++i) {
+        raw[i] = u32x4_t{0, 0, 0, 0};
+        if (row_ok[h] && el < D)
+          raw[i] = *reinterpret_cast<const u32x4_t*>(qp + el * EB + i * 16);
+        if (a.flip) {
+          const uint32_t sign = EB == 4 ? 0x80000000u : 0x80008000u;
+          raw[i] = a.flip < 0 ? raw[i] ^ u32x4_t{sign, sign, sign, sign} : u32x4_t{0, 0, 0, 0};
+        }
       }
-    }
-    if constexpr (DT == DT_F32) {
-      float f[8];
-      unpack<DT_F32>(raw[0], f);
-      unpack<DT_F32>(raw[1], f + 4);
+      if constexpr (DT == DT_F32) {
+        float f[8];
+        unpack<DT_F32>(raw[0], f);
+        unpack<DT_F32>(raw[1], f + 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t w[NQ];
-        split2<NQ>(f[2 * j], f[2 * j + 1], w);
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w[NQ];
+          split2<NQ>(f[2 * j], f[2 * j + 1], w);
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) qf[i][s][j] = w[i];
+          for (int i = 0; i < NQ; ++i) qf[h][i][s][j] = w[i];
+        }
+      } else {
+        qf[h][0][s] = raw[0];
       }
-    } else {
-      qf[0][s] = raw[0];
     }
   }
 
@@ -806,77 +812,100 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
       }
   };
 
-  float16_t acc[DB];
+  float16_t acc[NR][DB];
+  float m[NR], l[NR], fall[NR];
 #pragma unroll
-  for (int d = 0; d < DB; ++d) acc[d] = float16_t{};
-  float m = kLowest, l = 0.0f, fall = 1.0f;
+  for (int h = 0; h < NR; ++h) {
+    m[h] = kLowest;
+    l[h] = 0.0f;
+    fall[h] = 1.0f;
+#pragma unroll
+    for (int d = 0; d < DB; ++d) acc[h][d] = float16_t{};
+  }
   // LDS offsets that do not change from tile to tile
   const int krow = l32 * RB, ksw = (half ^ k_swizzle16<CPR>(l32)) * 16;
   const int i16 = lane & 15, vrow = 4 * half + (i16 >> 2);
   const int vchunk = ((lane >> 4) & 1) * 2 + ((i16 & 3) >> 1);
+  using Probabilities = u32x4_t[NR][NP][2];
 
-  auto score = [&](const unsigned char* kt, int b, float16_t& s) __attribute__((always_inline)) {
-    s = float16_t{};
+  auto score = [&](const unsigned char* kt, int b, float16_t* s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < NR; ++h) s[h] = float16_t{};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const u32x4_t kf =
           *reinterpret_cast<const u32x4_t*>(kt + krow + b * 32 * RB + (ksw ^ (ks * 32)));
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) Mma<KT>::step(kf, qf[i][ks], s, 0);
+      for (int h = 0; h < NR; ++h)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) Mma<KT>::step(kf, qf[h][i][ks], s[h], 0);
     }
   };
   // scores of block b of tile i as they count
-  auto settle = [&](int i, int b, float16_t& s) __attribute__((always_inline)) {
+  auto settle = [&](int i, int b, float16_t* s) __attribute__((always_inline)) {
     if constexpr (RestK) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const float by = group(by_k, i, 2 * b + g), add = General ? group(addend, i, 2 * b + g) : 0.0f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) s[8 * g + r] = fmaf(s[8 * g + r], by, add);
+        for (int h = 0; h < NR; ++h)
+#pragma unroll
+          for (int r = 0; r < 8; ++r) s[h][8 * g + r] = fmaf(s[h][8 * g + r], by, add);
       }
     }
     const int key0 = (t0 + i) * BN + b * 32;
-    if (key0 + 32 > whole) {
-      const int lane_lim = lim - key0 - 4 * half;
+    // (the first set's rows see the fewest keys)
+    if (key0 + 32 > whole[0]) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[r] : kNegInf;
+      for (int h = 0; h < NR; ++h) {
+        const int lane_lim = lim[h] - key0 - 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[h][r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[h][r] : kNegInf;
+      }
     }
   };
   // The maximum moves only when it falls behind by 2^SLACK: the sums are hardly
   // ever rescaled.
-  auto move_up = [&](const float16_t& s) __attribute__((always_inline)) {
-    float top = s[0];
+  auto move_up = [&](const float16_t* s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
-    top = swap_halves_max(top) * a.scale;
-    const float m_new = top > m + SLACK ? top : m;
-    fall = __builtin_amdgcn_exp2f(m - m_new);
-    m = m_new;
-    l *= fall;
-  };
-  auto probabilities = [&](int i, int b, float16_t& s, u32x4_t (*p)[2]) __attribute__((always_inline)) {
+    for (int h = 0; h < NR; ++h) {
+      float top = s[h][0];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale, -m));
-      l += s[r];
+      for (int r = 1; r < 16; ++r) top = fmaxf(top, s[h][r]);
+      top = swap_halves_max(top) * a.scale;
+      const float m_new = top > m[h] + SLACK ? top : m[h];
+      fall[h] = __builtin_amdgcn_exp2f(m[h] - m_new);
+      m[h] = m_new;
+      l[h] *= fall[h];
     }
-    if constexpr (General) {
+  };
+  auto probabilities = [&](int i, int b, float16_t* s, Probabilities& p) __attribute__((always_inline)) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float by = group(by_v, i, 2 * b + g);
+    for (int h = 0; h < NR; ++h) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) s[8 * g + r] *= by;
+      for (int r = 0; r < 16; ++r) {
+        s[h][r] = __builtin_amdgcn_exp2f(fmaf(s[h][r], a.scale, -m[h]));
+        l[h] += s[h][r];
+      }
+      if constexpr (General) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float by = group(by_v, i, 2 * b + g);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) s[h][8 * g + r] *= by;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        uint32_t w[NP];
+        split2<NP>(s[h][r], s[h][r + 1], w);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) p[h][j][r >> 3][(r & 7) >> 1] = w[j];
       }
     }
-#pragma unroll
-    for (int r = 0; r < 16; r += 2) {
-      uint32_t w[NP];
-      split2<NP>(s[r], s[r + 1], w);
-#pragma unroll
-      for (int j = 0; j < NP; ++j) p[j][r >> 3][(r & 7) >> 1] = w[j];
-    }
   };
-  auto add_values = [&](const unsigned char* vt, int b, const u32x4_t (*p)[2])
+  auto add_values = [&](const unsigned char* vt, int b, const Probabilities& p)
       __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < 2; ++g)
@@ -887,19 +916,28 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
         const u32x2_t lo = read_column(from), hi = read_column(from + 8 * RB);
         const u32x4_t vf = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-        for (int j = 0; j < NP; ++j) Mma<DT_BF16>::step(vf, p[j][g], acc[d], 0);
+        for (int h = 0; h < NR; ++h)
+#pragma unroll
+          for (int j = 0; j < NP; ++j) Mma<DT_BF16>::step(vf, p[h][j][g], acc[h][d], 0);
       }
   };
   // (p is formed up to here: its first use is past a branch, where the compiler
   // would take its computation, away from the matrix instructions)
-  auto follow = [&](u32x4_t (*p)[2]) __attribute__((always_inline)) {
+  auto follow = [&](Probabilities& p) __attribute__((always_inline)) {
+    bool any = false;
 #pragma unroll
-    for (int j = 0; j < NP; ++j) asm volatile("" : "+v"(p[j][0]), "+v"(p[j][1]), "+v"(l));
-    if (__any(fall != 1.0f)) {
+    for (int h = 0; h < NR; ++h) {
 #pragma unroll
-      for (int d = 0; d < DB; ++d)
+      for (int j = 0; j < NP; ++j) asm volatile("" : "+v"(p[h][j][0]), "+v"(p[h][j][1]), "+v"(l[h]));
+      any = any || fall[h] != 1.0f;
+    }
+    if (__any(any)) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[d][r] *= fall;
+      for (int h = 0; h < NR; ++h)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[h][d][r] *= fall[h];
     }
   };
 
@@ -910,8 +948,8 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
   unsigned char* const kt = lds;
   unsigned char* const vt = lds + 2 * Z::TILE;
   if (n > 0) {
-    float16_t s0, s1;           // scores of two blocks
-    u32x4_t p0[NP][2], p1[NP][2];   // probabilities of two blocks
+    float16_t s0[NR], s1[NR];   // scores of two blocks
+    Probabilities p0, p1;       // probabilities of two blocks
     Part xk = fetch(0, 0), xv = fetch(0, 1);
     {
       const Part x = fetch(1, 0);
@@ -979,43 +1017,36 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
     add_values(v0, 1, p1);
   }
 
-  l += __shfl_xor(l, 32);
-  if (!row_ok) return;
-  const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
-  const float lse2 = l == 0.0f ? kNegInf : m + __builtin_amdgcn_logf(l);
-  const long long t = job.e.row0 + qi;
   const int heads = c.Hk * a.G;
-  if (job.slot >= 0) {
-    const long long to = (job.slot * a.T + t) * heads + head;
-    if (half == 0) a.many_lse[to] = lse2;
-    float* po = a.many + to * D;
+#pragma unroll
+  for (int h = 0; h < NR; ++h) {
+    const float sum = l[h] + __shfl_xor(l[h], 32);
+    if (!row_ok[h]) continue;
+    const float inv = sum > 0.0f ? 1.0f / sum : sum;   // 0 keys: 0; a NaN stays
+    const float lse2 = sum == 0.0f ? kNegInf : m[h] + __builtin_amdgcn_logf(sum);
+    const long long t = job.e.row0 + qi[h], at = (job.slot * a.T + t) * heads + head[h];
+    if (half == 0) {
+      if (job.slot >= 0) a.many_lse[at] = lse2;
+      else if (a.lse) a.lse[t * heads + head[h]] = lse2 * kLn2;
+    }
+    char* const op = a.out + t * a.o_r + head[h] * a.o_h;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int comp = d * 32 + 8 * r + 4 * half;
-        if (comp < D)
-          *reinterpret_cast<float4_t*>(po + comp) =
-              float4_t{acc[d][4 * r] * inv, acc[d][4 * r + 1] * inv, acc[d][4 * r + 2] * inv,
-                       acc[d][4 * r + 3] * inv};
+        if (comp >= D) continue;
+        const float4_t o = {acc[h][d][4 * r] * inv, acc[h][d][4 * r + 1] * inv,
+                            acc[h][d][4 * r + 2] * inv, acc[h][d][4 * r + 3] * inv};
+        if (job.slot >= 0)
+          *reinterpret_cast<float4_t*>(a.many + at * D + comp) = o;
+        else if constexpr (EB == 4)
+          *reinterpret_cast<float4_t*>(op + comp * 4) = o;
+        else
+          *reinterpret_cast<u32x2_t*>(op + comp * 2) =
+              u32x2_t{pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3])};
       }
-    return;
   }
-  if (a.lse && half == 0) a.lse[t * heads + head] = lse2 * kLn2;
-  char* op = a.out + t * a.o_r + head * a.o_h;
-#pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int comp = d * 32 + 8 * r + 4 * half;
-      if (comp >= D) continue;
-      const float o0 = acc[d][4 * r] * inv, o1 = acc[d][4 * r + 1] * inv,
-                  o2 = acc[d][4 * r + 2] * inv, o3 = acc[d][4 * r + 3] * inv;
-      if constexpr (EB == 4)
-        *reinterpret_cast<float4_t*>(op + comp * 4) = float4_t{o0, o1, o2, o3};
-      else
-        *reinterpret_cast<u32x2_t*>(op + comp * 2) = u32x2_t{pack2<DT>(o0, o1), pack2<DT>(o2, o3)};
-    }
 }
 
 // The unit of number x of the sets of `size` rows of the entries with more than a
@@ -1051,14 +1082,18 @@ __global__ __launch_bounds__(kThreads, 2) void some_kernel(const CacheAttnArgs a
   attend_few<DT, CF, DP>(a, job, lds);
 }
 
-// 128 rows of a key head a workgroup; the keys in a.splits shares.
-template <int DT, int CF, int DP>
-__global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a, int all) {
+// 128 NR rows of a key head a workgroup; the keys in a.splits shares.
+template <int DT, int CF, int DP, int NR>
+__global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void many_kernel(const CacheAttnArgs a,
+                                                                         int all) {
   using Z = Wide<DP>;
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Z::LDS];
   const int per = gridDim.x / a.splits, split = blockIdx.x / per;
   Unit u;
-  if (!unit_of(a, xcd_order(blockIdx.x - split * per, per), kManyRows, all, &u)) return;
+  // (consecutive workgroups, which lie on different XCDs, are of different heads: an
+  // XCD then reads few heads of every entry, however long each is.  With an XCD to
+  // an entry the longest one held up the end.)
+  if (!unit_of(a, blockIdx.x - split * per, kManyRows * NR, all, &u)) return;
   const CacheView& c = a.c;
   const int tiles = (u.keys + Z::BN - 1) / Z::BN;
   const Job job = {u.e,
@@ -1081,8 +1116,8 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a
       plain = plain && is_power(c.scale[0][at]) && is_power(c.scale[1][at]);
     }
   }
-  if (__syncthreads_and(plain)) attend_many<DT, CF, DP, false>(a, job, lds);
-  else attend_many<DT, CF, DP, true>(a, job, lds);
+  if (__syncthreads_and(plain)) attend_many<DT, CF, DP, NR, false>(a, job, lds);
+  else attend_many<DT, CF, DP, NR, true>(a, job, lds);
 }
 
 // Joins the splits of a row of a set: LPR lanes a row, 4 components a lane.
@@ -1170,8 +1205,8 @@ void launch(const CacheAttnArgs& a, hipStream_t stream) {
   if (a.set == 32)
     hipLaunchKernelGGL((some_kernel<DT, CF, DP>), dim3(units), threads, 0, stream, a, all);
   else
-    hipLaunchKernelGGL((many_kernel<DT, CF, DP>), dim3(units * a.splits), dim3(kThreads), 0,
-                       stream, a, all);
+    hipLaunchKernelGGL((many_kernel<DT, CF, DP, 1>), dim3(units * a.splits), threads, 0, stream, a,
+                       all);
   if (a.splits > 1)
     hipLaunchKernelGGL((many_join_kernel<DT, LPR>), dim3(units, 4), threads, 0, stream, a, a.set,
                        all);
@@ -1198,11 +1233,13 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   const bool many = (long long)a->max_rows * a->G > kFewRows;
   if (many) {
     const long long n = row_sets(*a, kManyRows) * a->c.Hk;
-    if (n >= MANYMIN) a->set = kManyRows;
-    if (allowed && a->set == kManyRows) {
-      long long s = 2LL * cus / n;
-      if (s > keys / 512) s = keys / 512;
-      a->splits = (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+    long long s = 4LL * cus / n;
+    if (s > keys / 512) s = keys / 512;
+    if (s > 16) s = 16;
+    if (s < 1 || !allowed) s = 1;
+    if (n * s >= cus / 2) {
+      a->set = kManyRows;
+      a->splits = (int)s;
     }
   }
   if (!allowed) return 0;
