@@ -91,4 +91,20 @@ template <int CF> __device__ __forceinline__ uint32_t codes_of(const float* x) {
   }
 }
 
+// The same for numbers within the codes' range.
+template <int CF> __device__ __forceinline__ uint32_t codes_within(const float* x) {
+  if constexpr (CF == LIBCONV_CACHE_I8) {
+    // 1.5 * 2^23 + x: the sum's rounding is x's, and its lowest byte the code
+    uint32_t b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = __builtin_bit_cast(uint32_t, x[j] + 12582912.0f);
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+    return lo | hi;
+  } else {
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
+  }
+}
+
 }  // namespace libconv

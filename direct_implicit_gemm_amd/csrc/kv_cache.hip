@@ -17,8 +17,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWindow = 256;   // rows that a workgroup of the write looks over, at most: a
                                // block's, so that no two begin a block of the same entry
-constexpr int kHeld = 8;       // reads of a lane that stay in registers between the
-                               // largest magnitude and the rounding
 
 // idx / chunks of a row for idx below 256 rows of 32 chunks.
 struct RowOf {
@@ -27,16 +25,41 @@ struct RowOf {
   __device__ __forceinline__ int row(int i) const { return (int)((unsigned)i * m >> 18); }
 };
 
-// The largest magnitude so far, as bits; infinities and NaN do not count.
-template <int DT> __device__ __forceinline__ uint32_t top_of(uint32_t top, const u32x4_t& v) {
-  float f[16 / Elem<DT>::bytes];
-  unpack<DT>(v, f);
-#pragma unroll
-  for (int j = 0; j < 16 / Elem<DT>::bytes; ++j) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, f[j]) & 0x7fffffffu;
-    top = b < 0x7f800000u && b > top ? b : top;
+// The largest magnitudes so far, as bits: of a word's two 16-bit values side by
+// side, or of its one.
+template <int DT> __device__ __forceinline__ uint32_t larger(uint32_t top, uint32_t w) {
+  if constexpr (DT == DT_F32) {
+    w &= 0x7fffffffu;
+    return w > top ? w : top;
+  } else {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(
+        uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, top),
+                                            __builtin_bit_cast(u16x2_t, w & 0x7fff7fffu)));
   }
-  return top;
+}
+// ... over the wave, as the bits of a float; infinities and NaN are larger than all
+// others.
+template <int DT> __device__ __forceinline__ uint32_t top_of_wave(uint32_t top) {
+  if constexpr (DT != DT_F32) top = (top & 0xffffu) > (top >> 16) ? top & 0xffffu : top >> 16;
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    const uint32_t other = (uint32_t)__shfl_xor((int)top, m);
+    top = other > top ? other : top;
+  }
+  if constexpr (DT == DT_F32) return top;
+  return __builtin_bit_cast(uint32_t, Elem<DT>::bits_to_f32(top));
+}
+// The word without its infinities and NaN.
+template <int DT> __device__ __forceinline__ uint32_t finite_of(uint32_t w) {
+  if constexpr (DT == DT_F32) {
+    return (w & 0x7f800000u) == 0x7f800000u ? 0u : w;
+  } else {
+    constexpr uint32_t E = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+    if ((w & E) == E) w &= 0xffff0000u;
+    if ((w & (E << 16)) == E << 16) w &= 0xffffu;
+    return w;
+  }
 }
 
 // The least power of two, 2^-126 or more, that brings a magnitude (as bits) down
@@ -49,8 +72,9 @@ template <int CF> __device__ __forceinline__ float scale_for(uint32_t top) {
 }
 
 // One head's keys or values of a block: `rows` rows from x on become the tokens
-// from `held` on of the block at `codes`.
-template <int DT, int CF>
+// from `held` on of the block at `codes`.  HELD reads of a lane stay in registers
+// between the largest magnitude and the rounding, others are read again.
+template <int DT, int CF, int HELD>
 __device__ __forceinline__ void write_block(const char* x, long long x_row, char* codes,
                                             long long token, float* scale, int rows, int held,
                                             int D) {
@@ -63,20 +87,32 @@ __device__ __forceinline__ void write_block(const char* x, long long x_row, char
     const int row = by.row(i);
     return *reinterpret_cast<const u32x4_t*>(x + row * x_row + (i - row * chunks) * 16);
   };
-  u32x4_t raw[kHeld];
+  u32x4_t raw[HELD];
   uint32_t top = 0;
 #pragma unroll
-  for (int u = 0; u < kHeld; ++u) {
+  for (int u = 0; u < HELD; ++u) {
     raw[u] = u32x4_t{0, 0, 0, 0};
     if (u * 64 + lane < total) raw[u] = read(u * 64 + lane);
   }
 #pragma unroll
-  for (int u = 0; u < kHeld; ++u) top = top_of<DT>(top, raw[u]);
-  for (int i = kHeld * 64 + lane; i < total; i += 64) top = top_of<DT>(top, read(i));
+  for (int u = 0; u < HELD; ++u)
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const uint32_t other = (uint32_t)__shfl_xor((int)top, m);
-    top = other > top ? other : top;
+    for (int j = 0; j < 4; ++j) top = larger<DT>(top, raw[u][j]);
+  for (int i = HELD * 64 + lane; i < total; i += 64) {
+    const u32x4_t v = read(i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = larger<DT>(top, v[j]);
+  }
+  top = top_of_wave<DT>(top);
+  const bool finite = top < 0x7f800000u;
+  if (!finite) {   // once more, without them
+    top = 0;
+    for (int i = lane; i < total; i += 64) {
+      const u32x4_t v = read(i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = larger<DT>(top, finite_of<DT>(v[j]));
+    }
+    top = top_of_wave<DT>(top);
   }
   // (a scale that is no positive number stands for codes of no value)
   const float old = old_as_is > 0.0f && __builtin_isfinite(old_as_is) ? old_as_is : 0.0f;
@@ -88,15 +124,17 @@ __device__ __forceinline__ void write_block(const char* x, long long x_row, char
 #pragma unroll
     for (int j = 0; j < E; ++j) f[j] *= inv;
     char* at = codes + (held + row) * token + (i - row * chunks) * E;
-    if constexpr (EB == 4)
-      *reinterpret_cast<uint32_t*>(at) = codes_of<CF>(f);
-    else
-      *reinterpret_cast<u32x2_t*>(at) = u32x2_t{codes_of<CF>(f), codes_of<CF>(f + 4)};
+    u32x2_t w;
+#pragma unroll
+    for (int j = 0; j < E / 4; ++j)
+      w[j] = finite ? codes_within<CF>(f + 4 * j) : codes_of<CF>(f + 4 * j);
+    if constexpr (EB == 4) *reinterpret_cast<uint32_t*>(at) = w[0];
+    else *reinterpret_cast<u32x2_t*>(at) = w;
   };
 #pragma unroll
-  for (int u = 0; u < kHeld; ++u)
+  for (int u = 0; u < HELD; ++u)
     if (u * 64 + lane < total) write(u * 64 + lane, raw[u]);
-  for (int i = kHeld * 64 + lane; i < total; i += 64) write(i, read(i));
+  for (int i = HELD * 64 + lane; i < total; i += 64) write(i, read(i));
   if (held > 0 && s != old_as_is) {
     const float down = old / s;
     const int words = D / 4;
@@ -116,7 +154,7 @@ __device__ __forceinline__ void write_block(const char* x, long long x_row, char
 // A workgroup looks over a block's number of rows for those that are their entry's
 // first in a block, and its waves take the blocks' heads, keys and values, in turn (with
 // the gridDim.y workgroups of the same rows).
-template <int DT, int CF>
+template <int DT, int CF, int HELD>
 __global__ __launch_bounds__(kThreads) void write_kernel(const CacheCopyArgs a) {
   __shared__ int count, first[kWindow], rows[kWindow], held[kWindow], block[kWindow];
   const CacheView& c = a.c;
@@ -158,7 +196,7 @@ __global__ __launch_bounds__(kThreads) void write_kernel(const CacheCopyArgs a) 
     const int kv = of >= c.Hk, h = of - kv * c.Hk;
     const int t = __builtin_amdgcn_readfirstlane(first[f]);
     const int id = __builtin_amdgcn_readfirstlane(block[f]);
-    write_block<DT, CF>(a.x[kv] + t * a.row[kv] + h * a.head[kv], a.row[kv],
+    write_block<DT, CF, HELD>(a.x[kv] + t * a.row[kv] + h * a.head[kv], a.row[kv],
                         c.codes[kv] + id * c.block[kv] + h * c.head[kv], c.token[kv],
                         c.scale[kv] + (long long)id * c.Hk + h,
                         __builtin_amdgcn_readfirstlane(rows[f]),
@@ -244,8 +282,11 @@ struct Write {
     // rows of one entry: a block's heads; single tokens: those of each row
     const unsigned block = (2u * a.c.Hk + 3) / 4;
     const unsigned rows = turns(x, 2LL * a.c.Hk * (a.T < size ? a.T : size));
-    hipLaunchKernelGGL((write_kernel<DT, CF>), dim3((unsigned)x, block > rows ? block : rows),
-                       dim3(kThreads), 0, stream, a);
+    const dim3 grid((unsigned)x, block > rows ? block : rows), threads(kThreads);
+    if (size * a.c.D * Elem<DT>::bytes <= 8 * 1024)
+      hipLaunchKernelGGL((write_kernel<DT, CF, 8>), grid, threads, 0, stream, a);
+    else
+      hipLaunchKernelGGL((write_kernel<DT, CF, 16>), grid, threads, 0, stream, a);
   }
 };
 struct Read {
