@@ -18,7 +18,8 @@ namespace libconv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;       // keys of a tile: 32 for each of a workgroup's waves
+// Of few rows: waves that split a workgroup's keys, and keys of a tile, 32 for each.
+constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves, kTile = 32 * kFewWaves;
 constexpr int kFewRows = 32;     // rows of a key head that one set of matrix columns holds
 
 // Terms that q and the probabilities enter the matrix instructions as: bfloat16
@@ -52,7 +53,7 @@ template <int DP> struct Shape {
   static constexpr int COPIES = PART / 1024;       // 16 bytes a lane each
   static constexpr int WAVE = 2 * 2 * PART + 256 + 1024;   // stages of keys and values, blocks,
                                                            // scales
-  static constexpr int LDS = 4 * WAVE;
+  static constexpr int LDS = kFewWaves * WAVE;
 };
 // Chunk c of row r is kept at c ^ swizzle(r): 16 rows' reads of one chunk, and the
 // 8 rows that 16 lanes read a chunk of, hit all banks.
@@ -447,13 +448,14 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
   // join the waves: each leaves maximum, sum and outputs (DP components, 32 rows
   // fastest) in LDS and sums 32 components of all
   l += __shfl_xor(l, 32);
-  static_assert(4 * 32 * DP * 4 <= Z::LDS - 1024, "the join fits the stages");
-  float* const tops = reinterpret_cast<float*>(lds + Z::LDS - 1024);   // [4][32], then the sums
+  static_assert(kFewWaves * 32 * DP * 4 <= Z::LDS - 1024, "the join fits the stages");
+  float* const tops = reinterpret_cast<float*>(lds + Z::LDS - 1024);   // [wave][32], then the sums
+  constexpr int SUMS = kFewWaves * 32;
   lds_barrier();   // every wave is done with its stages, no copy is on its way
   float* const rooms = reinterpret_cast<float*>(lds);
   if (half == 0) {
     tops[wave * 32 + l32] = m;
-    tops[128 + wave * 32 + l32] = l;
+    tops[SUMS + wave * 32 + l32] = l;
   }
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -461,55 +463,41 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
     for (int r = 0; r < 16; ++r)
       rooms[(wave * DP + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32] = acc[d][r];
   lds_barrier();
-  if (wave < DB) {
+  for (int d = wave; d < DB; d += kFewWaves) {
     float m_all = tops[l32];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) m_all = fmaxf(m_all, tops[w * 32 + l32]);
+    for (int w = 1; w < kFewWaves; ++w) m_all = fmaxf(m_all, tops[w * 32 + l32]);
     float o[16] = {};
     l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kFewWaves; ++w) {
       const float g = __builtin_amdgcn_exp2f(tops[w * 32 + l32] - m_all);
-      l = fmaf(tops[128 + w * 32 + l32], g, l);
+      l = fmaf(tops[SUMS + w * 32 + l32], g, l);
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        o[r] = fmaf(rooms[(w * DP + wave * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32], g,
-                    o[r]);
+        o[r] = fmaf(rooms[(w * DP + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32], g, o[r]);
     }
-    if (row_ok) {
-      const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
-      const float lse2 = l == 0.0f ? kNegInf : m_all + __builtin_amdgcn_logf(l);
-      const bool first = wave == 0 && half == 0;
+    if (!row_ok) continue;
+    const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
+    const float lse2 = l == 0.0f ? kNegInf : m_all + __builtin_amdgcn_logf(l);
+    const long long slot = job.slot * kFewRows + local, t = job.e.row0 + qi;
+    const int head = hk * a.G + qg;
+    if (d == 0 && half == 0) {
+      if (job.slot >= 0) a.part_lse[slot] = lse2;
+      else if (a.lse) a.lse[t * (c.Hk * a.G) + head] = lse2 * kLn2;
+    }
+    char* const op = a.out + t * a.o_r + head * a.o_h;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) o[r] *= inv;
-      if (job.slot >= 0) {
-        const long long slot = job.slot * kFewRows + local;
-        if (first) a.part_lse[slot] = lse2;
-        float* po = a.part + slot * D;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int comp = wave * 32 + 8 * r + 4 * half;
-          if (comp < D)
-            *reinterpret_cast<float4_t*>(po + comp) =
-                float4_t{o[4 * r], o[4 * r + 1], o[4 * r + 2], o[4 * r + 3]};
-        }
-      } else {
-        const long long t = job.e.row0 + qi;
-        const int head = hk * a.G + qg;
-        if (a.lse && first) a.lse[t * (c.Hk * a.G) + head] = lse2 * kLn2;
-        char* op = a.out + t * a.o_r + head * a.o_h;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int comp = wave * 32 + 8 * r + 4 * half;
-          if (comp >= D) continue;
-          if constexpr (EB == 4)
-            *reinterpret_cast<float4_t*>(op + comp * 4) =
-                float4_t{o[4 * r], o[4 * r + 1], o[4 * r + 2], o[4 * r + 3]};
-          else
-            *reinterpret_cast<u32x2_t*>(op + comp * 2) =
-                u32x2_t{pack2<DT>(o[4 * r], o[4 * r + 1]), pack2<DT>(o[4 * r + 2], o[4 * r + 3])};
-        }
-      }
+    for (int r = 0; r < 4; ++r) {
+      const int comp = d * 32 + 8 * r + 4 * half;
+      if (comp >= D) continue;
+      const float4_t v = {o[4 * r] * inv, o[4 * r + 1] * inv, o[4 * r + 2] * inv, o[4 * r + 3] * inv};
+      if (job.slot >= 0)
+        *reinterpret_cast<float4_t*>(a.part + slot * D + comp) = v;
+      else if constexpr (EB == 4)
+        *reinterpret_cast<float4_t*>(op + comp * 4) = v;
+      else
+        *reinterpret_cast<u32x2_t*>(op + comp * 2) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
     }
   }
   lds_barrier();   // the joined results are read
@@ -520,7 +508,7 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
 // different lengths fill the GPU to the end).  A head whose tiles lie in one run
 // is written at once, of others the runs' parts are joined (few_join_kernel).
 template <int DT, int CF, int DP>
-__global__ __launch_bounds__(kThreads, 2) void few_kernel(const CacheAttnArgs a) {
+__global__ __launch_bounds__(kFewThreads, 2) void few_kernel(const CacheAttnArgs a) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
   Job job;
   job.row_tile = 0;
@@ -1074,7 +1062,7 @@ __device__ __forceinline__ bool unit_of(const CacheAttnArgs& a, int number, int 
 
 // 32 rows of a key head a workgroup, for calls that have few such sets.
 template <int DT, int CF, int DP>
-__global__ __launch_bounds__(kThreads, 2) void some_kernel(const CacheAttnArgs a, int all) {
+__global__ __launch_bounds__(kFewThreads, 2) void some_kernel(const CacheAttnArgs a, int all) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
   Unit u;
   if (!unit_of(a, blockIdx.x, 32, all, &u)) return;
@@ -1194,7 +1182,8 @@ void launch(const CacheAttnArgs& a, hipStream_t stream) {
   const int all = most > kFewRows && (long long)a.T == (long long)a.max_rows * a.c.B;
   if (!all && a.G <= kFewRows) {
     const int groups = a.few_groups > 0 ? a.few_groups : a.c.B * a.c.Hk;
-    hipLaunchKernelGGL((few_kernel<DT, CF, DP>), dim3((unsigned)groups), threads, 0, stream, a);
+    hipLaunchKernelGGL((few_kernel<DT, CF, DP>), dim3((unsigned)groups), dim3(kFewThreads), 0,
+                       stream, a);
     if (a.few_groups > 0)
       hipLaunchKernelGGL((few_join_kernel<DT, LPR>),
                          dim3((unsigned)(a.c.B * a.c.Hk), (unsigned)(most < 32 ? most : 32)),
@@ -1203,7 +1192,7 @@ void launch(const CacheAttnArgs& a, hipStream_t stream) {
   if (most <= kFewRows) return;
   const unsigned units = (unsigned)(row_sets(a, a.set) * a.c.Hk);
   if (a.set == 32)
-    hipLaunchKernelGGL((some_kernel<DT, CF, DP>), dim3(units), threads, 0, stream, a, all);
+    hipLaunchKernelGGL((some_kernel<DT, CF, DP>), dim3(units), dim3(kFewThreads), 0, stream, a, all);
   else
     hipLaunchKernelGGL((many_kernel<DT, CF, DP, 1>), dim3(units * a.splits), threads, 0, stream, a,
                        all);
@@ -1243,7 +1232,7 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
     }
   }
   if (!allowed) return 0;
-  if (a->G <= kFewRows && keys > 1024 && a->c.B <= 1024) a->few_groups = 2 * cus;
+  if (a->G <= kFewRows && keys > 1024 && a->c.B <= 1024) a->few_groups = 8 / kFewWaves * cus;
   const long long rows = a->splits > 1 ? (long long)a->T * a->G * a->c.Hk * a->splits : 0;
   return (2LL * a->few_groups * kFewRows + rows) * (a->c.D + 1) * 4;
 }

@@ -161,7 +161,11 @@ def attention(q, cache, row_starts, scale, causal):
             off = U32 * (2 * (terms * D + 8) * a + 2 * n + 64)
             mag = p @ v[:, g].abs()
             out[lo:hi, h] = p @ v[:, g]
-            bound[lo:hi, h] = (U[t] + P_ROUNDING[t] + off)[:, None] * mag + tiny(t)
+            # a probability (or it times its scale) below 2^-126 is 0 in the matrix
+            # instructions, which take numbers that small for 0: n terms of less than 2^-126
+            # times a code (or a value) are missing then
+            gone = n * 2.0 ** -126 * (448 + v[:, g].abs().amax())
+            bound[lo:hi, h] = (U[t] + P_ROUNDING[t] + off)[:, None] * mag + tiny(t) + gone
             lse[lo:hi, h] = torch.where(some, torch.logsumexp(s, -1), torch.full((), -math.inf).double())
             lse_bound[lo:hi, h] = off + U32 * 8 * (1 + a)
     return out, bound, lse, lse_bound

@@ -68,3 +68,193 @@ def test_against_64_bits(case, workspace):
     most = check(q, cache, C.starts(rows), causal, what="max_rows", workspace=workspace,
                  max_rows=max(rows))
     assert bool(torch.isfinite(most).all())
+
+
+@pytest.mark.parametrize("codes", ["i8", "e4m3"])
+@pytest.mark.parametrize("case", [
+    # enough rows that they share their tiles, in one share of the keys and in several
+    ([300, 270], [700, 271], 64, 8, 64, 16, True, "bf16"),
+    ([260, 1, 200], [300, 900, 1300], 32, 8, 128, 64, True, "bf16"),
+    ([129, 400], [2000, 400], 16, 4, 80, 32, True, "f16"),
+    ([513], [4200], 8, 4, 128, 128, True, "f16"),
+    ([200, 333], [1500, 40], 16, 8, 64, 16, True, "f32"),
+    ([300, 300], [290, 0], 32, 16, 96, 16, False, "bf16"),
+    ([140] * 3, [1100, 640, 576], 24, 3, 112, 256, True, "f32"),
+    ([40] * 9, [1000 + 31 * i for i in range(9)], 40, 10, 48, 32, True, "bf16"),
+], ids=str)
+def test_many_rows_against_64_bits(case, codes):
+    rows, lengths, hq, hk, d, block, causal, dtype = case
+    cache = C.Cache(len(rows), lengths, block, hk, d, codes, seed=3)
+    q = queries(sum(rows), hq, d, dtype, seed=4)
+    first = check(q, cache, C.starts(rows), causal, what=str(case), max_rows=max(rows))
+    again = check(q, cache, C.starts(rows), causal, what="alone", max_rows=max(rows),
+                  workspace=False)
+    third = L.cache_attention(q, *cache.operands(), C.starts(rows), cache.lengths, cache.table,
+                              causal=causal, max_rows=max(rows))
+    torch.cuda.synchronize()
+    assert torch.equal(first, third)
+    assert bool(torch.isfinite(again).all())
+
+
+SHAPES = [([1, 1, 1], [70, 1500, 2300], "bf16"), ([200, 300, 1], [700, 900, 2300], "bf16"),
+          ([200, 300, 1], [700, 900, 2300], "f16"), ([3, 150, 2], [70, 600, 1100], "f32")]
+
+
+@pytest.mark.parametrize("rows,lengths,dtype", SHAPES, ids=str)
+@pytest.mark.parametrize("codes", ["i8", "e4m3"])
+def test_scales_that_are_no_powers_of_two(rows, lengths, dtype, codes):
+    cache = C.Cache(len(rows), lengths, 16, 8, 64, codes, seed=5)
+    g = torch.Generator().manual_seed(6)
+    for s in (cache.ks, cache.vs):
+        s.mul_((0.5 + torch.rand(s.shape, generator=g)).cuda())
+    check(queries(sum(rows), 32, 64, dtype), cache, C.starts(rows), True, what="scales")
+
+
+@pytest.mark.parametrize("rows,lengths,dtype", SHAPES, ids=str)
+def test_blocks_that_are_not_there(rows, lengths, dtype):
+    """A window that has moved on, and holes; an entry without any block."""
+    cache = C.Cache(len(rows), lengths, 32, 8, 128, "e4m3", seed=7)
+    cache.table[1, :9] = -1
+    cache.table[2, 3::2] = 1 << 30
+    cache.table[0] = -7
+    out = check(queries(sum(rows), 16, 128, dtype), cache, C.starts(rows), True, what="holes")
+    assert bool((out[:rows[0]] == 0).all())
+
+
+@pytest.mark.parametrize("rows,lengths,dtype", SHAPES, ids=str)
+@pytest.mark.parametrize("block", [16, 128])
+def test_what_lies_past_the_length_is_not_read(rows, lengths, dtype, block):
+    """NaN codes and scales in blocks of nobody, and NaN codes behind the last token."""
+    cache = C.Cache(len(rows), lengths, block, 8, 64, "e4m3", seed=8, width=200)
+    q = queries(sum(rows), 8, 64, dtype)
+    want = check(q, cache, C.starts(rows), True, what="clean")
+    used = torch.zeros(len(cache.k), dtype=torch.bool)
+    for b, n in enumerate(lengths):
+        at = cache.table[b].cpu().long()
+        used[at[:-(-n // block)]] = True
+        for x in (cache.k, cache.v):
+            x.view(torch.uint8)[int(at[n // block]), n % block:] = 0x7f
+    for x, s in ((cache.k, cache.ks), (cache.v, cache.vs)):
+        x.view(torch.uint8)[~used.cuda()] = 0x7f
+        s[~used.cuda()] = math.nan
+    got = L.cache_attention(q, *cache.operands(), C.starts(rows), cache.lengths, cache.table)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1.1])
+@pytest.mark.parametrize("rows", [[1, 2], [250, 200]], ids=str)
+def test_scales(scale, rows):
+    cache = C.Cache(2, [300, 777], 16, 8, 64, "i8", seed=9)
+    check(queries(sum(rows), 16, 64, "bf16"), cache, C.starts(rows), True, scale=scale,
+          what=f"scale {scale}")
+
+
+def test_lengths_and_starts_out_of_range_are_clamped():
+    cache = C.Cache(3, [40, 40, 40], 16, 2, 64, "i8")
+    cache.lengths = torch.tensor([-5, 1 << 30, 30]).int().cuda()
+    starts = torch.tensor([-3, 2, 4, 900]).int().cuda()
+    check(queries(7, 4, 64, "bf16"), cache, starts, True, what="clamped")
+
+
+def test_rows_of_no_entry_and_past_max_rows_are_left():
+    cache = C.Cache(2, [40, 700], 16, 2, 64, "e4m3")
+    q = queries(60, 4, 64, "bf16")
+    out = torch.full_like(q, 3.0)
+    starts = torch.tensor([2, 4, 50]).int().cuda()
+    check(q, cache, starts, True, what="gaps", out=out)
+    assert bool((out[:2] == 3.0).all()) and bool((out[50:] == 3.0).all())
+    want, out = out.clone(), torch.full_like(q, 3.0)
+    L.cache_attention(q, *cache.operands(), starts, cache.lengths, cache.table, max_rows=10, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out[2:14], want[2:14]) and bool((out[14:] == 3.0).all())
+
+
+@pytest.mark.parametrize("rows", [[1, 1], [1, 300]], ids=str)
+def test_strides(rows):
+    """Queries from a fused projection, a strided output, keys and values of a block side by side."""
+    cache = C.Cache(2, [333, 900], 32, 4, 64, "i8", seed=11)
+    both = torch.empty(len(cache.k), 2, 32, 4, 64, dtype=torch.int8, device="cuda")
+    both[:, 0], both[:, 1] = cache.k, cache.v
+    cache.k, cache.v = both[:, 0], both[:, 1]
+    T = sum(rows)
+    fused = queries(T, 16, 64, "bf16")
+    out = torch.full((T, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    check(fused[:, 3:11], cache, C.starts(rows), True, what="strided", out=out[..., :64])
+    assert bool((out[..., 64:] == 5.0).all())
+
+
+def test_offsets_past_32_bits():
+    """Blocks more than 2^32 bytes apart."""
+    far = (1 << 32) + 4096
+    room = torch.zeros(2 * far + 65536, dtype=torch.int8, device="cuda")
+    cache = C.Cache(1, [40], 16, 2, 64, "i8", spare=0)
+    for rows in ([1], [70]):
+        k = room.as_strided((3, 16, 2, 64), (far, 64, 1024, 1))
+        k.copy_(cache.k)
+        cache.k, v = k, cache.v
+        check(queries(rows[0], 4, 64, "bf16"), cache, C.starts(rows), True, what="far")
+        cache.v = k
+        check(queries(rows[0], 4, 64, "bf16"), cache, C.starts(rows), True, what="far values")
+        cache.v = v
+
+
+@pytest.mark.parametrize("lengths", [[900, 1500, 2000], [100, 400, 5]], ids=str)
+def test_graph_replays(lengths):
+    """Lengths, tables and starts change between replays; a plan with partial results and one
+    without."""
+    cache = C.Cache(3, [2048] * 3, 16, 4, 128, "e4m3", seed=12)
+    q, starts = queries(300, 16, 128, "bf16"), C.starts([1, 298, 1])
+    cache.lengths = torch.tensor(lengths).int().cuda()
+    call = lambda: L.cache_attention(q, *cache.operands(), starts, cache.lengths, cache.table)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for i in range(4):
+        q.copy_(queries(300, 16, 128, "bf16", seed=20 + i))
+        starts.copy_(C.starts([[1, 298, 1], [298, 1, 1], [100, 100, 100], [0, 290, 10]][i]))
+        cache.lengths.copy_((cache.lengths + 7 * i) % 2048)
+        cache.table.copy_(cache.table[:, torch.randperm(cache.width)])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, call()), i
+        torch.cuda.synchronize()
+
+
+def test_scores_that_climb_and_fall():
+    """Scales of keys from 2^-20 to 2^6 from block to block: the maximum moves far."""
+    for rows in ([1, 1], [260, 200]):
+        for ramp in (range(-20, 7), range(6, -21, -1)):
+            cache = C.Cache(2, [27 * 16, 300], 16, 8, 64, "i8", seed=13)
+            for b in range(2):
+                n = min(27, cache.width)
+                cache.ks[cache.table[b, :n].long()] = torch.tensor(
+                    [2.0 ** (e - 4) for e in ramp][:n], device="cuda")[:, None]
+            check(queries(sum(rows), 8, 64, "bf16"), cache, C.starts(rows), True, what=str(ramp))
+
+
+def test_more_entries_than_a_wave_has_lanes():
+    n = 150
+    cache = C.Cache(n, [(37 * i) % 1300 for i in range(n)], 16, 2, 64, "i8", seed=14)
+    rows = [[1, 0, 2, 1, 40][i % 5] for i in range(n)]
+    check(queries(sum(rows), 4, 64, "bf16"), cache, C.starts(rows), True, what="entries")
+    one = C.starts([1] * n)
+    check(queries(n, 4, 64, "bf16"), cache, one, True, what="single tokens", max_rows=1)
+
+
+def test_nothing_to_do():
+    cache = C.Cache(2, [5, 5], 16, 2, 64, "i8")
+    q = queries(0, 4, 64, "bf16")
+    assert L.cache_attention(q, *cache.operands(), C.starts([0, 0]), cache.lengths,
+                             cache.table).shape == (0, 4, 64)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    out = torch.full((3, 4, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+    L.cache_attention(queries(3, 4, 64, "bf16"), *cache.operands(), C.starts([]), none,
+                      torch.zeros(0, 4, dtype=torch.int32, device="cuda"), out=out)
+    # a table of no blocks: entries without tokens
+    L.cache_attention(queries(3, 4, 64, "bf16"), *cache.operands(), C.starts([1, 1]), cache.lengths,
+                      cache.table[:, :0].contiguous(), out=out)
+    torch.cuda.synchronize()
+    assert bool((out[:2] == 0).all()) and bool((out[2] == 2.0).all())

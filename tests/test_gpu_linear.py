@@ -42,3 +42,83 @@ def test_against_64_bits(T, K, N, dtype, workspace):
     act = ACTS[(T + K + N) % 5]
     check(x, w, b, act, r, workspace=workspace)
     check(x, w, None, ACTS[(T + K + N + 2) % 5], None, workspace=workspace)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", C.TYPES)
+def test_activations(act, dtype):
+    """Every activation over small and large sums, in tiles of each size and in runs."""
+    for T, K, N in ((3, 520, 700), (300, 136, 530), (2500, 64, 3900)):
+        x, w, b, r = make(T, K, N, dtype, seed=2)
+        w = w * 4
+        check(x, w, b, act, r, what=f"{act} {T}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_large_tiles(dtype):
+    check(*(lambda x, w, b, r: (x, w, b, "gelu", r))(*make(4200, 200, 4300, dtype)), what="256 x 256")
+    check(*(lambda x, w, b, r: (x, w, b, "silu", r))(*make(4097, 1032, 4101, dtype)), what="odd")
+
+
+def test_strides_and_in_place():
+    x, w, b, r = make(70, 264, 130, "bf16")
+    wide = torch.zeros(70, 700, dtype=torch.bfloat16, device="cuda")   # rows of 1400 bytes
+    with pytest.raises(L.LibconvError, match="MISALIGNED"):
+        L.linear(wide[:, 8:272], w, b)
+    wide = torch.zeros(70, 704, dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:272] = x
+    wide[:, 400:530] = r
+    want = check(x, w, b, "gelu", r)
+    # rows of one buffer: inputs, residual and outputs (one byte off 16-byte boundaries)
+    check(wide[:, 8:272], w, b, "gelu", wide[:, 400:530], out=wide[:, 531:661])
+    assert torch.equal(wide[:, 531:661], want)
+    before = wide.clone()
+    y = wide[:, 400:530]
+    L.linear(wide[:, 8:272], w, b, act="gelu", residual=y, out=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(wide[:, 530:], before[:, 530:])
+    assert torch.equal(wide[:, :400], before[:, :400])
+    one = r[:1].expand(70, 130)     # one residual for all
+    assert torch.equal(check(x, w, b, "none", one), L.linear(x, w, b, residual=one.contiguous()))
+    # a single row twice over
+    same = x[:1].expand(70, 264)
+    assert torch.equal(check(same, w, b, "none", r)[3:4],
+                       L.linear(same, w, b, residual=r)[3:4])
+
+
+@pytest.mark.parametrize("T", [5, 400])
+@pytest.mark.parametrize("act", ACTS)
+def test_infinities_and_nan_stay_in_their_rows(T, act):
+    x, w, b, r = make(T, 128, 300, "bf16")
+    want = check(x, w, b, act, r)
+    x[1], x[3, 5], r[4, 7] = float("inf"), float("nan"), float("-inf")
+    got = L.linear(x, w, b, act=act, residual=r)
+    torch.cuda.synchronize()
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[[1, 3]] = False
+    keep = keep.cuda()
+    got[4, 7], want[4, 7] = 0, 0
+    assert torch.equal(got[keep], want[keep])
+    if act != "relu":   # which gives 0 for NaN
+        assert bool(torch.isnan(got[3]).all())
+
+
+def test_graph_replays():
+    for T in (8, 300):
+        x, w, b, r = make(T, 1024, 640, "bf16")
+        L.linear(x, w, b, act="silu", residual=r)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = L.linear(x, w, b, act="silu", residual=r)
+        for i in range(4):
+            x.copy_(make(T, 1024, 640, "bf16", seed=40 + i)[0])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, L.linear(x, w, b, act="silu", residual=r)), i
+            torch.cuda.synchronize()
+
+
+def test_no_rows():
+    x, w, b, _ = make(1, 64, 32, "f32")
+    assert L.linear(x[:0], w, b).shape == (0, 32)
