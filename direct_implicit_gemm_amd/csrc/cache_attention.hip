@@ -1038,7 +1038,8 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
 }
 
 // The unit of number x of the sets of `size` rows of the entries with more than a
-// few (with `all`, of any), and of a key head.
+// few (with `all`, of any), and of a key head.  a.sets: of every entry, some of them
+// empty; 0: as many as each has, side by side.
 struct Unit {
   Entry e;
   int b, hk, set, keys;   // keys: those that its last row sees
@@ -1047,15 +1048,23 @@ __device__ __forceinline__ bool unit_of(const CacheAttnArgs& a, int number, int 
                                         Unit* u) {
   const int x = number / a.c.Hk;
   u->hk = number - x * a.c.Hk;
-  auto weight = [=](const Entry& e) { return all || !few(e) ? (e.rows + size - 1) / size : 0; };
-  Entries<decltype(weight)> entries(a, weight);
-  const auto f = entries.find(x);
-  if (f.b >= a.c.B) return false;
-  u->b = f.b;
-  u->e = f.e;
-  u->set = f.weight - 1 - (x - (int)f.first);   // causal: the longest first
-  const int end = (u->set + 1) * size, last = (end < f.e.rows ? end : f.e.rows) - 1;
-  const int keys = a.causal ? f.e.len - f.e.n + last / a.G + 1 : f.e.len;
+  if (a.sets > 0) {
+    u->b = x / a.sets;
+    if (u->b >= a.c.B) return false;
+    u->e = entry_of(a, u->b);
+    u->set = a.sets - 1 - (x - u->b * a.sets);   // causal: the longest first
+    if ((!all && few(u->e)) || u->set * size >= u->e.rows) return false;
+  } else {
+    auto weight = [=](const Entry& e) { return all || !few(e) ? (e.rows + size - 1) / size : 0; };
+    Entries<decltype(weight)> entries(a, weight);
+    const auto f = entries.find(x);
+    if (f.b >= a.c.B) return false;
+    u->b = f.b;
+    u->e = f.e;
+    u->set = f.weight - 1 - (x - (int)f.first);
+  }
+  const int end = (u->set + 1) * size, last = (end < u->e.rows ? end : u->e.rows) - 1;
+  const int keys = a.causal ? u->e.len - u->e.n + last / a.G + 1 : u->e.len;
   u->keys = keys > 0 ? keys : 0;
   return true;
 }
@@ -1166,10 +1175,13 @@ __global__ __launch_bounds__(kThreads) void many_join_kernel(const CacheAttnArgs
   }
 }
 
-// Sets of `size` rows of a key head that a batch may have.
+// Sets of `size` rows of a key head that a batch may have: of each entry, or side by
+// side, which takes a look at all entries' rows (64 at a time).
+long long sets_of_each(const CacheAttnArgs& a, long long size) {
+  return ((long long)a.max_rows * a.G + size - 1) / size;
+}
 long long row_sets(const CacheAttnArgs& a, long long size) {
-  const long long each = ((long long)a.max_rows * a.G + size - 1) / size * a.c.B;
-  const long long all = (long long)a.T * a.G / size + a.c.B;
+  const long long each = sets_of_each(a, size) * a.c.B, all = (long long)a.T * a.G / size + a.c.B;
   return each < all ? each : all;
 }
 
@@ -1190,7 +1202,8 @@ void launch(const CacheAttnArgs& a, hipStream_t stream) {
                          threads, 0, stream, a);
   }
   if (most <= kFewRows) return;
-  const unsigned units = (unsigned)(row_sets(a, a.set) * a.c.Hk);
+  const unsigned units = (unsigned)((a.sets > 0 ? (long long)a.sets * a.c.B : row_sets(a, a.set)) *
+                                    a.c.Hk);
   if (a.set == 32)
     hipLaunchKernelGGL((some_kernel<DT, CF, DP>), dim3(units), dim3(kFewThreads), 0, stream, a, all);
   else
@@ -1217,6 +1230,7 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   a->few_groups = 0;
   a->splits = 1;
   a->set = 32;
+  a->sets = 0;
   if (a->T == 0 || a->c.B == 0) return 0;
   const long long keys = (long long)a->c.width << a->c.log_block;
   const bool many = (long long)a->max_rows * a->G > kFewRows;
@@ -1230,6 +1244,10 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
       a->set = kManyRows;
       a->splits = (int)s;
     }
+    // (empty sets end at once; many entries take long to look through)
+    const long long each = sets_of_each(*a, a->set) * a->c.B;
+    if (each <= 2 * row_sets(*a, a->set) || (a->c.B > 512 && each * a->c.Hk < (1 << 22)))
+      a->sets = (int)sets_of_each(*a, a->set);
   }
   if (!allowed) return 0;
   if (a->G <= kFewRows && keys > 1024 && a->c.B <= 1024) a->few_groups = 8 / kFewWaves * cus;

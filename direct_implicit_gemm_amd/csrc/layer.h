@@ -112,6 +112,7 @@ struct CacheAttnArgs {
   int few_groups;           // workgroups that share the keys of entries of few rows;
                             // 0: one to an entry and key head
   int set;                  // rows of a key head of entries of more rows to a workgroup
+  int sets;                 // of each entry; 0: side by side
   int splits;               // and shares of their keys
   // partial results of the former [2 few_groups][32] and of the latter [splits][T]
   // [q heads], normed: D outputs and the log2 of their sum, each

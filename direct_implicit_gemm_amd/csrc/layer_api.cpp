@@ -69,6 +69,13 @@ View view(const void* p, long long n0, long long s0, long long n1, long long s1,
   return v;
 }
 
+// Whether offsets into it fit 62 bits.
+bool in_reach(const View& v) {
+  double sum = (double)v.dense;
+  for (int i = 0; i < 3; ++i) sum += (double)v.n[i] * (double)v.s[i];
+  return sum < 4.6e18;
+}
+
 bool aligned16(const View& v) {
   return v.empty() || (((uintptr_t)v.p | (uintptr_t)(v.s[0] | v.s[1] | v.s[2])) & 15) == 0;
 }
@@ -185,7 +192,9 @@ libconv_status cache_operands(CacheView* c, CacheOperands* o, const void* k_cach
     o->codes[i] = view(codes[i], blocks, strides[3 * i], block_size, strides[3 * i + 1], k_heads,
                        strides[3 * i + 2], head_dim, 1);
     if (!aligned16(o->codes[i]) || ((uintptr_t)scale[i] & 3) != 0) return LIBCONV_ERR_MISALIGNED;
-    if (o->codes[i].s[1] > kMaxRowBytes) return LIBCONV_ERR_TOO_LARGE;
+    // (tokens over one another could not end where the entry does)
+    if (o->codes[i].s[1] < head_dim) return LIBCONV_ERR_BAD_SHAPE;
+    if (o->codes[i].s[1] > kMaxRowBytes || !in_reach(o->codes[i])) return LIBCONV_ERR_TOO_LARGE;
     c->codes[i] = const_cast<char*>(o->codes[i].p);
     c->scale[i] = const_cast<float*>(scale[i]);
     c->block[i] = o->codes[i].s[0];
@@ -513,6 +522,7 @@ libconv_status libconv_kv_cache_write(const void* k, const void* v, void* k_cach
   for (int i = 0; i < 2; ++i) {
     vx[i] = view(x[i], 1, 0, T, strides[2 * i], k_heads, strides[2 * i + 1], head_dim, eb);
     if (!aligned16(vx[i])) return LIBCONV_ERR_MISALIGNED;
+    if (!in_reach(vx[i])) return LIBCONV_ERR_TOO_LARGE;
     a.x[i] = const_cast<char*>(vx[i].p);
     a.row[i] = vx[i].s[1];
     a.head[i] = vx[i].s[2];
@@ -572,6 +582,7 @@ libconv_status libconv_kv_cache_read(const void* k_cache, const void* v_cache,
     vx[i] = view(x[i], B, strides[6 + 3 * i], S, strides[7 + 3 * i], k_heads, strides[8 + 3 * i],
                  head_dim, eb);
     if (!aligned16(vx[i])) return LIBCONV_ERR_MISALIGNED;
+    if (!in_reach(vx[i])) return LIBCONV_ERR_TOO_LARGE;
     a.x[i] = static_cast<char*>(x[i]);
     a.entry[i] = vx[i].s[0];
     a.row[i] = vx[i].s[1];
@@ -642,6 +653,7 @@ libconv_status libconv_cache_attention(const void* q, const void* k_cache, const
   if (!aligned16(vq) || !aligned16(vo) || (((uintptr_t)row_starts | (uintptr_t)lse) & 3) != 0 ||
       ((uintptr_t)workspace & 255) != 0)
     return LIBCONV_ERR_MISALIGNED;
+  if (!in_reach(vq) || !in_reach(vo)) return LIBCONV_ERR_TOO_LARGE;
   const long long lse_bytes = 4LL * T * q_heads;
   if (!vo.distinct() || meet(vo, vq) || meet(vo, o.codes[0]) || meet(vo, o.codes[1]) ||
       ranges_meet(out, vo.span(), lse, lse_bytes) ||
@@ -708,7 +720,7 @@ libconv_status libconv_linear(const void* x, const void* w, const void* bias,
   const View vx = view(x, 1, 0, T, x_stride, 1, 0, K, eb);
   const View vr = view(residual, 1, 0, T, residual_stride, 1, 0, N, eb);
   const View vy = view(y, 1, 0, T, y_stride, 1, 0, N, eb);
-  if (vx.s[1] > kMaxRowBytes) return LIBCONV_ERR_TOO_LARGE;
+  if (vx.s[1] > kMaxRowBytes || !in_reach(vr) || !in_reach(vy)) return LIBCONV_ERR_TOO_LARGE;
   if (!aligned16(vx) || ((uintptr_t)w & 15) != 0 || ((uintptr_t)workspace & 255) != 0 ||
       (((uintptr_t)y | (uintptr_t)bias | (uintptr_t)residual) & (eb - 1)) != 0)
     return LIBCONV_ERR_MISALIGNED;

@@ -72,9 +72,12 @@ template <int DT> struct Outputs {
   float bias[E];
 
   __device__ __forceinline__ Outputs(const LinearArgs& a, int first) : n(first) {
-    whole = n + E <= a.N && ((reinterpret_cast<uintptr_t>(a.y) + n * EB | a.y_row) & 15) == 0;
+    const unsigned at = (unsigned)n * EB;   // (modulo 16)
+    whole = n + E <= a.N && (((unsigned)reinterpret_cast<uintptr_t>(a.y) + at) & 15) == 0 &&
+            (a.y_row & 15) == 0;
     whole_r = a.residual && n + E <= a.N &&
-              ((reinterpret_cast<uintptr_t>(a.residual) + n * EB | a.r_row) & 15) == 0;
+              (((unsigned)reinterpret_cast<uintptr_t>(a.residual) + at) & 15) == 0 &&
+              (a.r_row & 15) == 0;
 #pragma unroll
     for (int j = 0; j < E; ++j)
       bias[j] = a.bias && n + j < a.N ? load1<DT>(a.bias, n + j) : 0.0f;

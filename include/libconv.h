@@ -695,7 +695,7 @@ long long libconv_lora_workspace(int T, int K, int N, int rank, int n_adapters, 
  *     block one after another reads best), and
  * k_scale, v_scale  [blocks][k_heads] fp32, dense: a code c stands for c * scale.
  * block_size: 16, 32, 64, 128 or 256 tokens.  head_dim: a multiple of 16 up to
- * 128 (else LIBCONV_ERR_UNSUPPORTED).
+ * 128 (else LIBCONV_ERR_UNSUPPORTED).  Tokens are at least head_dim apart.
  *
  * B entries (requests), whose rows lie one after another in T rows:
  * row_starts   [B + 1] ints, ascending: entry b has rows row_starts[b] <= t <

@@ -258,3 +258,15 @@ def test_nothing_to_do():
                       cache.table[:, :0].contiguous(), out=out)
     torch.cuda.synchronize()
     assert bool((out[:2] == 0).all()) and bool((out[2] == 2.0).all())
+
+
+@pytest.mark.parametrize("B", [3, 70, 600])
+def test_many_entries_of_many_rows(B):
+    """Sets of rows side by side and entry by entry, one with most of the rows among them."""
+    rows = [[40, 0, 33, 1][i % 4] for i in range(B)]
+    rows[B // 2] = 900
+    cache = C.Cache(B, [n + 11 * (i % 20) for i, n in enumerate(rows)], 16, 2, 16, "i8", seed=15)
+    q = queries(sum(rows), 4, 16, "bf16")
+    first = check(q, cache, C.starts(rows), True, what=str(B))
+    again = check(q, cache, C.starts(rows), True, what="max_rows", max_rows=900)
+    assert torch.equal(first, again)

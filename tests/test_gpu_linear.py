@@ -122,3 +122,21 @@ def test_graph_replays():
 def test_no_rows():
     x, w, b, _ = make(1, 64, 32, "f32")
     assert L.linear(x[:0], w, b).shape == (0, 32)
+
+
+def test_linear_of_many_outputs():
+    g = torch.Generator().manual_seed(2)
+    N, K = (1 << 27) + 20, 8
+    print(f"[gpu] linear 1 row of {N} outputs", flush=True)
+    x, w = torch.randn(1, K, generator=g).bfloat16().cuda(), torch.randn(N, K, dtype=torch.bfloat16,
+                                                                         device="cuda")
+    r = torch.randn(1, N, dtype=torch.bfloat16, device="cuda")
+    y = L.linear(x, w, act="silu", residual=r)
+    torch.cuda.synchronize()
+    at = torch.cat([torch.arange(300), torch.randint(300, N - 300, (3000,), generator=g),
+                    torch.arange(N - 300, N)]).cuda()
+    want, bound = C.linear(x, w[at], None, "silu", r[:, at])
+    C.assert_within(y[:, at], want, bound, "outputs")
+    assert bool(torch.isfinite(y[:, ::97]).all())
+    del x, w, y, r
+    torch.cuda.empty_cache()
