@@ -30,16 +30,18 @@ template <int DT> struct Terms {
   static constexpr int KT = DT == DT_F16 ? DT_F16 : DT_BF16;   // type of the first product
 };
 
-// x as N bfloat16 terms: each the rest of the ones before, rounded.
-template <int N> __device__ __forceinline__ void split2(float a, float b, uint32_t* w) {
+// Two numbers as N bfloat16 terms: each the rest of the ones before, rounded.
+// Infinite: they may be infinities, which then have no rest.
+template <int N, bool Infinite = false>
+__device__ __forceinline__ void split2(float a, float b, uint32_t* w) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     w[i] = pack2<DT_BF16>(a, b);
     if (i + 1 < N) {
-      const float ha = Elem<DT_BF16>::bits_to_f32(w[i] & 0xffffu);
-      const float hb = Elem<DT_BF16>::bits_to_f32(w[i] >> 16);
-      a = __builtin_isfinite(ha) ? a - ha : 0.0f;
-      b = __builtin_isfinite(hb) ? b - hb : 0.0f;
+      const float ha = __builtin_bit_cast(float, w[i] << 16);
+      const float hb = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+      a = !Infinite || __builtin_isfinite(ha) ? a - ha : 0.0f;
+      b = !Infinite || __builtin_isfinite(hb) ? b - hb : 0.0f;
     }
   }
 }
@@ -231,7 +233,7 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t w[NQ];
-        split2<NQ>(f[2 * j], f[2 * j + 1], w);
+        split2<NQ, true>(f[2 * j], f[2 * j + 1], w);
 #pragma unroll
         for (int i = 0; i < NQ; ++i) qf[i][s][j] = w[i];
       }
@@ -503,126 +505,13 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
   lds_barrier();   // the joined results are read
 }
 
-// Entries of few rows: the tiles of all their key heads in a row, entry after
-// entry, each workgroup a run of them of one length (so that entries of very
-// different lengths fill the GPU to the end).  A head whose tiles lie in one run
-// is written at once, of others the runs' parts are joined (few_join_kernel).
-template <int DT, int CF, int DP>
-__global__ __launch_bounds__(kFewThreads, 2) void few_kernel(const CacheAttnArgs a) {
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
-  Job job;
-  job.row_tile = 0;
-  if (a.few_groups == 0) {
-    job.b = blockIdx.x / a.c.Hk;
-    job.hk = blockIdx.x - job.b * a.c.Hk;
-    job.e = entry_of(a, job.b);
-    job.t0 = 0;
-    job.t1 = few_tiles(job.e);
-    job.slot = -1;
-    if (job.t1 > 0) attend_few<DT, CF, DP>(a, job, lds);
-    return;
-  }
-  auto weight = [](const Entry& e) { return few_tiles(e); };
-  Entries<decltype(weight)> entries(a, weight);
-  const int Hk = a.c.Hk;
-  const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
-  long long x = blockIdx.x * per;
-  const long long begin = x, end = x + per < total ? x + per : total;
-  while (x < end) {
-    const auto f = entries.find(x / Hk);
-    job.b = f.b;
-    job.e = f.e;
-    // the entry's heads one after another
-    while (x < end && x < (f.first + f.weight) * Hk) {
-      const int in = (int)(x - f.first * Hk);
-      job.hk = in / f.weight;
-      job.t0 = in - job.hk * f.weight;
-      job.t1 = f.weight - job.t0 < end - x ? f.weight : job.t0 + (int)(end - x);
-      job.slot = job.t0 == 0 && job.t1 == f.weight ? -1 : 2LL * blockIdx.x + (x == begin ? 0 : 1);
-      attend_few<DT, CF, DP>(a, job, lds);
-      x += job.t1 - job.t0;
-    }
-  }
-}
-
-// Joins the parts of row blockIdx.y of a key head of an entry:
-// out = sum_s 2^(lse_s - lse) o_s.  LPR lanes a part, 4 components a lane; the
-// workgroup's sets of lanes take parts in turn and meet in LDS, in order.
-template <int DT, int LPR>
-__global__ __launch_bounds__(kThreads) void few_join_kernel(const CacheAttnArgs a) {
-  constexpr int SETS = kThreads / LPR;
-  __shared__ float tops[SETS], sums[SETS];
-  __shared__ float4_t outs[SETS][LPR];
-  const int Hk = a.c.Hk, D = a.c.D;
-  const int b = blockIdx.x / Hk, hk = blockIdx.x - b * Hk, row = blockIdx.y;
-  const Entry e = entry_of(a, b);
-  const int tiles = few_tiles(e);
-  if (tiles < 2 || row >= e.rows) return;
-  auto weight = [](const Entry& x) { return few_tiles(x); };
-  Entries<decltype(weight)> entries(a, weight);
-  const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
-  const long long u0 = entries.begin_of(b) * Hk + (long long)hk * tiles, u1 = u0 + tiles;
-  const int g0 = (int)(u0 / per), g1 = (int)((u1 - 1) / per);
-  if (g0 == g1) return;
-  const int set = threadIdx.x / LPR, lane = threadIdx.x % LPR;
-  const bool live = 4 * lane < D;
-  float m = kLowest, sum = 0.0f;
-  float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int g = g0 + set; g <= g1; g += SETS) {
-    // a run's first part is its slot 0
-    const long long slot =
-        (2LL * g + (g == g0 && u0 != g * per ? 1 : 0)) * kFewRows + row;
-    const float w = a.part_lse[slot];
-    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) v = *reinterpret_cast<const float4_t*>(a.part + slot * D + 4 * lane);
-    const float m_new = fmaxf(m, w), fall = __builtin_amdgcn_exp2f(m - m_new),
-                p = __builtin_amdgcn_exp2f(w - m_new);
-    m = m_new;
-    sum = fmaf(sum, fall, p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j] * fall);
-  }
-  if (lane == 0) {
-    tops[set] = m;
-    sums[set] = sum;
-  }
-  outs[set][lane] = o;
-  __syncthreads();
-  if (set > 0) return;
-  float m_all = m;
-#pragma unroll
-  for (int s = 1; s < SETS; ++s) m_all = fmaxf(m_all, tops[s]);
-  sum = 0.0f;
-  o = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int s = 0; s < SETS; ++s) {
-    const float p = __builtin_amdgcn_exp2f(tops[s] - m_all);
-    sum = fmaf(sums[s], p, sum);
-    const float4_t v = outs[s][lane];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j]);
-  }
-  const float inv = sum > 0.0f ? 1.0f / sum : sum;
-  const int qi = row / a.G, head = hk * a.G + row - qi * a.G;
-  const long long t = e.row0 + qi;
-  if (a.lse && lane == 0)
-    a.lse[t * (Hk * a.G) + head] =
-        sum == 0.0f ? kNegInf : (m_all + __builtin_amdgcn_logf(sum)) * kLn2;
-  if (!live) return;
-  char* op = a.out + t * a.o_r + head * a.o_h;
-  if constexpr (DT == DT_F32)
-    *reinterpret_cast<float4_t*>(op + 16 * lane) = o * inv;
-  else
-    *reinterpret_cast<u32x2_t*>(op + 8 * lane) =
-        u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
-}
-
 // Many rows: four waves of 32 rows share tiles of 64 keys, widened to 16 bits once
 // for all of them.  A wave reads the codes of 16 rows of keys and of values a tile
 // ahead into registers, and widens them into LDS a tile (keys: two) before they
 // are used.  A power of two is taken into the widened numbers, which hold the
 // product exactly.  `General`, where a block that the workgroup reads is not there
-// or has another scale: scores and probabilities are multiplied instead.
+// or has a scale for which they do not: scores and probabilities are multiplied
+// instead.
 constexpr int kManyRows = 128;
 template <int DP> struct Wide {
   static constexpr int RAW = DP <= 64 ? 64 : 128;   // bytes of a row of codes
@@ -638,71 +527,78 @@ template <int CPR> __device__ __forceinline__ int v_swizzle16(int row) {
   // (the lowest bit for the writes, of every second chunk of two or four rows at a time)
   return CPR == 16 ? (row & 3) << 2 | (row & 1) : ((row >> 1) & 1) * 5;
 }
-// Whether a scale is a power of two.
-__device__ __forceinline__ bool is_power(float s) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, s);
-  return (b & 0x807fffffu) == 0 && b - 0x00800000u < 0x7f000000u;
+// Whether the scale is a power of two and all its products with codes, which are
+// multiples of 2^-9 up to 448, are numbers of the 16-bit type (bfloat16: no denormal
+// ones, and far enough from its largest for sums of them).
+template <int DT> __device__ __forceinline__ bool folds(float s) {
+  const bool power = (__builtin_bit_cast(uint32_t, s) & 0x007fffffu) == 0;
+  return power && (DT == DT_F16 ? s >= 0x1p-15f && s <= 0x1p7f : s >= 0x1p-117f && s <= 0x1p100f);
 }
 
-template <int DT, int CF, int DP, int NR, bool General>
+struct Keys {
+  static constexpr bool value = true;
+};
+struct Values {
+  static constexpr bool value = false;
+};
+
+template <int DT, int CF, int DP, bool General>
 __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& job,
                                             unsigned char* lds) {
   using Z = Wide<DP>;
   constexpr int EB = Elem<DT>::bytes, RAW = Z::RAW, RB = Z::RB, CPR = Z::CPR, BN = Z::BN;
   constexpr int KS = DP / 16, DB = DP / 32, LOADS = Z::LOADS;
-  constexpr int NQ = Terms<DT>::Q, NP = Terms<DT>::P, KT = Terms<DT>::KT;
-  constexpr bool RestK = General || KT == DT_F16;   // (fp16 might not hold the product)
-  constexpr float SLACK = 8.0f;   // log2 of how far a maximum may fall behind
+  // fp16 probabilities meet fp16 values, as in attention.hip: multiplied by 2^LIFT, so
+  // that those down to 2^-36 of the largest count.  (General: values as codes in
+  // bfloat16 and probabilities times their scales, which may be past fp16's range.)
+  constexpr bool HALF = DT == DT_F16 && !General;
+  constexpr int NQ = Terms<DT>::Q, KT = Terms<DT>::KT;
+  constexpr int NP = HALF ? 1 : Terms<DT>::P, VT = HALF ? DT_F16 : DT_BF16;
+  constexpr float SLACK = HALF ? 4.0f : 8.0f;   // log2 of how far a maximum may fall behind
+  constexpr float LIFT = HALF ? 15.0f - SLACK : 0.0f;
   const CacheView& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, half = lane >> 5;
   const int D = c.D, hk = job.hk, len = job.e.len, t0 = job.t0, t1 = job.t1, n = t1 - t0;
   const int mask = (1 << c.log_block) - 1;
 
-  // this lane's queries, one of each of NR sets of 32 rows
-  bool row_ok[NR];
-  int qi[NR], head[NR], lim[NR], whole[NR];
-  u32x4_t qf[NR][NQ][KS];
+  // this lane's query
+  const int first = (job.row_tile * 4 + wave) * 32, local = first + l32;
+  const bool row_ok = local < job.e.rows;
+  const int row = row_ok ? local : 0, qi = row / a.G, head = hk * a.G + row - qi * a.G;
+  const int lim = a.causal ? len - job.e.n + qi + 1 : len;
+  // every row of the wave sees the keys below this
+  const int all = a.causal ? len - job.e.n + (first < job.e.rows ? first / a.G : 0) + 1 : len;
+  const int whole = __builtin_amdgcn_readfirstlane(all < 0 ? 0 : all & ~31);
+  const char* qp = a.q + (long long)(job.e.row0 + qi) * a.q_r + (long long)head * a.q_h;
+  u32x4_t qf[NQ][KS];
 #pragma unroll
-  for (int h = 0; h < NR; ++h) {
-    const int first = (job.row_tile * 4 + wave) * (32 * NR) + h * 32, local = first + l32;
-    row_ok[h] = local < job.e.rows;
-    const int row = row_ok[h] ? local : 0;
-    qi[h] = row / a.G;
-    head[h] = hk * a.G + row - qi[h] * a.G;
-    lim[h] = a.causal ? len - job.e.n + qi[h] + 1 : len;
-    // every row of the set sees the keys below this
-    const int all = a.causal ? len - job.e.n + (first < job.e.rows ? first / a.G : 0) + 1 : len;
-    whole[h] = __builtin_amdgcn_readfirstlane(all < 0 ? 0 : all & ~31);
-    const char* qp = a.q + (long long)(job.e.row0 + qi[h]) * a.q_r + (long long)head[h] * a.q_h;
+  for (int s = 0; s < KS; ++s) {
+    const int el = (2 * s + half) * 8;
+    u32x4_t raw[EB / 2];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int el = (2 * s + half) * 8;
-      u32x4_t raw[EB / 2];
-#pragma unroll
-      for (int i = 0; i < EB / 2; ++i) {
-        raw[i] = u32x4_t{0, 0, 0, 0};
-        if (row_ok[h] && el < D)
-          raw[i] = *reinterpret_cast<const u32x4_t*>(qp + el * EB + i * 16);
-        if (a.flip) {
-          const uint32_t sign = EB == 4 ? 0x80000000u : 0x80008000u;
-          raw[i] = a.flip < 0 ? raw[i] ^ u32x4_t{sign, sign, sign, sign} : u32x4_t{0, 0, 0, 0};
-        }
+    for (int i = 0; i < EB / 2; ++i) {
+      raw[i] = u32x4_t{0, 0, 0, 0};
+      if (row_ok && el < D)
+        raw[i] = *reinterpret_cast<const u32x4_t*>(qp + el * EB + i * 16);
+      if (a.flip) {
+        const uint32_t sign = EB == 4 ? 0x80000000u : 0x80008000u;
+        raw[i] = a.flip < 0 ? raw[i] ^ u32x4_t{sign, sign, sign, sign} : u32x4_t{0, 0, 0, 0};
       }
-      if constexpr (DT == DT_F32) {
-        float f[8];
-        unpack<DT_F32>(raw[0], f);
-        unpack<DT_F32>(raw[1], f + 4);
+    }
+    if constexpr (DT == DT_F32) {
+      float f[8];
+      unpack<DT_F32>(raw[0], f);
+      unpack<DT_F32>(raw[1], f + 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t w[NQ];
-          split2<NQ>(f[2 * j], f[2 * j + 1], w);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[NQ];
+        split2<NQ, true>(f[2 * j], f[2 * j + 1], w);
 #pragma unroll
-          for (int i = 0; i < NQ; ++i) qf[h][i][s][j] = w[i];
-        }
-      } else {
-        qf[h][0][s] = raw[0];
+        for (int i = 0; i < NQ; ++i) qf[i][s][j] = w[i];
       }
+    } else {
+      qf[0][s] = raw[0];
     }
   }
 
@@ -786,7 +682,8 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
                         (kv == 0 ? k_swizzle16<CPR>(row) : v_swizzle16<CPR>(row))) * 16;
       }
   // Widens tile i's; odd: i & 1, a constant where it is called.
-  auto widen = [&](const Part& x, int i, int odd, int kv) __attribute__((always_inline)) {
+  auto widen = [&](const Part& x, int i, int odd, auto keys) __attribute__((always_inline)) {
+    constexpr int kv = decltype(keys)::value ? 0 : 1;
     const float scale = scale_of(i, kv);
 #pragma unroll
     for (int j = 0; j < LOADS; ++j)
@@ -794,103 +691,82 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
       for (int e = 0; e < 2; ++e) {
         const uint32_t w0 = x.codes[j][2 * e], w1 = x.codes[j][2 * e + 1];
         *reinterpret_cast<u32x4_t*>(lds + to[kv][j][e] + odd * Z::TILE) =
-            kv == 0 && KT == DT_F16 ? code_values16<CF, DT_F16>(w0, w1)
-            : General               ? code_values16<CF, DT_BF16>(w0, w1)
-                                    : code_values16<CF>(w0, w1, scale);
+            General ? code_values16<CF, (kv == 0 ? KT : VT)>(w0, w1)
+                    : code_values16<CF, KT>(w0, w1, scale);
       }
   };
 
-  float16_t acc[NR][DB];
-  float m[NR], l[NR], fall[NR];
+  float16_t acc[DB];
+  float m = kLowest, l = 0.0f, fall = 1.0f;
 #pragma unroll
-  for (int h = 0; h < NR; ++h) {
-    m[h] = kLowest;
-    l[h] = 0.0f;
-    fall[h] = 1.0f;
-#pragma unroll
-    for (int d = 0; d < DB; ++d) acc[h][d] = float16_t{};
-  }
+  for (int d = 0; d < DB; ++d) acc[d] = float16_t{};
   // LDS offsets that do not change from tile to tile
   const int krow = l32 * RB, ksw = (half ^ k_swizzle16<CPR>(l32)) * 16;
   const int i16 = lane & 15, vrow = 4 * half + (i16 >> 2);
   const int vchunk = ((lane >> 4) & 1) * 2 + ((i16 & 3) >> 1);
-  using Probabilities = u32x4_t[NR][NP][2];
+  using Probabilities = u32x4_t[NP][2];
 
-  auto score = [&](const unsigned char* kt, int b, float16_t* s) __attribute__((always_inline)) {
-#pragma unroll
-    for (int h = 0; h < NR; ++h) s[h] = float16_t{};
+  auto score = [&](const unsigned char* kt, int b, float16_t& s) __attribute__((always_inline)) {
+    s = float16_t{};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const u32x4_t kf =
           *reinterpret_cast<const u32x4_t*>(kt + krow + b * 32 * RB + (ksw ^ (ks * 32)));
 #pragma unroll
-      for (int h = 0; h < NR; ++h)
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) Mma<KT>::step(kf, qf[h][i][ks], s[h], 0);
+      for (int i = 0; i < NQ; ++i) Mma<KT>::step(kf, qf[i][ks], s, 0);
     }
   };
   // scores of block b of tile i as they count
-  auto settle = [&](int i, int b, float16_t* s) __attribute__((always_inline)) {
-    if constexpr (RestK) {
+  auto settle = [&](int i, int b, float16_t& s) __attribute__((always_inline)) {
+    if constexpr (General) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float by = group(by_k, i, 2 * b + g), add = General ? group(addend, i, 2 * b + g) : 0.0f;
+        const float by = group(by_k, i, 2 * b + g), add = group(addend, i, 2 * b + g);
 #pragma unroll
-        for (int h = 0; h < NR; ++h)
-#pragma unroll
-          for (int r = 0; r < 8; ++r) s[h][8 * g + r] = fmaf(s[h][8 * g + r], by, add);
+        for (int r = 0; r < 8; ++r) s[8 * g + r] = fmaf(s[8 * g + r], by, add);
       }
     }
     const int key0 = (t0 + i) * BN + b * 32;
-    // (the first set's rows see the fewest keys)
-    if (key0 + 32 > whole[0]) {
+    if (key0 + 32 > whole) {
+      const int lane_lim = lim - key0 - 4 * half;
 #pragma unroll
-      for (int h = 0; h < NR; ++h) {
-        const int lane_lim = lim[h] - key0 - 4 * half;
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[h][r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[h][r] : kNegInf;
-      }
+      for (int r = 0; r < 16; ++r)
+        s[r] = (r & 3) + 8 * (r >> 2) < lane_lim ? s[r] : kNegInf;
     }
   };
   // The maximum moves only when it falls behind by 2^SLACK: the sums are hardly
   // ever rescaled.
-  auto move_up = [&](const float16_t* s) __attribute__((always_inline)) {
+  auto move_up = [&](const float16_t& s) __attribute__((always_inline)) {
+    float top = s[0];
 #pragma unroll
-    for (int h = 0; h < NR; ++h) {
-      float top = s[h][0];
-#pragma unroll
-      for (int r = 1; r < 16; ++r) top = fmaxf(top, s[h][r]);
-      top = swap_halves_max(top) * a.scale;
-      const float m_new = top > m[h] + SLACK ? top : m[h];
-      fall[h] = __builtin_amdgcn_exp2f(m[h] - m_new);
-      m[h] = m_new;
-      l[h] *= fall[h];
-    }
+    for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+    top = swap_halves_max(top) * a.scale;
+    const float m_new = top > m + SLACK ? top : m;
+    fall = __builtin_amdgcn_exp2f(m - m_new);
+    m = m_new;
+    l *= fall;
   };
-  auto probabilities = [&](int i, int b, float16_t* s, Probabilities& p) __attribute__((always_inline)) {
+  auto probabilities = [&](int i, int b, float16_t& s, Probabilities& p) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < NR; ++h) {
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale, LIFT - m));
+      l += s[r];
+    }
+    if constexpr (General) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[h][r] = __builtin_amdgcn_exp2f(fmaf(s[h][r], a.scale, -m[h]));
-        l[h] += s[h][r];
+      for (int g = 0; g < 2; ++g) {
+        const float by = group(by_v, i, 2 * b + g);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s[8 * g + r] *= by;
       }
-      if constexpr (General) {
+    }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float by = group(by_v, i, 2 * b + g);
+    for (int r = 0; r < 16; r += 2) {
+      uint32_t w[NP];
+      if constexpr (NP == 1) w[0] = pack2<VT>(s[r], s[r + 1]);
+      else split2<NP>(s[r], s[r + 1], w);
 #pragma unroll
-          for (int r = 0; r < 8; ++r) s[h][8 * g + r] *= by;
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 16; r += 2) {
-        uint32_t w[NP];
-        split2<NP>(s[h][r], s[h][r + 1], w);
-#pragma unroll
-        for (int j = 0; j < NP; ++j) p[h][j][r >> 3][(r & 7) >> 1] = w[j];
-      }
+      for (int j = 0; j < NP; ++j) p[j][r >> 3][(r & 7) >> 1] = w[j];
     }
   };
   auto add_values = [&](const unsigned char* vt, int b, const Probabilities& p)
@@ -904,28 +780,19 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
         const u32x2_t lo = read_column(from), hi = read_column(from + 8 * RB);
         const u32x4_t vf = {lo[0], lo[1], hi[0], hi[1]};
 #pragma unroll
-        for (int h = 0; h < NR; ++h)
-#pragma unroll
-          for (int j = 0; j < NP; ++j) Mma<DT_BF16>::step(vf, p[h][j][g], acc[h][d], 0);
+        for (int j = 0; j < NP; ++j) Mma<VT>::step(vf, p[j][g], acc[d], 0);
       }
   };
   // (p is formed up to here: its first use is past a branch, where the compiler
   // would take its computation, away from the matrix instructions)
   auto follow = [&](Probabilities& p) __attribute__((always_inline)) {
-    bool any = false;
 #pragma unroll
-    for (int h = 0; h < NR; ++h) {
+    for (int j = 0; j < NP; ++j) asm volatile("" : "+v"(p[j][0]), "+v"(p[j][1]), "+v"(l));
+    if (__any(fall != 1.0f)) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) asm volatile("" : "+v"(p[h][j][0]), "+v"(p[h][j][1]), "+v"(l[h]));
-      any = any || fall[h] != 1.0f;
-    }
-    if (__any(any)) {
+      for (int d = 0; d < DB; ++d)
 #pragma unroll
-      for (int h = 0; h < NR; ++h)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[h][d][r] *= fall[h];
+        for (int r = 0; r < 16; ++r) acc[d][r] *= fall;
     }
   };
 
@@ -936,15 +803,15 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
   unsigned char* const kt = lds;
   unsigned char* const vt = lds + 2 * Z::TILE;
   if (n > 0) {
-    float16_t s0[NR], s1[NR];   // scores of two blocks
+    float16_t s0, s1;       // scores of two blocks
     Probabilities p0, p1;       // probabilities of two blocks
     Part xk = fetch(0, 0), xv = fetch(0, 1);
     {
       const Part x = fetch(1, 0);
-      if (RestK) look(0);
-      widen(xk, 0, 0, 0);
-      widen(xv, 0, 0, 1);
-      widen(x, 1, 1, 0);
+      if (General) look(0);
+      widen(xk, 0, 0, Keys{});
+      widen(xv, 0, 0, Values{});
+      widen(x, 1, 1, Keys{});
     }
     xk = fetch(2, 0);
     xv = fetch(1, 1);
@@ -971,14 +838,14 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
       move_up(s1);
       score(k1, 0, s0);
       // behind the first matrix instructions
-      widen(xk, i + 2, odd, 0);
-      widen(xv, i + 1, 1 - odd, 1);
+      widen(xk, i + 2, odd, Keys{});
+      widen(xv, i + 1, 1 - odd, Values{});
       xk = fetch(i + 3, 0);
       xv = fetch(i + 2, 1);
       probabilities(i, 1, s1, p1);
       add_values(v0, 0, p0);
       follow(p1);
-      if (RestK && (i & 15) == 15) {
+      if (General && (i & 15) == 15) {
         look(i + 1);
         asm volatile("" : "+v"(by_k), "+v"(by_v), "+v"(addend));
       }
@@ -1006,35 +873,32 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
   }
 
   const int heads = c.Hk * a.G;
-#pragma unroll
-  for (int h = 0; h < NR; ++h) {
-    const float sum = l[h] + __shfl_xor(l[h], 32);
-    if (!row_ok[h]) continue;
-    const float inv = sum > 0.0f ? 1.0f / sum : sum;   // 0 keys: 0; a NaN stays
-    const float lse2 = sum == 0.0f ? kNegInf : m[h] + __builtin_amdgcn_logf(sum);
-    const long long t = job.e.row0 + qi[h], at = (job.slot * a.T + t) * heads + head[h];
-    if (half == 0) {
-      if (job.slot >= 0) a.many_lse[at] = lse2;
-      else if (a.lse) a.lse[t * heads + head[h]] = lse2 * kLn2;
-    }
-    char* const op = a.out + t * a.o_r + head[h] * a.o_h;
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int comp = d * 32 + 8 * r + 4 * half;
-        if (comp >= D) continue;
-        const float4_t o = {acc[h][d][4 * r] * inv, acc[h][d][4 * r + 1] * inv,
-                            acc[h][d][4 * r + 2] * inv, acc[h][d][4 * r + 3] * inv};
-        if (job.slot >= 0)
-          *reinterpret_cast<float4_t*>(a.many + at * D + comp) = o;
-        else if constexpr (EB == 4)
-          *reinterpret_cast<float4_t*>(op + comp * 4) = o;
-        else
-          *reinterpret_cast<u32x2_t*>(op + comp * 2) =
-              u32x2_t{pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3])};
-      }
+  const float sum = l + __shfl_xor(l, 32);
+  if (!row_ok) return;
+  const float inv = sum > 0.0f ? 1.0f / sum : sum;   // 0 keys: 0; a NaN stays
+  const float lse2 = sum == 0.0f ? kNegInf : m + (__builtin_amdgcn_logf(sum) - LIFT);
+  const long long t = job.e.row0 + qi, at = (job.slot * a.T + t) * heads + head;
+  if (half == 0) {
+    if (job.slot >= 0) a.many_lse[at] = lse2;
+    else if (a.lse) a.lse[t * heads + head] = lse2 * kLn2;
   }
+  char* const op = a.out + t * a.o_r + head * a.o_h;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int comp = d * 32 + 8 * r + 4 * half;
+      if (comp >= D) continue;
+      const float4_t o = {acc[d][4 * r] * inv, acc[d][4 * r + 1] * inv,
+                          acc[d][4 * r + 2] * inv, acc[d][4 * r + 3] * inv};
+      if (job.slot >= 0)
+        *reinterpret_cast<float4_t*>(a.many + at * D + comp) = o;
+      else if constexpr (EB == 4)
+        *reinterpret_cast<float4_t*>(op + comp * 4) = o;
+      else
+        *reinterpret_cast<u32x2_t*>(op + comp * 2) =
+            u32x2_t{pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3])};
+    }
 }
 
 // The unit of number x of the sets of `size` rows of the entries with more than a
@@ -1069,28 +933,82 @@ __device__ __forceinline__ bool unit_of(const CacheAttnArgs& a, int number, int 
   return true;
 }
 
-// 32 rows of a key head a workgroup, for calls that have few such sets.
+// Entries of few rows: the tiles of all their key heads in a row, entry after
+// entry, each workgroup a run of them of one length (so that entries of very
+// different lengths fill the GPU to the end).  A head whose tiles lie in one run
+// is written at once, of others the runs' parts are joined (join_few).
 template <int DT, int CF, int DP>
-__global__ __launch_bounds__(kFewThreads, 2) void some_kernel(const CacheAttnArgs a, int all) {
+__device__ __forceinline__ void few_run(const CacheAttnArgs& a, int group, unsigned char* lds) {
+  Job job;
+  job.row_tile = 0;
+  if (a.few_groups == 0) {
+    job.b = group / a.c.Hk;
+    job.hk = group - job.b * a.c.Hk;
+    job.e = entry_of(a, job.b);
+    job.t0 = 0;
+    job.t1 = few_tiles(job.e);
+    job.slot = -1;
+    if (job.t1 > 0) attend_few<DT, CF, DP>(a, job, lds);
+    return;
+  }
+  auto weight = [](const Entry& e) { return few_tiles(e); };
+  Entries<decltype(weight)> entries(a, weight);
+  const int Hk = a.c.Hk;
+  const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
+  long long x = group * per;
+  const long long begin = x, end = x + per < total ? x + per : total;
+  while (x < end) {
+    const auto f = entries.find(x / Hk);
+    job.b = f.b;
+    job.e = f.e;
+    // the entry's heads one after another
+    while (x < end && x < (f.first + f.weight) * Hk) {
+      const int in = (int)(x - f.first * Hk);
+      job.hk = in / f.weight;
+      job.t0 = in - job.hk * f.weight;
+      job.t1 = f.weight - job.t0 < end - x ? f.weight : job.t0 + (int)(end - x);
+      job.slot = job.t0 == 0 && job.t1 == f.weight ? -1 : 2LL * group + (x == begin ? 0 : 1);
+      attend_few<DT, CF, DP>(a, job, lds);
+      x += job.t1 - job.t0;
+    }
+  }
+}
+
+// `units` workgroups of 32 rows of a key head, for calls that have few such sets,
+// and behind them those of the entries of few rows.
+template <int DT, int CF, int DP>
+__global__ __launch_bounds__(kFewThreads, 2) void few_kernel(const CacheAttnArgs a, int units,
+                                                             int all) {
   __shared__ __attribute__((aligned(1024))) unsigned char lds[Shape<DP>::LDS];
+  if ((int)blockIdx.x >= units) {
+    few_run<DT, CF, DP>(a, blockIdx.x - units, lds);
+    return;
+  }
   Unit u;
   if (!unit_of(a, blockIdx.x, 32, all, &u)) return;
   const Job job = {u.e, u.b, u.hk, u.set, 0, (u.keys + kTile - 1) / kTile, -1};
   attend_few<DT, CF, DP>(a, job, lds);
 }
 
-// 128 NR rows of a key head a workgroup; the keys in a.splits shares.
-template <int DT, int CF, int DP, int NR>
-__global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void many_kernel(const CacheAttnArgs a,
-                                                                         int all) {
+// `units` sets of 128 rows of a key head, the keys in a.splits shares, a workgroup
+// each, and behind them the workgroups of the entries of few rows, which fill the
+// GPU while the last sets end.
+template <int DT, int CF, int DP>
+__global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a, int units,
+                                                           int all) {
   using Z = Wide<DP>;
-  __shared__ __attribute__((aligned(1024))) unsigned char lds[Z::LDS];
-  const int per = gridDim.x / a.splits, split = blockIdx.x / per;
+  __shared__ __attribute__((aligned(1024))) unsigned char
+      lds[Z::LDS > Shape<DP>::LDS ? Z::LDS : Shape<DP>::LDS];
+  if ((int)blockIdx.x >= units * a.splits) {
+    few_run<DT, CF, DP>(a, blockIdx.x - units * a.splits, lds);
+    return;
+  }
+  const int split = blockIdx.x / units;
   Unit u;
   // (consecutive workgroups, which lie on different XCDs, are of different heads: an
   // XCD then reads few heads of every entry, however long each is.  With an XCD to
   // an entry the longest one held up the end.)
-  if (!unit_of(a, blockIdx.x - split * per, kManyRows * NR, all, &u)) return;
+  if (!unit_of(a, blockIdx.x - split * units, kManyRows, all, &u)) return;
   const CacheView& c = a.c;
   const int tiles = (u.keys + Z::BN - 1) / Z::BN;
   const Job job = {u.e,
@@ -1100,7 +1018,7 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void many_kernel(const C
                    (int)((long long)tiles * split / a.splits),
                    (int)((long long)tiles * (split + 1) / a.splits),
                    a.splits > 1 ? split : -1};
-  // whether all blocks are there, with powers of two
+  // whether all blocks are there, with scales that the widened numbers can take in
   bool plain = true;
   const int last = job.t1 * Z::BN < u.e.len ? job.t1 * Z::BN : u.e.len;
   const int b0 = (job.t0 * Z::BN) >> c.log_block, b1 = (last + (1 << c.log_block) - 1) >> c.log_block;
@@ -1110,24 +1028,97 @@ __global__ __launch_bounds__(kThreads, NR == 1 ? 2 : 1) void many_kernel(const C
       plain = false;
     } else {
       const long long at = (long long)id * c.Hk + u.hk;
-      plain = plain && is_power(c.scale[0][at]) && is_power(c.scale[1][at]);
+      plain = plain && folds<DT>(c.scale[0][at]) && folds<DT>(c.scale[1][at]);
     }
   }
-  if (__syncthreads_and(plain)) attend_many<DT, CF, DP, NR, false>(a, job, lds);
-  else attend_many<DT, CF, DP, NR, true>(a, job, lds);
+  if (__syncthreads_and(plain)) attend_many<DT, CF, DP, false>(a, job, lds);
+  else attend_many<DT, CF, DP, true>(a, job, lds);
 }
 
-// Joins the splits of a row of a set: LPR lanes a row, 4 components a lane.
+// Joins the parts of a row of key head number `unit` of the entries:
+// out = sum_s 2^(lse_s - lse) o_s.  LPR lanes a part, 4 components a lane; the
+// workgroup's sets of lanes take parts in turn and meet in LDS, in order.
 template <int DT, int LPR>
-__global__ __launch_bounds__(kThreads) void many_join_kernel(const CacheAttnArgs a, int size,
-                                                             int all) {
+__device__ __forceinline__ void join_few(const CacheAttnArgs& a, int unit, int row) {
+  constexpr int SETS = kThreads / LPR;
+  __shared__ float tops[SETS], sums[SETS];
+  __shared__ float4_t outs[SETS][LPR];
+  const int Hk = a.c.Hk, D = a.c.D;
+  const int b = unit / Hk, hk = unit - b * Hk;
+  const Entry e = entry_of(a, b);
+  const int tiles = few_tiles(e);
+  if (tiles < 2 || row >= e.rows) return;
+  auto weight = [](const Entry& x) { return few_tiles(x); };
+  Entries<decltype(weight)> entries(a, weight);
+  const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
+  const long long u0 = entries.begin_of(b) * Hk + (long long)hk * tiles, u1 = u0 + tiles;
+  const int g0 = (int)(u0 / per), g1 = (int)((u1 - 1) / per);
+  if (g0 == g1) return;
+  const int set = threadIdx.x / LPR, lane = threadIdx.x % LPR;
+  const bool live = 4 * lane < D;
+  float m = kLowest, sum = 0.0f;
+  float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g = g0 + set; g <= g1; g += SETS) {
+    // a run's first part is its slot 0
+    const long long slot =
+        (2LL * g + (g == g0 && u0 != g * per ? 1 : 0)) * kFewRows + row;
+    const float w = a.part_lse[slot];
+    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (live) v = *reinterpret_cast<const float4_t*>(a.part + slot * D + 4 * lane);
+    const float m_new = fmaxf(m, w), fall = __builtin_amdgcn_exp2f(m - m_new),
+                p = __builtin_amdgcn_exp2f(w - m_new);
+    m = m_new;
+    sum = fmaf(sum, fall, p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j] * fall);
+  }
+  if (lane == 0) {
+    tops[set] = m;
+    sums[set] = sum;
+  }
+  outs[set][lane] = o;
+  __syncthreads();
+  if (set > 0) return;
+  float m_all = m;
+#pragma unroll
+  for (int s = 1; s < SETS; ++s) m_all = fmaxf(m_all, tops[s]);
+  sum = 0.0f;
+  o = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < SETS; ++s) {
+    const float p = __builtin_amdgcn_exp2f(tops[s] - m_all);
+    sum = fmaf(sums[s], p, sum);
+    const float4_t v = outs[s][lane];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j]);
+  }
+  const float inv = sum > 0.0f ? 1.0f / sum : sum;
+  const int qi = row / a.G, head = hk * a.G + row - qi * a.G;
+  const long long t = e.row0 + qi;
+  if (a.lse && lane == 0)
+    a.lse[t * (Hk * a.G) + head] =
+        sum == 0.0f ? kNegInf : (m_all + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (!live) return;
+  char* op = a.out + t * a.o_r + head * a.o_h;
+  if constexpr (DT == DT_F32)
+    *reinterpret_cast<float4_t*>(op + 16 * lane) = o * inv;
+  else
+    *reinterpret_cast<u32x2_t*>(op + 8 * lane) =
+        u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
+}
+
+// Joins the splits of the rows of a set, the workgroup `part` of kParts of it: LPR
+// lanes a row, 4 components a lane.
+constexpr int kParts = 4;
+template <int DT, int LPR>
+__device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int part, int all) {
   Unit u;
-  if (!unit_of(a, blockIdx.x, size, all, &u)) return;
+  if (!unit_of(a, unit, kManyRows, all, &u)) return;
   const int lane = threadIdx.x % LPR, D = a.c.D, heads = a.c.Hk * a.G;
   const bool live = 4 * lane < D;
-  for (int r = threadIdx.x / LPR + blockIdx.y * (kThreads / LPR); r < size;
-       r += gridDim.y * (kThreads / LPR)) {
-    const int row = u.set * size + r;
+  for (int r = threadIdx.x / LPR + part * (kThreads / LPR); r < kManyRows;
+       r += kParts * (kThreads / LPR)) {
+    const int row = u.set * kManyRows + r;
     if (row >= u.e.rows) return;
     const int qi = row / a.G, head = u.hk * a.G + row - qi * a.G;
     const long long t = u.e.row0 + qi, step = (long long)a.T * heads, at = t * heads + head;
@@ -1175,6 +1166,20 @@ __global__ __launch_bounds__(kThreads) void many_join_kernel(const CacheAttnArgs
   }
 }
 
+// What has parts: kParts workgroups for each of `units` sets, and behind them one
+// for each of the `rows` that a key head of an entry of few may have.
+template <int DT, int LPR>
+__global__ __launch_bounds__(kThreads) void join_kernel(const CacheAttnArgs a, int units, int rows,
+                                                        int all) {
+  const int x = blockIdx.x;
+  if (x < units * kParts) {
+    join_many<DT, LPR>(a, x / kParts, x & (kParts - 1), all);
+  } else {
+    const int y = x - units * kParts;
+    join_few<DT, LPR>(a, y / rows, y % rows);
+  }
+}
+
 // Sets of `size` rows of a key head that a batch may have: of each entry, or side by
 // side, which takes a look at all entries' rows (64 at a time).
 long long sets_of_each(const CacheAttnArgs& a, long long size) {
@@ -1187,31 +1192,24 @@ long long row_sets(const CacheAttnArgs& a, long long size) {
 
 template <int DT, int CF, int DP>
 void launch(const CacheAttnArgs& a, hipStream_t stream) {
-  const dim3 threads(kThreads);
   constexpr int LPR = DP <= 64 ? 16 : 32;
   const long long most = (long long)a.max_rows * a.G;
   // all entries have the most rows, or (rows of no entry) none does
   const int all = most > kFewRows && (long long)a.T == (long long)a.max_rows * a.c.B;
-  if (!all && a.G <= kFewRows) {
-    const int groups = a.few_groups > 0 ? a.few_groups : a.c.B * a.c.Hk;
-    hipLaunchKernelGGL((few_kernel<DT, CF, DP>), dim3((unsigned)groups), dim3(kFewThreads), 0,
-                       stream, a);
-    if (a.few_groups > 0)
-      hipLaunchKernelGGL((few_join_kernel<DT, LPR>),
-                         dim3((unsigned)(a.c.B * a.c.Hk), (unsigned)(most < 32 ? most : 32)),
-                         threads, 0, stream, a);
-  }
-  if (most <= kFewRows) return;
-  const unsigned units = (unsigned)((a.sets > 0 ? (long long)a.sets * a.c.B : row_sets(a, a.set)) *
-                                    a.c.Hk);
-  if (a.set == 32)
-    hipLaunchKernelGGL((some_kernel<DT, CF, DP>), dim3(units), dim3(kFewThreads), 0, stream, a, all);
+  const int groups = all || a.G > kFewRows ? 0 : a.few_groups > 0 ? a.few_groups : a.c.B * a.c.Hk;
+  const int units = most <= kFewRows ? 0
+                    : (int)((a.sets > 0 ? (long long)a.sets * a.c.B : row_sets(a, a.set)) * a.c.Hk);
+  if (a.set == kManyRows)
+    hipLaunchKernelGGL((many_kernel<DT, CF, DP>), dim3((unsigned)(units * a.splits + groups)),
+                       dim3(kThreads), 0, stream, a, units, all);
   else
-    hipLaunchKernelGGL((many_kernel<DT, CF, DP, 1>), dim3(units * a.splits), threads, 0, stream, a,
-                       all);
-  if (a.splits > 1)
-    hipLaunchKernelGGL((many_join_kernel<DT, LPR>), dim3(units, 4), threads, 0, stream, a, a.set,
-                       all);
+    hipLaunchKernelGGL((few_kernel<DT, CF, DP>), dim3((unsigned)(units + groups)),
+                       dim3(kFewThreads), 0, stream, a, units, all);
+  const int sets = a.splits > 1 ? units : 0, rows = most < kFewRows ? (int)most : kFewRows;
+  const int heads = groups > 0 && a.few_groups > 0 ? a.c.B * a.c.Hk : 0;
+  if (sets + heads > 0)
+    hipLaunchKernelGGL((join_kernel<DT, LPR>), dim3((unsigned)(sets * kParts + heads * rows)),
+                       dim3(kThreads), 0, stream, a, sets, rows, all);
 }
 
 template <int DT, int CF> void launch_cf(const CacheAttnArgs& a, hipStream_t stream) {
@@ -1246,11 +1244,12 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
     }
     // (empty sets end at once; many entries take long to look through)
     const long long each = sets_of_each(*a, a->set) * a->c.B;
-    if (each <= 2 * row_sets(*a, a->set) || (a->c.B > 512 && each * a->c.Hk < (1 << 22)))
+    if (each * a->c.Hk < (1 << 22) && (each <= 2 * row_sets(*a, a->set) || a->c.B > 512))
       a->sets = (int)sets_of_each(*a, a->set);
   }
   if (!allowed) return 0;
-  if (a->G <= kFewRows && keys > 1024 && a->c.B <= 1024) a->few_groups = 8 / kFewWaves * cus;
+  if (a->G <= kFewRows && keys > 1024 && a->c.B <= 1024 && a->c.B * (long long)a->c.Hk < (1 << 17))
+    a->few_groups = 8 / kFewWaves * cus;
   const long long rows = a->splits > 1 ? (long long)a->T * a->G * a->c.Hk * a->splits : 0;
   return (2LL * a->few_groups * kFewRows + rows) * (a->c.D + 1) * 4;
 }

@@ -44,8 +44,8 @@ template <int CF, int DT> __device__ __forceinline__ u32x4_t code_values16(uint3
   return u32x4_t{a[0], a[1], b[0], b[1]};
 }
 
-// 8 codes times a power of two, in bfloat16.
-template <int CF>
+// 8 codes times a power of two, for products that the type holds.
+template <int CF, int DT>
 __device__ __forceinline__ u32x4_t code_values16(uint32_t w0, uint32_t w1, float power) {
   u32x4_t v;
 #pragma unroll
@@ -56,14 +56,18 @@ __device__ __forceinline__ u32x4_t code_values16(uint32_t w0, uint32_t w1, float
       code_values<CF>(w, f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] *= power;
-      v[2 * i] = pack2<DT_BF16>(f[0], f[1]);
-      v[2 * i + 1] = pack2<DT_BF16>(f[2], f[3]);
+      v[2 * i] = pack2<DT>(f[0], f[1]);
+      v[2 * i + 1] = pack2<DT>(f[2], f[3]);
+    } else if constexpr (DT == DT_F16) {   // (the conversions multiply by the power of two)
+      v[2 * i] = __builtin_bit_cast(uint32_t,
+                                    __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, power, false));
+      v[2 * i + 1] = __builtin_bit_cast(uint32_t,
+                                        __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, power, true));
     } else {
-      // (the conversion multiplies by the power of two)
-      v[2 * i] = __builtin_bit_cast(
-          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, false));
-      v[2 * i + 1] = __builtin_bit_cast(
-          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, true));
+      v[2 * i] = __builtin_bit_cast(uint32_t,
+                                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, false));
+      v[2 * i + 1] = __builtin_bit_cast(uint32_t,
+                                        __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, power, true));
     }
   }
   return v;

@@ -765,8 +765,10 @@ libconv_status libconv_kv_cache_read(const void* k_cache, const void* v_cache,
  * q_heads is a multiple of k_heads: query head h reads key head
  * h / (q_heads / k_heads).  Scores, softmax and sums are fp32; codes are exact in
  * the matrix instructions, q too (fp32 as three bfloat16 terms), and the
- * probabilities times their values' scale are rounded to 8 bits (bf16), 16
- * (fp16) or 24 (fp32) for the second product; `out` is rounded once.  Tokens past
+ * probabilities, times their values' scale or not, are rounded to 8 bits (bf16),
+ * 11 or 16 (fp16) or 24 (fp32) for the second product; `out` is rounded once.  Sums
+ * of probabilities times values are divided at the end: 256 times the sum of a
+ * query's values, and <q, k_j>, have to stay within fp32's range.  Tokens past
  * an entry's length are not read into any result, whatever their codes and
  * scales; a NaN that a causal mask hides from a query can reach that query.
  *   workspace  device, 256-byte aligned, at least

@@ -11,8 +11,9 @@ from layercheck import TYPES, U, U32, assert_within, tiny  # noqa: F401  (the te
 
 CODES = {"i8": torch.int8, "e4m3": torch.float8_e4m3fn}
 MOST = {torch.int8: 127.0, torch.float8_e4m3fn: 448.0}
-# roundings of a probability for the second product: one, two, three bfloat16 terms
-P_ROUNDING = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -24}
+# roundings of a probability for the second product: one bfloat16 term, one fp16 number (of a few
+# rows: two bfloat16 terms, 2^-16, which is less), three bfloat16 terms
+P_ROUNDING = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 
 
 class Cache:
@@ -165,6 +166,11 @@ def attention(q, cache, row_starts, scale, causal):
             # instructions, which take numbers that small for 0: n terms of less than 2^-126
             # times a code (or a value) are missing then
             gone = n * 2.0 ** -126 * (448 + v[:, g].abs().amax())
+            if t == torch.float16:
+                # as fp16 numbers, probabilities are multiplied by 2^11 relative to a maximum that
+                # theirs is not below: below 2^-14 each is off by half of fp16's last step, 2^-25,
+                # so 2^-36 of a sum that is 1 at least
+                gone = gone + n * 2.0 ** -36 * v[:, g].abs().amax()
             bound[lo:hi, h] = (U[t] + P_ROUNDING[t] + off)[:, None] * mag + tiny(t) + gone
             lse[lo:hi, h] = torch.where(some, torch.logsumexp(s, -1), torch.full((), -math.inf).double())
             lse_bound[lo:hi, h] = off + U32 * 8 * (1 + a)

@@ -110,6 +110,24 @@ def test_scales_that_are_no_powers_of_two(rows, lengths, dtype, codes):
     check(queries(sum(rows), 32, 64, dtype), cache, C.starts(rows), True, what="scales")
 
 
+@pytest.mark.parametrize("codes", ["i8", "e4m3"])
+@pytest.mark.parametrize("dtype,least,most", [("f16", -15, 7), ("bf16", -117, 100)])
+def test_scales_at_the_ends_of_the_16_bit_types(codes, dtype, least, most):
+    """Powers of two whose products with codes just fit the type, and the next ones.  (bfloat16's
+    last ones, from 2^119 on, are past what the operator allows: sums of 1300 values of 2^126 pass
+    fp32's range before they are divided.)"""
+    rows, lengths = [300, 1], [900, 1300]
+    q = queries(sum(rows), 16, 64, dtype)
+    for e in (least - 1, least, most, most + 1):
+        if dtype == "f16":   # (sums of products with bfloat16's would pass fp32's range)
+            cache = C.Cache(2, lengths, 32, 4, 64, codes, seed=15)
+            cache.ks.fill_(2.0 ** e)
+            check(q, cache, C.starts(rows), True, scale=2.0 ** (-e - 9), what=f"keys 2^{e}")
+        cache = C.Cache(2, lengths, 32, 4, 64, codes, seed=16)
+        cache.vs.fill_(2.0 ** e)
+        check(q, cache, C.starts(rows), True, what=f"values 2^{e}")
+
+
 @pytest.mark.parametrize("rows,lengths,dtype", SHAPES, ids=str)
 def test_blocks_that_are_not_there(rows, lengths, dtype):
     """A window that has moved on, and holes; an entry without any block."""
