@@ -405,8 +405,11 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
 #pragma unroll
     for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
     top = swap_halves_max(top);
-    if (__any(top > m)) {
-      const float m_new = fmaxf(m, top), fall = __builtin_amdgcn_exp2f(m - m_new);
+    // the maximum moves only when it falls behind by 2^SLACK: the sums are hardly ever
+    // rescaled
+    constexpr float SLACK = 8.0f;
+    if (__any(top > m + SLACK)) {
+      const float m_new = top > m + SLACK ? top : m, fall = __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
       l *= fall;
 #pragma unroll
