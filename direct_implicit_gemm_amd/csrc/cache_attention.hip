@@ -10,6 +10,11 @@
 // matrix instructions as 16-bit numbers, which hold them exactly; the scale of a
 // block's keys multiplies their scores, that of its values their probabilities
 // (16 consecutive keys always have one scale).
+//
+// Entries with up to 32 rows a key head (single tokens) are bound by memory: one
+// set of 32 columns holds all their queries, so that codes are read once, and
+// workgroups share the tiles of all heads.  Entries with more are bound by
+// the matrix and vector units: 128 rows share codes that are widened once.
 #include "codes.h"
 #include "internal.h"
 #include "layer.h"
@@ -105,51 +110,51 @@ __device__ __forceinline__ int few_tiles(const Entry& e) {
 }
 
 // Sum over the lanes up to this one.
-__device__ __forceinline__ int lanes_before(int v) {
+__device__ __forceinline__ long long lanes_before(long long v) {
   const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
+    const long long o = __shfl_up(v, d);
     v += lane >= d ? o : 0;
   }
   return v;
 }
+__device__ __forceinline__ long long of_lane(long long v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)v, lane);
+  return ((long long)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32) | lo;
+}
 
-// The entries' work, `weight(entry)` each, side by side.  64 entries at a time are
-// in the wave's lanes; up to 64 are read once.
+// The entries' work, `weight(entry)` each, side by side.  A lane looks at `chunk`
+// entries one after another; whoever needs one of them has the lanes look at those
+// of its chunk once more, 64 at a time.  (A workgroup that went through all entries
+// 64 at a time: 1024 entries, 2 heads of 64 228 us instead of 186.)
 template <class W> struct Entries {
   const CacheAttnArgs& a;
   W weight;
-  Entry mine;      // this lane's entry of those from b0 on
-  int b0 = 0, w, up_to;
+  int chunk;
+  Entry mine;          // this lane's entry of those that were looked at last
+  long long w, up_to;  // work of this lane's chunk, and of those up to it
 
-  __device__ __forceinline__ Entries(const CacheAttnArgs& args, W f) : a(args), weight(f) { load(0); }
-  __device__ __forceinline__ void load(int first) {
-    const int b = first + (int)(threadIdx.x & 63);
-    b0 = first;
+  __device__ __forceinline__ Entries(const CacheAttnArgs& args, W f) : a(args), weight(f) {
+    chunk = (a.c.B + 63) >> 6;
+    w = 0;
+    const int first = (int)(threadIdx.x & 63) * chunk;
     mine = Entry{0, 0, 0, 0};
-    if (b < a.c.B) mine = entry_of(a, b);
-    w = b < a.c.B ? weight(mine) : 0;
+#pragma unroll 4
+    for (int i = 0; i < chunk; ++i)
+      if (first + i < a.c.B) {
+        mine = entry_of(a, first + i);
+        w += weight(mine);
+      }
     up_to = lanes_before(w);
   }
-  // Work of all entries.
-  __device__ __forceinline__ long long total() {
-    long long sum = __builtin_amdgcn_readlane(up_to, 63);
-    for (int first = 64; first < a.c.B; first += 64) {
-      load(first);
-      sum += __builtin_amdgcn_readlane(up_to, 63);
-    }
-    return sum;
-  }
-  // Where an entry's work begins.
-  __device__ __forceinline__ long long begin_of(int b) {
-    long long sum = 0;
-    for (int first = 0; first < a.c.B; first += 64) {
-      if (first != b0) load(first);
-      if (b < first + 64) return sum + __builtin_amdgcn_readlane(up_to - w, b - first);
-      sum += __builtin_amdgcn_readlane(up_to, 63);
-    }
-    return sum;
+  __device__ __forceinline__ long long total() const { return of_lane(up_to, 63); }
+  // The lanes' entries from b on, up to `end`, and their work.
+  __device__ __forceinline__ int look(int b, int end) {
+    b += threadIdx.x & 63;
+    mine = Entry{0, 0, 0, 0};
+    if (b < end) mine = entry_of(a, b);
+    return b < end ? weight(mine) : 0;
   }
   // The entry that holds number x of the work, and where its own begins; b = B: none.
   struct Found {
@@ -157,30 +162,48 @@ template <class W> struct Entries {
     int b, weight;
     long long first;
   };
+  __device__ __forceinline__ Found entry(int l, int b, int weight, long long first) const {
+    Found f;
+    f.e.row0 = __builtin_amdgcn_readlane(mine.row0, l);
+    f.e.n = __builtin_amdgcn_readlane(mine.n, l);
+    f.e.rows = __builtin_amdgcn_readlane(mine.rows, l);
+    f.e.len = __builtin_amdgcn_readlane(mine.len, l);
+    f.b = b;
+    f.weight = weight;
+    f.first = first;
+    return f;
+  }
   __device__ __forceinline__ Found find(long long x) {
-    long long sum = 0;
-    for (int first = 0; first < a.c.B; first += 64) {
-      if (first != b0) load(first);
-      const uint64_t past = __ballot(sum + up_to > x);
-      if (past) {
-        const int l = __builtin_ctzll(past);
-        Found f;
-        f.e.row0 = __builtin_amdgcn_readlane(mine.row0, l);
-        f.e.n = __builtin_amdgcn_readlane(mine.n, l);
-        f.e.rows = __builtin_amdgcn_readlane(mine.rows, l);
-        f.e.len = __builtin_amdgcn_readlane(mine.len, l);
-        f.b = first + l;
-        f.weight = __builtin_amdgcn_readlane(w, l);
-        f.first = sum + __builtin_amdgcn_readlane(up_to, l) - f.weight;
-        return f;
+    const uint64_t past = __ballot(up_to > x);
+    if (!past) return {Entry{0, 0, 0, 0}, a.c.B, 0, total()};
+    const int l = __builtin_ctzll(past);
+    long long sum = of_lane(up_to - w, l);
+    if (chunk == 1) return entry(l, l, (int)of_lane(w, l), sum);
+    const int end = (l + 1) * chunk < a.c.B ? (l + 1) * chunk : a.c.B;
+    for (int first = l * chunk; first < end; first += 64) {
+      const int v = look(first, end);
+      const long long to = lanes_before(v);
+      const uint64_t in = __ballot(sum + to > x);
+      if (in) {
+        const int i = __builtin_ctzll(in);
+        const int weight = __builtin_amdgcn_readlane(v, i);
+        return entry(i, first + i, weight, sum + of_lane(to, i) - weight);
       }
-      sum += __builtin_amdgcn_readlane(up_to, 63);
+      sum += of_lane(to, 63);
     }
-    return {Entry{0, 0, 0, 0}, a.c.B, 0, sum};
+    return {Entry{0, 0, 0, 0}, a.c.B, 0, sum};   // (not reached)
   }
 };
 
-// How the few_groups workgroups share the tiles of all heads: each a run of `per`.
+// How the few_groups workgroups share the tiles of all heads: each a run of `per`,
+// where a head begins with kStart tiles' time of no keys (a workgroup reads queries and
+// table and fills its stages meanwhile): tile t of a head that begins at u is at
+// u + kStart + t.
+constexpr int kStart = 2;   // (that batch: 0 129 us, 2 117, 3 119, 5 120)
+__device__ __forceinline__ int few_units(const Entry& e) {
+  const int t = few_tiles(e);
+  return t > 0 ? t + kStart : 0;
+}
 __device__ __forceinline__ long long share_of(long long total, int groups) {
   const long long per = (total + groups - 1) / groups;
   return per < 2 ? 2 : per;   // (fewer keys are not worth a partial result)
@@ -194,6 +217,16 @@ struct Job {
   long long slot;
 };
 
+// One job of few rows.  Each wave of four takes 32 keys of a tile through LDS
+// stages of its own (two tiles of keys and of values, copied by it without
+// registers), with its own maximum and sum, and never waits for the others before
+// they are joined at the end.  Codes are read from LDS as 8-bit columns and rows
+// and widened in registers: what a wave does for its keys is about 550
+// instructions (128 components), two workgroups a compute unit, which keeps up
+// with memory: 64 entries of 8 heads with 4096 keys, 537 MB, take 107 us (5.0
+// TB/s).  Where few workgroups have keys the instructions bound it: a tile of 128
+// keys takes 1.4 us.  Eight waves: 1024 keys 17.1 -> 15.3 us, but 32 to 256 keys
+// 6.6 -> 9.1, for another copy of the kernel; two waves: 1000 keys 12.4 -> 19.7.
 template <int DT, int CF, int DP>
 __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& job,
                                            unsigned char* lds) {
@@ -255,7 +288,9 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
     int at[2][2];   // offset of the codes from the caches' first: low and high word
     int rows;       // 0: none
   };
-  auto position = [&](int first) { return (first + (lane >> 1)) * kTile + wave * 32 + (lane & 1) * 16; };
+  auto position = [&](int first) {
+    return (first + (lane >> 1)) * kTile + wave * 32 + (lane & 1) * 16;
+  };
   const int* const table = c.table + (long long)job.b * c.width;
   const int last = len - 1;   // (tiles are counted so that positions fit 31 bits)
   auto locate = [&](int first, int id) {
@@ -480,7 +515,8 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
       l = fmaf(tops[SUMS + w * 32 + l32], g, l);
 #pragma unroll
       for (int r = 0; r < 16; ++r)
-        o[r] = fmaf(rooms[(w * DP + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32], g, o[r]);
+        o[r] = fmaf(rooms[(w * DP + d * 32 + (r & 3) + 8 * (r >> 2) + 4 * half) * 32 + l32], g,
+                    o[r]);
     }
     if (!row_ok) continue;
     const float inv = l > 0.0f ? 1.0f / l : l;   // 0 keys: 0; a NaN stays
@@ -496,25 +532,30 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
     for (int r = 0; r < 4; ++r) {
       const int comp = d * 32 + 8 * r + 4 * half;
       if (comp >= D) continue;
-      const float4_t v = {o[4 * r] * inv, o[4 * r + 1] * inv, o[4 * r + 2] * inv, o[4 * r + 3] * inv};
+      const float4_t v = {o[4 * r] * inv, o[4 * r + 1] * inv, o[4 * r + 2] * inv,
+                          o[4 * r + 3] * inv};
       if (job.slot >= 0)
         *reinterpret_cast<float4_t*>(a.part + slot * D + comp) = v;
       else if constexpr (EB == 4)
         *reinterpret_cast<float4_t*>(op + comp * 4) = v;
       else
-        *reinterpret_cast<u32x2_t*>(op + comp * 2) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+        *reinterpret_cast<u32x2_t*>(op + comp * 2) =
+            u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
     }
   }
   lds_barrier();   // the joined results are read
 }
 
 // Many rows: four waves of 32 rows share tiles of 64 keys, widened to 16 bits once
-// for all of them.  A wave reads the codes of 16 rows of keys and of values a tile
-// ahead into registers, and widens them into LDS a tile (keys: two) before they
-// are used.  A power of two is taken into the widened numbers, which hold the
-// product exactly.  `General`, where a block that the workgroup reads is not there
-// or has a scale for which they do not: scores and probabilities are multiplied
-// instead.
+// for all of them (each wave widening the keys that it meets, as few rows do: 8 x
+// 2048 rows behind 4096 tokens, 32 / 8 heads of 128, 1500 us; shared: 820, 1.0
+// PFLOP/s in bfloat16; matrix units 44 % busy, vector units 51, LDS 55).  64 rows
+// a wave: 1009 instead of 848 us, one workgroup of eight waves: 1300.  A wave
+// reads the codes of 16 rows of keys and of values a tile ahead into registers,
+// and widens them into LDS a tile (keys: two) before they are used.  A power of
+// two is taken into the widened numbers, which hold the product exactly.
+// `General`, where a block that the workgroup reads is not there or has a scale
+// for which they do not: scores and probabilities are multiplied instead.
 constexpr int kManyRows = 128;
 template <int DP> struct Wide {
   static constexpr int RAW = DP <= 64 ? 64 : 128;   // bytes of a row of codes
@@ -667,8 +708,8 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
     Part x;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j)
-      x.codes[j] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off[kv], j * PASS * (int)c.token[kv], 0));
+      x.codes[j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   r, off[kv], j * PASS * (int)c.token[kv], 0));
     return x;
   };
   // where a lane's 16 codes go, of even and odd chunks
@@ -749,7 +790,8 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
     m = m_new;
     l *= fall;
   };
-  auto probabilities = [&](int i, int b, float16_t& s, Probabilities& p) __attribute__((always_inline)) {
+  auto probabilities = [&](int i, int b, float16_t& s, Probabilities& p)
+      __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale, LIFT - m));
@@ -939,7 +981,9 @@ __device__ __forceinline__ bool unit_of(const CacheAttnArgs& a, int number, int 
 // Entries of few rows: the tiles of all their key heads in a row, entry after
 // entry, each workgroup a run of them of one length (so that entries of very
 // different lengths fill the GPU to the end).  A head whose tiles lie in one run
-// is written at once, of others the runs' parts are joined (join_few).
+// is written at once, of others the runs' parts are joined (join_few).  64 entries
+// of 1 to 8192 keys and 8 heads of 128, 540 MB: 117 us, where one workgroup takes 95
+// for the longest entry alone.
 template <int DT, int CF, int DP>
 __device__ __forceinline__ void few_run(const CacheAttnArgs& a, int group, unsigned char* lds) {
   Job job;
@@ -954,7 +998,7 @@ __device__ __forceinline__ void few_run(const CacheAttnArgs& a, int group, unsig
     if (job.t1 > 0) attend_few<DT, CF, DP>(a, job, lds);
     return;
   }
-  auto weight = [](const Entry& e) { return few_tiles(e); };
+  auto weight = [](const Entry& e) { return few_units(e); };
   Entries<decltype(weight)> entries(a, weight);
   const int Hk = a.c.Hk;
   const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
@@ -968,11 +1012,13 @@ __device__ __forceinline__ void few_run(const CacheAttnArgs& a, int group, unsig
     while (x < end && x < (f.first + f.weight) * Hk) {
       const int in = (int)(x - f.first * Hk);
       job.hk = in / f.weight;
-      job.t0 = in - job.hk * f.weight;
-      job.t1 = f.weight - job.t0 < end - x ? f.weight : job.t0 + (int)(end - x);
-      job.slot = job.t0 == 0 && job.t1 == f.weight ? -1 : 2LL * group + (x == begin ? 0 : 1);
-      attend_few<DT, CF, DP>(a, job, lds);
-      x += job.t1 - job.t0;
+      const int from = in - job.hk * f.weight;
+      const int to = f.weight - from < end - x ? f.weight : from + (int)(end - x);
+      job.t0 = from > kStart ? from - kStart : 0;
+      job.t1 = to - kStart;
+      job.slot = job.t0 == 0 && to == f.weight ? -1 : 2LL * group + (x == begin ? 0 : 1);
+      if (job.t1 > job.t0) attend_few<DT, CF, DP>(a, job, lds);
+      x += to - from;
     }
   }
 }
@@ -1024,7 +1070,8 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a
   // whether all blocks are there, with scales that the widened numbers can take in
   bool plain = true;
   const int last = job.t1 * Z::BN < u.e.len ? job.t1 * Z::BN : u.e.len;
-  const int b0 = (job.t0 * Z::BN) >> c.log_block, b1 = (last + (1 << c.log_block) - 1) >> c.log_block;
+  const int b0 = (job.t0 * Z::BN) >> c.log_block;
+  const int b1 = (last + (1 << c.log_block) - 1) >> c.log_block;
   for (int i = b0 + threadIdx.x; i < b1; i += kThreads) {
     const int id = c.table[(long long)u.b * c.width + i];
     if (id < 0 || id >= c.blocks) {
@@ -1038,76 +1085,107 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a
   else attend_many<DT, CF, DP, true>(a, job, lds);
 }
 
-// Joins the parts of a row of key head number `unit` of the entries:
-// out = sum_s 2^(lse_s - lse) o_s.  LPR lanes a part, 4 components a lane; the
-// workgroup's sets of lanes take parts in turn and meet in LDS, in order.
+// Adds U parts (their sums' log2 and normed outputs) to a maximum, a sum and outputs.
+template <int U>
+__device__ __forceinline__ void take_parts(const float* w, const float4_t* v, float* m, float* sum,
+                                           float4_t* o) {
+  float m_new = *m;
+#pragma unroll
+  for (int i = 0; i < U; ++i) m_new = fmaxf(m_new, w[i]);
+  const float fall = __builtin_amdgcn_exp2f(*m - m_new);
+  *m = m_new;
+  *sum *= fall;
+  *o *= fall;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const float p = __builtin_amdgcn_exp2f(w[i] - m_new);
+    *sum += p;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) (*o)[j] = fmaf(p, v[i][j], (*o)[j]);
+  }
+}
+
+// Joins the parts of a row of the key head in which run number g + 1 begins, if
+// its first keys are of run g: out = sum_s 2^(lse_s - lse) o_s.  (Not a workgroup
+// for each head's rows, of which there may be far more than runs.)  LPR lanes a
+// part, 4 components a lane; the workgroup's sets of lanes take parts in turn and
+// meet in LDS, in order.  (A workgroup takes every kRows-th row.)
+constexpr int kRows = 4;
 template <int DT, int LPR>
-__device__ __forceinline__ void join_few(const CacheAttnArgs& a, int unit, int row) {
+__device__ __forceinline__ void join_few(const CacheAttnArgs& a, int g, int part) {
   constexpr int SETS = kThreads / LPR;
   __shared__ float tops[SETS], sums[SETS];
   __shared__ float4_t outs[SETS][LPR];
   const int Hk = a.c.Hk, D = a.c.D;
-  const int b = unit / Hk, hk = unit - b * Hk;
-  const Entry e = entry_of(a, b);
-  const int tiles = few_tiles(e);
-  if (tiles < 2 || row >= e.rows) return;
-  auto weight = [](const Entry& x) { return few_tiles(x); };
+  auto weight = [](const Entry& x) { return few_units(x); };
   Entries<decltype(weight)> entries(a, weight);
   const long long total = entries.total() * Hk, per = share_of(total, a.few_groups);
-  const long long u0 = entries.begin_of(b) * Hk + (long long)hk * tiles, u1 = u0 + tiles;
-  const int g0 = (int)(u0 / per), g1 = (int)((u1 - 1) / per);
-  if (g0 == g1) return;
+  const long long x = (g + 1) * per;
+  if (x >= total) return;
+  const auto f = entries.find(x / Hk);
+  const Entry e = f.e;
+  const int hk = (int)(x - f.first * Hk) / f.weight;
+  const long long u0 = f.first * Hk + (long long)hk * f.weight;
+  const int g0 = (int)((u0 + kStart) / per), g1 = (int)((u0 + f.weight - 1) / per);
+  if (g0 != g || g1 == g) return;
   const int set = threadIdx.x / LPR, lane = threadIdx.x % LPR;
   const bool live = 4 * lane < D;
-  float m = kLowest, sum = 0.0f;
-  float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int g = g0 + set; g <= g1; g += SETS) {
-    // a run's first part is its slot 0
-    const long long slot =
-        (2LL * g + (g == g0 && u0 != g * per ? 1 : 0)) * kFewRows + row;
-    const float w = a.part_lse[slot];
-    float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) v = *reinterpret_cast<const float4_t*>(a.part + slot * D + 4 * lane);
-    const float m_new = fmaxf(m, w), fall = __builtin_amdgcn_exp2f(m - m_new),
-                p = __builtin_amdgcn_exp2f(w - m_new);
-    m = m_new;
-    sum = fmaf(sum, fall, p);
+  for (int row = part; row < e.rows; row += kRows) {
+    float m = kLowest, sum = 0.0f;
+    float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int U = 4;   // parts that are on their way at a time
+    for (int g = g0 + set; g <= g1; g += U * SETS) {
+      float w[U];
+      float4_t v[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j] * fall);
+      for (int i = 0; i < U; ++i) {
+        const int gi = g + i * SETS;
+        // a run's first part is its slot 0
+        const long long slot = (2LL * gi + (gi == g0 && u0 > g0 * per ? 1 : 0)) * kFewRows + row;
+        w[i] = kNegInf;
+        v[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (gi <= g1) {
+          w[i] = a.part_lse[slot];
+          if (live) v[i] = *reinterpret_cast<const float4_t*>(a.part + slot * D + 4 * lane);
+        }
+      }
+      take_parts<U>(w, v, &m, &sum, &o);
+    }
+    __syncthreads();   // the last row's are read
+    if (lane == 0) {
+      tops[set] = m;
+      sums[set] = sum;
+    }
+    outs[set][lane] = o;
+    __syncthreads();
+    if (set > 0) continue;
+    float m_all = m;
+#pragma unroll
+    for (int s = 1; s < SETS; ++s) m_all = fmaxf(m_all, tops[s]);
+    sum = 0.0f;
+    o = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+      const float p = __builtin_amdgcn_exp2f(tops[s] - m_all);
+      sum = fmaf(sums[s], p, sum);
+      const float4_t v = outs[s][lane];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j]);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : sum;
+    const int qi = row / a.G, head = hk * a.G + row - qi * a.G;
+    const long long t = e.row0 + qi;
+    if (a.lse && lane == 0)
+      a.lse[t * (Hk * a.G) + head] =
+          sum == 0.0f ? kNegInf : (m_all + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (!live) continue;
+    char* op = a.out + t * a.o_r + head * a.o_h;
+    if constexpr (DT == DT_F32)
+      *reinterpret_cast<float4_t*>(op + 16 * lane) = o * inv;
+    else
+      *reinterpret_cast<u32x2_t*>(op + 8 * lane) =
+          u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
   }
-  if (lane == 0) {
-    tops[set] = m;
-    sums[set] = sum;
-  }
-  outs[set][lane] = o;
-  __syncthreads();
-  if (set > 0) return;
-  float m_all = m;
-#pragma unroll
-  for (int s = 1; s < SETS; ++s) m_all = fmaxf(m_all, tops[s]);
-  sum = 0.0f;
-  o = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int s = 0; s < SETS; ++s) {
-    const float p = __builtin_amdgcn_exp2f(tops[s] - m_all);
-    sum = fmaf(sums[s], p, sum);
-    const float4_t v = outs[s][lane];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[j], o[j]);
-  }
-  const float inv = sum > 0.0f ? 1.0f / sum : sum;
-  const int qi = row / a.G, head = hk * a.G + row - qi * a.G;
-  const long long t = e.row0 + qi;
-  if (a.lse && lane == 0)
-    a.lse[t * (Hk * a.G) + head] =
-        sum == 0.0f ? kNegInf : (m_all + __builtin_amdgcn_logf(sum)) * kLn2;
-  if (!live) return;
-  char* op = a.out + t * a.o_r + head * a.o_h;
-  if constexpr (DT == DT_F32)
-    *reinterpret_cast<float4_t*>(op + 16 * lane) = o * inv;
-  else
-    *reinterpret_cast<u32x2_t*>(op + 8 * lane) =
-        u32x2_t{pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv)};
 }
 
 // Joins the splits of the rows of a set, the workgroup `part` of kParts of it: LPR
@@ -1138,23 +1216,11 @@ __device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int 
         if (s + i < a.splits) {
           w[i] = a.many_lse[(s + i) * step + at];
           if (live)
-            v[i] = *reinterpret_cast<const float4_t*>(a.many + ((s + i) * step + at) * D + 4 * lane);
+            v[i] =
+                *reinterpret_cast<const float4_t*>(a.many + ((s + i) * step + at) * D + 4 * lane);
         }
       }
-      float m_new = m;
-#pragma unroll
-      for (int i = 0; i < U; ++i) m_new = fmaxf(m_new, w[i]);
-      const float fall = __builtin_amdgcn_exp2f(m - m_new);
-      m = m_new;
-      sum *= fall;
-      o *= fall;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const float p = __builtin_amdgcn_exp2f(w[i] - m);
-        sum += p;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = fmaf(p, v[i][j], o[j]);
-      }
+      take_parts<U>(w, v, &m, &sum, &o);
     }
     const float inv = sum > 0.0f ? 1.0f / sum : sum;
     if (a.lse && lane == 0)
@@ -1169,8 +1235,8 @@ __device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int 
   }
 }
 
-// What has parts: kParts workgroups for each of `units` sets, and behind them one
-// for each of the `rows` that a key head of an entry of few may have.
+// What has parts: kParts workgroups for each of `units` sets, and behind them, for each
+// run but the last of the few rows, `rows` of them, kRows if there are that many.
 template <int DT, int LPR>
 __global__ __launch_bounds__(kThreads) void join_kernel(const CacheAttnArgs a, int units, int rows,
                                                         int all) {
@@ -1208,10 +1274,10 @@ void launch(const CacheAttnArgs& a, hipStream_t stream) {
   else
     hipLaunchKernelGGL((few_kernel<DT, CF, DP>), dim3((unsigned)(units + groups)),
                        dim3(kFewThreads), 0, stream, a, units, all);
-  const int sets = a.splits > 1 ? units : 0, rows = most < kFewRows ? (int)most : kFewRows;
-  const int heads = groups > 0 && a.few_groups > 0 ? a.c.B * a.c.Hk : 0;
-  if (sets + heads > 0)
-    hipLaunchKernelGGL((join_kernel<DT, LPR>), dim3((unsigned)(sets * kParts + heads * rows)),
+  const int sets = a.splits > 1 ? units : 0, rows = most < kRows ? (int)most : kRows;
+  const int runs = groups > 0 && a.few_groups > 0 ? a.few_groups - 1 : 0;
+  if (sets + runs > 0)
+    hipLaunchKernelGGL((join_kernel<DT, LPR>), dim3((unsigned)(sets * kParts + runs * rows)),
                        dim3(kThreads), 0, stream, a, sets, rows, all);
 }
 
@@ -1236,6 +1302,11 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   const long long keys = (long long)a->c.width << a->c.log_block;
   const bool many = (long long)a->max_rows * a->G > kFewRows;
   if (many) {
+    // Sets of 128 rows, each with its keys in as many shares as make 4 workgroups
+    // a compute unit, of 512 keys at least: 9 entries of 517 rows in all behind up to 4096
+    // keys, 4 heads of 80 in fp16: 67 us; 2 a unit 77, 3: 69, 6: 71.  Where that is not
+    // one for every second unit, sets of 32 rows: 2 entries of 130 rows and 8 heads
+    // of 64, 520 keys, fp32: 13 us, with sets of 128 rows 25.
     const long long n = row_sets(*a, kManyRows) * a->c.Hk;
     long long s = 4LL * cus / n;
     if (s > keys / 512) s = keys / 512;
@@ -1245,14 +1316,21 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
       a->set = kManyRows;
       a->splits = (int)s;
     }
-    // (empty sets end at once; many entries take long to look through)
+    // Empty sets of an entry end at once, but each takes a workgroup; where only some
+    // entries have many rows, sets side by side have each workgroup look over all
+    // entries.  One prompt of 600 rows among others of 1 to 39, 2 heads of 64, side by
+    // side / of each entry: 300 entries 29 / 39 us, 700 56 / 76, 2000 258 / 197.
     const long long each = sets_of_each(*a, a->set) * a->c.B;
-    if (each * a->c.Hk < (1 << 22) && (each <= 2 * row_sets(*a, a->set) || a->c.B > 512))
+    if (each * a->c.Hk < (1 << 22) && (each <= 2 * row_sets(*a, a->set) || a->c.B > 1024))
       a->sets = (int)sets_of_each(*a, a->set);
   }
-  if (!allowed) return 0;
-  if (a->G <= kFewRows && keys > 1024 && a->c.B <= 1024 && a->c.B * (long long)a->c.Hk < (1 << 17))
-    a->few_groups = 8 / kFewWaves * cus;
+  // Few rows share their keys where the longest head alone may take longer than all
+  // together.  Heads of 128, ragged entries, shared / alone: up to 1100 keys, 32
+  // heads 15 / 18 us, 256 heads 24 / 19; up to 2048, 128 heads 22 / 28, 256 heads 31 / 30;
+  // up to 8192, 32 heads 26 / 94, 512 heads 115 / 128, 1024 heads 228 / 250.  Heads of 64:
+  // up to 2048 keys, 64 heads 16 / 19, 256 heads 27 / 20.
+  if (allowed && a->G <= kFewRows && keys >= 1024 && keys >= 16LL * a->c.B * a->c.Hk)
+    a->few_groups = 2 * cus;
   const long long rows = a->splits > 1 ? (long long)a->T * a->G * a->c.Hk * a->splits : 0;
   return (2LL * a->few_groups * kFewRows + rows) * (a->c.D + 1) * 4;
 }

@@ -39,7 +39,8 @@ template <int CF, int DT> __device__ __forceinline__ u32x2_t code_values16(uint3
   }
 }
 // 8 codes: an operand of a matrix instruction.
-template <int CF, int DT> __device__ __forceinline__ u32x4_t code_values16(uint32_t w0, uint32_t w1) {
+template <int CF, int DT>
+__device__ __forceinline__ u32x4_t code_values16(uint32_t w0, uint32_t w1) {
   const u32x2_t a = code_values16<CF, DT>(w0), b = code_values16<CF, DT>(w1);
   return u32x4_t{a[0], a[1], b[0], b[1]};
 }

@@ -262,6 +262,25 @@ def test_more_entries_than_a_wave_has_lanes():
     check(queries(n, 4, 64, "bf16"), cache, one, True, what="single tokens", max_rows=1)
 
 
+@pytest.mark.parametrize("B", [5, 64, 130])
+@pytest.mark.parametrize("codes", ["i8", "e4m3"])
+def test_keys_shared_by_workgroups(B, codes):
+    """Entries of very different lengths, some empty, whose keys workgroups share."""
+    g = torch.Generator().manual_seed(B)
+    lengths = torch.randint(0, 200, (B,), generator=g).tolist()
+    lengths[1], lengths[3], lengths[-1] = 4096, 0, 3001
+    cache = C.Cache(B, lengths, 64, 2, 64, codes, seed=17, width=80)
+    check(queries(B, 8, 64, "bf16"), cache, C.starts([1] * B), True, what=f"{B} entries")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_whose_keys_are_shared(dtype, d):
+    """Up to 32 rows of a key head, in parts of several workgroups."""
+    cache = C.Cache(4, [5000, 33, 2500, 129], 32, 2, d, "e4m3", seed=18)
+    check(queries(10, 16, d, dtype), cache, C.starts([3, 1, 4, 2]), True, max_rows=4, what="32 rows")
+
+
 def test_nothing_to_do():
     cache = C.Cache(2, [5, 5], 16, 2, 64, "i8")
     q = queries(0, 4, 64, "bf16")
