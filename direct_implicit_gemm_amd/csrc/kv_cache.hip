@@ -7,7 +7,9 @@
 //
 // The unit of either is one head's keys or values of one block: a wave takes
 // one, so that the largest magnitude is a reduction over its lanes.  Both are
-// bound by memory.
+// bound by memory: 12 entries of 3200 tokens, 20 heads of 128 in blocks of 64, written
+// in 121 us and read in 128 (591 MB each, bfloat16 and E4M3: 4.9 and 4.6 TB/s, where a
+// copy of 1 GiB reaches 5.1).  One token of each of 64 entries, 8 heads: 5 us, a launch.
 #include "codes.h"
 #include "layer.h"
 
@@ -73,7 +75,9 @@ template <int CF> __device__ __forceinline__ float scale_for(uint32_t top) {
 
 // One head's keys or values of a block: `rows` rows from x on become the tokens
 // from `held` on of the block at `codes`.  HELD reads of a lane stay in registers
-// between the largest magnitude and the rounding, others are read again.
+// between the largest magnitude and the rounding, others are read again.  (Above:
+// largest magnitudes of two 16-bit values at a time, no look for infinities where
+// there are none, and all of a block's 16 KB in registers 168 -> 124 us.)
 template <int DT, int CF, int HELD>
 __device__ __forceinline__ void write_block(const char* x, long long x_row, char* codes,
                                             long long token, float* scale, int rows, int held,
@@ -153,7 +157,8 @@ __device__ __forceinline__ void write_block(const char* x, long long x_row, char
 
 // A workgroup looks over a block's number of rows for those that are their entry's
 // first in a block, and its waves take the blocks' heads, keys and values, in turn (with
-// the gridDim.y workgroups of the same rows).
+// the gridDim.y workgroups of the same rows).  Windows of 16 rows, whatever the block's
+// size: 520 us instead of 168.
 template <int DT, int CF, int HELD>
 __global__ __launch_bounds__(kThreads) void write_kernel(const CacheCopyArgs a) {
   __shared__ int count, first[kWindow], rows[kWindow], held[kWindow], block[kWindow];
@@ -197,10 +202,10 @@ __global__ __launch_bounds__(kThreads) void write_kernel(const CacheCopyArgs a) 
     const int t = __builtin_amdgcn_readfirstlane(first[f]);
     const int id = __builtin_amdgcn_readfirstlane(block[f]);
     write_block<DT, CF, HELD>(a.x[kv] + t * a.row[kv] + h * a.head[kv], a.row[kv],
-                        c.codes[kv] + id * c.block[kv] + h * c.head[kv], c.token[kv],
-                        c.scale[kv] + (long long)id * c.Hk + h,
-                        __builtin_amdgcn_readfirstlane(rows[f]),
-                        __builtin_amdgcn_readfirstlane(held[f]), c.D);
+                              c.codes[kv] + id * c.block[kv] + h * c.head[kv], c.token[kv],
+                              c.scale[kv] + (long long)id * c.Hk + h,
+                              __builtin_amdgcn_readfirstlane(rows[f]),
+                              __builtin_amdgcn_readfirstlane(held[f]), c.D);
   }
 }
 
@@ -283,6 +288,7 @@ struct Write {
     const unsigned block = (2u * a.c.Hk + 3) / 4;
     const unsigned rows = turns(x, 2LL * a.c.Hk * (a.T < size ? a.T : size));
     const dim3 grid((unsigned)x, block > rows ? block : rows), threads(kThreads);
+    // (registers for no more than a block has: blocks of 16 tokens leave most idle)
     if (size * a.c.D * Elem<DT>::bytes <= 8 * 1024)
       hipLaunchKernelGGL((write_kernel<DT, CF, 8>), grid, threads, 0, stream, a);
     else

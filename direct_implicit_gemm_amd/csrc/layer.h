@@ -136,6 +136,7 @@ struct LinearArgs {
   // plan: sums of runs of the sum's axis [splits][T][N up to 64s], the runs' bytes
   float* part;
   int splits, run, tile;
+  int stages;   // of tiles of 128
 };
 long long linear_plan(LinearArgs* a, int dtype, int cus, bool allowed);
 libconv_status linear_launch(LinearArgs a, int dtype, hipStream_t stream);

@@ -16,7 +16,8 @@ namespace {
 // hardware's (about one step each); what is left is far below a 16-bit output's
 // step, and a few steps of a 32-bit one.
 template <int DT, int ACT> __device__ __forceinline__ float activated(float v) {
-  constexpr float kLog2e = 1.4426950408889634f, kTwoC = 2.0f * 0.7978845608028654f;   // sqrt(2 / pi)
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float kTwoC = 2.0f * 0.7978845608028654f;   // sqrt(2 / pi)
   if constexpr (ACT == LIBCONV_ACT_RELU) return v > 0.0f ? v : 0.0f;
   if constexpr (ACT == LIBCONV_ACT_GELU) {
     if constexpr (DT == DT_F32) {
@@ -121,9 +122,16 @@ __device__ __forceinline__ int chunk_at(int row, int c) { return c ^ ((row >> 1)
 
 // BM tokens x BN outputs, WM x WN waves; stages of 128 bytes of the sums' axis, NS
 // of them in LDS or on their way.  Runs: the sums of a run of the sum's axis.
+// 256 x 256 with 8 waves of 128 x 64: each number from LDS meets as many others as the
+// registers of 2 waves a SIMD hold sums.  8192 x 4096 x 8192 in bfloat16: 437 us (1.26
+// PFLOP/s; the library's product 420, matrix instructions alone 311), with bias, tanh
+// GELU and residual 459: the matrix units, at the clock that they leave (1.7 GHz).  4
+// waves of 128 x 128: 445; stages of 64 bytes, 4 of them: 475; a stage's copies in one
+// step 443, over four 455.  fp32, 4096 x 4096 x 4096: 148 TFLOP/s (the library 139).
 template <int DT, int BM, int BN, int WM, int WN, int NS, int SPREAD, bool Runs>
-__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LinearArgs a, int tiles_m,
-                                                               int tiles_n) {
+__global__
+__launch_bounds__(64 * WM * WN, WM * WN == 4 && NS * (BM + BN) > 640 ? 1 : 2)   // by their room
+void tile_kernel(const LinearArgs a, int tiles_m, int tiles_n) {
   constexpr int SB = 128;
   constexpr int EB = Elem<DT>::bytes;
   constexpr int THREADS = 64 * WM * WN;
@@ -198,7 +206,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LinearArgs 
   }
   auto read = [&](int at, int k, int n, u32x4_t* w, u32x4_t* x) __attribute__((always_inline)) {
     if (n >= 1 && n <= MB) {
-      x[n - 1] = *reinterpret_cast<const u32x4_t*>(lds + at_x[k] + (at * STAGE + (n - 1) * 32 * SB));
+      x[n - 1] =
+          *reinterpret_cast<const u32x4_t*>(lds + at_x[k] + (at * STAGE + (n - 1) * 32 * SB));
     } else {
       const int i = n == 0 ? 0 : n - MB;
       w[i] = *reinterpret_cast<const u32x4_t*>(lds + at_w[k] + (at * STAGE + i * 32 * SB));
@@ -334,7 +343,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const LinearArgs 
   }
 }
 
-// y from the sums of its runs, in their order; a thread 16 bytes of a token.
+// y from the sums of its runs, in their order; a thread 16 bytes of a token.  Few rows
+// are bound by the weights' way to the compute units, which takes them all: 64 rows of
+// 4096 sums and outputs have 64 tiles, in 4 runs each (8.5 us, 38 MB at 4.4 TB/s) and
+// the runs' sums 3.5 us later; twice the runs 14.1 us instead of 12.2.
 template <int DT> __global__ __launch_bounds__(256) void sum_kernel(const LinearArgs a) {
   constexpr int E = 16 / Elem<DT>::bytes, U = 8;
   const int n = (blockIdx.x * 256 + threadIdx.x) * E, t = blockIdx.y;
@@ -352,7 +364,8 @@ template <int DT> __global__ __launch_bounds__(256) void sum_kernel(const Linear
       for (int e = 0; e < E / 4; ++e) {
         p[u][e] = float4_t{0, 0, 0, 0};
         if (s + u < a.splits)
-          p[u][e] = *reinterpret_cast<const float4_t*>(part + (long long)(s + u) * a.T * n_pad + 4 * e);
+          p[u][e] = *reinterpret_cast<const float4_t*>(part + (long long)(s + u) * a.T * n_pad +
+                                                       4 * e);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -384,17 +397,23 @@ template <int DT> void launch_dt(const LinearArgs& a, hipStream_t stream) {
       launch_tile<DT, 256, 256, 2, 4, 2, 2>(a, stream);
       return;
     }
+    if (a.tile == 128 && a.stages == 4) {
+      launch_tile<DT, 128, 128, 2, 2, 4, 4>(a, stream);
+      return;
+    }
   }
-  if (a.tile >= 128) launch_tile<DT, 128, 128, 2, 2, 2, 4>(a, stream);
+  if (a.tile == 128) launch_tile<DT, 128, 128, 2, 2, 2, 4>(a, stream);
   else launch_tile<DT, 64, 64, 2, 2, 4, 1>(a, stream);
 }
 
 // Time of a launch in units of one 256 x 256 tile: rounds of workgroups over
 // the compute units, each as long as its workgroups together on one unit.
-double tile_cost(const LinearArgs& a, int cus, int b, int per_cu, double speed) {
+// `alone`: the speed of workgroups that have a unit for themselves.
+double tile_cost(const LinearArgs& a, int cus, int b, int per_cu, double speed, double alone) {
   const double tiles = (double)((a.T + b - 1) / b) * ((a.N + b - 1) / b);
+  if (tiles <= cus) return b * b / alone;
   const double rounds = (double)(long long)((tiles + (double)cus * per_cu - 1) / (cus * per_cu));
-  const double share = tiles < (double)cus * per_cu ? (tiles > cus ? tiles / cus : 1.0) : per_cu;
+  const double share = tiles < (double)cus * per_cu ? tiles / cus : per_cu;
   return rounds * share * b * b / speed;
 }
 
@@ -403,9 +422,16 @@ double tile_cost(const LinearArgs& a, int cus, int b, int per_cu, double speed) 
 long long linear_plan(LinearArgs* a, int dtype, int cus, bool allowed) {
   a->splits = a->run = 0;
   const bool f32 = dtype == LIBCONV_F32;
-  const double c256 = tile_cost(*a, cus, 256, 1, 1.0), c128 = tile_cost(*a, cus, 128, 2, 0.75),
-               c64 = tile_cost(*a, cus, 64, 4, 0.4);
+  // The speeds are from products with 4096 sums and 4096 outputs in bfloat16, by tiles of
+  // 64 / 128 / 256 (us): 256 rows 18 / 26 / 74, 1000 rows 59 / 37 / 78, 2048 rows 134 / 73 / 89,
+  // 4096 rows 257 / 161 / 132; 2167 rows of 1280, 3840 outputs 41 / 27 / 34.
+  const double c256 = tile_cost(*a, cus, 256, 1, 1.0, 1.0),
+               c128 = tile_cost(*a, cus, 128, 2, 0.75, f32 ? 0.75 : 0.88),
+               c64 = tile_cost(*a, cus, 64, 4, 0.4, 0.4);
   a->tile = !f32 && c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+  // One workgroup a compute unit: its room goes into stages (1000 rows 48 -> 37 us;
+  // fp32, bound by the matrix units, 296 -> 299).
+  a->stages = !f32 && (long long)((a->T + 127) / 128) * ((a->N + 127) / 128) <= cus ? 4 : 2;
   if (!allowed || a->T == 0) return 0;
   const long long row = (long long)a->K * (f32 ? 4 : 2), n_pad = (a->N + 63) / 64 * 64;
   const long long tiles = ((a->T + 63LL) / 64) * (n_pad / 64);
@@ -413,7 +439,7 @@ long long linear_plan(LinearArgs* a, int dtype, int cus, bool allowed) {
   if (splits > row / 512) splits = row / 512;
   if (splits > 16) splits = 16;
   if (splits < 2) return 0;
-  a->tile = 64;
+  a->tile = 64;   // (64 rows, 4096 sums and outputs: 12.2 us, without runs 15.4)
   a->run = (int)((row + splits - 1) / splits + 127) / 128 * 128;
   a->splits = (int)((row + a->run - 1) / a->run);
   return 4LL * a->splits * a->T * n_pad;

@@ -60,6 +60,14 @@ def test_large_tiles(dtype):
     check(*(lambda x, w, b, r: (x, w, b, "silu", r))(*make(4097, 1032, 4101, dtype)), what="odd")
 
 
+@pytest.mark.parametrize("dtype", C.TYPES)
+@pytest.mark.parametrize("T,K,N", [(1000, 72, 2500), (1030, 640, 3700), (513, 1032, 5000)])
+def test_tiles_of_128_with_a_compute_unit_each(T, K, N, dtype):
+    """Stages that lie further ahead, fewer of them than places too."""
+    x, w, b, r = make(T, K, N, dtype, seed=3)
+    check(x, w, b, "silu", r, what="4 stages")
+
+
 def test_strides_and_in_place():
     x, w, b, r = make(70, 264, 130, "bf16")
     wide = torch.zeros(70, 700, dtype=torch.bfloat16, device="cuda")   # rows of 1400 bytes
