@@ -8,7 +8,6 @@
 namespace libconv {
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLowest = -3.402823466e38f;   // the maximum of no keys: finite, so that no
                                               // difference of maxima is a NaN
