@@ -1321,7 +1321,9 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
     // entries.  One prompt of 600 rows among others of 1 to 39, 2 heads of 64, side by
     // side / of each entry: 300 entries 29 / 39 us, 700 56 / 76, 2000 258 / 197.
     const long long each = sets_of_each(*a, a->set) * a->c.B;
-    if (each * a->c.Hk < (1 << 22) && (each <= 2 * row_sets(*a, a->set) || a->c.B > 1024))
+    // (2^24 workgroups of 256 lanes are the most of a launch)
+    if ((each + a->c.B) * a->c.Hk < (1 << 24) - 4096 &&
+        (each <= 2 * row_sets(*a, a->set) || a->c.B > 1024))
       a->sets = (int)sets_of_each(*a, a->set);
   }
   // Few rows share their keys where the longest head alone may take longer than all

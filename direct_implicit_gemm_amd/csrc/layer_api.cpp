@@ -161,9 +161,10 @@ libconv_status cache_shape(int B, int blocks, int block_size, int width, int k_h
   if (head_dim > 128 || head_dim % 16 != 0 || block_size < 16 || block_size > 256 ||
       (block_size & (block_size - 1)) != 0)
     return LIBCONV_ERR_UNSUPPORTED;
-  // positions and heads are counted in 31 bits, bytes of scales too
+  // positions and heads are counted in 31 bits, bytes of scales too; a workgroup may
+  // have to look over all entries
   if ((long long)width * block_size > kMaxInt - 8192 || k_heads > (1 << 20) ||
-      (double)blocks * k_heads * 4 > (double)(kMaxInt - 8192) || B > (1 << 24) - 4096)
+      (double)blocks * k_heads * 4 > (double)(kMaxInt - 8192) || B > 65536)
     return LIBCONV_ERR_TOO_LARGE;
   return LIBCONV_OK;
 }

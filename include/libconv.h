@@ -697,7 +697,7 @@ long long libconv_lora_workspace(int T, int K, int N, int rank, int n_adapters, 
  * block_size: 16, 32, 64, 128 or 256 tokens.  head_dim: a multiple of 16 up to
  * 128 (else LIBCONV_ERR_UNSUPPORTED).  Tokens are at least head_dim apart.
  *
- * B entries (requests), whose rows lie one after another in T rows:
+ * B entries (requests), 65536 at most, whose rows lie one after another in T rows:
  * row_starts   [B + 1] ints, ascending: entry b has rows row_starts[b] <= t <
  *              row_starts[b + 1] (clamped to [0, T]), n of them, maybe none.
  * lengths      [B] ints: the entry's tokens in the cache with those of this call,

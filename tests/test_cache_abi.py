@@ -46,7 +46,7 @@ COMMON = [
     (dict(block_size=8), UNSUPPORTED), (dict(block_size=48), UNSUPPORTED),
     (dict(block_size=512), UNSUPPORTED),
     (dict(table_width=1 << 28), LARGE), (dict(blocks=1 << 30), LARGE), (dict(k_heads=1 << 21), LARGE),
-    (dict(B=1 << 24), LARGE),
+    (dict(B=1 << 24), LARGE), (dict(B=65537), LARGE),
     (dict(k_cache=KC + 8), ALIGN), (dict(v_scale=VS + 2), ALIGN), (dict(lengths=LN + 1), ALIGN),
     (dict(block_table=TB + 2), ALIGN),
 ]
@@ -123,6 +123,7 @@ def attention(s=None, **kw):
     (dict(q_heads=0), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(scale=float("inf")), SHAPE),
     (dict(workspace_bytes=-1), SHAPE), (dict(s={0: -1}), SHAPE), (dict(s={2: 1 << 40}), SHAPE),
     (dict(T=1 << 26), LARGE), (dict(T=1 << 25, q_heads=64), LARGE), (dict(B=1 << 23), LARGE),
+    (dict(B=65537), LARGE),
     (dict(q=Q + 8), ALIGN), (dict(s={3: 60}), ALIGN), (dict(lse=LSE + 2), ALIGN),
     (dict(workspace=WS + 16, workspace_bytes=64), ALIGN),
     (dict(out=Q), ALIAS), (dict(out=KC), ALIAS), (dict(lse=OUT), ALIAS), (dict(lse=VC), ALIAS),

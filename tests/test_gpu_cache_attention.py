@@ -307,3 +307,15 @@ def test_many_entries_of_many_rows(B):
     first = check(q, cache, C.starts(rows), True, what=str(B))
     again = check(q, cache, C.starts(rows), True, what="max_rows", max_rows=900)
     assert torch.equal(first, again)
+
+
+def test_the_most_entries():
+    """65536 entries, few of them with rows; one with many."""
+    n = 65536
+    cache = C.Cache(n, [1 + i % 16 for i in range(n)], 16, 1, 16, "i8", seed=19)
+    rows = [1 if i % 97 == 0 else 0 for i in range(n)]
+    check(queries(sum(rows), 2, 16, "bf16"), cache, C.starts(rows), True, what="single", max_rows=1)
+    rows[40000] = 50
+    check(queries(sum(rows), 2, 16, "bf16"), cache, C.starts(rows), True, what="and one of 50")
+    check(queries(sum(rows), 2, 16, "bf16"), cache, C.starts(rows), True, what="max_rows",
+          max_rows=50)
