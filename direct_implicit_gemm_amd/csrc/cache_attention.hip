@@ -1039,7 +1039,16 @@ __global__ __launch_bounds__(kFewThreads, 2) void few_kernel(const CacheAttnArgs
   attend_few<DT, CF, DP>(a, job, lds);
 }
 
-// `units` sets of 128 rows of a key head, the keys in a.splits shares, a workgroup
+// Shares of a set's keys: up to a.splits, of kShare tiles at least.  (As many of every
+// set: prompts of 600 rows with 2000 keys beside 20 single tokens 56 us, like this 41;
+// 512 rows with 16384 keys beside 512 139 and 124.  4 or 8 tiles: the same within 3 %.)
+constexpr int kShare = 6;
+__device__ __forceinline__ int shares_of(const CacheAttnArgs& a, const Unit& u, int tile) {
+  const int s = (u.keys + tile - 1) / tile / kShare;
+  return s < 1 ? 1 : s > a.splits ? a.splits : s;
+}
+
+// `units` sets of 128 rows of a key head, the keys in up to a.splits shares, a workgroup
 // each, and behind them the workgroups of the entries of few rows, which fill the
 // GPU while the last sets end.
 template <int DT, int CF, int DP>
@@ -1059,14 +1068,15 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a
   // an entry the longest one held up the end.)
   if (!unit_of(a, blockIdx.x - split * units, kManyRows, all, &u)) return;
   const CacheView& c = a.c;
-  const int tiles = (u.keys + Z::BN - 1) / Z::BN;
+  const int tiles = (u.keys + Z::BN - 1) / Z::BN, shares = shares_of(a, u, Z::BN);
+  if (split >= shares) return;
   const Job job = {u.e,
                    u.b,
                    u.hk,
                    u.set,
-                   (int)((long long)tiles * split / a.splits),
-                   (int)((long long)tiles * (split + 1) / a.splits),
-                   a.splits > 1 ? split : -1};
+                   (int)((long long)tiles * split / shares),
+                   (int)((long long)tiles * (split + 1) / shares),
+                   shares > 1 ? split : -1};
   // whether all blocks are there, with scales that the widened numbers can take in
   bool plain = true;
   const int last = job.t1 * Z::BN < u.e.len ? job.t1 * Z::BN : u.e.len;
@@ -1195,6 +1205,8 @@ template <int DT, int LPR>
 __device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int part, int all) {
   Unit u;
   if (!unit_of(a, unit, kManyRows, all, &u)) return;
+  const int shares = shares_of(a, u, Wide<128>::BN);
+  if (shares == 1) return;
   const int lane = threadIdx.x % LPR, D = a.c.D, heads = a.c.Hk * a.G;
   const bool live = 4 * lane < D;
   for (int r = threadIdx.x / LPR + part * (kThreads / LPR); r < kManyRows;
@@ -1206,14 +1218,14 @@ __device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int 
     float m = kLowest, sum = 0.0f;
     float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
     constexpr int U = 4;
-    for (int s = 0; s < a.splits; s += U) {
+    for (int s = 0; s < shares; s += U) {
       float w[U];
       float4_t v[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         w[i] = kNegInf;
         v[i] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        if (s + i < a.splits) {
+        if (s + i < shares) {
           w[i] = a.many_lse[(s + i) * step + at];
           if (live)
             v[i] =
@@ -1302,8 +1314,8 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   const long long keys = (long long)a->c.width << a->c.log_block;
   const bool many = (long long)a->max_rows * a->G > kFewRows;
   if (many) {
-    // Sets of 128 rows, each with its keys in as many shares as make 4 workgroups
-    // a compute unit, of 512 keys at least: 9 entries of 517 rows in all behind up to 4096
+    // Sets of 128 rows, each with its keys in up to as many shares as make 4 workgroups
+    // a compute unit: 9 entries of 517 rows in all behind up to 4096
     // keys, 4 heads of 80 in fp16: 67 us; 2 a unit 77, 3: 69, 6: 71.  Where that is not
     // one for every second unit, sets of 32 rows: 2 entries of 130 rows and 8 heads
     // of 64, 520 keys, fp32: 13 us, with sets of 128 rows 25.

@@ -57,14 +57,16 @@ def starts(rows):
 
 def of_entry(cache, b, name):
     """(values [n, Hk, D] in 64 bits, which positions lie in a block)."""
-    codes, scale = cache.host(name)
+    codes, scale = getattr(cache, name), getattr(cache, name + "s").cpu().double()
     table = cache.table[b].cpu().long()
     n = max(0, min(int(cache.lengths[b]), table.numel() * cache.block))
     p = torch.arange(n)
     at = table[p // cache.block]
     there = (at >= 0) & (at < len(codes))
     at = torch.where(there, at, torch.zeros_like(at))
-    value = codes[at, p % cache.block] * scale[at][..., None]
+    used, of = at.unique(return_inverse=True)   # (the entry's blocks only: caches are large)
+    part = codes.view(torch.uint8)[used.to(codes.device)].view(codes.dtype).cpu().float().double()
+    value = part[of, p % cache.block] * scale[at][..., None]
     return torch.where(there[:, None, None], value, torch.zeros(()).double()), there
 
 
