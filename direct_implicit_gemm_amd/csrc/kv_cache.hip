@@ -73,6 +73,26 @@ template <int CF> __device__ __forceinline__ float scale_for(uint32_t top) {
   return __builtin_bit_cast(float, (uint32_t)e << 23);
 }
 
+// Whether products with it and quotients by it are exact, as those of the scales
+// written here (powers of two, no denormal ones) are.
+__device__ __forceinline__ bool divides(float s) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, s);
+  return (u & 0x7fffffu) == 0 && u != 0;
+}
+// A number in fp32 from which its code is rounded as from itself: inexact ones get
+// an odd last bit, and lie on no border between two codes.  (The quotients of other
+// scales in fp32, and then rounded to codes: 45.5 / 7 = 6.5 became 7, and of the
+// bfloat16 numbers 1 in 100 met another code by a scale of 0.3.)
+__device__ __forceinline__ float round_to_odd(double q) {
+  const float f = (float)q;
+  uint32_t u = __builtin_bit_cast(uint32_t, f);
+  if ((double)f != q) {
+    if (__builtin_fabs((double)f) > __builtin_fabs(q)) --u;
+    u |= 1u;
+  }
+  return __builtin_bit_cast(float, u);
+}
+
 // One head's keys or values of a block: `rows` rows from x on become the tokens
 // from `held` on of the block at `codes`.  HELD reads of a lane stay in registers
 // between the largest magnitude and the rounding, others are read again.  (Above:
@@ -121,26 +141,33 @@ __device__ __forceinline__ void write_block(const char* x, long long x_row, char
   // (a scale that is no positive number stands for codes of no value)
   const float old = old_as_is > 0.0f && __builtin_isfinite(old_as_is) ? old_as_is : 0.0f;
   const float s = fmaxf(scale_for<CF>(top), old), inv = 1.0f / s;
-  auto write = [&](int i, const u32x4_t& v) {
+  auto write = [&](int i, const u32x4_t& v, bool exact) __attribute__((always_inline)) {
     const int row = by.row(i);
     float f[E];
     unpack<DT>(v, f);
 #pragma unroll
-    for (int j = 0; j < E; ++j) f[j] *= inv;
+    for (int j = 0; j < E; ++j)
+      f[j] = exact ? f[j] * inv : round_to_odd((double)f[j] / (double)s);
     char* at = codes + (held + row) * token + (i - row * chunks) * E;
     u32x2_t w;
 #pragma unroll
     for (int j = 0; j < E / 4; ++j)
-      w[j] = finite ? codes_within<CF>(f + 4 * j) : codes_of<CF>(f + 4 * j);
+      w[j] = finite && exact ? codes_within<CF>(f + 4 * j) : codes_of<CF>(f + 4 * j);
     if constexpr (EB == 4) *reinterpret_cast<uint32_t*>(at) = w[0];
     else *reinterpret_cast<u32x2_t*>(at) = w;
   };
+  if (divides(s)) {
 #pragma unroll
-  for (int u = 0; u < HELD; ++u)
-    if (u * 64 + lane < total) write(u * 64 + lane, raw[u]);
-  for (int i = HELD * 64 + lane; i < total; i += 64) write(i, read(i));
-  if (held > 0 && s != old_as_is) {
+    for (int u = 0; u < HELD; ++u)
+      if (u * 64 + lane < total) write(u * 64 + lane, raw[u], true);
+    for (int i = HELD * 64 + lane; i < total; i += 64) write(i, read(i), true);
+  } else {   // (a scale that others wrote; read again, for one copy of the division)
+#pragma unroll 1
+    for (int i = lane; i < total; i += 64) write(i, read(i), false);
+  }
+  if (held > 0 && s != old_as_is) {   // (s is a power of two then, and its quotients exact)
     const float down = old / s;
+    const bool exact = divides(old);
     const int words = D / 4;
     for (int i = lane; i < held * words; i += 64) {
       const int row = i / words;
@@ -148,7 +175,8 @@ __device__ __forceinline__ void write_block(const char* x, long long x_row, char
       float f[4];
       code_values<CF>(*at, f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] *= down;
+      for (int j = 0; j < 4; ++j)
+        f[j] = exact ? f[j] * down : round_to_odd((double)f[j] * ((double)old * (double)inv));
       *at = codes_of<CF>(f);
     }
   }
