@@ -9,6 +9,8 @@
 #include "device_common.h"
 #include "layer.h"
 
+#include <cmath>
+
 namespace libconv {
 namespace {
 
@@ -414,15 +416,15 @@ template <int DT> void launch_dt(const LinearArgs& a, hipStream_t stream) {
   else launch_tile<DT, 64, 64, 2, 2, 4, 1>(a, stream);
 }
 
-// Time of a launch in units of one 256 x 256 tile: rounds of workgroups over
-// the compute units, each as long as its workgroups together on one unit.
-// `alone`: the speed of workgroups that have a unit for themselves.
-double tile_cost(const LinearArgs& a, int cus, int b, int per_cu, double speed, double alone) {
-  const double tiles = (double)((a.T + b - 1) / b) * ((a.N + b - 1) / b);
-  if (tiles <= cus) return b * b / alone;
-  const double rounds = (double)(long long)((tiles + (double)cus * per_cu - 1) / (cus * per_cu));
-  const double share = tiles < (double)cus * per_cu ? tiles / cus : per_cu;
-  return rounds * share * b * b / speed;
+// Time that a launch's sums of one element take on the fullest compute unit, with the
+// sums' axis in `runs` runs, in units of one element of 256 x 256 tiles on it.  `alone`:
+// the speed where no unit has a second workgroup.  (Workgroups on one unit share its
+// matrix units: how many its LDS holds at a time does not count.)
+double fullest(const LinearArgs& a, int cus, int side, int runs, double speed, double alone) {
+  const double tiles =
+      (double)((a.T + side - 1) / side) * ((a.N + side - 1) / side) * runs;
+  const double most = std::ceil(tiles / cus);
+  return most * side * side / (most > 1.0 ? speed : alone);
 }
 
 }  // namespace
@@ -430,26 +432,48 @@ double tile_cost(const LinearArgs& a, int cus, int b, int per_cu, double speed, 
 long long linear_plan(LinearArgs* a, int dtype, int cus, bool allowed) {
   a->splits = a->run = 0;
   const bool f32 = dtype == LIBCONV_F32;
-  // The speeds are from products with 4096 sums and 4096 outputs in bfloat16, by tiles of
+  // 16 bits, from products with 4096 sums and 4096 outputs in bfloat16, by tiles of
   // 64 / 128 / 256 (us): 256 rows 18 / 26 / 74, 1000 rows 59 / 37 / 78, 2048 rows 134 / 73 / 89,
-  // 4096 rows 257 / 161 / 132; 2167 rows of 1280, 3840 outputs 41 / 27 / 34.
-  const double c256 = tile_cost(*a, cus, 256, 1, 1.0, 1.0),
-               c128 = tile_cost(*a, cus, 128, 2, 0.75, f32 ? 0.75 : 0.88),
-               c64 = tile_cost(*a, cus, 64, 4, 0.4, 0.4);
+  // 4096 rows 257 / 161 / 132; 2167 rows of 1280, 3840 outputs 41 / 27 / 34.  fp32 is bound
+  // by the matrix instructions, whatever the tile, and what is left idle decides: 625 rows
+  // of 2728, 3884 outputs (610 and 155 tiles of 64 and 128) 132 / 167, 2837 of 1304, 279 outputs
+  // 26 / 84, 3769 of 368, 4123 outputs (3835 and 990) 116 / 113.
+  const double c256 = fullest(*a, cus, 256, 1, 1.0, 1.0),
+               c128 = f32 ? fullest(*a, cus, 128, 1, 1.0, 1.0)
+                          : fullest(*a, cus, 128, 1, 0.75, 0.75);
+  const double s64 = f32 ? 0.94 : 0.4, alone64 = f32 ? 0.94 : 0.3;
+  const double c64 = fullest(*a, cus, 64, 1, s64, alone64);
   a->tile = !f32 && c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
   // One workgroup a compute unit: its room goes into stages (1000 rows 48 -> 37 us;
   // fp32, bound by the matrix units, 296 -> 299).
   a->stages = !f32 && (long long)((a->T + 127) / 128) * ((a->N + 127) / 128) <= cus ? 4 : 2;
-  if (!allowed || a->T == 0) return 0;
+  if (!allowed || a->T == 0 || a->T > 65535) return 0;   // (a row of the sums' grid each)
+  // Runs of the sums' axis, in tiles of 64, where the fullest unit is done sooner by more
+  // than the runs' sums take.  Microseconds: a stage of 128 bytes of a 64 x 64 tile at speed
+  // 1, three stages for a tile's start and end, `sum` for the second launch (16 bits: with
+  // what a first load waits for), 6 bytes a picosecond for the partial sums.  Of 220
+  // sizes of 1 to 8192 rows, 128 to 4096 sums, 64 to 14336 outputs in each type, times are
+  // 1.4 % (fp32) and 0.7 % (bfloat16) over the best of all tiles and runs; as many runs as
+  // have a compute unit each: 5.8 and 7.6 %.  136 rows of 3624, 3934 outputs in fp32 (186
+  // tiles) 61 us, in runs 52; 1462 rows of 688, 188 outputs in bfloat16 6.0, in runs 8.0.
   const long long row = (long long)a->K * (f32 ? 4 : 2), n_pad = (a->N + 63) / 64 * 64;
-  const long long tiles = ((a->T + 63LL) / 64) * (n_pad / 64);
-  long long splits = cus / tiles;
-  if (splits > row / 512) splits = row / 512;
-  if (splits > 16) splits = 16;
-  if (splits < 2) return 0;
-  a->tile = 64;   // (64 rows, 4096 sums and outputs: 12.2 us, without runs 15.4)
-  a->run = (int)((row + splits - 1) / splits + 127) / 128 * 128;
-  a->splits = (int)((row + a->run - 1) / a->run);
+  const int stages = (int)((row + 127) / 128);
+  const double stage = (f32 ? 0.46 : 0.08) / (64 * 64), sum = f32 ? 2.0 : 4.0;
+  const double worth = f32 ? 1.0 : 0.9;   // (16 bits: less is not sure)
+  const double tile = a->tile == 256 ? c256 : a->tile == 128 ? c128 : c64;
+  double best = tile * stage * (stages + 3);
+  for (int runs = 2; runs <= 16 && runs * (f32 ? 2 : 4) <= stages; ++runs) {
+    const int run = (stages + runs - 1) / runs;
+    if ((stages + run - 1) / run != runs) continue;
+    const double t = fullest(*a, cus, 64, runs, s64, alone64) * stage * (run + 3) + sum +
+                     8.0 * runs * a->T * n_pad / 6e6;
+    if (t >= worth * best) continue;
+    best = t;
+    a->splits = runs;
+    a->run = run * 128;
+  }
+  if (a->splits == 0) return 0;
+  a->tile = 64;
   return 4LL * a->splits * a->T * n_pad;
 }
 
