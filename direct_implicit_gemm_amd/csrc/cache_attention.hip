@@ -1316,15 +1316,21 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   if (many) {
     // Sets of 128 rows, each with its keys in up to as many shares as make 4 workgroups
     // a compute unit: 9 entries of 517 rows in all behind up to 4096
-    // keys, 4 heads of 80 in fp16: 67 us; 2 a unit 77, 3: 69, 6: 71.  Where that is not
-    // one for every second unit, sets of 32 rows: 2 entries of 130 rows and 8 heads
-    // of 64, 520 keys, fp32: 13 us, with sets of 128 rows 25.
+    // keys, 4 heads of 80 in fp16: 67 us; 2 a unit 77, 3: 69, 6: 71.  Shares of 512 keys or
+    // more, past 32 of them of 2048 (what they leave has to be joined): 16 rows of 4 heads of 128,
+    // 131072 keys, bfloat16, 16 shares 194 us, 32: 112, 64: 84, 128: 100; 100 rows of 2 heads, 32768
+    // keys 68, 60, 75 us.
     const long long n = row_sets(*a, kManyRows) * a->c.Hk;
+    const long long of512 = keys / 512 < 32 ? keys / 512 : 32, of2048 = keys / 2048;
     long long s = 4LL * cus / n;
-    if (s > keys / 512) s = keys / 512;
-    if (s > 16) s = 16;
+    if (s > (of512 > of2048 ? of512 : of2048)) s = of512 > of2048 ? of512 : of2048;
     if (s < 1 || !allowed) s = 1;
-    if (n * s >= cus / 2) {
+    // Where that is not one for every second unit, sets of 32 rows, a workgroup with all
+    // keys of its set each: 2 entries of 130 rows and 8 heads of 64, 520 keys, fp32: 13 us, with
+    // sets of 128 rows 25.  But only while there are few keys: 16 rows of 4 heads of 128,
+    // sets of 32 / 128 rows, 1024 keys 17 / 22 us, 2048: 27 / 23, 8192: 87 / 28, 131072: 1289 / 84;
+    // one token of 64 heads that share one, 1024: 16 / 21, 2048: 26 / 22, 131072: 1283 / 81.
+    if (n * s >= cus / 2 || s >= 4) {
       a->set = kManyRows;
       a->splits = (int)s;
     }

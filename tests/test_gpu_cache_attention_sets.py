@@ -20,8 +20,9 @@ def plan(B, T, most, hq, hk, positions, workspace=True):
     in a table of that many positions."""
     G = hq // hk
     sets = min(-(-most * G // 128) * B, T * G // 128 + B) * hk
-    shares = max(1, min(4 * CUS // sets, positions // 512, 16)) if workspace else 1
-    return (128, shares) if sets * shares >= CUS // 2 else (32, 1)
+    most = max(min(positions // 512, 32), positions // 2048)
+    shares = max(1, min(4 * CUS // sets, most)) if workspace else 1
+    return (128, shares) if sets * shares >= CUS // 2 or shares >= 4 else (32, 1)
 
 
 def of_sets(q, cache, rows, causal=True, workspace=True, **kw):
@@ -49,6 +50,9 @@ def test_the_rule():
     assert plan(2, 301, 300, 16, 4, 1312) == (32, 1)      # too few sets
     assert plan(1, 513, 513, 8, 4, 4224) == (128, 8)
     assert plan(1, 513, 513, 8, 4, 4224, False) == (32, 1)
+    assert plan(1, 16, 16, 16, 4, 131072) == (128, 64)    # few sets, many keys
+    assert plan(1, 1, 1, 64, 1, 16384) == (128, 32)
+    assert plan(1, 16, 16, 16, 4, 2032) == (32, 1)
 
 
 ROWS, LENGTHS, HEADS = [400, 300], [520, 333], 20   # 140 sets
@@ -184,3 +188,21 @@ def test_long_keys_in_shares(dtype):
         cache = C.Cache(2, [20011, 6000], 64, hk, 64, "i8", seed=22)
         _, tiles = of_sets(queries(sum(rows), hk, 64, dtype), cache, rows, what="shares")
         assert tiles > least
+
+
+@pytest.mark.parametrize("codes,dtype", [("i8", "bf16"), ("e4m3", "f16"), ("i8", "f32")])
+@pytest.mark.parametrize("rows,lengths,hq,hk,d", [
+    ([16], [20011], 16, 4, 128),            # a chunk of one long request
+    ([1], [20011], 64, 1, 64),              # a token of heads that all share one
+    ([1] * 4, [9001, 3, 8192, 5000], 64, 1, 128),
+    ([100], [16400], 2, 2, 64),
+    ([3, 40, 0, 1], [700, 12345, 9000, 2049], 4, 1, 80),
+    ([40], [70001], 1, 1, 64),              # shares of more than 512 keys
+], ids=str)
+def test_few_sets_of_long_keys(rows, lengths, hq, hk, d, codes, dtype):
+    cache = C.Cache(len(rows), lengths, 16, hk, d, codes, seed=23)
+    q = queries(sum(rows), hq, d, dtype)
+    first, tiles = of_sets(q, cache, rows, what="few sets")
+    assert tiles <= max(32, -(-max(lengths) // 64) // 4)
+    alone = check(q, cache, C.starts(rows), True, max_rows=max(rows), workspace=False, what="alone")
+    assert bool(torch.isfinite(alone).all()) and bool(torch.isfinite(first).all())
