@@ -29,7 +29,10 @@ constexpr int kFewRows = 32;     // rows of a key head that one set of matrix co
 
 // Terms that q and the probabilities enter the matrix instructions as: bfloat16
 // holds 8 bits, fp16's 11 and fp32's 24 take two and three.  (q in fp16 meets
-// codes in fp16; the probabilities times their scale may be past its range.)
+// codes in fp16; the probabilities times their scale may be past its range.)  q is
+// exact.  The probabilities are rounded to what the output holds, as in attention.hip:
+// each is off by half a step of it, which a sum of many evens out (bfloat16: 0.0023 of
+// the output in all, of which the output's own rounding is 0.0016).
 template <int DT> struct Terms {
   static constexpr int Q = DT == DT_F32 ? 3 : 1, P = DT == DT_F32 ? 3 : DT == DT_F16 ? 2 : 1;
   static constexpr int KT = DT == DT_F16 ? DT_F16 : DT_BF16;   // type of the first product
@@ -199,7 +202,8 @@ template <class W> struct Entries {
 // where a head begins with kStart tiles' time of no keys (a workgroup reads queries and
 // table and fills its stages meanwhile): tile t of a head that begins at u is at
 // u + kStart + t.
-constexpr int kStart = 2;   // (that batch: 0 129 us, 2 117, 3 119, 5 120)
+constexpr int kStart = 2;   // (64 entries of 1 to 8192 keys and 8 heads of 128: 0 129 us, 2 117,
+                            // 3 119, 5 120)
 __device__ __forceinline__ int few_units(const Entry& e) {
   const int t = few_tiles(e);
   return t > 0 ? t + kStart : 0;
@@ -549,7 +553,8 @@ __device__ __forceinline__ void attend_few(const CacheAttnArgs& a, const Job& jo
 // Many rows: four waves of 32 rows share tiles of 64 keys, widened to 16 bits once
 // for all of them (each wave widening the keys that it meets, as few rows do: 8 x
 // 2048 rows behind 4096 tokens, 32 / 8 heads of 128, 1500 us; shared: 820, 1.0
-// PFLOP/s in bfloat16; matrix units 44 % busy, vector units 51, LDS 55).  64 rows
+// PFLOP/s in bfloat16; matrix units 45 % busy, vector units 55, LDS 45, a quarter of
+// that with bank conflicts).  64 rows
 // a wave: 1009 instead of 848 us, one workgroup of eight waves: 1300.  A wave
 // reads the codes of 16 rows of keys and of values a tile ahead into registers,
 // and widens them into LDS a tile (keys: two) before they are used.  A power of
@@ -1023,8 +1028,8 @@ __device__ __forceinline__ void few_run(const CacheAttnArgs& a, int group, unsig
   }
 }
 
-// `units` workgroups of 32 rows of a key head, for calls that have few such sets,
-// and behind them those of the entries of few rows.
+// `units` workgroups of 32 rows of a key head, for calls that have few such sets and
+// few keys, and behind them those of the entries of few rows.
 template <int DT, int CF, int DP>
 __global__ __launch_bounds__(kFewThreads, 2) void few_kernel(const CacheAttnArgs a, int units,
                                                              int all) {

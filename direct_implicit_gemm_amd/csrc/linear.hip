@@ -18,9 +18,8 @@ namespace {
 // quotient are the hardware's (about one step each), but an exponent u is off by
 // half steps of itself, so that results of large negative sums are off by 6 |u|
 // of fp32's half steps (less than a 16-bit output's step up to |u| = 80).
-// GELU = v Phi(v): Phi(-a) = erfcx(a / sqrt 2) exp(-a^2 / 2) / 2, for its tail (by
-// 1 + erf, or an erf of bounded absolute error, nothing right is left of the
-// results from v = -5 on).
+// GELU = v Phi(v): Phi(-a) = erfcx(a / sqrt 2) exp(-a^2 / 2) / 2, for its tail (1 + erf
+// is 4 % off at v = -5 in fp32, and 0 from -5.6 on).
 template <int DT, int ACT> __device__ __forceinline__ float activated(float v) {
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr float kTwoC = 2.0f * 0.7978845608028654f;   // sqrt(2 / pi)
