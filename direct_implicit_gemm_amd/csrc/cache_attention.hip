@@ -214,7 +214,8 @@ __device__ __forceinline__ long long share_of(long long total, int groups) {
 }
 
 // Rows `row_tile` * 32 .. of key head hk of an entry over tiles t0 .. t1 - 1 of its
-// keys, in order; slot: where the partial result goes (-1: to the output).
+// keys, in order; slot: where the partial result goes (-1: to the output), in units of
+// the rows that a workgroup takes.
 struct Job {
   Entry e;
   int b, hk, row_tile, t0, t1;
@@ -927,7 +928,7 @@ __device__ __forceinline__ void attend_many(const CacheAttnArgs& a, const Job& j
   if (!row_ok) return;
   const float inv = sum > 0.0f ? 1.0f / sum : sum;   // 0 keys: 0; a NaN stays
   const float lse2 = sum == 0.0f ? kNegInf : m + (__builtin_amdgcn_logf(sum) - LIFT);
-  const long long t = job.e.row0 + qi, at = (job.slot * a.T + t) * heads + head;
+  const long long t = job.e.row0 + qi, at = job.slot * kManyRows + wave * 32 + l32;
   if (half == 0) {
     if (job.slot >= 0) a.many_lse[at] = lse2;
     else if (a.lse) a.lse[t * heads + head] = lse2 * kLn2;
@@ -1066,12 +1067,12 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a
     few_run<DT, CF, DP>(a, blockIdx.x - units * a.splits, lds);
     return;
   }
-  const int split = blockIdx.x / units;
+  const int split = blockIdx.x / units, unit = blockIdx.x - split * units;
   Unit u;
   // (consecutive workgroups, which lie on different XCDs, are of different heads: an
   // XCD then reads few heads of every entry, however long each is.  With an XCD to
   // an entry the longest one held up the end.)
-  if (!unit_of(a, blockIdx.x - split * units, kManyRows, all, &u)) return;
+  if (!unit_of(a, unit, kManyRows, all, &u)) return;
   const CacheView& c = a.c;
   const int tiles = (u.keys + Z::BN - 1) / Z::BN, shares = shares_of(a, u, Z::BN);
   if (split >= shares) return;
@@ -1081,7 +1082,7 @@ __global__ __launch_bounds__(kThreads, 2) void many_kernel(const CacheAttnArgs a
                    u.set,
                    (int)((long long)tiles * split / shares),
                    (int)((long long)tiles * (split + 1) / shares),
-                   shares > 1 ? split : -1};
+                   shares > 1 ? (long long)split * units + unit : -1};
   // whether all blocks are there, with scales that the widened numbers can take in
   bool plain = true;
   const int last = job.t1 * Z::BN < u.e.len ? job.t1 * Z::BN : u.e.len;
@@ -1207,7 +1208,8 @@ __device__ __forceinline__ void join_few(const CacheAttnArgs& a, int g, int part
 // lanes a row, 4 components a lane.
 constexpr int kParts = 4;
 template <int DT, int LPR>
-__device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int part, int all) {
+__device__ __forceinline__ void join_many(const CacheAttnArgs& a, int units, int unit, int part,
+                                          int all) {
   Unit u;
   if (!unit_of(a, unit, kManyRows, all, &u)) return;
   const int shares = shares_of(a, u, Wide<128>::BN);
@@ -1219,7 +1221,8 @@ __device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int 
     const int row = u.set * kManyRows + r;
     if (row >= u.e.rows) return;
     const int qi = row / a.G, head = u.hk * a.G + row - qi * a.G;
-    const long long t = u.e.row0 + qi, step = (long long)a.T * heads, at = t * heads + head;
+    const long long t = u.e.row0 + qi, step = (long long)units * kManyRows;
+    const long long at = (long long)unit * kManyRows + r;
     float m = kLowest, sum = 0.0f;
     float4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
     constexpr int U = 4;
@@ -1241,7 +1244,7 @@ __device__ __forceinline__ void join_many(const CacheAttnArgs& a, int unit, int 
     }
     const float inv = sum > 0.0f ? 1.0f / sum : sum;
     if (a.lse && lane == 0)
-      a.lse[at] = sum == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+      a.lse[t * heads + head] = sum == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(sum)) * kLn2;
     if (!live) continue;
     char* op = a.out + t * a.o_r + head * a.o_h;
     if constexpr (DT == DT_F32)
@@ -1259,7 +1262,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const CacheAttnArgs a, i
                                                         int all) {
   const int x = blockIdx.x;
   if (x < units * kParts) {
-    join_many<DT, LPR>(a, x / kParts, x & (kParts - 1), all);
+    join_many<DT, LPR>(a, units, x / kParts, x & (kParts - 1), all);
   } else {
     const int y = x - units * kParts;
     join_few<DT, LPR>(a, y / rows, y % rows);
@@ -1283,8 +1286,7 @@ void launch(const CacheAttnArgs& a, hipStream_t stream) {
   // all entries have the most rows, or (rows of no entry) none does
   const int all = most > kFewRows && (long long)a.T == (long long)a.max_rows * a.c.B;
   const int groups = all || a.G > kFewRows ? 0 : a.few_groups > 0 ? a.few_groups : a.c.B * a.c.Hk;
-  const int units = most <= kFewRows ? 0
-                    : (int)((a.sets > 0 ? (long long)a.sets * a.c.B : row_sets(a, a.set)) * a.c.Hk);
+  const int units = a.units;
   if (a.set == kManyRows)
     hipLaunchKernelGGL((many_kernel<DT, CF, DP>), dim3((unsigned)(units * a.splits + groups)),
                        dim3(kThreads), 0, stream, a, units, all);
@@ -1315,6 +1317,7 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   a->splits = 1;
   a->set = 32;
   a->sets = 0;
+  a->units = 0;
   if (a->T == 0 || a->c.B == 0) return 0;
   const long long keys = (long long)a->c.width << a->c.log_block;
   const bool many = (long long)a->max_rows * a->G > kFewRows;
@@ -1356,13 +1359,15 @@ long long cache_attn_plan(CacheAttnArgs* a, int dtype, int cus, bool allowed) {
   // up to 2048 keys, 64 heads 16 / 19, 256 heads 27 / 20.
   if (allowed && a->G <= kFewRows && keys >= 1024 && keys >= 16LL * a->c.B * a->c.Hk)
     a->few_groups = 2 * cus;
-  const long long rows = a->splits > 1 ? (long long)a->T * a->G * a->c.Hk * a->splits : 0;
+  if (many)
+    a->units = (int)((a->sets > 0 ? (long long)a->sets * a->c.B : row_sets(*a, a->set)) * a->c.Hk);
+  const long long rows = a->splits > 1 ? (long long)a->units * kManyRows * a->splits : 0;
   return (2LL * a->few_groups * kFewRows + rows) * (a->c.D + 1) * 4;
 }
 
 void cache_attn_place(CacheAttnArgs* a, char* workspace) {
   const long long few = 2LL * a->few_groups * kFewRows;
-  const long long rows = (long long)a->T * a->G * a->c.Hk * a->splits;
+  const long long rows = (long long)a->units * kManyRows * a->splits;
   a->part = reinterpret_cast<float*>(workspace);
   a->many = a->part + few * a->c.D;
   a->part_lse = a->many + (a->splits > 1 ? rows * a->c.D : 0);

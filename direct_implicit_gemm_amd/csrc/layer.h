@@ -113,9 +113,11 @@ struct CacheAttnArgs {
                             // 0: one to an entry and key head
   int set;                  // rows of a key head of entries of more rows to a workgroup
   int sets;                 // of each entry; 0: side by side
+  int units;                // sets in all, with their key heads
   int splits;               // and shares of their keys
-  // partial results of the former [2 few_groups][32] and of the latter [splits][T]
-  // [q heads], normed: D outputs and the log2 of their sum, each
+  // partial results of the former [2 few_groups][32] and of the latter [splits][units]
+  // [set] (rows of no entry take no room), normed: D outputs and the log2 of their sum,
+  // each
   float *part, *part_lse, *many, *many_lse;
 };
 // Fills the plan for `cus` compute units and returns the workspace bytes it

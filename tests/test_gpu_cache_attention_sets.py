@@ -35,7 +35,10 @@ def of_sets(q, cache, rows, causal=True, workspace=True, **kw):
     # the same rule in the library, as far as its workspace tells: rows' partial results of each
     # share, and 64 for each of 512 workgroups that share the keys of few rows
     few = 512 if hq // hk <= 32 and positions >= max(1024, 16 * B * hk) else 0
-    want = (64 * few + (T * hq * shares if shares > 1 else 0)) * (d + 1) * 4
+    each = -(-most * (hq // hk) // 128) * B
+    side = min(each, T * (hq // hk) // 128 + B)
+    units = (each if each <= 2 * side else side) * hk
+    want = (64 * few + (units * 128 * shares if shares > 1 else 0)) * (d + 1) * 4
     if workspace:
         assert L.libconv_cache_attention_workspace(
             B, T, most, cache.block, cache.width, hq, hk, d,
@@ -206,3 +209,14 @@ def test_few_sets_of_long_keys(rows, lengths, hq, hk, d, codes, dtype):
     assert tiles <= max(32, -(-max(lengths) // 64) // 4)
     alone = check(q, cache, C.starts(rows), True, max_rows=max(rows), workspace=False, what="alone")
     assert bool(torch.isfinite(alone).all()) and bool(torch.isfinite(first).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_padded_batch_in_shares(dtype):
+    """Rows of no entry before, between and behind, in a buffer of far more rows than sets."""
+    cache = C.Cache(3, [5000, 300, 9000], 16, 2, 64, "i8", seed=24)
+    q = queries(3000, 8, 64, dtype)
+    starts = torch.tensor([7, 47, 48, 178]).int().cuda()
+    out = torch.full_like(q, 3.0)
+    check(q, cache, starts, True, what="padded", max_rows=130, out=out)
+    assert bool((out[:7] == 3.0).all()) and bool((out[178:] == 3.0).all())
