@@ -315,7 +315,8 @@ struct Write {
     // rows of one entry: a block's heads; single tokens: those of each row
     const unsigned block = (2u * a.c.Hk + 3) / 4;
     const unsigned rows = turns(x, 2LL * a.c.Hk * (a.T < size ? a.T : size));
-    const dim3 grid((unsigned)x, block > rows ? block : rows), threads(kThreads);
+    const unsigned y = block > rows ? block : rows;
+    const dim3 grid((unsigned)x, y > 65535 ? 65535 : y), threads(kThreads);
     // (registers for no more than a block has: blocks of 16 tokens leave most idle)
     if (size * a.c.D * Elem<DT>::bytes <= 8 * 1024)
       hipLaunchKernelGGL((write_kernel<DT, CF, 8>), grid, threads, 0, stream, a);

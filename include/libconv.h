@@ -808,8 +808,9 @@ long long libconv_cache_attention_workspace(int B, int T, int max_rows, int bloc
  * K: a multiple of 8; x and w on 16-byte boundaries; rows of x and w below 2^23
  * bytes, T below 2^26 - 64.
  *   workspace  device, 256-byte aligned, at least libconv_linear_workspace bytes
- *              for the best plan, which splits the sums of few rows over
- *              workgroups; NULL or smaller: a plan without.
+ *              for the best plan, which splits the sums of few rows, and others
+ *              whose tiles would leave compute units idle, over workgroups; NULL or
+ *              smaller: a plan without.
  */
 libconv_status libconv_linear(const void* x, const void* w, const void* bias,
                               const void* residual, void* y, int T, int K, int N,
